@@ -25,6 +25,8 @@ __all__ = [
     "dflash2_ragged_offsets", "dflash2_conv_finish_ragged", "dflash2_score_edges_ragged",
     "dflash2_conv_coefficients", "dflash2_proj", "dflash2_proj_conv_in", "dflash2_proj_conv_out",
     "dflash2_proj_workspace_bytes",
+    "dflash2_kv4_page_bytes", "dflash2_kv4_cache", "dflash2_kv4_append", "dflash2_kv4_read",
+    "dflash2_kv4_attention_workspace_bytes", "dflash2_kv4_attention",
     "DTYPE_CODES",
 ]
 
@@ -38,6 +40,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_i64 = ctypes.c_int64
 
 _SIGNATURES = {
     "dflash2_version": (_i, []),
@@ -69,6 +72,12 @@ _SIGNATURES = {
     "dflash2_proj_conv_in": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _sz, _vp]),
     "dflash2_proj_conv_out": (_i, [_vp, _i, _i, _vp, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _sz,
                                    _vp]),
+    "dflash2_kv4_page_bytes": (_sz, [_i, _i, _i]),
+    "dflash2_kv4_append": (_i, [_vp, _vp, _i64, _i64, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp]),
+    "dflash2_kv4_read": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "dflash2_kv4_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "dflash2_kv4_attention": (_i, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
+                                   _i, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -516,4 +525,124 @@ def dflash2_proj_conv_out(a, w, coef1, base, G, group_size, residual=None, w_sca
         _dev(a, "a", torch.bfloat16), M, K, *wp, wbits, N, _dev(coef1, "coef1", torch.bfloat16),
         _dev(base, "base", torch.float32), G, group_size, _dev(residual, "residual", torch.bfloat16, True), BF16,
         _dev(out, "out", torch.bfloat16), *ws, _stream(stream)))
+    return out
+
+
+def dflash2_kv4_page_bytes(heads, head_dim, page_size) -> int:
+    return library().dflash2_kv4_page_bytes(heads, head_dim, page_size)
+
+
+def dflash2_kv4_cache(num_pages, heads, head_dim, page_size, device="cuda"):
+    """An empty 4-bit key/value cache: uint8 [num_pages, heads, 2 (keys, values), page_size / 16,
+    granule bytes] (its contents are whatever the memory held; attention reads only what ctx_len covers)."""
+    n = dflash2_kv4_page_bytes(heads, head_dim, page_size)
+    if n == 0:
+        raise ValueError(library().dflash2_last_error_message().decode(errors="replace"))
+    return torch.empty((num_pages, heads, 2, page_size // 16, n // (2 * heads * (page_size // 16))), dtype=torch.uint8,
+                       device=device)
+
+
+def _kv4_cache_shape(cache, head_dim, page_size):
+    """(num_pages, heads) of a cache tensor, checked against the head and page sizes."""
+    if cache.dim() != 5 or cache.shape[2] != 2 or cache.shape[3] * 16 != page_size \
+            or cache.shape[4] != 16 * (head_dim // 2 + head_dim // 64 * 4):
+        raise ValueError(f"cache must be [pages, heads, 2, {page_size} / 16, {16 * (head_dim // 2 + head_dim // 64 * 4)}] "
+                         f"for head_dim {head_dim}, got {tuple(cache.shape)}")
+    return cache.shape[0], cache.shape[1]
+
+
+def _kv4_rows(t, name, rows, heads, head_dim):
+    """(pointer, row stride) of a [..., heads, head_dim] bf16 tensor whose leading dimensions walk
+    `rows` equally spaced rows; the last two are dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    shape, stride = t.shape, t.stride()
+    if shape[-2:] != (heads, head_dim) or t.numel() != rows * heads * head_dim:
+        raise ValueError(f"{name} must hold {rows} rows of [{heads}, {head_dim}], got {tuple(shape)}")
+    if stride[-1] != 1 or (heads > 1 and stride[-2] != head_dim):
+        raise ValueError(f"{name}: each row's [{heads}, {head_dim}] must be dense")
+    if len(shape) == 3:
+        step = stride[0] if rows > 1 else heads * head_dim
+    else:  # [B, G, heads, head_dim]
+        B, G = shape[0], shape[1]
+        step = stride[1] if G > 1 else (stride[0] if B > 1 else heads * head_dim)
+        if B > 1 and stride[0] != G * step:
+            raise ValueError(f"{name}: its {B} x {G} rows must be equally spaced")
+    return _vp(t.data_ptr()), step
+
+
+def dflash2_kv4_append(k, v, slots, cache, page_size, stream=None):
+    """Quantise rows of keys and values [T, heads, head_dim] (bf16; rows may be strided) into the
+    cache's slots [T] (int64; negative: skip the row)."""
+    if k.dim() != 3:
+        raise ValueError(f"k must be [T, heads, head_dim], got shape {tuple(k.shape)}")
+    T, heads, D = k.shape
+    pages, cache_heads = _kv4_cache_shape(cache, D, page_size)
+    if cache_heads != heads:
+        raise ValueError(f"the cache holds {cache_heads} heads, k has {heads}")
+    if slots.numel() != T:
+        raise ValueError(f"slots holds {slots.numel()} entries, expected {T}")
+    kp, ks = _kv4_rows(k, "k", T, heads, D)
+    vp, vs = _kv4_rows(v, "v", T, heads, D)
+    _check(library().dflash2_kv4_append(kp, vp, ks, vs, _dev(slots, "slots", torch.int64), T, heads, D, page_size, pages,
+                                        BF16, _dev(cache, "cache", torch.uint8), _stream(stream)))
+    return cache
+
+
+def dflash2_kv4_read(cache, slots, head_dim, page_size, k=None, v=None, stream=None):
+    """The values of the cache's slots [T]: (k, v), each [T, heads, head_dim] bf16 (zeros for negative slots)."""
+    pages, heads = _kv4_cache_shape(cache, head_dim, page_size)
+    T = slots.numel()
+    shape = (T, heads, head_dim)
+    k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
+    v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
+    for t, name in ((k, "k"), (v, "v")):
+        if t.numel() < T * heads * head_dim:
+            raise ValueError(f"{name} holds {t.numel()} elements, fewer than the {T * heads * head_dim} the call writes")
+    _check(library().dflash2_kv4_read(_dev(cache, "cache", torch.uint8), _dev(slots, "slots", torch.int64), T, heads,
+                                      head_dim, page_size, pages, BF16, _dev(k, "k", torch.bfloat16),
+                                      _dev(v, "v", torch.bfloat16), _stream(stream)))
+    return k, v
+
+
+def dflash2_kv4_attention_workspace_bytes(B, G, q_heads, kv_heads, head_dim, page_size, max_pages) -> int:
+    return library().dflash2_kv4_attention_workspace_bytes(B, G, q_heads, kv_heads, head_dim, page_size, max_pages)
+
+
+def dflash2_kv4_attention(q, cache, page_table, ctx_len, page_size, scale, k_new=None, v_new=None, causal=False,
+                          window=0, out=None, workspace=None, stream=None):
+    """Attention of q [B, G, q_heads, head_dim] (bf16, rows may be strided) over each sequence's cached
+    rows (page_table [B, max_pages], ctx_len [B], int32) and its own rows k_new, v_new
+    [B, G, kv_heads, head_dim] when given; see dflash2.h for what a row sees. Returns out
+    [B, G, q_heads, head_dim] bf16."""
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, G, q_heads, head_dim], got shape {tuple(q.shape)}")
+    B, G, Hq, D = q.shape
+    pages, Hkv = _kv4_cache_shape(cache, D, page_size)
+    if page_table.dim() != 2 or page_table.shape[0] != B or ctx_len.numel() != B:
+        raise ValueError(f"page_table must be [{B}, max_pages] and ctx_len [{B}]")
+    qp, qs = _kv4_rows(q, "q", B * G, Hq, D)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    kp = vp = None
+    ns = 0
+    if k_new is not None:
+        kp, ns = _kv4_rows(k_new, "k_new", B * G, Hkv, D)
+        vp, vs = _kv4_rows(v_new, "v_new", B * G, Hkv, D)
+        if vs != ns:
+            raise ValueError(f"k_new and v_new must have the same row stride, got {ns} and {vs}")
+    if out is None:
+        out = torch.empty((B, G, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if out.numel() < B * G * Hq * D:
+        raise ValueError(f"out holds {out.numel()} elements, fewer than the {B * G * Hq * D} the call writes")
+    width = page_table.shape[1]
+    lib = library()
+    if workspace is None:
+        need = lib.dflash2_kv4_attention_workspace_bytes(B, G, Hq, Hkv, D, page_size, width)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    wp, wn = (None, 0) if workspace is None else (_dev(workspace, "workspace"), workspace.numel())
+    _check(lib.dflash2_kv4_attention(
+        qp, qs, _dev(cache, "cache", torch.uint8), _dev(page_table, "page_table", torch.int32),
+        _dev(ctx_len, "ctx_len", torch.int32), kp, vp, ns, B, G, Hq, Hkv, D, page_size, pages, width, int(bool(causal)),
+        window, scale, BF16, _dev(out, "out", torch.bfloat16), wp, wn, _stream(stream)))
     return out

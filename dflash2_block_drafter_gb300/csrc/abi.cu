@@ -443,6 +443,96 @@ int dflash2_select_path(const float* S, const int32_t* cand, int B, int steps, i
   return launch_select_path(S, cand, B, steps, K, path, static_cast<cudaStream_t>(stream));
 }
 
+static int check_kv4(int heads, int D, int page_size, int num_pages, int dtype) {
+  if (dtype != DFLASH2_BF16) return fail(DFLASH2_ERR_UNSUPPORTED, "the 4-bit cache takes bf16 rows only (dtype=%d)", dtype);
+  REQUIRE(heads >= 1, "heads=%d must be >= 1", heads);
+  REQUIRE(D == 64 || D == 128, "head_dim=%d must be 64 or 128", D);
+  REQUIRE(page_size >= 16 && page_size <= 4096 && (page_size & (page_size - 1)) == 0,
+          "page_size=%d must be a power of two in [16, 4096]", page_size);
+  REQUIRE(num_pages >= 1, "num_pages=%d must be >= 1", num_pages);
+  return DFLASH2_OK;
+}
+
+size_t dflash2_kv4_page_bytes(int heads, int D, int page_size) {
+  if (check_kv4(heads, D, page_size, 1, DFLASH2_BF16) != DFLASH2_OK) return 0;
+  return static_cast<size_t>(heads) * 2 * page_size * (D / 2 + D / 64 * 4);
+}
+
+int dflash2_kv4_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int64_t* slots, int T,
+                       int heads, int D, int page_size, int num_pages, int dtype, void* cache, void* stream) {
+  int rc = check_kv4(heads, D, page_size, num_pages, dtype);
+  if (rc != DFLASH2_OK) return rc;
+  REQUIRE(T >= 0, "T=%d must be >= 0", T);
+  if (T == 0) return DFLASH2_OK;
+  REQUIRE(k && v && slots && cache, "a required pointer is NULL");
+  REQUIRE(aligned16(k) && aligned16(v) && aligned16(cache), "k, v and cache must be 16-byte aligned");
+  const int64_t row = static_cast<int64_t>(heads) * D;
+  REQUIRE(k_stride >= row && k_stride % 8 == 0 && v_stride >= row && v_stride % 8 == 0,
+          "row strides %lld, %lld must be multiples of 8 and at least heads * head_dim = %lld",
+          static_cast<long long>(k_stride), static_cast<long long>(v_stride), static_cast<long long>(row));
+  const Kv4Rows r{k, v, k_stride, v_stride, slots, T, heads, D, page_size, num_pages, cache, nullptr, nullptr};
+  return launch_kv4_rows(r, static_cast<cudaStream_t>(stream));
+}
+
+int dflash2_kv4_read(const void* cache, const int64_t* slots, int T, int heads, int D, int page_size, int num_pages,
+                     int dtype, void* k, void* v, void* stream) {
+  int rc = check_kv4(heads, D, page_size, num_pages, dtype);
+  if (rc != DFLASH2_OK) return rc;
+  REQUIRE(T >= 0, "T=%d must be >= 0", T);
+  if (T == 0) return DFLASH2_OK;
+  REQUIRE(k && v && slots && cache, "a required pointer is NULL");
+  REQUIRE(aligned16(k) && aligned16(v) && aligned16(cache), "k, v and cache must be 16-byte aligned");
+  const Kv4Rows r{nullptr, nullptr, 0, 0, slots, T, heads, D, page_size, num_pages, const_cast<void*>(cache), k, v};
+  return launch_kv4_rows(r, static_cast<cudaStream_t>(stream));
+}
+
+static int check_kv4_attention(int B, int G, int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages,
+                               int dtype) {
+  int rc = check_kv4(Hkv, D, page_size, num_pages, dtype);
+  if (rc != DFLASH2_OK) return rc;
+  REQUIRE(B >= 1, "B=%d must be >= 1", B);
+  REQUIRE(G >= 1 && G <= 64, "G=%d must be in [1, 64]", G);
+  REQUIRE(Hq >= Hkv && Hq % Hkv == 0 && Hq / Hkv <= 64, "Hq=%d must be 1 to 64 times Hkv=%d", Hq, Hkv);
+  REQUIRE(max_pages >= 1 && static_cast<int64_t>(max_pages) * page_size <= 0x7fffff00LL,
+          "max_pages=%d must be >= 1, and a sequence's pages hold less than 2^31 tokens", max_pages);
+  return DFLASH2_OK;
+}
+
+size_t dflash2_kv4_attention_workspace_bytes(int B, int G, int Hq, int Hkv, int D, int page_size, int max_pages) {
+  if (check_kv4_attention(B, G, Hq, Hkv, D, page_size, 1, max_pages, DFLASH2_BF16) != DFLASH2_OK) return 0;
+  return kv4_attention_workspace(B, G, Hq, Hkv, D, page_size, max_pages, sm_count());
+}
+
+int dflash2_kv4_attention(const void* q, int64_t q_stride, const void* cache, const int32_t* page_table,
+                          const int32_t* ctx_len, const void* k_new, const void* v_new, int64_t new_stride, int B, int G,
+                          int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages, int causal, int window,
+                          float scale, int dtype, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_kv4_attention(B, G, Hq, Hkv, D, page_size, num_pages, max_pages, dtype);
+  if (rc != DFLASH2_OK) return rc;
+  REQUIRE(q && cache && page_table && ctx_len && out, "a required pointer is NULL");
+  REQUIRE((k_new == nullptr) == (v_new == nullptr), "k_new and v_new must be both set or both NULL");
+  REQUIRE(aligned16(q) && aligned16(cache) && aligned16(out) && aligned16(k_new) && aligned16(v_new),
+          "q, cache, k_new, v_new and out must be 16-byte aligned");
+  REQUIRE(q_stride >= static_cast<int64_t>(Hq) * D && q_stride % 8 == 0,
+          "q_stride=%lld must be a multiple of 8 and at least Hq * head_dim", static_cast<long long>(q_stride));
+  if (k_new != nullptr)
+    REQUIRE(new_stride >= static_cast<int64_t>(Hkv) * D && new_stride % 8 == 0,
+            "new_stride=%lld must be a multiple of 8 and at least Hkv * head_dim", static_cast<long long>(new_stride));
+  REQUIRE(window >= 0, "window=%d must be >= 0 (0: none)", window);
+  REQUIRE(causal == 0 || causal == 1, "causal=%d must be 0 or 1", causal);
+  REQUIRE(scale == scale && scale - scale == 0.f, "scale must be finite");
+  const size_t need = kv4_attention_workspace(B, G, Hq, Hkv, D, page_size, max_pages, sm_count());
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(DFLASH2_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes,
+                  need);
+    REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, "workspace must be 256-byte aligned");
+  }
+  const Kv4Attention r{q, q_stride, cache, page_table, ctx_len, k_new, v_new, new_stride, B, G, Hq, Hkv, D, page_size,
+                       num_pages, max_pages, causal, window, scale, out, workspace};
+  return launch_kv4_attention(r, static_cast<cudaStream_t>(stream));
+}
+
 int dflash2_selftest_bounded_wait(int limit_us, void* stream) {
   REQUIRE(limit_us >= 1 && limit_us <= 1000000, "limit_us=%d must be in [1, 1000000]", limit_us);
   return launch_wait_selftest(limit_us, static_cast<cudaStream_t>(stream));

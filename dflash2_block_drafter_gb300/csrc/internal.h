@@ -178,6 +178,30 @@ int launch_proj(const ProjSpec& p, cudaStream_t st);
 int launch_conv_coefficients(const float* part, int k_splits, int M, int groups, int dtype, float* d0, void* coef1,
                              cudaStream_t st);
 
+// ---------------------------------------------------------------- 4-bit key/value cache (kv4.cu)
+struct Kv4Rows {  // k_out / v_out null: k, v -> cache; else cache -> k_out, v_out
+  const void *k, *v;
+  int64_t k_stride, v_stride;  // elements between rows
+  const int64_t* slots;
+  int T, heads, D, page_size, num_pages;
+  void* cache;
+  void *k_out, *v_out;
+};
+int launch_kv4_rows(const Kv4Rows& r, cudaStream_t st);
+struct Kv4Attention {
+  const void* q;
+  int64_t q_stride;
+  const void* cache;
+  const int32_t *table, *ctx;
+  const void *k_new, *v_new;  // both null: no rows of its own
+  int64_t new_stride;
+  int B, G, Hq, Hkv, D, page_size, num_pages, max_pages, causal, window;
+  float scale;
+  void *out, *workspace;
+};
+size_t kv4_attention_workspace(int B, int G, int Hq, int Hkv, int D, int page_size, int max_pages, int sms);
+int launch_kv4_attention(const Kv4Attention& r, cudaStream_t st);
+
 // ---------------------------------------------------------------- selector (selector.cu)
 // depths (nullable): per-block draft length of a mixed-depth batch; slots past it get path -1.
 // row_off (nullable): a ragged batch, block b's slots are rows row_off[b] .. row_off[b + 1] - 1 of

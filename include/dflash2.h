@@ -336,6 +336,65 @@ DFLASH2_API int dflash2_proj_conv_out(const void* a, int M, int K, const void* w
                                       int G, int group_size, const void* residual, int dtype, void* out,
                                       void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * The attention sublayer's key/value cache in 4 bits, and attention over it.
+ * (dflash2.ts #contextKV and #block: the block's queries attend to the context's keys and values and,
+ * bidirectionally, to the block's own; MAX DFlash2Qwen3_5.materialize, DRAFT_SLIDING_WINDOW. The
+ * 4-bit form is dflash2.ts quantizedWeight's affine one: groups of 64, scale and bias.) The pages do
+ * not quantise the cache; positions (rotary) are applied to q and k before these calls.
+ * bf16 only (DFLASH2_BF16; anything else returns DFLASH2_ERR_UNSUPPORTED); head_dim D 64 or 128.
+ *
+ * Cache: num_pages pages of dflash2_kv4_page_bytes(heads, D, page_size) bytes, 16-byte aligned;
+ *   page_size a power of two in [16, 4096]. A page is [heads][2: keys, values][page_size / 16]
+ *   granules; a granule holds 16 tokens: codes [16][D / 2] bytes (channel d's code in bits
+ *   4 (d % 8) .. 4 (d % 8) + 3 of the token's little-endian 32-bit word d / 8), then [16][D / 64]
+ *   pairs of bf16 (scale, bias). Per token, head and group of 64 channels:
+ *   bias = bf16(min x), scale = bf16((max x - min x) / 15), code = clamp(round((x - bias) / scale), 0, 15)
+ *   (fp32, ties to even; scale = 0 gives code 0). A code stands for scale * code + bias.
+ *   Slot s of the cache is token s % page_size of page s / page_size.
+ *
+ * dflash2_kv4_append: writes T rows (T >= 0) of keys and values into slots.
+ *   k, v       rows of [heads, D] dtype, k_stride / v_stride elements apart (multiples of 8, so that
+ *              slices of a fused projection's output can be passed).
+ *   slots [T]  int64: a negative slot skips its row; one past the cache records
+ *              DFLASH2_ERR_BAD_INDEX and skips it. A slot must not appear twice in a call.
+ * dflash2_kv4_read: the values of T slots, rounded to dtype: k, v [T, heads, D] dense; rows of
+ *   negative slots (and of slots past the cache, recorded as above) are zeros.
+ *
+ * dflash2_kv4_attention: G query rows of each of B sequences (G = 1: one token; a draft block's G
+ *   rows; 1 <= G <= 64) over its cached rows and, unless k_new is NULL, its own G rows in dtype.
+ *   q          [B, G, Hq, D]: rows q_stride elements apart (row b G + t). Query head h reads
+ *              key/value head h / (Hq / Hkv), Hq / Hkv <= 64.
+ *   page_table [B, max_pages] int32: page of tokens i page_size .. of each sequence. Entries that
+ *              no row needs (past ctx_len, or before every row's window) are not looked at; one
+ *              outside [0, num_pages) records DFLASH2_ERR_BAD_INDEX and its tokens count as unseen.
+ *   ctx_len    [B] int32 cached tokens L of each sequence, in [0, max_pages * page_size] (recorded as
+ *              DFLASH2_ERR_INVALID_ARG and clamped otherwise). Cache contents past L may be anything.
+ *   k_new, v_new [B, G, Hkv, D] or both NULL: rows new_stride elements apart; keys L .. L + G - 1.
+ *   Row t stands at position L + N - G + t (N = G with own rows, else 0: the rows' own keys are then
+ *   the last cached ones). causal = 1: it sees keys up to its position; 0: every key (the draft
+ *   block is bidirectional). window > 0: only keys after its position - window.
+ *   out        [B, G, Hq, D] dense: softmax(scale q k^T) v over the keys a row sees (fp32 scores,
+ *              statistics and sums; probabilities and dequantised values are rounded to bf16 for the
+ *              tensor cores); a row that sees no key gives zeros.
+ *   workspace  at least dflash2_kv4_attention_workspace_bytes(...) bytes, 256-byte aligned (NULL
+ *              when that is 0): partial results of contexts that several CTAs share. Needs no
+ *              initialisation. Results do not depend on timing: the same call gives the same bits.
+ * ---------------------------------------------------------------------------------- */
+DFLASH2_API size_t dflash2_kv4_page_bytes(int heads, int D, int page_size);
+DFLASH2_API int dflash2_kv4_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
+                                   const int64_t* slots, int T, int heads, int D, int page_size, int num_pages,
+                                   int dtype, void* cache, void* stream);
+DFLASH2_API int dflash2_kv4_read(const void* cache, const int64_t* slots, int T, int heads, int D, int page_size,
+                                 int num_pages, int dtype, void* k, void* v, void* stream);
+DFLASH2_API size_t dflash2_kv4_attention_workspace_bytes(int B, int G, int Hq, int Hkv, int D, int page_size,
+                                                         int max_pages);
+DFLASH2_API int dflash2_kv4_attention(const void* q, int64_t q_stride, const void* cache, const int32_t* page_table,
+                                      const int32_t* ctx_len, const void* k_new, const void* v_new, int64_t new_stride,
+                                      int B, int G, int Hq, int Hkv, int D, int page_size, int num_pages,
+                                      int max_pages, int causal, int window, float scale, int dtype, void* out,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
 /* Self-test of the bounded-wait machinery: launches one block that waits on an mbarrier that
  * nothing completes, with a limit of `limit_us` microseconds (1..1000000). The wait gives up,
  * records DFLASH2_ERR_TIMEOUT in the device error word and the kernel returns; read it with
