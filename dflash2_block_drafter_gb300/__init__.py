@@ -27,6 +27,7 @@ __all__ = [
     "dflash2_proj_workspace_bytes",
     "dflash2_kv4_page_bytes", "dflash2_kv4_cache", "dflash2_kv4_append", "dflash2_kv4_read",
     "dflash2_kv4_attention_workspace_bytes", "dflash2_kv4_attention",
+    "dflash2_gated_ffn_workspace_bytes", "dflash2_gated_ffn", "dflash2_gated_ffn_backward", "ACT_CODES",
     "DTYPE_CODES",
 ]
 
@@ -36,6 +37,7 @@ _LIB = None
 
 BF16, F32 = 0, 1
 DTYPE_CODES = {torch.bfloat16: BF16, torch.float32: F32}
+ACT_CODES = {"silu": 0, "gelu_tanh": 1}
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
@@ -78,6 +80,9 @@ _SIGNATURES = {
     "dflash2_kv4_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "dflash2_kv4_attention": (_i, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                                    _i, _vp, _vp, _sz, _vp]),
+    "dflash2_gated_ffn_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "dflash2_gated_ffn": (_i, [_vp, _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+    "dflash2_gated_ffn_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -646,3 +651,77 @@ def dflash2_kv4_attention(q, cache, page_table, ctx_len, page_size, scale, k_new
         _dev(ctx_len, "ctx_len", torch.int32), kp, vp, ns, B, G, Hq, Hkv, D, page_size, pages, width, int(bool(causal)),
         window, scale, BF16, _dev(out, "out", torch.bfloat16), wp, wn, _stream(stream)))
     return out
+
+
+def dflash2_gated_ffn_workspace_bytes(M, H, F, backward) -> int:
+    return library().dflash2_gated_ffn_workspace_bytes(M, H, F, int(bool(backward)))
+
+
+def _act(act):
+    try:
+        return ACT_CODES[act]
+    except KeyError:
+        raise ValueError(f"act must be one of {sorted(ACT_CODES)}, got {act!r}") from None
+
+
+def _ffn_weights(w_gate, w_up, H):
+    if w_gate.dim() != 2 or w_gate.shape[1] != H or w_up.shape != w_gate.shape:
+        raise ValueError(f"w_gate and w_up must both be [F, {H}], got {tuple(w_gate.shape)} and {tuple(w_up.shape)}")
+    return w_gate.shape[0]
+
+
+def _sized(t, n, name, shape, device):
+    """The output tensor `name` of n elements: allocated when not given, else checked for size."""
+    if t is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} elements, fewer than the {n} the call writes")
+    return t
+
+
+def _ffn_ws(M, H, F, backward, device, workspace):
+    if workspace is None:
+        need = library().dflash2_gated_ffn_workspace_bytes(M, H, F, backward)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
+
+
+def dflash2_gated_ffn(x, w_gate, w_up, act="silu", out=None, pre=None, want_pre=False, workspace=None, stream=None):
+    """h = act(x w_gate^T) * (x w_up^T): x [M, H], weights [F, H], bf16. With ``pre`` [2, M, F] (or
+    want_pre) the products g and u are kept for dflash2_gated_ffn_backward. Returns h [M, F], or
+    (h, pre) with want_pre."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, H], got shape {tuple(x.shape)}")
+    M, H = x.shape
+    F = _ffn_weights(w_gate, w_up, H)
+    out = _sized(out, M * F, "out", (M, F), x.device)
+    if want_pre or pre is not None:
+        pre = _sized(pre, 2 * M * F, "pre", (2, M, F), x.device)
+    wp, wn, _keep = _ffn_ws(M, H, F, 0, x.device, workspace)
+    bf = torch.bfloat16
+    _check(library().dflash2_gated_ffn(_dev(x, "x", bf), M, H, _dev(w_gate, "w_gate", bf), _dev(w_up, "w_up", bf), F,
+                                       _act(act), BF16, _dev(out, "out", bf), _dev(pre, "pre", bf, True), wp, wn,
+                                       _stream(stream)))
+    return (out, pre) if want_pre else out
+
+
+def dflash2_gated_ffn_backward(dh, pre, x, w_gate, w_up, act="silu", want_dx=True, want_dw=True, dx=None, dw_gate=None,
+                               dw_up=None, workspace=None, stream=None):
+    """Gradients of dflash2_gated_ffn from dh [M, F] and the kept pre [2, M, F]: (dx [M, H], dw_gate,
+    dw_up [F, H]); None for what is not wanted."""
+    M, H = x.shape
+    F = _ffn_weights(w_gate, w_up, H)
+    if tuple(dh.shape) != (M, F) or pre.numel() != 2 * M * F:
+        raise ValueError(f"dh must be [{M}, {F}] and pre [2, {M}, {F}], got {tuple(dh.shape)} and {tuple(pre.shape)}")
+    if (dw_gate is None) != (dw_up is None):
+        raise ValueError("dw_gate and dw_up go together")
+    dx = _sized(dx, M * H, "dx", (M, H), x.device) if want_dx else None
+    dw_gate = _sized(dw_gate, F * H, "dw_gate", (F, H), x.device) if want_dw else None
+    dw_up = _sized(dw_up, F * H, "dw_up", (F, H), x.device) if want_dw else None
+    wp, wn, _keep = _ffn_ws(M, H, F, 1, x.device, workspace)
+    bf = torch.bfloat16
+    _check(library().dflash2_gated_ffn_backward(
+        _dev(dh, "dh", bf), _dev(pre, "pre", bf), _dev(x, "x", bf), _dev(w_gate, "w_gate", bf), _dev(w_up, "w_up", bf),
+        M, H, F, _act(act), BF16, _dev(dx, "dx", bf, True), _dev(dw_gate, "dw_gate", bf, True),
+        _dev(dw_up, "dw_up", bf, True), wp, wn, _stream(stream)))
+    return dx, dw_gate, dw_up

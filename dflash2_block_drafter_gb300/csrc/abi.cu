@@ -533,6 +533,72 @@ int dflash2_kv4_attention(const void* q, int64_t q_stride, const void* cache, co
   return launch_kv4_attention(r, static_cast<cudaStream_t>(stream));
 }
 
+static int check_ffn(int M, int H, int F, int act, int dtype) {
+  if (dtype != DFLASH2_BF16) return fail(DFLASH2_ERR_UNSUPPORTED, "the gated feed-forward runs in bf16 only (dtype=%d)", dtype);
+  REQUIRE(M >= 0, "M=%d must be >= 0", M);
+  REQUIRE(H >= 8 && H % 8 == 0 && F >= 8 && F % 8 == 0, "H=%d and F=%d must be positive multiples of 8", H, F);
+  REQUIRE(act == DFLASH2_ACT_SILU || act == DFLASH2_ACT_GELU_TANH, "act=%d is not a dflash2_act", act);
+  // tiles of 256 rows by 128 columns (and twice 256 by 256 for the weights' gradients) are counted in int
+  const int64_t m = (M + 255LL) / 256, h = (H + 127LL) / 128, f = (F + 127LL) / 128;
+  REQUIRE(m * f <= 0x3fffffff && m * h <= 0x3fffffff && f * h <= 0x3fffffff, "M=%d, H=%d, F=%d are too large", M, H, F);
+  return DFLASH2_OK;
+}
+
+static int check_ffn_workspace(int M, int H, int F, bool backward, const void* workspace, size_t workspace_bytes) {
+  const size_t need = gated_ffn_workspace(M, H, F, backward, sm_count());
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(DFLASH2_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed",
+                workspace == nullptr ? 0 : workspace_bytes, need);
+  REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, "workspace must be 256-byte aligned");
+  return DFLASH2_OK;
+}
+
+size_t dflash2_gated_ffn_workspace_bytes(int M, int H, int F, int backward) {
+  if (check_ffn(M, H, F, DFLASH2_ACT_SILU, DFLASH2_BF16) != DFLASH2_OK) return 0;
+  return gated_ffn_workspace(M, H, F, backward != 0, sm_count());
+}
+
+int dflash2_gated_ffn(const void* x, int M, int H, const void* w_gate, const void* w_up, int F, int act, int dtype,
+                      void* h, void* pre, void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_ffn(M, H, F, act, dtype);
+  if (rc != DFLASH2_OK || M == 0) return rc;
+  REQUIRE(x && w_gate && w_up && h, "a required pointer is NULL");
+  REQUIRE(aligned16(x) && aligned16(w_gate) && aligned16(w_up) && aligned16(h) && aligned16(pre),
+          "x, w_gate, w_up, h and pre must be 16-byte aligned");
+  if ((rc = check_ffn_workspace(M, H, F, false, workspace, workspace_bytes)) != DFLASH2_OK) return rc;
+  GatedFfn r{};
+  r.x = x; r.w_gate = w_gate; r.w_up = w_up; r.h = h; r.pre = pre;
+  r.M = M; r.H = H; r.F = F; r.act = act; r.workspace = workspace;
+  return launch_gated_ffn(r, static_cast<cudaStream_t>(stream));
+}
+
+int dflash2_gated_ffn_backward(const void* dh, const void* pre, const void* x, const void* w_gate, const void* w_up,
+                               int M, int H, int F, int act, int dtype, void* dx, void* dw_gate, void* dw_up,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  int rc = check_ffn(M, H, F, act, dtype);
+  if (rc != DFLASH2_OK) return rc;
+  REQUIRE((dw_gate == nullptr) == (dw_up == nullptr), "dw_gate and dw_up must be both set or both NULL");
+  if (M == 0) {  // no rows: the weights' gradients are zero
+    const size_t n = static_cast<size_t>(F) * H * 2;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dw_gate != nullptr && (cudaMemsetAsync(dw_gate, 0, n, st) != cudaSuccess ||
+                               cudaMemsetAsync(dw_up, 0, n, st) != cudaSuccess))
+      return fail(DFLASH2_ERR_CUDA, "clearing the weights' gradients failed");
+    return DFLASH2_OK;
+  }
+  REQUIRE(dx || dw_gate, "nothing to compute: dx and the weights' gradients are all NULL");
+  REQUIRE(dh && pre && (!dw_gate || x) && (!dx || (w_gate && w_up)), "a required pointer is NULL");
+  REQUIRE(aligned16(dh) && aligned16(pre) && aligned16(x) && aligned16(w_gate) && aligned16(w_up) && aligned16(dx) &&
+              aligned16(dw_gate) && aligned16(dw_up),
+          "every tensor must be 16-byte aligned");
+  if ((rc = check_ffn_workspace(M, H, F, true, workspace, workspace_bytes)) != DFLASH2_OK) return rc;
+  GatedFfn r{};
+  r.x = x; r.w_gate = w_gate; r.w_up = w_up; r.dh = dh; r.pre = const_cast<void*>(pre);
+  r.dx = dx; r.dw_gate = dw_gate; r.dw_up = dw_up;
+  r.M = M; r.H = H; r.F = F; r.act = act; r.workspace = workspace;
+  return launch_gated_ffn_backward(r, static_cast<cudaStream_t>(stream));
+}
+
 int dflash2_selftest_bounded_wait(int limit_us, void* stream) {
   REQUIRE(limit_us >= 1 && limit_us <= 1000000, "limit_us=%d must be in [1, 1000000]", limit_us);
   return launch_wait_selftest(limit_us, static_cast<cudaStream_t>(stream));

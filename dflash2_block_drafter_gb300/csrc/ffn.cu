@@ -1,0 +1,596 @@
+// The gated feed-forward sublayer (dflash2.ts #block: silu(gate(a)) * up(a), the MLP between a site's
+// prepare and finish) and its gradients, on the tcgen05 tensor cores:
+//
+//   forward    g = x Wg^T, u = x Wu^T, h = act(g) * u                 x [M, H], Wg, Wu [F, H], h [M, F]
+//   backward   dg = dh * u * act'(g), du = dh * act(g)                (one elementwise pass, bf16)
+//              dx = dg Wg + du Wu;  dWg = dg^T x, dWu = du^T x
+//
+// with act(g) = g s(w(g)), s the logistic function and w(g) = g (silu) or 2 sqrt(2 / pi) (g + 0.044715 g^3)
+// (gelu in its tanh form: (1 + tanh z) / 2 = s(2 z)).
+//
+// All three products run in one kernel on CTA pairs (cta_group::2) over 256 x 256 tiles:
+//   forward: the pair's 256 weight rows are 128 rows of Wg (the leader's half) and the same 128 rows of
+//            Wu (the peer's), so that a thread of the epilogue holds g and u of the same channels and
+//            h leaves the kernel without g and u ever being stored (unless the caller keeps them).
+//   dx:      K runs over the 2 F channels of (dg, du); the weights are read as they lie, [F, H], as an
+//            operand whose H (not K) is contiguous ("MN-major").
+//   dW:      K runs over the M rows; both operands are MN-major, so nothing is transposed in memory.
+// Operands are 64-deep k-blocks in 128-byte-swizzled shared memory, filled by TMA through a ring of
+// stages; the accumulator is double-buffered in TMEM (2 x 256 columns), so an epilogue overlaps the next
+// tile's MMAs. Rows and columns past the matrices read as zeros and are not stored.
+//
+// Work: whole rounds of tiles go one tile per pair; what a last, partly filled round would leave idle is
+// avoided by cutting the remaining tiles' k-blocks into equal shares, one per pair. A tile whose
+// k-blocks fall to several pairs is finished by the pair that holds its last ones: the earlier pairs
+// leave fp32 partial tiles in the workspace and raise flags, and the owner adds them in K order (so
+// results do not depend on timing). Every pair takes its shares from the last piece to the first: the
+// piece it gives away comes first, and an owner waits only for pairs of lower index, which were
+// dispatched before it. The flags lie in the call's workspace and hold the call's own 64-bit number, so
+// the workspace needs no initialisation and calls on different streams (with their own workspaces) are
+// independent; an owner clears what it has read, so a captured call can be replayed.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <atomic>
+#include <chrono>
+#include <mutex>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace dfl {
+namespace {
+
+constexpr int kFK = 64;                        // k per stage
+constexpr int kFTile = 256;                    // rows and columns of a pair's tile
+constexpr int kFHalf = 128 * 128;              // one CTA's half of an operand k-block, bytes
+constexpr int kFStage = 2 * kFHalf;
+constexpr int kFStages = 7;
+constexpr int kFBar = 256;
+constexpr int kFSmem = 1024 + kFStages * kFStage + kFBar;
+constexpr int kFThreads = 192;                 // warps: TMA, MMA, 4 x epilogue
+constexpr int kFGroupM = 8;                    // tiles are walked in strips of 8 row tiles: neighbours share operands in L2
+constexpr int kFSlot = 128 * kFTile;           // fp32 values of one CTA's partial tile
+constexpr int kFMinPiece = 8;                  // k-blocks of a share at least
+constexpr uint64_t kFDrainNs = 100000000ull;
+
+enum FfnMode { kForward = 0, kDx = 1, kDw = 2 };
+
+struct FfnArgs {
+  int M, H, F;
+  int rows, cols;         // of the output: M x F (forward, per projection), M x H, F x H (per projection)
+  int tiles_m, tiles_n, n_tiles;
+  int kblocks;            // of one tile
+  int kblocks0;           // dx: those of dg
+  int sk_tiles, sk_units; // tiles cut into shares, and the pairs that take them
+  int act;
+  __nv_bfloat16 *out0, *out1, *pre;  // h | dx | dWg, dWu; pre: g and u [2][M][F] or null
+  float* slots;           // [CTA][128][256]
+  unsigned long long* flags;  // [CTA][4]
+  unsigned long long call;
+  int* err;
+};
+struct FfnMaps {
+  CUtensorMap a0, a1, b0, b1;
+};
+
+// MN-major operand of 128-byte swizzled rows: 64 elements of M (or N) per row, one row per k, chunks
+// of 64 columns `8192` bytes apart (64 k rows). Leading byte offset = the next 64 columns, stride
+// byte offset = the next 8 k rows.
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(8192 >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+__host__ __device__ constexpr uint32_t ffn_idesc(bool a_mn, bool b_mn) {
+  return make_idesc(false, kFTile, kFTile) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+
+// One piece of a pair's work: tile t, k-blocks [kb0, kb1).
+struct FfnPiece {
+  int t, kb0, kb1;
+};
+__device__ __forceinline__ long long ffn_share(const FfnArgs& a, int unit) {
+  return static_cast<long long>(a.sk_tiles) * a.kblocks * unit / a.sk_units;
+}
+// Piece `idx` of pair `unit`: its share of the cut tiles from the last piece to the first, then whole tiles.
+__device__ __forceinline__ bool ffn_piece(const FfnArgs& a, int unit, int units, int idx, FfnPiece& p) {
+  int pieces = 0;
+  if (unit < a.sk_units && a.sk_tiles > 0) {
+    const long long s = ffn_share(a, unit), e = ffn_share(a, unit + 1);
+    const int t0 = static_cast<int>(s / a.kblocks), t1 = static_cast<int>((e - 1) / a.kblocks);
+    pieces = t1 - t0 + 1;
+    if (idx < pieces) {
+      p.t = t1 - idx;
+      const long long first = static_cast<long long>(p.t) * a.kblocks;
+      p.kb0 = static_cast<int>(max(s - first, 0LL));
+      p.kb1 = static_cast<int>(min(e - first, static_cast<long long>(a.kblocks)));
+      return true;
+    }
+  }
+  const long long t = static_cast<long long>(a.sk_tiles) + unit + static_cast<long long>(idx - pieces) * units;
+  if (t >= a.n_tiles) return false;
+  p.t = static_cast<int>(t);
+  p.kb0 = 0;
+  p.kb1 = a.kblocks;
+  return true;
+}
+// Tile -> (projection, row tile, column tile), walked in strips of kFGroupM row tiles.
+__device__ __forceinline__ void ffn_tile(const FfnArgs& a, int t, int& proj, int& tm, int& tn) {
+  const int per = a.tiles_m * a.tiles_n;
+  proj = t / per;
+  t -= proj * per;
+  const int strip = t / (kFGroupM * a.tiles_n);
+  const int left = min(kFGroupM, a.tiles_m - strip * kFGroupM);
+  const int in = t - strip * kFGroupM * a.tiles_n;
+  tn = in / left;
+  tm = strip * kFGroupM + in - tn * left;
+}
+
+__device__ __forceinline__ void ffn_abort(volatile int* abort_flag, int* err) {
+  *abort_flag = 1;
+  atomicCAS(err, 0, static_cast<int>(DFLASH2_ERR_TIMEOUT));
+}
+__device__ __forceinline__ unsigned long long ld_acquire_u64(const unsigned long long* p) {
+  unsigned long long v;
+  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_release_u64(unsigned long long* p, unsigned long long v) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+// Waits (bounded) until a partial tile's flag holds this call's number.
+__device__ __forceinline__ bool ffn_wait_flag(const unsigned long long* flag, unsigned long long call,
+                                              const volatile int* abort_flag) {
+  const uint64_t t0 = globaltimer_ns();
+  for (uint32_t i = 1; ld_acquire_u64(flag) != call; ++i) {
+    __nanosleep(64);
+    if ((i & 15u) == 0u && (*abort_flag != 0 || globaltimer_ns() - t0 > kWaitLimitNs)) return false;
+  }
+  return true;
+}
+
+__device__ __forceinline__ float logistic(float w) { return __fdividef(1.f, 1.f + __expf(-w)); }
+// s(w(g)) and w'(g): act(g) = g s, act'(g) = s + g s (1 - s) w'.
+__device__ __forceinline__ float ffn_gate(float g, int act, float& slope) {
+  if (act == DFLASH2_ACT_SILU) {
+    slope = 1.f;
+    return logistic(g);
+  }
+  constexpr float k = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+  const float g2 = g * g;
+  slope = k * fmaf(3.f * 0.044715f, g2, 1.f);
+  return logistic(k * g * fmaf(0.044715f, g2, 1.f));
+}
+__device__ __forceinline__ uint32_t ffn_pack(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Stores 32 consecutive values of a row (columns col .. col + 31 of `cols`, a multiple of 8) as bf16.
+__device__ __forceinline__ void ffn_store(__nv_bfloat16* row, int col, int cols, const float (&y)[32]) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v)
+    if (col + 8 * v < cols)
+      *reinterpret_cast<uint4*>(row + col + 8 * v) =
+          make_uint4(ffn_pack(y[8 * v], y[8 * v + 1]), ffn_pack(y[8 * v + 2], y[8 * v + 3]),
+                     ffn_pack(y[8 * v + 4], y[8 * v + 5]), ffn_pack(y[8 * v + 6], y[8 * v + 7]));
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant__ FfnMaps maps, const FfnArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kFStages * kFStage);  // the leader's: both halves landed
+  uint64_t* empty = full + kFStages;                                       // MMAs done reading the stage
+  uint64_t* acc_full = empty + kFStages;                                   // [2]
+  uint64_t* acc_empty = acc_full + 2;                                      // [2], the leader's
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int unit = static_cast<int>(blockIdx.x >> 1);
+  const int units = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kFStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_u32(&acc_full[b]), 1);
+      mbar_init(smem_u32(&acc_empty[b]), 8);  // both CTAs' epilogue warps
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&maps.a0);
+    prefetch_tmap(&maps.b0);
+    if (kMode != kForward) prefetch_tmap(&maps.a1);
+    prefetch_tmap(&maps.b1);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();  // both CTAs' barriers exist before the peer arrives on the leader's
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_trigger();
+  pdl_wait();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      const uint64_t pol = policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      FfnPiece p;
+      for (int idx = 0; ok && ffn_piece(a, unit, units, idx, p); ++idx) {
+        int proj, tm, tn;
+        ffn_tile(a, p.t, proj, tm, tn);
+        // this CTA's 128 rows of A; its 128 columns of the output (B's rows)
+        const int m0 = tm * kFTile + static_cast<int>(rank) * 128;
+        const int n0 = kMode == kForward ? tn * 128 : tn * kFTile + static_cast<int>(rank) * 128;
+        for (int kb = p.kb0; kb < p.kb1; ++kb) {
+          if (!mbar_wait_bounded(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fb = smem_u32(&full[stage]);
+          const uint32_t fbl = mapa_shared(fb, 0);  // both CTAs' copies complete on the leader's barrier
+          if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kFStage);
+          const uint32_t sa = smem_u32(smem + stage * kFStage), sb = sa + kFHalf;
+          if (kMode == kForward) {
+            tma_load_2d_pair(sa, &maps.a0, fbl, kb * kFK, m0, pol);
+            tma_load_2d_pair(sb, rank == 0 ? &maps.b0 : &maps.b1, fbl, kb * kFK, n0, pol);
+          } else if (kMode == kDx) {
+            const bool second = kb >= a.kblocks0;
+            const int k = (second ? kb - a.kblocks0 : kb) * kFK;
+            const CUtensorMap* mb = second ? &maps.b1 : &maps.b0;
+            tma_load_2d_pair(sa, second ? &maps.a1 : &maps.a0, fbl, k, m0, pol);
+            tma_load_2d_pair(sb, mb, fbl, n0, k, pol);
+            tma_load_2d_pair(sb + kFHalf / 2, mb, fbl, n0 + 64, k, pol);
+          } else {
+            const CUtensorMap* ma = proj == 0 ? &maps.a0 : &maps.a1;
+            tma_load_2d_pair(sa, ma, fbl, m0, kb * kFK, pol);
+            tma_load_2d_pair(sa + kFHalf / 2, ma, fbl, m0 + 64, kb * kFK, pol);
+            tma_load_2d_pair(sb, &maps.b0, fbl, n0, kb * kFK, pol);
+            tma_load_2d_pair(sb + kFHalf / 2, &maps.b0, fbl, n0 + 64, kb * kFK, pol);
+          }
+          if (++stage == kFStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        // copies in flight complete on the leader's barriers: give them a fixed time before leaving
+        ffn_abort(abort_flag, a.err);
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer (the leader's lane 0)
+    if (lane == 0 && rank == 0) {
+      constexpr bool kAMn = kMode == kDw, kBMn = kMode != kForward;
+      constexpr uint32_t idesc = ffn_idesc(kAMn, kBMn);
+      constexpr uint64_t kStepA = kAMn ? 16 * 128 / 16 : 2, kStepB = kBMn ? 16 * 128 / 16 : 2;  // 16 k further
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true, any = false;
+      FfnPiece p;
+      for (int idx = 0; ok && ffn_piece(a, unit, units, idx, p); ++idx) {
+        const int ab = idx & 1;
+        if (!mbar_wait_bounded(smem_u32(&acc_empty[ab]), ((static_cast<uint32_t>(idx) >> 1) & 1u) ^ 1u, abort_flag,
+                               kWaitLimitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        for (int kb = p.kb0; kb < p.kb1; ++kb) {
+          if (!mbar_wait_bounded(smem_u32(&full[stage]), phase, abort_flag, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + stage * kFStage);
+          const uint64_t adesc = kAMn ? desc_mnmajor_sw128(sa) : desc_kmajor_sw128(sa);
+          const uint64_t bdesc = kBMn ? desc_mnmajor_sw128(sa + kFHalf) : desc_kmajor_sw128(sa + kFHalf);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_f16_pair(tmem_base + static_cast<uint32_t>(ab * kFTile), adesc + kStepA * k, bdesc + kStepB * k, idesc,
+                         (kb > p.kb0 || k > 0) ? 1u : 0u);
+          mma_commit_pair(smem_u32(&empty[stage]), 0x3);  // frees the stage in both CTAs
+          any = true;
+          if (++stage == kFStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair(smem_u32(&acc_full[ab]), 0x3);
+      }
+      if (!ok) {
+        ffn_abort(abort_flag, a.err);
+        if (any) {
+          mma_commit_pair(smem_u32(drain), 0x1);
+          mbar_wait_bounded(smem_u32(drain), 0, nullptr, kFDrainNs);
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // TMEM lanes 32 q ..
+    const int cta = static_cast<int>(blockIdx.x);
+    FfnPiece p;
+    for (int idx = 0; ffn_piece(a, unit, units, idx, p); ++idx) {
+      int proj, tm, tn;
+      ffn_tile(a, p.t, proj, tm, tn);
+      const int ab = idx & 1;
+      const bool partial = p.kb1 < a.kblocks;
+      // the pairs [u_first, unit) hold the tile's earlier k-blocks
+      int u_first = unit;
+      if (!partial && p.kb0 > 0) {
+        const long long first = static_cast<long long>(p.t) * a.kblocks;
+        while (u_first > 0 && ffn_share(a, u_first) > first) --u_first;
+      }
+      if (!mbar_wait_bounded_suspend(smem_u32(&acc_full[ab]), (static_cast<uint32_t>(idx) >> 1) & 1u, abort_flag,
+                                     kWaitLimitNs)) {
+        if (lane == 0) ffn_abort(abort_flag, a.err);
+        break;
+      }
+      tc_fence_after();
+      if (u_first < unit) {
+        int got = 1;
+        if (lane == 0)
+          for (int u = u_first; got && u < unit; ++u)
+            got = ffn_wait_flag(a.flags + (2 * u + static_cast<int>(rank)) * 4 + q, a.call, abort_flag) ? 1 : 0;
+        got = __shfl_sync(0xffffffffu, got, 0);
+        if (!got) {
+          if (lane == 0) ffn_abort(abort_flag, a.err);
+          break;
+        }
+      }
+      const uint32_t tm0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(ab * kFTile);
+      const int lrow = q * 32 + lane;                                // of the CTA's 128
+      const int row = tm * kFTile + static_cast<int>(rank) * 128 + lrow;
+      const bool valid = row < a.rows;
+      // columns c0 .. c0 + 31 of the tile, the earlier pairs' parts included
+      auto load = [&](int c0, float (&y)[32]) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(tm0 + static_cast<uint32_t>(c0), r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(r[j]);
+        if (u_first == unit) return;
+        float sum[32] = {};
+        for (int u = u_first; u < unit; ++u) {
+          const float* src = a.slots + static_cast<size_t>(2 * u + static_cast<int>(rank)) * kFSlot +
+                             static_cast<size_t>(lrow) * kFTile + c0;
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(src + 4 * v));
+            sum[4 * v] += f.x; sum[4 * v + 1] += f.y; sum[4 * v + 2] += f.z; sum[4 * v + 3] += f.w;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) y[j] += sum[j];
+      };
+      if (partial) {
+        float* dst = a.slots + static_cast<size_t>(cta) * kFSlot + static_cast<size_t>(lrow) * kFTile;
+        for (int c0 = 0; c0 < kFTile; c0 += 32) {
+          float y[32];
+          load(c0, y);
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            *reinterpret_cast<float4*>(dst + c0 + 4 * v) = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
+        }
+      } else if (kMode == kForward) {
+        const size_t at = static_cast<size_t>(valid ? row : 0) * a.F;
+        const size_t plane = static_cast<size_t>(a.M) * a.F;
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          float g[32], u[32];
+          load(c0, g);
+          load(128 + c0, u);
+          const int col = tn * 128 + c0;
+          if (valid && a.pre != nullptr) {
+            ffn_store(a.pre + at, col, a.F, g);
+            ffn_store(a.pre + plane + at, col, a.F, u);
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float slope;
+            g[j] = g[j] * ffn_gate(g[j], a.act, slope) * u[j];
+          }
+          if (valid) ffn_store(a.out0 + at, col, a.F, g);
+        }
+      } else {
+        __nv_bfloat16* out = (proj == 0 ? a.out0 : a.out1) + static_cast<size_t>(valid ? row : 0) * a.cols;
+        for (int c0 = 0; c0 < kFTile; c0 += 32) {
+          float y[32];
+          load(c0, y);
+          if (valid) ffn_store(out, tn * kFTile + c0, a.cols, y);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[ab]), 0));
+      if (partial) {
+        __threadfence();  // every lane's rows are visible before the flag
+        __syncwarp();
+        if (lane == 0) st_release_u64(a.flags + cta * 4 + q, a.call);
+      }
+      if (lane == 0)  // read: ready for a replay
+        for (int u = u_first; u < unit; ++u) a.flags[(2 * u + static_cast<int>(rank)) * 4 + q] = 0ull;
+    }
+  }
+
+  tc_fence_before();
+  cluster_sync_all();  // no MMA, commit or remote arrival is in flight towards either CTA
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem_base, 512);
+  }
+}
+
+// dg = dh u act'(g), du = dh act(g): thread = 8 channels of one row, [2][M][F] in and out.
+__global__ void __launch_bounds__(256)
+    ffn_gate_grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restrict__ pre, size_t n8, int act,
+                         __nv_bfloat16* __restrict__ dgu) {
+  pdl_trigger();
+  pdl_wait();
+  const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= n8) return;
+  const uint4 d4 = __ldg(reinterpret_cast<const uint4*>(dh) + i);
+  const uint4 g4 = __ldg(reinterpret_cast<const uint4*>(pre) + i);
+  const uint4 u4 = __ldg(reinterpret_cast<const uint4*>(pre) + n8 + i);
+  const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w}, gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+  uint32_t og[4], ou[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 d = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&dw[j]));
+    const float2 g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&gw[j]));
+    const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&uw[j]));
+    float kx, ky;
+    const float sx = ffn_gate(g.x, act, kx), sy = ffn_gate(g.y, act, ky);
+    og[j] = ffn_pack(d.x * u.x * fmaf(g.x * sx * (1.f - sx), kx, sx), d.y * u.y * fmaf(g.y * sy * (1.f - sy), ky, sy));
+    ou[j] = ffn_pack(d.x * g.x * sx, d.y * g.y * sy);
+  }
+  reinterpret_cast<uint4*>(dgu)[i] = make_uint4(og[0], og[1], og[2], og[3]);
+  reinterpret_cast<uint4*>(dgu)[n8 + i] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+}
+
+size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+int ffn_units(int sms) { return std::max(1, sms / 2); }
+
+size_t ffn_share_bytes(int sms) {
+  const size_t ctas = 2 * static_cast<size_t>(ffn_units(sms));
+  return align256(ctas * kFSlot * sizeof(float)) + align256(ctas * 4 * sizeof(unsigned long long));
+}
+
+// A number that no other call of this process uses, and that stale memory will hardly hold.
+unsigned long long ffn_call_number() {
+  static const unsigned long long seed =
+      static_cast<unsigned long long>(std::chrono::high_resolution_clock::now().time_since_epoch().count()) *
+      0x9E3779B97F4A7C15ull;
+  static std::atomic<unsigned long long> count{0};
+  const unsigned long long n = seed + count.fetch_add(1, std::memory_order_relaxed) + 1;
+  return n != 0 ? n : 1;
+}
+
+template <int kMode>
+int launch_ffn_gemm(const FfnMaps& maps, FfnArgs a, void* share_ws, cudaStream_t st) {
+  const int units = ffn_units(sm_count());
+  a.slots = static_cast<float*>(share_ws);
+  a.flags = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(share_ws) +
+                                                  align256(2 * static_cast<size_t>(units) * kFSlot * sizeof(float)));
+  a.call = ffn_call_number();
+  a.err = device_error_word();
+  if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
+  // The last round's tiles are cut into shares unless they nearly fill it: a cut tile costs its partial
+  // sums' way through the workspace. A share is at least kFMinPiece k-blocks.
+  const int rest = a.n_tiles % units;
+  a.sk_tiles = 10 * rest > 9 * units ? 0 : rest;
+  const long long total = static_cast<long long>(a.sk_tiles) * a.kblocks;
+  a.sk_units = static_cast<int>(std::max<long long>(1, std::min<long long>(units, total / kFMinPiece)));
+  if (a.sk_units < a.sk_tiles) a.sk_tiles = 0;  // k too short to cut
+  const int grid = 2 * std::min(units, a.sk_tiles > 0 ? std::max(a.sk_units, a.n_tiles - a.sk_tiles) : a.n_tiles);
+  static unsigned done = 0;
+  auto kern = ffn_kernel<kMode>;
+  if (!ensure_smem_attr(kern, kFSmem, &done)) return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (gated FFN)");
+  cudaLaunchAttribute cl[1];
+  cl[0].id = cudaLaunchAttributeClusterDimension;
+  cl[0].val.clusterDim.x = 2;
+  cl[0].val.clusterDim.y = 1;
+  cl[0].val.clusterDim.z = 1;
+  const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(kFThreads), kFSmem, st, cl, 1, maps, a);
+  return e == cudaSuccess ? DFLASH2_OK : fail(DFLASH2_ERR_CUDA, "gated FFN launch failed: %s", cudaGetErrorString(e));
+}
+
+int tiles_of(int n, int tile) { return (n + tile - 1) / tile; }
+
+bool ffn_map(CUtensorMap* m, const void* p, int rows, int cols, int box_rows) {
+  return make_tmap_sw128(m, p, static_cast<uint64_t>(rows), static_cast<uint64_t>(cols), static_cast<uint32_t>(box_rows));
+}
+
+}  // namespace
+
+// Workspace: [partial tiles][flags] and, for the backward pass, [dg, du: 2 x M x F bf16].
+size_t gated_ffn_workspace(int M, int H, int F, bool backward, int sms) {
+  (void)H;
+  return ffn_share_bytes(sms) + (backward ? align256(2 * static_cast<size_t>(M) * F * 2) : 0);
+}
+
+int launch_gated_ffn(const GatedFfn& r, cudaStream_t st) {
+  FfnMaps maps;
+  if (!ffn_map(&maps.a0, r.x, r.M, r.H, 128) || !ffn_map(&maps.b0, r.w_gate, r.F, r.H, 128) ||
+      !ffn_map(&maps.b1, r.w_up, r.F, r.H, 128))
+    return fail(DFLASH2_ERR_CUDA, "tensor map encode failed (gated FFN)");
+  maps.a1 = maps.a0;
+  FfnArgs a{};
+  a.M = r.M; a.H = r.H; a.F = r.F;
+  a.rows = r.M;
+  a.cols = r.F;
+  a.tiles_m = tiles_of(r.M, kFTile);
+  a.tiles_n = tiles_of(r.F, 128);
+  a.n_tiles = a.tiles_m * a.tiles_n;
+  a.kblocks = tiles_of(r.H, kFK);
+  a.act = r.act;
+  a.out0 = static_cast<__nv_bfloat16*>(r.h);
+  a.pre = static_cast<__nv_bfloat16*>(r.pre);
+  return launch_ffn_gemm<kForward>(maps, a, r.workspace, st);
+}
+
+int launch_gated_ffn_backward(const GatedFfn& r, cudaStream_t st) {
+  __nv_bfloat16* dgu = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(r.workspace) + ffn_share_bytes(sm_count()));
+  const size_t plane = static_cast<size_t>(r.M) * r.F;
+  const size_t n8 = plane / 8;
+  const cudaError_t e =
+      launch_pdl(ffn_gate_grad_kernel, dim3(static_cast<unsigned>((n8 + 255) / 256)), dim3(256), 0, st, nullptr, 0,
+                 static_cast<const __nv_bfloat16*>(r.dh), static_cast<const __nv_bfloat16*>(r.pre), n8, r.act, dgu);
+  if (e != cudaSuccess) return fail(DFLASH2_ERR_CUDA, "gated FFN gradient launch failed: %s", cudaGetErrorString(e));
+  FfnArgs a{};
+  a.M = r.M; a.H = r.H; a.F = r.F;
+  a.cols = r.H;
+  a.tiles_n = tiles_of(r.H, kFTile);
+  FfnMaps maps;
+  if (r.dx != nullptr) {
+    if (!ffn_map(&maps.a0, dgu, r.M, r.F, 128) || !ffn_map(&maps.a1, dgu + plane, r.M, r.F, 128) ||
+        !ffn_map(&maps.b0, r.w_gate, r.F, r.H, kFK) || !ffn_map(&maps.b1, r.w_up, r.F, r.H, kFK))
+      return fail(DFLASH2_ERR_CUDA, "tensor map encode failed (gated FFN dx)");
+    a.rows = r.M;
+    a.tiles_m = tiles_of(r.M, kFTile);
+    a.n_tiles = a.tiles_m * a.tiles_n;
+    a.kblocks0 = tiles_of(r.F, kFK);
+    a.kblocks = 2 * a.kblocks0;
+    a.out0 = a.out1 = static_cast<__nv_bfloat16*>(r.dx);
+    const int rc = launch_ffn_gemm<kDx>(maps, a, r.workspace, st);
+    if (rc != DFLASH2_OK) return rc;
+  }
+  if (r.dw_gate != nullptr) {
+    if (!ffn_map(&maps.a0, dgu, r.M, r.F, kFK) || !ffn_map(&maps.a1, dgu + plane, r.M, r.F, kFK) ||
+        !ffn_map(&maps.b0, r.x, r.M, r.H, kFK))
+      return fail(DFLASH2_ERR_CUDA, "tensor map encode failed (gated FFN dW)");
+    maps.b1 = maps.b0;
+    a.rows = r.F;
+    a.tiles_m = tiles_of(r.F, kFTile);
+    a.n_tiles = 2 * a.tiles_m * a.tiles_n;
+    a.kblocks = tiles_of(r.M, kFK);
+    a.out0 = static_cast<__nv_bfloat16*>(r.dw_gate);
+    a.out1 = static_cast<__nv_bfloat16*>(r.dw_up);
+    return launch_ffn_gemm<kDw>(maps, a, r.workspace, st);
+  }
+  return DFLASH2_OK;
+}
+
+}  // namespace dfl

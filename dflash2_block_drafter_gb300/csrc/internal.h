@@ -178,6 +178,20 @@ int launch_proj(const ProjSpec& p, cudaStream_t st);
 int launch_conv_coefficients(const float* part, int k_splits, int M, int groups, int dtype, float* d0, void* coef1,
                              cudaStream_t st);
 
+// ---------------------------------------------------------------- gated feed-forward (ffn.cu)
+struct GatedFfn {
+  const void *x, *w_gate, *w_up;
+  const void* dh;  // backward
+  void* pre;       // forward: written if not null; backward: read
+  void* h;
+  void *dx, *dw_gate, *dw_up;  // dx null, or both dw null: not wanted
+  int M, H, F, act;
+  void* workspace;
+};
+size_t gated_ffn_workspace(int M, int H, int F, bool backward, int sms);
+int launch_gated_ffn(const GatedFfn& r, cudaStream_t st);
+int launch_gated_ffn_backward(const GatedFfn& r, cudaStream_t st);
+
 // ---------------------------------------------------------------- 4-bit key/value cache (kv4.cu)
 struct Kv4Rows {  // k_out / v_out null: k, v -> cache; else cache -> k_out, v_out
   const void *k, *v;

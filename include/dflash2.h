@@ -395,6 +395,35 @@ DFLASH2_API int dflash2_kv4_attention(const void* q, int64_t q_stride, const voi
                                       int max_pages, int causal, int window, float scale, int dtype, void* out,
                                       void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------
+ * The gated feed-forward sublayer and its gradients (dflash2.ts #block: down(silu(gate(a)) * up(a));
+ * the down projection is dflash2_proj or dflash2_proj_conv_out). The pages train nothing; the
+ * gradients are the formulas' own.
+ * bf16 only (DFLASH2_BF16; anything else returns DFLASH2_ERR_UNSUPPORTED), fp32 accumulation.
+ *
+ *   x [M, H]; w_gate, w_up [F, H] (out, in); H, F positive multiples of 8; M >= 0 (M = 0: nothing but
+ *   zeroed weight gradients).
+ *   forward:  g = x w_gate^T, u = x w_up^T (fp32), h [M, F] = act(g) * u, rounded once.
+ *             pre [2, M, F] or NULL: g and u rounded to dtype, for the backward call.
+ *   backward: from dh [M, F] and pre: dg = dh * u * act'(g), du = dh * act(g) (each rounded once to
+ *             dtype, the operands of the products), then dx [M, H] = dg w_gate + du w_up (NULL: not
+ *             wanted; the weights may then be NULL) and dw_gate, dw_up [F, H] = dg^T x, du^T x (both
+ *             NULL: not wanted; x may then be NULL).
+ *   workspace at least dflash2_gated_ffn_workspace_bytes(M, H, F, backward) bytes, 256-byte aligned,
+ *             no initialisation (the backward size serves both). Calls that can run at the same time
+ *             need workspaces of their own. The same call gives the same bits.
+ * ---------------------------------------------------------------------------------- */
+typedef enum { DFLASH2_ACT_SILU = 0, DFLASH2_ACT_GELU_TANH = 1 } dflash2_act;
+
+DFLASH2_API size_t dflash2_gated_ffn_workspace_bytes(int M, int H, int F, int backward);
+DFLASH2_API int dflash2_gated_ffn(const void* x, int M, int H, const void* w_gate, const void* w_up, int F, int act,
+                                  int dtype, void* h, void* pre, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+DFLASH2_API int dflash2_gated_ffn_backward(const void* dh, const void* pre, const void* x, const void* w_gate,
+                                           const void* w_up, int M, int H, int F, int act, int dtype, void* dx,
+                                           void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes,
+                                           void* stream);
+
 /* Self-test of the bounded-wait machinery: launches one block that waits on an mbarrier that
  * nothing completes, with a limit of `limit_us` microseconds (1..1000000). The wait gives up,
  * records DFLASH2_ERR_TIMEOUT in the device error word and the kernel returns; read it with
