@@ -687,32 +687,35 @@ def _ffn_ws(M, H, F, backward, device, workspace):
 
 
 def dflash2_gated_ffn(x, w_gate, w_up, act="silu", out=None, pre=None, want_pre=False, workspace=None, stream=None):
-    """h = act(x w_gate^T) * (x w_up^T): x [M, H], weights [F, H], bf16. With ``pre`` [2, M, F] (or
-    want_pre) the products g and u are kept for dflash2_gated_ffn_backward. Returns h [M, F], or
-    (h, pre) with want_pre."""
+    """h = act(x w_gate^T) * (x w_up^T): x [M, H], weights [F, H], bf16. With ``pre`` (any dense tensor of
+    4 M F bytes) or want_pre the products g and u are kept, as dflash2.h lays them out, for
+    dflash2_gated_ffn_backward. Returns h [M, F], or (h, pre int32 [M, F]) with want_pre."""
     if x.dim() != 2:
         raise ValueError(f"x must be [M, H], got shape {tuple(x.shape)}")
     M, H = x.shape
     F = _ffn_weights(w_gate, w_up, H)
     out = _sized(out, M * F, "out", (M, F), x.device)
-    if want_pre or pre is not None:
-        pre = _sized(pre, 2 * M * F, "pre", (2, M, F), x.device)
+    if want_pre and pre is None:
+        pre = torch.empty((M, F), dtype=torch.int32, device=x.device)
+    if pre is not None and pre.numel() * pre.element_size() < 4 * M * F:
+        raise ValueError(f"pre holds {pre.numel() * pre.element_size()} bytes, fewer than the {4 * M * F} the call writes")
     wp, wn, _keep = _ffn_ws(M, H, F, 0, x.device, workspace)
     bf = torch.bfloat16
     _check(library().dflash2_gated_ffn(_dev(x, "x", bf), M, H, _dev(w_gate, "w_gate", bf), _dev(w_up, "w_up", bf), F,
-                                       _act(act), BF16, _dev(out, "out", bf), _dev(pre, "pre", bf, True), wp, wn,
+                                       _act(act), BF16, _dev(out, "out", bf), _dev(pre, "pre", None, True), wp, wn,
                                        _stream(stream)))
     return (out, pre) if want_pre else out
 
 
 def dflash2_gated_ffn_backward(dh, pre, x, w_gate, w_up, act="silu", want_dx=True, want_dw=True, dx=None, dw_gate=None,
                                dw_up=None, workspace=None, stream=None):
-    """Gradients of dflash2_gated_ffn from dh [M, F] and the kept pre [2, M, F]: (dx [M, H], dw_gate,
+    """Gradients of dflash2_gated_ffn from dh [M, F] and the pre that call kept: (dx [M, H], dw_gate,
     dw_up [F, H]); None for what is not wanted."""
     M, H = x.shape
     F = _ffn_weights(w_gate, w_up, H)
-    if tuple(dh.shape) != (M, F) or pre.numel() != 2 * M * F:
-        raise ValueError(f"dh must be [{M}, {F}] and pre [2, {M}, {F}], got {tuple(dh.shape)} and {tuple(pre.shape)}")
+    if tuple(dh.shape) != (M, F) or pre.numel() * pre.element_size() < 4 * M * F:
+        raise ValueError(f"dh must be [{M}, {F}] and pre hold {4 * M * F} bytes, got {tuple(dh.shape)} and "
+                         f"{pre.numel() * pre.element_size()} bytes")
     if (dw_gate is None) != (dw_up is None):
         raise ValueError("dw_gate and dw_up go together")
     dx = _sized(dx, M * H, "dx", (M, H), x.device) if want_dx else None
@@ -721,7 +724,7 @@ def dflash2_gated_ffn_backward(dh, pre, x, w_gate, w_up, act="silu", want_dx=Tru
     wp, wn, _keep = _ffn_ws(M, H, F, 1, x.device, workspace)
     bf = torch.bfloat16
     _check(library().dflash2_gated_ffn_backward(
-        _dev(dh, "dh", bf), _dev(pre, "pre", bf), _dev(x, "x", bf), _dev(w_gate, "w_gate", bf), _dev(w_up, "w_up", bf),
+        _dev(dh, "dh", bf), _dev(pre, "pre"), _dev(x, "x", bf), _dev(w_gate, "w_gate", bf), _dev(w_up, "w_up", bf),
         M, H, F, _act(act), BF16, _dev(dx, "dx", bf, True), _dev(dw_gate, "dw_gate", bf, True),
         _dev(dw_up, "dw_up", bf, True), wp, wn, _stream(stream)))
     return dx, dw_gate, dw_up

@@ -35,6 +35,7 @@
 #include <chrono>
 #include <mutex>
 
+#include "ffn.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -62,9 +63,11 @@ struct FfnArgs {
   int tiles_m, tiles_n, n_tiles;
   int kblocks;            // of one tile
   int kblocks0;           // dx: those of dg
+  int a_rows;             // rows of a K-major A box: fewer than 128 when M is (the rest of the operand is not read out)
   int sk_tiles, sk_units; // tiles cut into shares, and the pairs that take them
   int act;
-  __nv_bfloat16 *out0, *out1, *pre;  // h | dx | dWg, dWu; pre: g and u [2][M][F] or null
+  __nv_bfloat16 *out0, *out1;  // h | dx | dWg, dWu
+  uint32_t* pre;          // [M][F] kept g and u, or null
   float* slots;           // [CTA][128][256]
   unsigned long long* flags;  // [CTA][4]
   unsigned long long call;
@@ -150,22 +153,6 @@ __device__ __forceinline__ bool ffn_wait_flag(const unsigned long long* flag, un
   return true;
 }
 
-__device__ __forceinline__ float logistic(float w) { return __fdividef(1.f, 1.f + __expf(-w)); }
-// s(w(g)) and w'(g): act(g) = g s, act'(g) = s + g s (1 - s) w'.
-__device__ __forceinline__ float ffn_gate(float g, int act, float& slope) {
-  if (act == DFLASH2_ACT_SILU) {
-    slope = 1.f;
-    return logistic(g);
-  }
-  constexpr float k = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-  const float g2 = g * g;
-  slope = k * fmaf(3.f * 0.044715f, g2, 1.f);
-  return logistic(k * g * fmaf(0.044715f, g2, 1.f));
-}
-__device__ __forceinline__ uint32_t ffn_pack(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 // Stores 32 consecutive values of a row (columns col .. col + 31 of `cols`, a multiple of 8) as bf16.
 __device__ __forceinline__ void ffn_store(__nv_bfloat16* row, int col, int cols, const float (&y)[32]) {
 #pragma unroll
@@ -243,7 +230,8 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant
           }
           const uint32_t fb = smem_u32(&full[stage]);
           const uint32_t fbl = mapa_shared(fb, 0);  // both CTAs' copies complete on the leader's barrier
-          if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kFStage);
+          if (rank == 0)
+            mbar_arrive_expect_tx(fb, 2 * static_cast<uint32_t>(kMode == kDw ? kFStage : a.a_rows * 128 + kFHalf));
           const uint32_t sa = smem_u32(smem + stage * kFStage), sb = sa + kFHalf;
           if (kMode == kForward) {
             tma_load_2d_pair(sa, &maps.a0, fbl, kb * kFK, m0, pol);
@@ -372,7 +360,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(r[j]);
-        if (u_first == unit) return;
+        if (u_first == unit || !valid) return;
         float sum[32] = {};
         for (int u = u_first; u < unit; ++u) {
           const float* src = a.slots + static_cast<size_t>(2 * u + static_cast<int>(rank)) * kFSlot +
@@ -391,21 +379,25 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant
         for (int c0 = 0; c0 < kFTile; c0 += 32) {
           float y[32];
           load(c0, y);
+          if (!valid) continue;
 #pragma unroll
           for (int v = 0; v < 8; ++v)
             *reinterpret_cast<float4*>(dst + c0 + 4 * v) = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
         }
       } else if (kMode == kForward) {
         const size_t at = static_cast<size_t>(valid ? row : 0) * a.F;
-        const size_t plane = static_cast<size_t>(a.M) * a.F;
         for (int c0 = 0; c0 < 128; c0 += 32) {
           float g[32], u[32];
           load(c0, g);
           load(128 + c0, u);
           const int col = tn * 128 + c0;
           if (valid && a.pre != nullptr) {
-            ffn_store(a.pre + at, col, a.F, g);
-            ffn_store(a.pre + plane + at, col, a.F, u);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              if (col + 4 * v < a.F)
+                *reinterpret_cast<uint4*>(a.pre + at + col + 4 * v) =
+                    make_uint4(ffn_keep(g[4 * v], u[4 * v]), ffn_keep(g[4 * v + 1], u[4 * v + 1]),
+                               ffn_keep(g[4 * v + 2], u[4 * v + 2]), ffn_keep(g[4 * v + 3], u[4 * v + 3]));
           }
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
@@ -443,28 +435,37 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant
   }
 }
 
-// dg = dh u act'(g), du = dh act(g): thread = 8 channels of one row, [2][M][F] in and out.
+// dg = dh u act'(g), du = dh act(g), rounded to bf16 (the operands of the products): thread = 8
+// channels of one row; out [2][M][F].
 __global__ void __launch_bounds__(256)
-    ffn_gate_grad_kernel(const __nv_bfloat16* __restrict__ dh, const __nv_bfloat16* __restrict__ pre, size_t n8, int act,
+    ffn_gate_grad_kernel(const __nv_bfloat16* __restrict__ dh, const uint32_t* __restrict__ pre, size_t n8, int act,
                          __nv_bfloat16* __restrict__ dgu) {
   pdl_trigger();
   pdl_wait();
   const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= n8) return;
   const uint4 d4 = __ldg(reinterpret_cast<const uint4*>(dh) + i);
-  const uint4 g4 = __ldg(reinterpret_cast<const uint4*>(pre) + i);
-  const uint4 u4 = __ldg(reinterpret_cast<const uint4*>(pre) + n8 + i);
-  const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w}, gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+  const uint4 p4[2] = {__ldg(reinterpret_cast<const uint4*>(pre) + 2 * i),
+                       __ldg(reinterpret_cast<const uint4*>(pre) + 2 * i + 1)};
+  const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w};
+  const uint32_t pw[8] = {p4[0].x, p4[0].y, p4[0].z, p4[0].w, p4[1].x, p4[1].y, p4[1].z, p4[1].w};
   uint32_t og[4], ou[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 d = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&dw[j]));
-    const float2 g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&gw[j]));
-    const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&uw[j]));
-    float kx, ky;
-    const float sx = ffn_gate(g.x, act, kx), sy = ffn_gate(g.y, act, ky);
-    og[j] = ffn_pack(d.x * u.x * fmaf(g.x * sx * (1.f - sx), kx, sx), d.y * u.y * fmaf(g.y * sy * (1.f - sy), ky, sy));
-    ou[j] = ffn_pack(d.x * g.x * sx, d.y * g.y * sy);
+    const float dd[2] = {d.x, d.y};
+    float dg[2], du[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t w = pw[2 * j + e];
+      const float g = ffn_kept1(w & 0xffffu), u = ffn_kept1(w >> 16);
+      float slope;
+      const float s = ffn_gate(g, act, slope);
+      dg[e] = dd[e] * u * fmaf(g * s * (1.f - s), slope, s);
+      du[e] = dd[e] * g * s;
+    }
+    og[j] = ffn_pack(dg[0], dg[1]);
+    ou[j] = ffn_pack(du[0], du[1]);
   }
   reinterpret_cast<uint4*>(dgu)[i] = make_uint4(og[0], og[1], og[2], og[3]);
   reinterpret_cast<uint4*>(dgu)[n8 + i] = make_uint4(ou[0], ou[1], ou[2], ou[3]);
@@ -532,8 +533,10 @@ size_t gated_ffn_workspace(int M, int H, int F, bool backward, int sms) {
 }
 
 int launch_gated_ffn(const GatedFfn& r, cudaStream_t st) {
+  if (r.M <= kFfnSmallRows) return launch_gated_ffn_small(r, st);
   FfnMaps maps;
-  if (!ffn_map(&maps.a0, r.x, r.M, r.H, 128) || !ffn_map(&maps.b0, r.w_gate, r.F, r.H, 128) ||
+  const int a_rows = std::min(128, (r.M + 7) / 8 * 8);
+  if (!ffn_map(&maps.a0, r.x, r.M, r.H, a_rows) || !ffn_map(&maps.b0, r.w_gate, r.F, r.H, 128) ||
       !ffn_map(&maps.b1, r.w_up, r.F, r.H, 128))
     return fail(DFLASH2_ERR_CUDA, "tensor map encode failed (gated FFN)");
   maps.a1 = maps.a0;
@@ -541,13 +544,14 @@ int launch_gated_ffn(const GatedFfn& r, cudaStream_t st) {
   a.M = r.M; a.H = r.H; a.F = r.F;
   a.rows = r.M;
   a.cols = r.F;
+  a.a_rows = a_rows;
   a.tiles_m = tiles_of(r.M, kFTile);
   a.tiles_n = tiles_of(r.F, 128);
   a.n_tiles = a.tiles_m * a.tiles_n;
   a.kblocks = tiles_of(r.H, kFK);
   a.act = r.act;
   a.out0 = static_cast<__nv_bfloat16*>(r.h);
-  a.pre = static_cast<__nv_bfloat16*>(r.pre);
+  a.pre = static_cast<uint32_t*>(r.pre);
   return launch_ffn_gemm<kForward>(maps, a, r.workspace, st);
 }
 
@@ -557,7 +561,7 @@ int launch_gated_ffn_backward(const GatedFfn& r, cudaStream_t st) {
   const size_t n8 = plane / 8;
   const cudaError_t e =
       launch_pdl(ffn_gate_grad_kernel, dim3(static_cast<unsigned>((n8 + 255) / 256)), dim3(256), 0, st, nullptr, 0,
-                 static_cast<const __nv_bfloat16*>(r.dh), static_cast<const __nv_bfloat16*>(r.pre), n8, r.act, dgu);
+                 static_cast<const __nv_bfloat16*>(r.dh), static_cast<const uint32_t*>(r.pre), n8, r.act, dgu);
   if (e != cudaSuccess) return fail(DFLASH2_ERR_CUDA, "gated FFN gradient launch failed: %s", cudaGetErrorString(e));
   FfnArgs a{};
   a.M = r.M; a.H = r.H; a.F = r.F;
@@ -565,7 +569,8 @@ int launch_gated_ffn_backward(const GatedFfn& r, cudaStream_t st) {
   a.tiles_n = tiles_of(r.H, kFTile);
   FfnMaps maps;
   if (r.dx != nullptr) {
-    if (!ffn_map(&maps.a0, dgu, r.M, r.F, 128) || !ffn_map(&maps.a1, dgu + plane, r.M, r.F, 128) ||
+    a.a_rows = std::min(128, (r.M + 7) / 8 * 8);
+    if (!ffn_map(&maps.a0, dgu, r.M, r.F, a.a_rows) || !ffn_map(&maps.a1, dgu + plane, r.M, r.F, a.a_rows) ||
         !ffn_map(&maps.b0, r.w_gate, r.F, r.H, kFK) || !ffn_map(&maps.b1, r.w_up, r.F, r.H, kFK))
       return fail(DFLASH2_ERR_CUDA, "tensor map encode failed (gated FFN dx)");
     a.rows = r.M;

@@ -190,6 +190,8 @@ struct GatedFfn {
 };
 size_t gated_ffn_workspace(int M, int H, int F, bool backward, int sms);
 int launch_gated_ffn(const GatedFfn& r, cudaStream_t st);
+constexpr int kFfnSmallRows = 128;  // up to here the forward pass is a weight stream (ffn_small.cu)
+int launch_gated_ffn_small(const GatedFfn& r, cudaStream_t st);
 int launch_gated_ffn_backward(const GatedFfn& r, cudaStream_t st);
 
 // ---------------------------------------------------------------- 4-bit key/value cache (kv4.cu)

@@ -45,7 +45,26 @@ def _forward_bound(x, wg, wu, g, u, kind):
         U * a * np.abs(u) + 1e-30
 
 
-SIZES = [(1, 8, 8), (16, 64, 128), (3, 200, 136), (130, 72, 1000), (257, 512, 392), (64, 1352, 2600), (300, 2568, 264),
+def _keep(g, u):
+    """The kept words: sign, 6 exponent bits (bias 31), 9 mantissa bits each, ties to even."""
+    def half(x):
+        m, e = np.frexp(np.abs(x))
+        e = np.where(x == 0, -30, np.maximum(e - 1, -30))                      # steps of 2^-39 below 2^-30
+        units = np.rint(np.abs(x) / 2.0 ** (e - 9))     # 512 .. 1024, or less for the smallest
+        code = ((e + 30) * 512 + units).astype(np.uint32)
+        return (np.signbit(x).astype(np.uint32) << 15) | code
+    return (half(g) | (half(u) << 16)).astype(np.uint32)
+
+
+def _kept(words):
+    def value(h):
+        e, m = (h >> 9) & 63, h & 511
+        v = np.where(e > 0, (512.0 + m) * 2.0 ** (e.astype(np.float64) - 31 - 9), m * 2.0 ** -39)
+        return np.where(h & 0x8000, -v, v)
+    return value(words & 0xFFFF), value(words >> 16)
+
+
+SIZES = [(1, 8, 8), (1, 2560, 72), (48, 5128, 1096), (128, 640, 13824), (16, 64, 128), (3, 200, 136), (130, 72, 1000), (257, 512, 392), (64, 1352, 2600), (300, 2568, 264),
          (1000, 128, 512)]
 
 
@@ -58,8 +77,9 @@ def test_forward(torch, M, H, F, kind):
     h, pre = d.dflash2_gated_ffn(_dev(torch, x), _dev(torch, wg), _dev(torch, wu), act=kind, want_pre=True)
     assert d.dflash2_poll_error() == 0
     assert np.all(np.abs(_host(h) - want) <= _forward_bound(x, wg, wu, g, u, kind))
-    for got, ref, w in ((pre[0], g, wg), (pre[1], u, wu)):
-        assert np.all(np.abs(_host(got) - ref) <= (1 + U) * H * E * _abs_product(x, w.T) + U * np.abs(ref))
+    for got, ref, w in zip(_kept(pre.cpu().numpy().view(np.uint32)), (g, u), (wg, wu)):
+        # 10 significant bits: half a step is 2^-10, and 2^-40 below 2^-30
+        assert np.all(np.abs(got - ref) <= (1 + U) * H * E * _abs_product(x, w.T) + 2.0 ** -10 * np.abs(ref) + 2.0 ** -40)
     h2 = d.dflash2_gated_ffn(_dev(torch, x), _dev(torch, wg), _dev(torch, wu), act=kind)
     assert torch.equal(h, h2)  # the same bits, with and without the kept products
 
@@ -67,15 +87,16 @@ def test_forward(torch, M, H, F, kind):
 @pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
 @pytest.mark.parametrize("M,H,F", SIZES)
 def test_backward(torch, M, H, F, kind):
-    """From given pre-activations (bf16 values), so that the bound is the backward pass's own: dg and
+    """From given pre-activations (exact in the kept form), so that the bound is the backward pass's own: dg and
     du carry one bf16 rounding (and a few fp32 steps) each, the products fp32 accumulation, the
     results one bf16 rounding."""
     import dflash2_block_drafter_gb300 as d
     x, wg, wu, dh = _inputs(M + F, M, H, F)
     _, g, u = S.gated_ffn(x, wg, wu, kind)
-    g, u = S.bf16(g), S.bf16(u)
+    words = _keep(g, u)
+    g, u = _kept(words)
     dx, dwg, dwu, dg, du = S.gated_ffn_backward(dh, g, u, x, wg, wu, kind)
-    pre = torch.stack([_dev(torch, g), _dev(torch, u)])
+    pre = torch.from_numpy(words.view(np.int32)).cuda()
     args = (_dev(torch, dh), pre, _dev(torch, x), _dev(torch, wg), _dev(torch, wu))
     got = d.dflash2_gated_ffn_backward(*args, act=kind)
     assert d.dflash2_poll_error() == 0
