@@ -49,9 +49,11 @@ constexpr int kFStage = 2 * kFHalf;
 constexpr int kFStages = 7;
 constexpr int kFBar = 256;
 constexpr int kFSmem = 1024 + kFStages * kFStage + kFBar;
-constexpr int kFThreads = 192;                 // warps: TMA, MMA, 4 x epilogue
+constexpr int kFEpiWarps = 8;                  // two per 32 TMEM lanes, half of the columns each
+constexpr int kFThreads = 64 + 32 * kFEpiWarps;  // warps: TMA, MMA, epilogue
 constexpr int kFGroupM = 8;                    // tiles are walked in strips of 8 row tiles: neighbours share operands in L2
 constexpr int kFSlot = 128 * kFTile;           // fp32 values of one CTA's partial tile
+constexpr int kFMaxParts = 6;                  // pairs that share a tile at most, when there are few tiles
 constexpr int kFMinPiece = 8;                  // k-blocks of a share at least
 constexpr uint64_t kFDrainNs = 100000000ull;
 
@@ -68,8 +70,9 @@ struct FfnArgs {
   int act;
   __nv_bfloat16 *out0, *out1;  // h | dx | dWg, dWu
   uint32_t* pre;          // [M][F] kept g and u, or null
-  float* slots;           // [CTA][128][256]
-  unsigned long long* flags;  // [CTA][4]
+  float* slots;           // [CTA][64][128][4]: ffn_slot
+  unsigned long long* flags;  // [CTA][epilogue warp]
+  int wide;               // outputs take 32-byte stores (16-column rows, 32-byte aligned)
   unsigned long long call;
   int* err;
 };
@@ -130,6 +133,10 @@ __device__ __forceinline__ void ffn_tile(const FfnArgs& a, int t, int& proj, int
   tm = strip * kFGroupM + in - tn * left;
 }
 
+// Where row r's columns c .. c + 3 of a partial tile lie in its slot: [column / 4][row], so that a warp
+// (32 rows, the same columns) moves 512 contiguous bytes.
+__device__ __forceinline__ int ffn_slot(int r, int c) { return (c / 4 * 128 + r) * 4; }
+
 __device__ __forceinline__ void ffn_abort(volatile int* abort_flag, int* err) {
   *abort_flag = 1;
   atomicCAS(err, 0, static_cast<int>(DFLASH2_ERR_TIMEOUT));
@@ -153,14 +160,43 @@ __device__ __forceinline__ bool ffn_wait_flag(const unsigned long long* flag, un
   return true;
 }
 
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 // Stores 32 consecutive values of a row (columns col .. col + 31 of `cols`, a multiple of 8) as bf16.
-__device__ __forceinline__ void ffn_store(__nv_bfloat16* row, int col, int cols, const float (&y)[32]) {
+__device__ __forceinline__ void ffn_store(__nv_bfloat16* row, int col, int cols, bool wide, const float (&y)[32]) {
 #pragma unroll
-  for (int v = 0; v < 4; ++v)
-    if (col + 8 * v < cols)
-      *reinterpret_cast<uint4*>(row + col + 8 * v) =
-          make_uint4(ffn_pack(y[8 * v], y[8 * v + 1]), ffn_pack(y[8 * v + 2], y[8 * v + 3]),
-                     ffn_pack(y[8 * v + 4], y[8 * v + 5]), ffn_pack(y[8 * v + 6], y[8 * v + 7]));
+  for (int v = 0; v < 2; ++v) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = ffn_pack(y[16 * v + 2 * j], y[16 * v + 2 * j + 1]);
+    const int c = col + 16 * v;
+    if (wide) {
+      if (c < cols) st_global_v8(row + c, w);
+    } else {
+      if (c < cols) *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (c + 8 < cols) *reinterpret_cast<uint4*>(row + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+// The same for the kept products of 32 channels (32 words).
+__device__ __forceinline__ void ffn_store_kept(uint32_t* row, int col, int cols, bool wide, const float (&g)[32],
+                                               const float (&u)[32]) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = ffn_keep(g[8 * v + j], u[8 * v + j]);
+    if (col + 8 * v >= cols) continue;
+    if (wide) {
+      st_global_v8(row + col + 8 * v, w);
+    } else {
+      *reinterpret_cast<uint4*>(row + col + 8 * v) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(row + col + 8 * v + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
 }
 
 template <int kMode>
@@ -188,7 +224,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&acc_full[b]), 1);
-      mbar_init(smem_u32(&acc_empty[b]), 8);  // both CTAs' epilogue warps
+      mbar_init(smem_u32(&acc_empty[b]), 2 * kFEpiWarps);  // both CTAs' epilogue warps
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
@@ -212,7 +248,13 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      const uint64_t pol = policy_evict_normal();
+      // L2: the operand that is read again stays, one that is read once goes first. A strip's rows are
+      // done with when its columns fit about one round; the columns are read once if there is one strip
+      // (1001 x 2568 x 6920: forward 91 -> 70 us, dx 100 -> 86, dW 122 -> 100; nothing at 4096 rows).
+      const bool once = a.tiles_m <= kFGroupM;
+      const uint64_t pol_a = kMode != kDw ? policy_evict_last()
+                                          : (2 * kFGroupM * a.tiles_n <= 3 * units ? policy_evict_first() : policy_evict_normal());
+      const uint64_t pol_b = kMode == kDw ? policy_evict_last() : (once ? policy_evict_first() : policy_evict_normal());
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -234,21 +276,21 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant
             mbar_arrive_expect_tx(fb, 2 * static_cast<uint32_t>(kMode == kDw ? kFStage : a.a_rows * 128 + kFHalf));
           const uint32_t sa = smem_u32(smem + stage * kFStage), sb = sa + kFHalf;
           if (kMode == kForward) {
-            tma_load_2d_pair(sa, &maps.a0, fbl, kb * kFK, m0, pol);
-            tma_load_2d_pair(sb, rank == 0 ? &maps.b0 : &maps.b1, fbl, kb * kFK, n0, pol);
+            tma_load_2d_pair(sa, &maps.a0, fbl, kb * kFK, m0, pol_a);
+            tma_load_2d_pair(sb, rank == 0 ? &maps.b0 : &maps.b1, fbl, kb * kFK, n0, pol_b);
           } else if (kMode == kDx) {
             const bool second = kb >= a.kblocks0;
             const int k = (second ? kb - a.kblocks0 : kb) * kFK;
             const CUtensorMap* mb = second ? &maps.b1 : &maps.b0;
-            tma_load_2d_pair(sa, second ? &maps.a1 : &maps.a0, fbl, k, m0, pol);
-            tma_load_2d_pair(sb, mb, fbl, n0, k, pol);
-            tma_load_2d_pair(sb + kFHalf / 2, mb, fbl, n0 + 64, k, pol);
+            tma_load_2d_pair(sa, second ? &maps.a1 : &maps.a0, fbl, k, m0, pol_a);
+            tma_load_2d_pair(sb, mb, fbl, n0, k, pol_b);
+            tma_load_2d_pair(sb + kFHalf / 2, mb, fbl, n0 + 64, k, pol_b);
           } else {
             const CUtensorMap* ma = proj == 0 ? &maps.a0 : &maps.a1;
-            tma_load_2d_pair(sa, ma, fbl, m0, kb * kFK, pol);
-            tma_load_2d_pair(sa + kFHalf / 2, ma, fbl, m0 + 64, kb * kFK, pol);
-            tma_load_2d_pair(sb, &maps.b0, fbl, n0, kb * kFK, pol);
-            tma_load_2d_pair(sb + kFHalf / 2, &maps.b0, fbl, n0 + 64, kb * kFK, pol);
+            tma_load_2d_pair(sa, ma, fbl, m0, kb * kFK, pol_a);
+            tma_load_2d_pair(sa + kFHalf / 2, ma, fbl, m0 + 64, kb * kFK, pol_a);
+            tma_load_2d_pair(sb, &maps.b0, fbl, n0, kb * kFK, pol_b);
+            tma_load_2d_pair(sb + kFHalf / 2, &maps.b0, fbl, n0 + 64, kb * kFK, pol_b);
           }
           if (++stage == kFStages) {
             stage = 0;
@@ -318,6 +360,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant
   } else {
     // ------------------------------------------------------------------ epilogue
     const int q = warp & 3;  // TMEM lanes 32 q ..
+    const int ew = warp - 2, half = ew >> 2;  // its half of the columns
     const int cta = static_cast<int>(blockIdx.x);
     FfnPiece p;
     for (int idx = 0; ffn_piece(a, unit, units, idx, p); ++idx) {
@@ -341,7 +384,7 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant
         int got = 1;
         if (lane == 0)
           for (int u = u_first; got && u < unit; ++u)
-            got = ffn_wait_flag(a.flags + (2 * u + static_cast<int>(rank)) * 4 + q, a.call, abort_flag) ? 1 : 0;
+            got = ffn_wait_flag(a.flags + (2 * u + static_cast<int>(rank)) * kFEpiWarps + ew, a.call, abort_flag) ? 1 : 0;
         got = __shfl_sync(0xffffffffu, got, 0);
         if (!got) {
           if (lane == 0) ffn_abort(abort_flag, a.err);
@@ -363,11 +406,10 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant
         if (u_first == unit || !valid) return;
         float sum[32] = {};
         for (int u = u_first; u < unit; ++u) {
-          const float* src = a.slots + static_cast<size_t>(2 * u + static_cast<int>(rank)) * kFSlot +
-                             static_cast<size_t>(lrow) * kFTile + c0;
+          const float* src = a.slots + static_cast<size_t>(2 * u + static_cast<int>(rank)) * kFSlot;
 #pragma unroll
           for (int v = 0; v < 8; ++v) {
-            const float4 f = __ldcg(reinterpret_cast<const float4*>(src + 4 * v));
+            const float4 f = __ldcg(reinterpret_cast<const float4*>(src + ffn_slot(lrow, c0 + 4 * v)));
             sum[4 * v] += f.x; sum[4 * v + 1] += f.y; sum[4 * v + 2] += f.z; sum[4 * v + 3] += f.w;
           }
         }
@@ -375,43 +417,38 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant
         for (int j = 0; j < 32; ++j) y[j] += sum[j];
       };
       if (partial) {
-        float* dst = a.slots + static_cast<size_t>(cta) * kFSlot + static_cast<size_t>(lrow) * kFTile;
-        for (int c0 = 0; c0 < kFTile; c0 += 32) {
+        // this warp's columns of the tile: for the forward pass half of g's and half of u's
+        float* dst = a.slots + static_cast<size_t>(cta) * kFSlot;
+        for (int i = 0; i < kFTile / 64; ++i) {
+          const int c0 = kMode == kForward ? (i >> 1) * 128 + half * 64 + (i & 1) * 32 : half * 128 + i * 32;
           float y[32];
           load(c0, y);
           if (!valid) continue;
 #pragma unroll
           for (int v = 0; v < 8; ++v)
-            *reinterpret_cast<float4*>(dst + c0 + 4 * v) = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
+            *reinterpret_cast<float4*>(dst + ffn_slot(lrow, c0 + 4 * v)) = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
         }
       } else if (kMode == kForward) {
         const size_t at = static_cast<size_t>(valid ? row : 0) * a.F;
-        for (int c0 = 0; c0 < 128; c0 += 32) {
+        for (int c0 = half * 64; c0 < half * 64 + 64; c0 += 32) {
           float g[32], u[32];
           load(c0, g);
           load(128 + c0, u);
           const int col = tn * 128 + c0;
-          if (valid && a.pre != nullptr) {
-#pragma unroll
-            for (int v = 0; v < 8; ++v)
-              if (col + 4 * v < a.F)
-                *reinterpret_cast<uint4*>(a.pre + at + col + 4 * v) =
-                    make_uint4(ffn_keep(g[4 * v], u[4 * v]), ffn_keep(g[4 * v + 1], u[4 * v + 1]),
-                               ffn_keep(g[4 * v + 2], u[4 * v + 2]), ffn_keep(g[4 * v + 3], u[4 * v + 3]));
-          }
+          if (valid && a.pre != nullptr) ffn_store_kept(a.pre + at, col, a.F, a.wide, g, u);
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             float slope;
             g[j] = g[j] * ffn_gate(g[j], a.act, slope) * u[j];
           }
-          if (valid) ffn_store(a.out0 + at, col, a.F, g);
+          if (valid) ffn_store(a.out0 + at, col, a.F, a.wide, g);
         }
       } else {
         __nv_bfloat16* out = (proj == 0 ? a.out0 : a.out1) + static_cast<size_t>(valid ? row : 0) * a.cols;
-        for (int c0 = 0; c0 < kFTile; c0 += 32) {
+        for (int c0 = half * 128; c0 < half * 128 + 128; c0 += 32) {
           float y[32];
           load(c0, y);
-          if (valid) ffn_store(out, tn * kFTile + c0, a.cols, y);
+          if (valid) ffn_store(out, tn * kFTile + c0, a.cols, a.wide, y);
         }
       }
       tc_fence_before();
@@ -420,10 +457,10 @@ __global__ void __launch_bounds__(kFThreads, 1) ffn_kernel(const __grid_constant
       if (partial) {
         __threadfence();  // every lane's rows are visible before the flag
         __syncwarp();
-        if (lane == 0) st_release_u64(a.flags + cta * 4 + q, a.call);
+        if (lane == 0) st_release_u64(a.flags + cta * kFEpiWarps + ew, a.call);
       }
       if (lane == 0)  // read: ready for a replay
-        for (int u = u_first; u < unit; ++u) a.flags[(2 * u + static_cast<int>(rank)) * 4 + q] = 0ull;
+        for (int u = u_first; u < unit; ++u) a.flags[(2 * u + static_cast<int>(rank)) * kFEpiWarps + ew] = 0ull;
     }
   }
 
@@ -476,7 +513,7 @@ int ffn_units(int sms) { return std::max(1, sms / 2); }
 
 size_t ffn_share_bytes(int sms) {
   const size_t ctas = 2 * static_cast<size_t>(ffn_units(sms));
-  return align256(ctas * kFSlot * sizeof(float)) + align256(ctas * 4 * sizeof(unsigned long long));
+  return align256(ctas * kFSlot * sizeof(float)) + align256(ctas * kFEpiWarps * sizeof(unsigned long long));
 }
 
 // A number that no other call of this process uses, and that stale memory will hardly hold.
@@ -496,15 +533,22 @@ int launch_ffn_gemm(const FfnMaps& maps, FfnArgs a, void* share_ws, cudaStream_t
   a.flags = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(share_ws) +
                                                   align256(2 * static_cast<size_t>(units) * kFSlot * sizeof(float)));
   a.call = ffn_call_number();
+  auto is32 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; };
+  a.wide = a.cols % 16 == 0 && is32(a.out0) && is32(a.out1) && is32(a.pre);
   a.err = device_error_word();
   if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
-  // The last round's tiles are cut into shares unless they nearly fill it: a cut tile costs its partial
-  // sums' way through the workspace. A share is at least kFMinPiece k-blocks.
+  // The last round's tiles are cut into shares unless they nearly fill it (a cut tile costs its partial
+  // sums' way through the workspace). Few tiles over all pairs would leave an owner many parts to add
+  // (19 of them at 1024 x 5120 with K = 27648: 320 us against 142 us of MMAs), so the round before is
+  // cut with them where there is one: then a share is a tile and a bit, and a tile has at most three
+  // parts. Without one, at most kFMaxParts pairs share a tile. A share has at least kFMinPiece k-blocks.
   const int rest = a.n_tiles % units;
   a.sk_tiles = 10 * rest > 9 * units ? 0 : rest;
+  if (a.sk_tiles > 0 && 3 * rest < units && a.n_tiles > units) a.sk_tiles += units;
   const long long total = static_cast<long long>(a.sk_tiles) * a.kblocks;
-  a.sk_units = static_cast<int>(std::max<long long>(1, std::min<long long>(units, total / kFMinPiece)));
-  if (a.sk_units < a.sk_tiles) a.sk_tiles = 0;  // k too short to cut
+  a.sk_units = static_cast<int>(std::max<long long>(
+      1, std::min({static_cast<long long>(units), total / kFMinPiece, static_cast<long long>(a.sk_tiles) * kFMaxParts})));
+  if (a.sk_units < units && a.sk_units <= a.sk_tiles) a.sk_tiles = 0;  // K too short to cut
   const int grid = 2 * std::min(units, a.sk_tiles > 0 ? std::max(a.sk_units, a.n_tiles - a.sk_tiles) : a.n_tiles);
   static unsigned done = 0;
   auto kern = ffn_kernel<kMode>;
