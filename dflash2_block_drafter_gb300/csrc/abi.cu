@@ -1,5 +1,7 @@
 // C ABI entry points: host-side validation, workspace carving and dispatch to the kernels.
 // Nothing here allocates device memory; every failure returns a status before any launch.
+#include <atomic>
+#include <chrono>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -42,6 +44,15 @@ int* device_error_word() {
     g_err_ptr_ready[dev] = 1;
   }
   return g_err_ptr[dev];
+}
+
+unsigned long long next_call_number() {
+  static const unsigned long long seed =
+      static_cast<unsigned long long>(std::chrono::high_resolution_clock::now().time_since_epoch().count()) *
+      0x9E3779B97F4A7C15ull;
+  static std::atomic<unsigned long long> count{0};
+  const unsigned long long n = seed + count.fetch_add(1, std::memory_order_relaxed) + 1;
+  return n != 0 ? n : 1;
 }
 
 int sm_count() {

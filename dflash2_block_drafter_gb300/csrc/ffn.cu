@@ -31,9 +31,6 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <atomic>
-#include <chrono>
-#include <mutex>
 
 #include "ffn.cuh"
 #include "internal.h"
@@ -140,14 +137,6 @@ __device__ __forceinline__ int ffn_slot(int r, int c) { return (c / 4 * 128 + r)
 __device__ __forceinline__ void ffn_abort(volatile int* abort_flag, int* err) {
   *abort_flag = 1;
   atomicCAS(err, 0, static_cast<int>(DFLASH2_ERR_TIMEOUT));
-}
-__device__ __forceinline__ unsigned long long ld_acquire_u64(const unsigned long long* p) {
-  unsigned long long v;
-  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_release_u64(unsigned long long* p, unsigned long long v) {
-  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
 // Waits (bounded) until a partial tile's flag holds this call's number.
 __device__ __forceinline__ bool ffn_wait_flag(const unsigned long long* flag, unsigned long long call,
@@ -516,23 +505,13 @@ size_t ffn_share_bytes(int sms) {
   return align256(ctas * kFSlot * sizeof(float)) + align256(ctas * kFEpiWarps * sizeof(unsigned long long));
 }
 
-// A number that no other call of this process uses, and that stale memory will hardly hold.
-unsigned long long ffn_call_number() {
-  static const unsigned long long seed =
-      static_cast<unsigned long long>(std::chrono::high_resolution_clock::now().time_since_epoch().count()) *
-      0x9E3779B97F4A7C15ull;
-  static std::atomic<unsigned long long> count{0};
-  const unsigned long long n = seed + count.fetch_add(1, std::memory_order_relaxed) + 1;
-  return n != 0 ? n : 1;
-}
-
 template <int kMode>
 int launch_ffn_gemm(const FfnMaps& maps, FfnArgs a, void* share_ws, cudaStream_t st) {
   const int units = ffn_units(sm_count());
   a.slots = static_cast<float*>(share_ws);
   a.flags = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(share_ws) +
                                                   align256(2 * static_cast<size_t>(units) * kFSlot * sizeof(float)));
-  a.call = ffn_call_number();
+  a.call = next_call_number();
   auto is32 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; };
   a.wide = a.cols % 16 == 0 && is32(a.out0) && is32(a.out1) && is32(a.pre);
   a.err = device_error_word();

@@ -22,6 +22,10 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 // Records a message for dflash2_last_error_message() and returns `status`.
 int fail(int status, const char* fmt, ...);
 
+// A number that no other call of this process uses, and that stale memory will hardly hold: flags in a
+// workspace that is never initialised carry it.
+unsigned long long next_call_number();
+
 int sm_count();  // multiprocessors of the current device (cached per device)
 
 // Raises a kernel's dynamic shared-memory limit once per (kernel, device), outside any stream
@@ -194,7 +198,7 @@ constexpr int kFfnSmallRows = 128;  // up to here the forward pass is a weight s
 int launch_gated_ffn_small(const GatedFfn& r, cudaStream_t st);
 int launch_gated_ffn_backward(const GatedFfn& r, cudaStream_t st);
 
-// ---------------------------------------------------------------- 4-bit key/value cache (kv4.cu)
+// ---------------------------------------------------------------- 4-bit key/value cache (kv4.cu, kv4_attention.cu)
 struct Kv4Rows {  // k_out / v_out null: k, v -> cache; else cache -> k_out, v_out
   const void *k, *v;
   int64_t k_stride, v_stride;  // elements between rows

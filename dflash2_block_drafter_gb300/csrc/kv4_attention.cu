@@ -1,0 +1,1220 @@
+// Attention over the 4-bit key/value cache on the tcgen05 tensor cores (dflash2.ts #block: the block's queries
+// attend to the context's keys and values and, bidirectionally, to the block's own).
+//
+// One sequence: key i < L is cached row i, key L + j its own row j (unquantised, N of them, or none); query
+// row t stands at position p_t = L + N - G + t and sees key i if i < L + N, and i <= p_t (causal), and
+// i > p_t - window (window > 0);
+//   out_t = sum_i softmax_i(scale q_t . k_i) v_i over the keys it sees, 0 if it sees none.
+//
+// One CTA works on one (sequence, key/value head) and up to 80 query rows at a time, over tiles of 128
+// keys. Keys are the tensor core's 128-row side in both products, so nothing is padded but the rows
+// (to N, a multiple of 16):
+//   S^T [128 keys x N rows]   = K tile [keys][D] . Q [rows][D]^T         (K-major operands)
+//   O^T [D channels x N rows] += V tile [keys][D]^T . P^T [keys][rows]   (both MN-major: V as it lies)
+// A softmax thread holds one key's scores of all (half of the) rows. It needs no reduction over keys:
+// the rows' reference (the number subtracted before the exponential) is only raised when some score
+// passes it by 2^8, which all threads agree on by one barrier a tile; then, rarely, the rows' maxima are
+// taken, and O and the sums rescaled. The sums stay per thread until the end.
+//
+// Precision: operands are fp16 (11 significant bits; with bf16 the keys', the values' and the
+// probabilities' roundings add up to twice the rounding of the bf16 result). fp16's range does not hold
+// every bf16 value, so each key row and each value row is divided by a power of two that brings its
+// largest value to [1, 2), and Q by one for all rows. The keys' factor multiplies the thread's scores (an
+// FMA that is there anyway), the values' the thread's probabilities, relative to the largest so far.
+//
+// Warps: 8 softmax (two per 32 TMEM lanes, half of the rows each), 8 dequant (four for K, four for V, 32
+// keys of a tile each: codes -> fp16 operand tiles in shared memory, 128-byte swizzle), 2 MMA (one thread
+// each for S and for O: issuing eight MMAs takes about as long as running them), 2 copy (a ring of bulk
+// copies for K, one for V). K, V and S are double-buffered. The block is launched with 96 registers a
+// thread; the softmax warps, whose sums stay in registers, take some of the others'. Issue slots bound a
+// tile (a warp's fixed instructions per tile count: sixteen softmax warps were slower than eight), so
+// addresses are kept ready in registers and waiting warps are suspended.
+//
+// CTAs are persistent, one an SM: all (sequence, head, row tile) items, each its tiles and a constant for
+// the change from one item to the next, form one line that is cut into equal ranges, whatever the lengths.
+// An item that spans up to eight ranges is finished by the range that holds its last tile: the earlier ones
+// leave partial results in the workspace, raise a flag there, and the owner adds them in order at its end
+// (so results do not depend on timing; it waits only for CTAs dispatched before it). A flag holds the
+// call's own 64-bit number, so the workspace needs no initialisation, and the owner clears it for a
+// replay. Items of more parts (a long context alone) are joined by kv4_join_kernel, many CTAs each.
+//
+// No wait blocks for ever, and none is skipped: after a timeout the roles run on (their results are void
+// and the error word says so), so that every barrier stays balanced.
+#include <algorithm>
+
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "kv4.cuh"
+#include "ptx.cuh"
+
+namespace dfl {
+namespace {
+
+constexpr int kBTile = 128;                 // keys per tile
+constexpr int kBSoftWarps = 8, kBDeqWarps = 8, kBMmaWarp = 16, kBCopyWarp = 18;  // two each
+constexpr int kBSoft = 32 * kBSoftWarps;    // softmax threads
+constexpr int kBThreads = 640;
+constexpr int kBSoftRegs = 120, kBOtherRegs = 80;  // 256 x 120 + 384 x 80 = 640 x 96
+constexpr int kBJoin = 8;                  // parts that an item's last range joins itself
+constexpr float kBSlack = 8.f;              // scores may pass the reference by 2^8
+constexpr float kBUnseen = 3e38f;           // minus the reference of a row that has seen no key: any score passes it
+constexpr float kBPadding = -1e30f;         // of a row that does not exist: no score passes it, and it counts nothing
+
+template <int D, int NK>                    // N = 16 NK rows
+struct BlockCfg {
+  static constexpr int N = 16 * NK;
+  // the change from one item to the next, in tiles (measured: 15 of 3.1 thousand cycles with 80 rows, 5 of
+  // 2.0 with 16)
+  static constexpr int kSetup = NK <= 2 ? 3 : NK;
+  static constexpr int kHalves = D / 64;                     // 64-channel halves of a K or V tile
+  static constexpr int kTileBytes = kHalves * kBTile * 128;  // fp16 [half][key][64]
+  static constexpr int kPBytes = (N > 64 ? 2 : 1) * kBTile * 128;
+  static constexpr int kQBytes = kHalves * N * 128;
+  static constexpr int kOffV = 2 * kTileBytes;
+  static constexpr int kOffP = kOffV + 2 * kTileBytes;  // (D = 64: the MMA reads one half past V: P)
+  static constexpr int kOffQ = kOffP + kPBytes;
+  static constexpr int kRaw = kBTile / kKvGranule * KvLayout<D>::kGranuleBytes;  // a tile of one side: [granule]
+  static constexpr int kRawStages = NK == 5 ? 2 : 3;
+  static constexpr int kOffRaw = kOffQ + kQBytes;            // [side][stage]
+  static constexpr int kOffInfo = kOffRaw + 2 * kRawStages * kRaw;           // float2 [4][128]: key factor, value factor
+  static constexpr int kOffRow = kOffInfo + 4 * kBTile * 8;  // per row: t, lo, hi, factor, offset
+  static constexpr int kOffSum = kOffRow + 5 * N * 4;        // float [4][N]
+  static constexpr int kOffBar = (kOffSum + 4 * N * 4 + 15) / 16 * 16;
+  static constexpr int kSmem = 1024 + kOffBar + 384;
+  static constexpr uint32_t kTmemCols = 3 * N <= 64 ? 64 : (3 * N <= 128 ? 128 : (3 * N <= 256 ? 256 : 512));
+};
+
+struct BlockArgs {
+  const __nv_bfloat16* q;
+  int64_t q_stride;
+  const uint8_t* cache;
+  const int32_t *table, *ctx;
+  const __nv_bfloat16 *k_new, *v_new;
+  int64_t new_stride;
+  int B, G, Hq, Hkv, R, r_magic, rows, tile_rows, row_tiles, page_shift, num_pages, width, cap, causal, window;
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* part_o;    // [CTA][2][N][D]
+  float2* part_ml;  // [CTA][2][N]
+  unsigned long long* flags;  // [CTA]
+  unsigned long long call;
+  int* err;
+};
+
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ bool bar_or(bool p) {  // over the softmax threads
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.s32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+      "selp.s32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<int>(p)), "n"(kBSoft)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void bar_soft() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kBSoft) : "memory"); }
+
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// One MMA whose descriptors share the upper words; `first` overwrites the accumulator.
+template <bool first>
+__device__ __forceinline__ void mma_lean(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t a_hi, uint32_t b_hi,
+                                         uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(a_hi), "r"(b_hi), "r"(idesc), "n"(first ? 0 : 1)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t t, float* x) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t t, const float* x) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// (Suspended, not spinning: the issue slots belong to the warps that work.)
+__device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait_suspend(bar, parity, 20000))
+    if (*abort_flag != 0 || globaltimer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      atomicCAS(err, 0, static_cast<int>(DFLASH2_ERR_TIMEOUT));
+      break;
+    }
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Token of query row r (r / R): r < 64 R, so ceil(2^20 / R) r is below 2^27 and exact after the shift.
+__device__ __forceinline__ int row_token(const BlockArgs& a, int r) { return (r * a.r_magic) >> 20; }
+
+// The keys of one sequence: [lo, hi) cached ones that some row sees, in `cached` tiles from lo / 128 on,
+// then (own) one tile of its own rows. At least one tile, so that every item is visited.
+struct BlockSeq {
+  int L, base, lo, hi, cached, tiles;
+};
+__device__ __forceinline__ BlockSeq block_seq(const BlockArgs& a, int b) {
+  BlockSeq s;
+  const int own = a.k_new != nullptr ? 1 : 0;
+  s.L = min(max(__ldg(a.ctx + b), 0), a.cap);  // (block_range records a length outside)
+  s.base = s.L + (own - 1) * a.G;
+  s.lo = a.window > 0 ? max(0, min(s.L, s.base - a.window + 1)) : 0;
+  s.hi = a.causal ? max(0, min(s.L, s.base + a.G)) : s.L;
+  s.cached = s.hi > s.lo ? (s.hi + kBTile - 1) / kBTile - s.lo / kBTile : 0;
+  s.tiles = max(1, s.cached + own);
+  return s;
+}
+
+// A CTA's range of the line of all tiles: where it starts and how many tiles it has.
+struct BlockRange {
+  long long total, first, count;  // in units: a tile, or a part of an item's setup
+  int b;                          // the sequence of its first unit, and that unit's place among the sequence's
+  long long in_seq;
+};
+// Block-wide (every thread calls it): sums the sequences' tiles and finds the range of CTA `c` of `n`.
+__device__ __forceinline__ BlockRange block_range(const BlockArgs& a, int setup, int c, int n, long long* scratch) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = (nt + 31) / 32;
+  const int hr = a.Hkv * a.row_tiles;
+  BlockRange r;
+  long long sum = 0;
+  for (int b = tid; b < a.B; b += nt) {
+    const int n = __ldg(a.ctx + b);
+    if (n < 0 || n > a.cap) atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_INVALID_ARG));
+    sum += block_seq(a, b).tiles + setup;
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+  if (lane == 0) scratch[warp] = sum;
+  __syncthreads();
+  sum = 0;
+  for (int w = 0; w < warps; ++w) sum += scratch[w];
+  r.total = sum * hr;
+  r.first = r.total * c / n;
+  r.count = r.total * (c + 1) / n - r.first;
+  __syncthreads();
+  long long before = 0;  // tiles of the sequences before this chunk of `nt`
+  if (tid == 0) scratch[34] = -1;
+  for (int b0 = 0; b0 < a.B; b0 += nt) {
+    const int b = b0 + tid;
+    const long long mine = b < a.B ? static_cast<long long>(block_seq(a, b).tiles + setup) * hr : 0;
+    long long inc = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, m);
+      if (lane >= m) inc += v;
+    }
+    if (lane == 31) scratch[warp] = inc;
+    __syncthreads();
+    long long off = before, chunk = 0;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) off += scratch[w];
+      chunk += scratch[w];
+    }
+    if (mine > 0 && r.first >= off + inc - mine && r.first < off + inc) {
+      scratch[34] = b;
+      scratch[35] = r.first - (off + inc - mine);
+    }
+    before += chunk;
+    __syncthreads();
+    if (scratch[34] >= 0) break;
+  }
+  r.b = static_cast<int>(scratch[34]);
+  r.in_seq = scratch[35];
+  return r;
+}
+
+// The range that holds unit g: the smallest c with floor((c + 1) total / n) > g.
+__device__ __forceinline__ int range_of(long long g, long long total, int n) {
+  return static_cast<int>(((g + 1) * n + total - 1) / total) - 1;
+}
+
+// Walks a range piece by piece: piece = consecutive tiles [j0, j1) of one item (sequence b, head and row tile
+// hr), none empty.
+template <int kSetup>
+struct BlockWalk {
+  int left;  // units (a cache that fits the memory has far fewer tiles than 2^31)
+  int b, hr, j0, j1, hrs;
+  long long start;  // the item's first unit
+  BlockSeq seq;
+  __device__ __forceinline__ BlockWalk(const BlockArgs& a, const BlockRange& r) {
+    left = static_cast<int>(r.count);
+    hrs = a.Hkv * a.row_tiles;
+    b = r.b;
+    j1 = -1;
+    if (left <= 0) return;
+    seq = block_seq(a, b);
+    hr = static_cast<int>(r.in_seq / (seq.tiles + kSetup));
+    const int u = static_cast<int>(r.in_seq - static_cast<long long>(hr) * (seq.tiles + kSetup));
+    start = r.first - u;
+    enter(u);
+  }
+  // at unit u of the item; a range that ends within the setup has nothing left
+  __device__ __forceinline__ void enter(int u) {
+    j0 = max(0, u - kSetup);
+    j1 = min(seq.tiles, u + left - kSetup);
+    left -= min(left, seq.tiles + kSetup - u);
+    if (j1 <= j0) j1 = -1;
+  }
+  __device__ __forceinline__ bool valid() const { return j1 > 0; }
+  __device__ __forceinline__ void next(const BlockArgs& a) {
+    if (left <= 0) {
+      j1 = -1;
+      return;
+    }
+    start += seq.tiles + kSetup;
+    if (++hr == hrs) {
+      hr = 0;
+      seq = block_seq(a, ++b);
+    }
+    enter(0);
+  }
+};
+
+// The ranges [c0, c1] that hold the tiles of the item that starts at unit `start`.
+struct BlockParts {
+  int c0, c1;
+  long long total;
+  int n;
+  __device__ __forceinline__ BlockParts(long long start, int setup, int tiles, long long total_, int n_) : total(total_), n(n_) {
+    c0 = range_of(start + setup, total, n);
+    c1 = range_of(start + setup + tiles - 1, total, n);
+  }
+  // (with fewer units than CTAs some ranges between are empty)
+  __device__ __forceinline__ bool empty(int c) const { return total * (c + 1) / n == total * c / n; }
+  // where the part of range c lies: the first part is a range's last piece, the others a range's first
+  __device__ __forceinline__ int64_t slot(int c) const { return c * 2LL + (c == c0 ? 1 : 0); }
+};
+
+// 2^floor(log2 x) of a positive float (bits below the exponent dropped), kept inside [2^-118, 2^118].
+__device__ __forceinline__ float pow2_of(float x) {
+  const uint32_t u = __float_as_uint(x) & 0x7f800000u;
+  return __uint_as_float(min(max(u, 0x04800000u), 0x7a800000u));
+}
+__device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float(0x7f000000u - __float_as_uint(p)); }
+
+// Channels (0, 4), (1, 5), (2, 6), (3, 7) of a word of codes: scale * code + bias. A code masked out at
+// bit 0 or 4 of a half-word is the fp16 subnormal n 2^-24 or n 2^-20; s24, s20: scale 2^24, scale 2^20.
+__device__ __forceinline__ uint4 dequant_word(uint32_t w, __half2 s24, __half2 s20, __half2 b) {
+  const uint32_t h = w >> 8;
+  const uint32_t n[4] = {w & 0x000F000Fu, w & 0x00F000F0u, h & 0x000F000Fu, h & 0x00F000F0u};
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 v = __hfma2((i & 1) ? s20 : s24, *reinterpret_cast<const __half2*>(&n[i]), b);
+    o[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+// Eight bf16 channels times a factor, in the same order.
+__device__ __forceinline__ uint4 convert_word(const uint4& u, float f) {
+  float x[8];
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = __bfloat1622float2(as_bf162(w[i]));
+    x[2 * i] = v.x * f;
+    x[2 * i + 1] = v.y * f;
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 v = __floats2half2_rn(x[i], x[i + 4]);
+    o[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ float max_abs8(const uint4& u) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t m = 0;  // magnitudes of bf16 compare as integers
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+  return __uint_as_float(m << 16);
+}
+
+// A row's (scale, bias) pairs as operands of dequant_word: half2 (scale 2^24, bias) over the row's power
+// of two, and that power times 2^7 (the factor to undo it).
+template <int kGroups>
+__device__ __forceinline__ float row_params(const uint32_t (&par)[2], uint32_t (&out)[2]) {
+  float2 p[2];
+  float m = 0.f;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    p[g] = __bfloat1622float2(as_bf162(par[g]));
+    m = fmaxf(m, fmaxf(fabsf(p[g].y), fabsf(fmaf(15.f, p[g].x, p[g].y))));
+  }
+  const float f = pow2_of(m), inv = pow2_inverse(f) * 0.0078125f;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const __half2 h = __floats2half2_rn(p[g].x * inv * 16777216.f, p[g].y * inv);
+    out[g] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return f * 128.f;
+}
+
+// Eight values reduced over a warp's lanes, halving the values a lane carries with each step: afterwards the
+// lanes 4 m .. 4 m + 3 hold value warp_reduce8_row.
+template <typename F>
+__device__ __forceinline__ float warp_reduce8(const float* x, int lane, F op) {
+  float s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float give = (lane & 16) ? x[i] : x[4 + i];
+    s[i] = op((lane & 16) ? x[4 + i] : x[i], __shfl_xor_sync(0xffffffffu, give, 16));
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float give = (lane & 8) ? s[i] : s[2 + i];
+    s[i] = op((lane & 8) ? s[2 + i] : s[i], __shfl_xor_sync(0xffffffffu, give, 8));
+  }
+  const float give = (lane & 4) ? s[0] : s[1];
+  float v = op((lane & 4) ? s[1] : s[0], __shfl_xor_sync(0xffffffffu, give, 4));
+  v = op(v, __shfl_xor_sync(0xffffffffu, v, 2));
+  return op(v, __shfl_xor_sync(0xffffffffu, v, 1));
+}
+__device__ __forceinline__ int warp_reduce8_row(int lane) {
+  return ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1);
+}
+
+// Where the eight channels of code word w of a row (w = D / 32 chunks of four words) lie among the operands'
+// 16-byte pieces, the same for K, Q and V: with D = 128 the four chunks' words k of a key, and those of its
+// neighbour, fall on eight different pieces of the swizzled 128 bytes, so neither the loads of codes
+// (two rows of 64 contiguous bytes a phase) nor the stores conflict.
+template <int D>
+__device__ __forceinline__ constexpr int piece_of_word(int w) {
+  return D == 128 ? ((w >> 1) & 1) * 8 + (w >> 2) * 2 + (w & 1) : w;
+}
+template <int D>
+__device__ __forceinline__ constexpr int word_of_piece(int p) {
+  return D == 128 ? ((p & 7) >> 1) * 4 + (p >> 3) * 2 + (p & 1) : p;
+}
+
+// Operand descriptor of MN-major fp16 tiles: 64-wide chunks 16 KB apart, 8 keys = 1024 bytes.
+__device__ __forceinline__ uint64_t desc_keys_sw128(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(kBTile * 128 >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+
+template <int D, int NK>
+__global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const BlockArgs a) {
+  using C = BlockCfg<D, NK>;
+  using L = KvLayout<D>;
+  using Walk = BlockWalk<C::kSetup>;
+  constexpr int N = C::N, NH = N / 2;  // rows, a softmax thread's rows
+  constexpr int NCH = D / 32;   // 32-channel chunks of a row
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align1024(smem_raw);
+  float2* info = reinterpret_cast<float2*>(smem + C::kOffInfo);      // [4][128]
+  float* row_t = reinterpret_cast<float*>(smem + C::kOffRow);        // minus the reference
+  int* row_lo = reinterpret_cast<int*>(row_t + N);                   // keys [lo, hi) that the row sees
+  int* row_hi = row_lo + N;
+  float* row_f = reinterpret_cast<float*>(row_hi + N);               // what the row's sum and O shrink by; at the end, O's factor
+  int* row_off = reinterpret_cast<int*>(row_f + N);                  // where the row starts in the sequence's out
+  float* row_red = reinterpret_cast<float*>(smem + C::kOffSum);      // [4][N] the TMEM quarters' maxima or sums
+  // barriers, as shared addresses
+  const uint32_t bars = smem_u32(smem + C::kOffBar);
+  const uint32_t kfull = bars, kempty = bars + 16, vfull = bars + 32, vempty = bars + 48;     // [2] each
+  const uint32_t sfull = bars + 64, sempty = bars + 80, pfull = bars + 96, odone = bars + 104, qfull = bars + 112;
+  const uint32_t raw_full = bars + 120, raw_empty = bars + 168;                               // [side][3]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 216);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* vref_s = reinterpret_cast<float*>(tmem_slot + 2);
+  uint32_t* vkey = tmem_slot + 3;
+  uint32_t* qmax = tmem_slot + 4;
+  uint32_t* came_s = tmem_slot + 5;  // [side][3]: the granules that came
+  __shared__ long long scratch[36];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(kfull + 8 * i, kBDeqWarps / 2);
+      mbar_init(vfull + 8 * i, kBDeqWarps / 2);
+      mbar_init(kempty + 8 * i, 1);
+      mbar_init(vempty + 8 * i, 1);
+      mbar_init(sfull + 8 * i, 1);
+      mbar_init(sempty + 8 * i, kBSoftWarps);
+    }
+    mbar_init(pfull, kBSoftWarps);
+    mbar_init(odone, 1);
+    mbar_init(qfull, kBSoftWarps);
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(raw_full + 8 * i, 1);
+      mbar_init(raw_empty + 8 * i, kBDeqWarps / 2);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == kBMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+  pdl_wait();
+  const BlockRange range = block_range(a, C::kSetup, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), scratch);
+
+  if (warp >= kBSoftWarps && warp < kBSoftWarps + kBDeqWarps) {
+    // ------------------------------------------------------------------ dequant
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBOtherRegs));
+    const int side = (warp - kBSoftWarps) >> 2, dw = warp & 3;  // K or V; keys 32 dw .. of each tile
+    const int ch = lane % NCH;
+    constexpr int kStep = 32 / NCH;                        // step i converts keys sub + i kStep of the warp's 32
+    const int sub = lane / NCH;
+    const uint8_t* ring = smem + C::kOffRaw + side * C::kRawStages * C::kRaw + dw * 2 * L::kGranuleBytes;
+    const uint32_t rfull = raw_full + side * 24, rempty = raw_empty + side * 24;
+    const uint32_t full = side == 0 ? kfull : vfull, empty = side == 0 ? kempty : vempty;
+    // where the lane's four 16-byte pieces of its first key go (key & 7 is the same in every step)
+    uint32_t to[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int pc = piece_of_word<D>(ch * 4 + k);
+      to[k] = smem_u32(smem) + side * C::kOffV + (pc >> 3) * (kBTile * 128) + (dw * 32 + sub) * 128 +
+              (((pc & 7) ^ (sub & 7)) << 4);
+    }
+    const uint8_t* codes0 = ring + sub * L::kRow + ch * 16;
+    const uint8_t* par0 = ring + (lane >> 4) * L::kGranuleBytes + L::kCodes + (lane & 15) * L::kGroups * 4;
+    uint32_t it = 0, stage = 0, rphase = 0;
+    for (Walk w(a, range); w.valid(); w.next(a)) {
+      const __nv_bfloat16* own_src = (side == 0 ? a.k_new : a.v_new);
+      if (own_src != nullptr) {
+        own_src += static_cast<int64_t>(w.b) * a.G * a.new_stride + w.hr / a.row_tiles * D;
+        if (w.j1 > w.seq.cached && dw * 32 + lane < a.G)  // the piece ends with its own rows
+#pragma unroll
+          for (int x = 0; x < D; x += 64) prefetch_l1(own_src + (dw * 32 + lane) * a.new_stride + x);
+      }
+      // the lane's key of the piece's tile j is seen for 128 j in [seen_lo, seen_hi)
+      const int at = w.seq.lo / kBTile * kBTile + dw * 32 + lane;
+      const int seen_lo = w.seq.lo - at, seen_hi = w.seq.hi - at;
+#pragma unroll 1
+      for (int j = w.j0; j < w.j1; ++j, ++it) {
+        const uint32_t buf = it & 1u;
+        const uint32_t par = ((it >> 1) & 1u) ^ 1u;
+        const uint32_t tile = buf * C::kTileBytes;
+        // the factors travel in a ring of four: tile it - 4's were read before tile it - 2's operands were
+        // released, which `empty` reports
+        float* inf = reinterpret_cast<float*>(info + (it & 3u) * kBTile + dw * 32) + side;
+        const bool cached = j < w.seq.cached;
+        if (cached || own_src == nullptr) {
+          // 32 keys from the ring. Rows that no query sees may hold anything: they count as zeros.
+          bool in = false;  // (neither cached nor own: a tile without keys)
+          if (cached) {
+            wait_on(rfull + 8 * stage, rphase, abort_flag, a.err);
+            in = ((came_s[side * 3 + stage] >> (2 * dw + (lane >> 4))) & 1u) && j * kBTile >= seen_lo && j * kBTile < seen_hi;
+          }
+          const uint32_t raw = stage * C::kRaw;
+          uint4 c[NCH];
+#pragma unroll
+          for (int i = 0; i < NCH; ++i)  // every load before the first store
+            c[i] = *reinterpret_cast<const uint4*>(
+                codes0 + raw + (D == 128 ? (i >> 1) * L::kGranuleBytes + (i & 1) * 8 * L::kRow : i * L::kGranuleBytes));
+          uint32_t pr[2] = {0u, 0u}, po[2] = {0u, 0u};
+          if (in) {
+            pr[0] = *reinterpret_cast<const uint32_t*>(par0 + raw);
+            if (L::kGroups == 2) pr[1] = *reinterpret_cast<const uint32_t*>(par0 + raw + 4);
+          }
+          const float f = row_params<L::kGroups>(pr, po);
+          uint32_t sb_bits[NCH];
+#pragma unroll
+          for (int i = 0; i < NCH; ++i) {
+            const uint32_t w0 = __shfl_sync(0xffffffffu, po[0], sub + i * kStep);
+            const uint32_t w1 = L::kGroups == 2 ? __shfl_sync(0xffffffffu, po[1], sub + i * kStep) : w0;
+            sb_bits[i] = ch >= 2 ? w1 : w0;
+          }
+          if (cached) {  // read out (the shuffles joined the lanes)
+            if (lane == 0) mbar_arrive(rempty + 8 * stage);
+            if (++stage == C::kRawStages) {
+              stage = 0;
+              rphase ^= 1u;
+            }
+          }
+          wait_on(empty + 8 * buf, par, abort_flag, a.err);
+          inf[2 * lane] = side == 0 || in ? f : -1.f;  // values' -1: the key is not there
+#pragma unroll
+          for (int i = 0; i < NCH; ++i) {
+            const __half2 sb = *reinterpret_cast<const __half2*>(&sb_bits[i]);
+            const __half2 s24 = __low2half2(sb), b = __high2half2(sb);
+            const __half2 s20 = __hmul2(s24, __float2half2_rn(0.0625f));
+            const uint32_t cw[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) st_shared_v4(to[k] + tile + i * kStep * 128, dequant_word(cw[k], s24, s20, b));
+          }
+        } else {
+          // the sequence's own rows
+          wait_on(empty + 8 * buf, par, abort_flag, a.err);
+#pragma unroll 1
+          for (int i = 0; i < NCH; ++i) {
+            const int t = sub + i * kStep, key = dw * 32 + t;
+            float f = 0.f;
+            uint4 u[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (dw * 32 + i * kStep < a.G) {
+              float m = 0.f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (key < a.G) u[k] = __ldg(reinterpret_cast<const uint4*>(own_src + key * a.new_stride + ch * 32 + 8 * k));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) m = fmaxf(m, max_abs8(u[k]));
+#pragma unroll
+              for (int x = 1; x < NCH; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+              f = pow2_of(m) * 128.f;
+              const float inv = pow2_inverse(pow2_of(m)) * 0.0078125f;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) u[k] = convert_word(u[k], inv);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) st_shared_v4(to[k] + tile + i * kStep * 128, u[k]);
+            if (ch == 0) inf[2 * t] = side == 0 || key < a.G ? f : -1.f;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + 8 * buf);
+      }
+    }
+  } else if (warp == kBMmaWarp || warp == kBMmaWarp + 1) {
+    // ------------------------------------------------------------------ MMA issuers: S, and O
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBOtherRegs));
+    if (lane == 0) {
+      constexpr uint32_t kFmt = (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);  // f32 <- f16, M = 128
+      uint32_t it = 0, piece = 0;
+      // descriptors: the lower words of the operands' first steps (address / 16, leading offset), and the
+      // upper word (stride 1024 bytes, 128-byte swizzle), the same for all
+      if (warp == kBMmaWarp) {
+        const uint64_t kd = desc_kmajor_sw128(smem_u32(smem)), qd = desc_kmajor_sw128(smem_u32(smem + C::kOffQ));
+        const uint32_t hi = static_cast<uint32_t>(kd >> 32), k_lo = static_cast<uint32_t>(kd), q = static_cast<uint32_t>(qd);
+        for (Walk w(a, range); w.valid(); w.next(a), ++piece) {
+          wait_on(qfull, piece & 1u, abort_flag, a.err);
+          for (int j = w.j0; j < w.j1; ++j, ++it) {
+            const uint32_t buf = it & 1u;
+            wait_on(sempty + 8 * buf, ((it >> 1) & 1u) ^ 1u, abort_flag, a.err);
+            wait_on(kfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
+            tc_fence_after();
+            const uint32_t k = k_lo + buf * (C::kTileBytes / 16), d = tmem + buf * N;
+            mma_lean<true>(d, k, q, hi, hi, kFmt);
+#pragma unroll
+            for (int s = 1; s < D / 16; ++s)
+              mma_lean<false>(d, k + (s >> 2) * (kBTile * 128 / 16) + 2 * (s & 3), q + (s >> 2) * (N * 128 / 16) + 2 * (s & 3),
+                              hi, hi, kFmt);
+            mma_commit(sfull + 8 * buf);
+            mma_commit(kempty + 8 * buf);
+          }
+        }
+      } else {
+        const uint64_t vd = desc_keys_sw128(smem_u32(smem + C::kOffV)), pd = desc_keys_sw128(smem_u32(smem + C::kOffP));
+        const uint32_t hi = static_cast<uint32_t>(vd >> 32), v_lo = static_cast<uint32_t>(vd), p = static_cast<uint32_t>(pd);
+        constexpr uint32_t id = kFmt | (1u << 15) | (1u << 16);
+        const uint32_t d = tmem + 2 * N;
+        for (Walk w(a, range); w.valid(); w.next(a))
+          for (int j = w.j0; j < w.j1; ++j, ++it) {
+            const uint32_t buf = it & 1u;
+            wait_on(vfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
+            wait_on(pfull, it & 1u, abort_flag, a.err);
+            tc_fence_after();
+            const uint32_t v = v_lo + buf * (C::kTileBytes / 16);
+            if (j > w.j0)
+              mma_lean<false>(d, v, p, hi, hi, id);
+            else
+              mma_lean<true>(d, v, p, hi, hi, id);
+#pragma unroll
+            for (int s = 1; s < kBTile / 16; ++s) mma_lean<false>(d, v + 128 * s, p + 128 * s, hi, hi, id);
+            mma_commit(odone);
+            mma_commit(vempty + 8 * buf);
+          }
+      }
+      if (*abort_flag != 0) {  // the MMAs in flight end before the CTA leaves
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kBCopyWarp) {
+    // ------------------------------------------------------------------ copies of one side
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBOtherRegs));
+    // A lane per granule looks up its page; the first granule of each run that lies together in a page
+    // (the tile, a page, or a granule) is copied with the rest of its run.
+    const int side = warp - kBCopyWarp;
+    const int granules = (1 << a.page_shift) / kKvGranule, run = min(granules, kBTile / kKvGranule);
+    const uint32_t rfull = raw_full + side * 24, rempty = raw_empty + side * 24;
+    uint32_t stage = 0, phase = 1;
+    for (Walk w(a, range); w.valid(); w.next(a)) {
+      const int last = min(w.j1, w.seq.cached);
+      for (int j0 = w.j0; j0 < last; j0 += 4) {  // pages of four tiles at a time: 32 granules
+        const int g0 = (w.seq.lo / kBTile + j0) * (kBTile / kKvGranule) + lane;  // the lane's granule of the sequence
+        const int key = g0 * kKvGranule;
+        int page = -1;
+        // a granule that some row sees (a window may have left the others' pages behind)
+        if (j0 + lane / 8 < last && key < w.seq.hi && key + kKvGranule > w.seq.lo) {
+          page = __ldg(a.table + static_cast<int64_t>(w.b) * a.width + (key >> a.page_shift));
+          if (page < 0 || page >= a.num_pages) {
+            atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_BAD_INDEX));
+            page = -1;
+          }
+        }
+        const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+        for (int j = j0; j < min(j0 + 4, last); ++j) {
+          const uint32_t got = (have >> (8 * (j - j0))) & 0xffu;
+          wait_on(rempty + 8 * stage, phase, abort_flag, a.err);
+          if (lane == 0) {
+            came_s[side * 3 + stage] = got;
+            mbar_arrive_expect_tx(rfull + 8 * stage, static_cast<uint32_t>(__popc(got)) * L::kGranuleBytes);
+          }
+          __syncwarp();
+          const int g = lane & 7, first = g & ~(run - 1);
+          // the granules of this lane's run that came, copied by the lane of the first of them (those no
+          // row sees lie at the run's ends, so what came is contiguous)
+          const uint32_t mine = (got >> first) & ((1u << run) - 1u);
+          if (lane / 8 == j - j0 && mine != 0u && g == first + __ffs(mine) - 1)
+            bulk_load(smem_u32(smem + C::kOffRaw + (side * C::kRawStages + stage) * C::kRaw + g * L::kGranuleBytes),
+                      a.cache + (((static_cast<int64_t>(page) * a.Hkv + w.hr / a.row_tiles) * 2 + side) * granules +
+                                 (g0 & (granules - 1))) *
+                                    static_cast<int64_t>(L::kGranuleBytes),
+                      static_cast<uint32_t>(__popc(mine)) * L::kGranuleBytes, rfull + 8 * stage);
+          __syncwarp();
+          if (++stage == C::kRawStages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBSoftRegs));
+    const int quad = warp & 3;                    // TMEM lanes 32 quad .., rows (warp / 4) NH ..
+    const int key_in = quad * 32 + lane;          // the thread's key of each tile; at the end, its channel
+    const int r0 = (warp >> 2) * NH;
+    const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(r0);
+    uint32_t to[NK];                              // where eight rows' probabilities of the thread's key go
+#pragma unroll
+    for (int c = 0; c < NK; ++c) {
+      const int r8 = r0 / 8 + c;
+      to[c] = smem_u32(smem + C::kOffP) + key_in * 128 + (r8 >> 3) * (kBTile * 128) + (((r8 & 7) ^ (key_in & 7)) << 4);
+    }
+    // Q of a piece: its rows as fp16 over their common power of two (returned), channels in the codes' order
+    auto load_q = [&](const Walk& w) {
+      const int head = w.hr / a.row_tiles, row_first = (w.hr % a.row_tiles) * a.tile_rows;
+      const int nrows = min(a.tile_rows, a.rows - row_first);
+      constexpr int kQItems = (N * (D / 8) + kBSoft - 1) / kBSoft;
+      uint4 qv[kQItems];
+      float qm = 0.f;
+#pragma unroll
+      for (int i = 0; i < kQItems; ++i) {
+        const int x = threadIdx.x + i * kBSoft, r = x / (D / 8), c = x % (D / 8);
+        qv[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < nrows) {
+          const int rr = row_first + r, t = row_token(a, rr);
+          qv[i] = __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(w.b) * a.G + t) * a.q_stride +
+                                                       (head * a.R + rr - t * a.R) * D + 8 * c));
+        }
+      }
+      if (threadIdx.x == 0) *qmax = 0u;
+      bar_soft();
+#pragma unroll
+      for (int i = 0; i < kQItems; ++i) qm = fmaxf(qm, max_abs8(qv[i]));
+      const uint32_t qk = __reduce_max_sync(0xffffffffu, __float_as_uint(qm));
+      if (lane == 0) atomicMax(qmax, qk);
+      bar_soft();
+      const float qf = pow2_of(__uint_as_float(*qmax));
+#pragma unroll
+      for (int i = 0; i < kQItems; ++i) {
+        const int x = threadIdx.x + i * kBSoft, r = x / (D / 8), c = x % (D / 8);
+        const int pc = piece_of_word<D>(c);
+        if (r < N)
+          *reinterpret_cast<uint4*>(smem + C::kOffQ + (pc >> 3) * (N * 128) + r * 128 + (((pc & 7) ^ (r & 7)) << 4)) =
+              convert_word(qv[i], pow2_inverse(qf));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qfull);
+      return qf;
+    };
+    uint32_t it = 0;
+    Walk w(a, range);
+    // the first piece may end an item that earlier ranges began: joined with their parts at the end
+    const bool joins = w.valid() && w.j0 > 0 && w.j1 == w.seq.tiles;
+    const int join_b = w.b, join_hr = w.hr, join_tiles = w.seq.tiles;
+    const long long join_start = w.start;
+    bool gave = false;
+    float qf = 1.f;
+    for (bool start = true; w.valid(); start = false) {
+      if (start) qf = load_q(w);
+      const int head = w.hr / a.row_tiles, row_first = (w.hr % a.row_tiles) * a.tile_rows;
+      const int nrows = min(a.tile_rows, a.rows - row_first);
+      if (threadIdx.x == 0) {
+        *vkey = 0u;
+        *vref_s = 0.f;
+      }
+      if (threadIdx.x < N) {
+        const int r = threadIdx.x, rr = row_first + r, t = row_token(a, rr), pos = w.seq.base + t;
+        const int all = w.seq.L + (a.k_new != nullptr ? a.G : 0);
+        row_t[r] = r < nrows ? kBUnseen : kBPadding;
+        row_lo[r] = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+        row_hi[r] = r < nrows ? (a.causal ? min(all, pos + 1) : all) : 0;
+        row_off[r] = (t * a.Hq + head * a.R + rr - t * a.R) * D;
+      }
+      bar_soft();
+      const float qscale = qf * a.scale_log2;
+      // seen by every row of the tile: [all_lo, all_hi)
+      const int t_first = row_token(a, row_first), t_last = row_token(a, row_first + nrows - 1);
+      const int all_lo = a.window > 0 ? w.seq.base + t_last - a.window + 1 : 0;
+      const int all_hi = a.causal ? w.seq.base + t_first + 1 : 0x7fffffff;
+
+      float l[NH];
+#pragma unroll
+      for (int r = 0; r < NH; ++r) l[r] = 0.f;
+      float vinv = 0.f;  // 1 / the values' reference (0: none yet)
+
+      float x[NH];
+      auto ready = [&](uint32_t i) {  // S of tile i and its values' factors, without waiting
+        return __all_sync(0xffffffffu, mbar_test(vfull + 8 * (i & 1u), (i >> 1) & 1u) &&
+                                           mbar_test(sfull + 8 * (i & 1u), (i >> 1) & 1u));
+      };
+      auto load_s = [&](uint32_t i) {
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < NH; c += 8) tmem_ld8(tl + (i & 1u) * N + static_cast<uint32_t>(c), x + c);
+      };
+      bool loaded = false;  // this tile's scores were requested behind the last one's probabilities
+      for (int j = w.j0; j < w.j1; ++j, ++it) {
+        const uint32_t buf = it & 1u;
+        const int key0 = j >= w.seq.cached ? w.seq.L : (w.seq.lo / kBTile + j) * kBTile;
+        const int key = key0 + key_in;
+        if (!loaded) {
+          wait_on(vfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
+          wait_on(sfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
+          __syncwarp();
+          load_s(it);
+        }
+        const float2 inf = info[(it & 3) * kBTile + key_in];
+        const float f = inf.x * qscale;
+        const bool there = inf.y >= 0.f;
+        const bool masked = key0 < all_lo || key0 + kBTile > all_hi || __any_sync(0xffffffffu, !there);
+        tmem_ld_wait();
+        for (;;) {
+          // scores (log2 domain) relative to the rows' references
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int r = 0; r < NH; r += 4) {
+            const float4 t = *reinterpret_cast<const float4*>(row_t + r0 + r);
+            const float2 y0 = __ffma2_rn(make_float2(x[r], x[r + 1]), make_float2(f, f), make_float2(t.x, t.y));
+            const float2 y1 = __ffma2_rn(make_float2(x[r + 2], x[r + 3]), make_float2(f, f), make_float2(t.z, t.w));
+            x[r] = y0.x; x[r + 1] = y0.y; x[r + 2] = y1.x; x[r + 3] = y1.y;
+          }
+          if (masked) {
+#pragma unroll
+            for (int r = 0; r < NH; r += 4) {
+              const int4 lo = *reinterpret_cast<const int4*>(row_lo + r0 + r), hi = *reinterpret_cast<const int4*>(row_hi + r0 + r);
+              if (!there || key < lo.x || key >= hi.x) x[r] = -INFINITY;
+              if (!there || key < lo.y || key >= hi.y) x[r + 1] = -INFINITY;
+              if (!there || key < lo.z || key >= hi.z) x[r + 2] = -INFINITY;
+              if (!there || key < lo.w || key >= hi.w) x[r + 3] = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < NH; ++r) top[r & 3] = fmaxf(top[r & 3], x[r]);
+          top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+          if (!bar_or(top[0] > kBSlack || (there && !(inf.y * vinv <= 1.f && vinv > 0.f)))) break;
+          // ---- raise the references: the rows' maxima over the tile, the values' largest power of two
+          __syncwarp();
+          load_s(it);
+          tmem_ld_wait();
+#pragma unroll
+          for (int r = 0; r < NH; r += 4) {
+            const int4 lo = *reinterpret_cast<const int4*>(row_lo + r0 + r), hi = *reinterpret_cast<const int4*>(row_hi + r0 + r);
+            x[r] = there && key >= lo.x && key < hi.x ? x[r] * f : -INFINITY;
+            x[r + 1] = there && key >= lo.y && key < hi.y ? x[r + 1] * f : -INFINITY;
+            x[r + 2] = there && key >= lo.z && key < hi.z ? x[r + 2] * f : -INFINITY;
+            x[r + 3] = there && key >= lo.w && key < hi.w ? x[r + 3] * f : -INFINITY;
+          }
+#pragma unroll
+          for (int c = 0; c < NH; c += 8) {
+            const float v = warp_reduce8(x + c, lane, [](float p, float q) { return fmaxf(p, q); });
+            if ((lane & 3) == 0) row_red[quad * N + r0 + c + warp_reduce8_row(lane)] = v;
+          }
+          const uint32_t vk = __reduce_max_sync(0xffffffffu, there ? __float_as_uint(inf.y) : 0u);
+          if (lane == 0) atomicMax(vkey, vk);
+          bar_soft();
+          const float vold = *vref_s, vnew = fmaxf(vold, __uint_as_float(*vkey));
+          if (threadIdx.x < N) {
+            const int r = threadIdx.x;
+            const float told = row_t[r];
+            const float mx = fmaxf(fmaxf(row_red[r], row_red[N + r]), fmaxf(row_red[2 * N + r], row_red[3 * N + r]));
+            float shrink = 1.f;
+            if (told != kBPadding && mx > -INFINITY && mx > -told) {
+              shrink = told == kBUnseen ? 0.f : ex2_approx(-told - mx);
+              row_t[r] = -mx;
+            }
+            row_f[r] = shrink;
+          }
+          bar_soft();
+          if (threadIdx.x == 0) {
+            *vref_s = vnew;
+            *vkey = 0u;
+          }
+          vinv = vnew > 0.f ? pow2_inverse(vnew) : 0.f;
+#pragma unroll
+          for (int r = 0; r < NH; r += 4) {
+            const float4 g = *reinterpret_cast<const float4*>(row_f + r0 + r);
+            l[r] *= g.x; l[r + 1] *= g.y; l[r + 2] *= g.z; l[r + 3] *= g.w;
+          }
+          if (j > w.j0) {
+            const float vscale = vold > 0.f ? vold * pow2_inverse(vnew) : 0.f;
+            wait_on(odone, (it - 1) & 1u, abort_flag, a.err);
+            tc_fence_after();
+            __syncwarp();
+#pragma unroll 1
+            for (int c = 0; c < NH; c += 8) {
+              float o[8];
+              tmem_ld8(tl + static_cast<uint32_t>(2 * N + c), o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[i] *= row_f[r0 + c + i] * vscale;
+              tmem_st8(tl + static_cast<uint32_t>(2 * N + c), o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          __syncwarp();
+          load_s(it);
+          tmem_ld_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sempty + 8 * buf);
+        // ---- probabilities: fp32 sums, fp16 operand
+        const __half2 w2 = __float2half2_rn(there ? inf.y * vinv : 0.f);
+        if (it > 0) wait_on(odone, (it - 1) & 1u, abort_flag, a.err);  // the operand tile is free
+#pragma unroll
+        for (int c = 0; c < NK; ++c) {
+          uint32_t p[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int r = 8 * c + 2 * i;
+            const float2 e = make_float2(ex2_approx(x[r]), ex2_approx(x[r + 1]));
+            const float2 sum = __fadd2_rn(make_float2(l[r], l[r + 1]), e);
+            l[r] = sum.x;
+            l[r + 1] = sum.y;
+            const __half2 h = __hmul2(__floats2half2_rn(e.x, e.y), w2);
+            p[i] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          st_shared_v4(to[c], make_uint4(p[0], p[1], p[2], p[3]));
+        }
+        // the next tile's scores travel while the fence completes (x is free), if they are there
+        loaded = j + 1 < w.j1 && ready(it + 1);
+        if (loaded) load_s(it + 1);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull);
+      }
+
+      // ---- the item's (or its part's) result
+#pragma unroll
+      for (int c = 0; c < NH; c += 8) {
+        const float v = warp_reduce8(l + c, lane, [](float p, float q) { return p + q; });
+        if ((lane & 3) == 0) row_red[quad * N + r0 + c + warp_reduce8_row(lane)] = v;
+      }
+      const bool complete = w.j0 == 0 && w.j1 == w.seq.tiles;
+      if (w.j1 < w.seq.tiles) {  // the last piece goes on in the next range: does that range join it?
+        const BlockParts parts(w.start, C::kSetup, w.seq.tiles, range.total, static_cast<int>(gridDim.x));
+        gave = parts.c1 - parts.c0 < kBJoin;
+      }
+      Walk next = w;
+      next.next(a);
+      if (next.valid()) qf = load_q(next);  // (every S of this piece is done): its scores start meanwhile
+      bar_soft();
+      const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (w.j0 > 0 ? 0 : 1)) * N;
+      if (threadIdx.x < N) {
+        const int r = threadIdx.x;
+        const float sum = row_red[r] + row_red[N + r] + row_red[2 * N + r] + row_red[3 * N + r];
+        const bool some = row_t[r] != kBUnseen;
+        row_f[r] = some ? (complete ? (sum > 0.f ? *vref_s / sum : 0.f) : *vref_s) : 0.f;
+        if (!complete && r < nrows) a.part_ml[slot + r] = make_float2(some ? -row_t[r] : -INFINITY, sum);
+      }
+      bar_soft();
+      // the thread's channel: operand position p of each eight holds channel p / 2 + 4 (p % 2) of its word
+      const int ch = word_of_piece<D>(key_in >> 3) * 8 + ((key_in & 7) >> 1) + 4 * (key_in & 1);
+      wait_on(odone, (it - 1) & 1u, abort_flag, a.err);
+      tc_fence_after();
+      __syncwarp();
+      __nv_bfloat16* out = a.out + static_cast<int64_t>(w.b) * a.G * a.Hq * D + ch;
+      float* part = a.part_o + (slot + r0) * D + ch;
+#pragma unroll
+      for (int c = 0; c < NH; c += 8) tmem_ld8(tl + static_cast<uint32_t>(2 * N + c), x + c);
+      tmem_ld_wait();
+      if (key_in < D) {
+        const int n = nrows - r0;
+#pragma unroll
+        for (int r = 0; r < NH; r += 4) {
+          const float4 g4 = *reinterpret_cast<const float4*>(row_f + r0 + r);
+          const int4 o4 = *reinterpret_cast<const int4*>(row_off + r0 + r);
+          const float g[4] = {g4.x, g4.y, g4.z, g4.w};
+          const int off[4] = {o4.x, o4.y, o4.z, o4.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float v = g[i] != 0.f ? x[r + i] * g[i] : 0.f;  // (O of a row that saw nothing is not looked at)
+            if (r + i < n) {
+              if (complete)
+                out[off[i]] = __float2bfloat16_rn(v);
+              else
+                part[(r + i) * D] = v;
+            }
+          }
+        }
+      }
+      __syncwarp();
+      tc_fence_before();
+      bar_soft();  // the rows' data are read before the next piece sets them
+      w = next;
+    }
+    if (gave) {  // the last piece goes on in the next range
+      __threadfence();
+      bar_soft();
+      if (threadIdx.x == 0) st_release_u64(a.flags + blockIdx.x, a.call);
+    }
+    if (joins) {
+      const BlockParts parts(join_start, C::kSetup, join_tiles, range.total, static_cast<int>(gridDim.x));
+      const int c0 = parts.c0, me = parts.c1;
+      if (me - c0 < kBJoin) {
+        if (threadIdx.x < me - c0 && !parts.empty(c0 + threadIdx.x)) {
+          unsigned long long* flag = a.flags + c0 + threadIdx.x;
+          const uint64_t t0 = globaltimer_ns();
+          while (ld_acquire_u64(flag) != a.call) {
+            __nanosleep(64);
+            if (*abort_flag != 0 || globaltimer_ns() - t0 > kWaitLimitNs) {
+              *abort_flag = 1;
+              atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_TIMEOUT));
+              break;
+            }
+          }
+          *flag = 0ull;  // read: ready for a replay
+        }
+        bar_soft();
+        const int head = join_hr / a.row_tiles, row_first = (join_hr % a.row_tiles) * a.tile_rows;
+        const int nrows = min(a.tile_rows, a.rows - row_first);
+        // the parts' weights per row (over the sum of all), in the keys' factors' place
+        float* weight = reinterpret_cast<float*>(info);  // [kBJoin][N]
+        if (threadIdx.x < nrows) {
+          float2 ml[kBJoin];
+          float mm = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int p = 0; p < kBJoin; ++p) {
+            const bool in = c0 + p <= me && !parts.empty(c0 + p);
+            ml[p] = in ? __ldcg(a.part_ml + parts.slot(c0 + p) * N + threadIdx.x) : make_float2(-INFINITY, 0.f);
+            mm = fmaxf(mm, ml[p].x);
+          }
+#pragma unroll
+          for (int p = 0; p < kBJoin; ++p) {
+            ml[p].x = ml[p].x == -INFINITY ? 0.f : ex2_approx(ml[p].x - mm);
+            sum += ml[p].x * ml[p].y;
+          }
+#pragma unroll
+          for (int p = 0; p < kBJoin; ++p) weight[p * N + threadIdx.x] = sum > 0.f ? ml[p].x / sum : 0.f;
+        }
+        bar_soft();
+#pragma unroll 2
+        for (int i = threadIdx.x; i < nrows * (D / 4); i += kBSoft) {
+          const int r = i / (D / 4), col = i % (D / 4) * 4;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int p = 0; p < kBJoin; ++p) {
+            const float f = c0 + p <= me ? weight[p * N + r] : 0.f;  // 0: nothing of the row there
+            if (f == 0.f) continue;
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (parts.slot(c0 + p) * N + r) * D + col));
+            acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
+          }
+          const int rr = row_first + r, t = row_token(a, rr);
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
+          uint2 u;
+          u.x = *reinterpret_cast<const uint32_t*>(&lo);
+          u.y = *reinterpret_cast<const uint32_t*>(&hi);
+          *reinterpret_cast<uint2*>(
+              a.out + ((static_cast<int64_t>(join_b) * a.G + t) * a.Hq + head * a.R + rr - t * a.R) * D + col) = u;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kBMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+// Joins the items of more than kBJoin parts. CTA (c, 1024 / D rows): the item that goes from range c, where it
+// starts, into the next; a thread per 4 channels of a row.
+template <int D>
+__global__ void __launch_bounds__(256) kv4_join_kernel(const BlockArgs a, int N, int setup, int ctas) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ long long scratch[36];
+  // the item of the first unit after range c
+  const int c = static_cast<int>(blockIdx.x);
+  const BlockRange next = block_range(a, setup, c + 1, ctas, scratch);
+  if (next.b < 0) return;  // (past the end)
+  const int tiles = block_seq(a, next.b).tiles;
+  const int hr = static_cast<int>(next.in_seq / (tiles + setup));
+  const BlockParts parts(next.first - (next.in_seq - static_cast<long long>(hr) * (tiles + setup)), setup, tiles, next.total, ctas);
+  if (parts.c0 != c || parts.c1 - c < kBJoin) return;
+  const int head = hr / a.row_tiles, row_first = (hr % a.row_tiles) * a.tile_rows;
+  const int r = static_cast<int>(blockIdx.y) * (1024 / D) + static_cast<int>(threadIdx.x) / (D / 4);
+  const int col = static_cast<int>(threadIdx.x) % (D / 4) * 4;
+  if (r >= min(a.tile_rows, a.rows - row_first)) return;
+  float mm = -INFINITY;
+#pragma unroll 4
+  for (int p = c; p <= parts.c1; ++p)
+    if (!parts.empty(p)) mm = fmaxf(mm, a.part_ml[parts.slot(p) * N + r].x);
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int p = c; p <= parts.c1; ++p) {
+    if (parts.empty(p)) continue;
+    const float2 ml = a.part_ml[parts.slot(p) * N + r];
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + (parts.slot(p) * N + r) * D + col);
+    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
+    sum += f * ml.y;
+    acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const int rr = row_first + r, t = row_token(a, rr);
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  uint2 u;
+  u.x = *reinterpret_cast<const uint32_t*>(&lo);
+  u.y = *reinterpret_cast<const uint32_t*>(&hi);
+  *reinterpret_cast<uint2*>(
+      a.out + ((static_cast<int64_t>(next.b) * a.G + t) * a.Hq + head * a.R + rr - t * a.R) * D + col) = u;
+}
+
+// Row tiles of equal size, at most 80 rows each (the softmax threads keep a sum and a score of half of
+// them in registers).
+struct BlockPlan {
+  int row_tiles, tile_rows, nk, ctas;
+  bool many;  // an item may have more than kBJoin parts (the longest context next to the shortest ones)
+};
+BlockPlan block_plan(int B, int G, int Hq, int Hkv, int64_t max_ctx, int sms) {
+  BlockPlan p;
+  const int rows = G * (Hq / Hkv);
+  p.row_tiles = (rows + 79) / 80;
+  p.tile_rows = (rows + p.row_tiles - 1) / p.row_tiles;
+  p.nk = p.tile_rows <= 16 ? 1 : (p.tile_rows <= 32 ? 2 : (p.tile_rows <= 64 ? 4 : 5));
+  const int64_t items = static_cast<int64_t>(B) * Hkv * p.row_tiles;
+  const int64_t setup = p.nk <= 2 ? 3 : p.nk, longest = (max_ctx + kBTile - 1) / kBTile + 1 + setup;
+  // CTAs: every SM; but where the ranges would only be cut finer than an item's last range joins (six
+  // parts), for less than the join kernel's cost (about five tiles), fewer
+  p.ctas = static_cast<int>(std::min<int64_t>(sms, items * (longest - setup)));
+  if (6 * items < p.ctas && longest / 6 - items * longest / p.ctas < 5) p.ctas = static_cast<int>(6 * items);
+  const int64_t share = std::max<int64_t>(1, ((items - 1) * (setup + 1) + longest) / p.ctas);
+  p.many = longest / share + 2 > kBJoin;
+  return p;
+}
+
+template <int D, int NK>
+int launch_block_t(const BlockArgs& a, const BlockPlan& p, cudaStream_t st) {
+  using C = BlockCfg<D, NK>;
+  static_assert(C::kSmem <= 232448, "shared memory");
+  static unsigned done = 0;
+  auto kern = kv4_attention_kernel<D, NK>;
+  if (!ensure_smem_attr(kern, C::kSmem, &done)) return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (attention)");
+  cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(p.ctas)), dim3(kBThreads), C::kSmem, st, nullptr, 0, a);
+  if (e == cudaSuccess && p.many && p.ctas > 1)
+    e = launch_pdl(kv4_join_kernel<D>,
+                   dim3(static_cast<unsigned>(p.ctas - 1), static_cast<unsigned>((p.tile_rows * D + 1023) / 1024)),
+                   dim3(256), 0, st, nullptr, 0, a, C::N, C::kSetup, p.ctas);
+  return e == cudaSuccess ? DFLASH2_OK : fail(DFLASH2_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
+}
+
+}  // namespace
+
+size_t kv4_attention_workspace(int B, int G, int Hq, int Hkv, int D, int page_size, int max_pages, int sms) {
+  const BlockPlan p = block_plan(B, G, Hq, Hkv, static_cast<int64_t>(max_pages) * page_size, sms);
+  const size_t slots = static_cast<size_t>(p.ctas) * 2 * (16 * p.nk);
+  return slots * D * sizeof(float) + slots * sizeof(float2) + static_cast<size_t>(p.ctas) * sizeof(unsigned long long);
+}
+
+int launch_kv4_attention(const Kv4Attention& r, cudaStream_t st) {
+  const BlockPlan p = block_plan(r.B, r.G, r.Hq, r.Hkv, static_cast<int64_t>(r.max_pages) * r.page_size, sm_count());
+  BlockArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(r.q);
+  a.q_stride = r.q_stride;
+  a.cache = static_cast<const uint8_t*>(r.cache);
+  a.table = r.table;
+  a.ctx = r.ctx;
+  a.k_new = static_cast<const __nv_bfloat16*>(r.k_new);
+  a.v_new = static_cast<const __nv_bfloat16*>(r.v_new);
+  a.new_stride = r.new_stride;
+  a.B = r.B; a.G = r.G; a.Hq = r.Hq; a.Hkv = r.Hkv;
+  a.R = r.Hq / r.Hkv;
+  a.r_magic = ((1 << 20) + a.R - 1) / a.R;
+  a.rows = r.G * a.R;
+  a.tile_rows = p.tile_rows;
+  a.row_tiles = p.row_tiles;
+  while ((1 << a.page_shift) < r.page_size) ++a.page_shift;
+  a.num_pages = r.num_pages;
+  a.width = r.max_pages;
+  a.cap = r.max_pages * r.page_size;  // (below 2^31: checked)
+  a.causal = r.causal;
+  a.window = r.window;
+  a.scale_log2 = r.scale * 1.4426950408889634f;
+  a.out = static_cast<__nv_bfloat16*>(r.out);
+  const size_t slots = static_cast<size_t>(p.ctas) * 2 * (16 * p.nk);
+  a.part_o = static_cast<float*>(r.workspace);
+  a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * r.D);
+  a.flags = reinterpret_cast<unsigned long long*>(a.part_ml + slots);
+  a.call = next_call_number();
+  a.err = device_error_word();
+  if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
+  if (r.D == 64) {
+    switch (p.nk) {
+      case 1: return launch_block_t<64, 1>(a, p, st);
+      case 2: return launch_block_t<64, 2>(a, p, st);
+      case 4: return launch_block_t<64, 4>(a, p, st);
+      default: return launch_block_t<64, 5>(a, p, st);
+    }
+  }
+  switch (p.nk) {
+    case 1: return launch_block_t<128, 1>(a, p, st);
+    case 2: return launch_block_t<128, 2>(a, p, st);
+    case 4: return launch_block_t<128, 4>(a, p, st);
+    default: return launch_block_t<128, 5>(a, p, st);
+  }
+}
+
+}  // namespace dfl
