@@ -118,6 +118,8 @@ def _check(rc: int):
 
 def _stream(stream):
     if stream is None:
+        if torch.cuda.is_initialized():  # the handle alone: a Stream object costs more than the call's checks
+            return _vp(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
         stream = torch.cuda.current_stream()
     return _vp(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -598,12 +600,12 @@ def dflash2_kv4_read(cache, slots, head_dim, page_size, k=None, v=None, stream=N
     """The values of the cache's slots [T]: (k, v), each [T, heads, head_dim] bf16 (zeros for negative slots)."""
     pages, heads = _kv4_cache_shape(cache, head_dim, page_size)
     T = slots.numel()
-    shape = (T, heads, head_dim)
-    k = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if k is None else k
-    v = torch.empty(shape, dtype=torch.bfloat16, device=cache.device) if v is None else v
-    for t, name in ((k, "k"), (v, "v")):
-        if t.numel() < T * heads * head_dim:
-            raise ValueError(f"{name} holds {t.numel()} elements, fewer than the {T * heads * head_dim} the call writes")
+    n = T * heads * head_dim
+    if k is None and v is None:
+        k, v = torch.empty((2, T, heads, head_dim), dtype=torch.bfloat16, device=cache.device).unbind(0)
+    else:
+        k = _sized(k, n, "k", (T, heads, head_dim), cache.device)
+        v = _sized(v, n, "v", (T, heads, head_dim), cache.device)
     _check(library().dflash2_kv4_read(_dev(cache, "cache", torch.uint8), _dev(slots, "slots", torch.int64), T, heads,
                                       head_dim, page_size, pages, BF16, _dev(k, "k", torch.bfloat16),
                                       _dev(v, "v", torch.bfloat16), _stream(stream)))

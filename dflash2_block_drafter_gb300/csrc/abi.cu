@@ -456,7 +456,7 @@ int dflash2_select_path(const float* S, const int32_t* cand, int B, int steps, i
 
 static int check_kv4(int heads, int D, int page_size, int num_pages, int dtype) {
   if (dtype != DFLASH2_BF16) return fail(DFLASH2_ERR_UNSUPPORTED, "the 4-bit cache takes bf16 rows only (dtype=%d)", dtype);
-  REQUIRE(heads >= 1, "heads=%d must be >= 1", heads);
+  REQUIRE(heads >= 1 && heads <= 512, "heads=%d must be in [1, 512]", heads);
   REQUIRE(D == 64 || D == 128, "head_dim=%d must be 64 or 128", D);
   REQUIRE(page_size >= 16 && page_size <= 4096 && (page_size & (page_size - 1)) == 0,
           "page_size=%d must be a power of two in [16, 4096]", page_size);

@@ -4,6 +4,8 @@
 // Quantisation, per token, head and group of 64 channels (affine, as dflash2.ts quantizedWeight's):
 //   bias = bf16(min x), scale = bf16((max x - min x) / 15), code = clamp(round((x - bias) / scale), 0, 15)
 // in IEEE fp32 with ties to even (scale = 0: code 0).
+#include <algorithm>
+
 #include "internal.h"
 #include "kv4.cuh"
 #include "ptx.cuh"
@@ -17,118 +19,176 @@ struct KvRowsArgs {
   int64_t k_stride, v_stride;  // elements between rows
   const int64_t* slots;
   int T, heads, page_shift, num_pages;
+  int chunks, per_block;       // 16-byte chunks of a token's keys (and of its values); tokens of a CTA
   uint8_t* cache;
   __nv_bfloat16 *k_out, *v_out;
   int* err;
 };
 
-// The granule of a slot, or null (a negative slot: skipped; one past the cache: recorded, skipped).
-template <int D>
-__device__ __forceinline__ uint8_t* kv_slot(const KvRowsArgs& a, int64_t slot, int head, int side, int& token) {
-  if (slot < 0) return nullptr;
-  const int64_t page = slot >> a.page_shift;
-  if (page >= a.num_pages) {
-    atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_BAD_INDEX));
-    return nullptr;
-  }
-  const int in = static_cast<int>(slot & ((1 << a.page_shift) - 1));
-  const int granules = (1 << a.page_shift) / kKvGranule;
-  token = in % kKvGranule;
-  return a.cache + (((page * a.heads + head) * 2 + side) * granules + in / kKvGranule) *
-                       static_cast<int64_t>(KvLayout<D>::kGranuleBytes);
+constexpr int kRowsThreads = 256;
+constexpr int kRowsUnroll = 2;  // tokens of a thread in flight
+
+__device__ __forceinline__ uint32_t bf162_min(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmin2(as_bf162(a), as_bf162(b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+__device__ __forceinline__ uint32_t bf162_max(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2(as_bf162(a), as_bf162(b));
+  return *reinterpret_cast<const uint32_t*>(&m);
 }
 
-// Eight lanes per group of 64 channels: lane i loads channels 8 i .. 8 i + 7 (16 bytes), the group's
-// minimum and maximum come from three shuffles, and each lane stores one word of codes. One pass over
-// the rows, so the bytes bound it. Blocks walk (token, side, head, group) in memory order of the rows.
+// Codes of eight values (pairs of bf16) of a group with minimum b and step s. The division is a product with
+// the reciprocal, rounded by adding 2^23 + 2^22 and made exact afterwards: with d = x - b and n the
+// rounded product, the residual d - n s comes from one FMA, and n moves by one where that is more than
+// half a step (or half a step, and n odd): ties to even, as rounding the quotient gives. The values are
+// bf16, so b is their exact minimum and n ends in [0, 15] (15 steps fall short of the range by less than
+// half a step). The word is summed with the rounding constant still in every n, taken off at the end.
+__device__ __forceinline__ uint32_t kv_quantise8(const uint32_t (&w)[4], float s, float b) {
+  constexpr float kRound = 12582912.f;
+  constexpr uint32_t kBits = 0x4b400000u;
+  uint32_t word = 0;
+  if (s >= 1.17549435e-38f) {
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const uint32_t past_half = __float_as_uint(0.5f * s) + 1u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = __uint_as_float((i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+      const float d = x - b;
+      const float m = fmaf(d, inv, kRound);
+      const float r = fmaf(kRound - m, s, d);
+      uint32_t n = __float_as_uint(m);
+      const uint32_t rb = __float_as_uint(r);
+      if ((rb & 0x7fffffffu) >= past_half - (n & 1u)) n += (static_cast<int>(rb) >> 31) | 1;
+      word += n << (4 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) word -= kBits << (4 * i);
+  } else if (s > 0.f) {  // a subnormal step has no finite reciprocal
+    for (int i = 0; i < 8; ++i) {
+      const float x = __uint_as_float((i & 1) ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+      word |= static_cast<uint32_t>(fminf(fmaxf(rintf((x - b) / s), 0.f), 15.f)) << (4 * i);
+    }
+  }
+  return word;
+}
+
+// Rows into slots (kRead: slots into rows). A thread takes one 16-byte chunk (8 channels) of the keys and the
+// same one of the values of each of its tokens, two tokens in flight (what finds the slot is shared by
+// both); eight lanes share a group of 64, whose minimum and (negated) maximum come from three shuffles of
+// a pair. One pass over the rows; issue bounds the way in, the bytes the way out.
 template <int D, bool kRead>
-__global__ void __launch_bounds__(256) kv4_rows_kernel(const KvRowsArgs a) {
+__global__ void __launch_bounds__(kRowsThreads) kv4_rows_kernel(const KvRowsArgs a) {
+  using L = KvLayout<D>;
   pdl_trigger();
   pdl_wait();
-  using L = KvLayout<D>;
   const int lane8 = threadIdx.x & 7;
-  const int per_side = a.heads * L::kGroups;
-  const int64_t item = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) >> 3;
-  const int64_t items = static_cast<int64_t>(a.T) * 2 * per_side;
-  const bool in_range = item < items;
-  const int64_t it = in_range ? item : 0;
-  const int t = static_cast<int>(it / (2 * per_side));
-  const int rest = static_cast<int>(it - static_cast<int64_t>(t) * 2 * per_side);
-  const int side = rest / per_side;
-  const int head = (rest - side * per_side) / L::kGroups;
-  const int grp = rest % L::kGroups;
-  const int col = head * D + grp * kKvGroup + lane8 * 8;
-  int token = 0;
-  uint8_t* gran = in_range ? kv_slot<D>(a, a.slots[t], head, side, token) : nullptr;
-  const int code_at = token * L::kRow + grp * (kKvGroup / 2) + lane8 * 4;
-  const int par_at = L::kCodes + (token * L::kGroups + grp) * 4;
-  if (kRead) {
-    if (!in_range) return;
-    uint4 o = make_uint4(0u, 0u, 0u, 0u);
-    if (gran != nullptr) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(gran + code_at);
-      const uint32_t par = *reinterpret_cast<const uint32_t*>(gran + par_at);
-      const __nv_bfloat162 sb = as_bf162(par);
-      const __nv_bfloat162 s2 = __low2bfloat162(sb), b2 = __high2bfloat162(sb);
-      uint32_t p[4];  // channels (i, i + 4)
+  const uint32_t group = 0xffu << (threadIdx.x & 24);  // the group's eight lanes, which stay together
+  // fewer chunks than threads: several tokens side by side
+  const int rows = max(1, kRowsThreads / a.chunks), row = static_cast<int>(threadIdx.x) / a.chunks;
+  const int granules = (1 << a.page_shift) / kKvGranule;
+  const int page_bytes = a.heads * 2 * granules * L::kGranuleBytes;  // (heads, page size: below 2^31)
+  const int to_values = granules * L::kGranuleBytes;
+  const int64_t end = static_cast<int64_t>(a.num_pages) << a.page_shift;
+  const int t_end = min(a.T, static_cast<int>(blockIdx.x + 1) * a.per_block);
+  for (int x = a.chunks <= kRowsThreads ? threadIdx.x - row * a.chunks : threadIdx.x; x < a.chunks && row < rows;
+       x += kRowsThreads) {
+    const int col = x * 8, grp = col / kKvGroup % L::kGroups;
+    uint8_t* base = a.cache + col / D * 2 * to_values;
+    const int code_at = grp * (kKvGroup / 2) + lane8 * 4, par_at = L::kCodes + grp * 4;
+    for (int t0 = static_cast<int>(blockIdx.x) * a.per_block + row; t0 < t_end; t0 += kRowsUnroll * rows) {
+      uint8_t* g[kRowsUnroll];  // the keys' granule of the slot; null: not there
+      int tok[kRowsUnroll];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = kv_value(w >> (4 * i), s2, b2);
-      o.x = __byte_perm(p[0], p[1], 0x5410);
-      o.y = __byte_perm(p[2], p[3], 0x5410);
-      o.z = __byte_perm(p[0], p[1], 0x7632);
-      o.w = __byte_perm(p[2], p[3], 0x7632);
+      for (int u = 0; u < kRowsUnroll; ++u) {
+        const int t = t0 + u * rows;
+        int64_t slot = t < t_end ? __ldg(a.slots + t) : -1;
+        if (slot >= end) {  // past the cache: recorded, skipped
+          atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_BAD_INDEX));
+          slot = -1;
+        }
+        const int in = static_cast<int>(slot) & ((1 << a.page_shift) - 1);
+        tok[u] = in % kKvGranule;
+        g[u] = slot < 0 ? nullptr
+                        : base + (static_cast<int64_t>(static_cast<int>(slot >> a.page_shift)) * page_bytes +
+                                  in / kKvGranule * L::kGranuleBytes);
+      }
+      if (kRead) {
+        uint32_t code[kRowsUnroll][2], par[kRowsUnroll][2];
+#pragma unroll
+        for (int u = 0; u < kRowsUnroll; ++u) {
+          code[u][0] = code[u][1] = par[u][0] = par[u][1] = 0u;
+          if (g[u] == nullptr) continue;
+          const uint8_t *c = g[u] + code_at + tok[u] * L::kRow, *p = g[u] + par_at + tok[u] * L::kGroups * 4;
+          code[u][0] = *reinterpret_cast<const uint32_t*>(c);
+          code[u][1] = *reinterpret_cast<const uint32_t*>(c + to_values);
+          par[u][0] = *reinterpret_cast<const uint32_t*>(p);
+          par[u][1] = *reinterpret_cast<const uint32_t*>(p + to_values);
+        }
+#pragma unroll
+        for (int u = 0; u < kRowsUnroll; ++u) {
+          const int t = t0 + u * rows;
+          if (t >= t_end) continue;
+          const int64_t at = static_cast<int64_t>(t) * (a.heads * D) + col;
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            const __nv_bfloat162 sb = as_bf162(par[u][side]);
+            const __nv_bfloat162 s2 = __low2bfloat162(sb), b2 = __high2bfloat162(sb);
+            uint32_t p[4];  // channels (i, i + 4); zeros for a slot that is not there
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[i] = kv_value(code[u][side] >> (4 * i), s2, b2);
+            *reinterpret_cast<uint4*>((side == 0 ? a.k_out : a.v_out) + at) =
+                make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410),
+                           __byte_perm(p[0], p[1], 0x7632), __byte_perm(p[2], p[3], 0x7632));
+          }
+        }
+      } else {
+        uint4 raw[kRowsUnroll][2];
+#pragma unroll
+        for (int u = 0; u < kRowsUnroll; ++u) {
+          raw[u][0] = raw[u][1] = make_uint4(0u, 0u, 0u, 0u);
+          if (g[u] == nullptr) continue;
+          raw[u][0] = __ldg(reinterpret_cast<const uint4*>(a.k + (t0 + u * rows) * a.k_stride + col));
+          raw[u][1] = __ldg(reinterpret_cast<const uint4*>(a.v + (t0 + u * rows) * a.v_stride + col));
+        }
+#pragma unroll
+        for (int u = 0; u < kRowsUnroll; ++u) {
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            const uint4 v = raw[u][side];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            const uint32_t lo2 = bf162_min(bf162_min(w[0], w[1]), bf162_min(w[2], w[3]));
+            const uint32_t hi2 = bf162_max(bf162_max(w[0], w[1]), bf162_max(w[2], w[3])) ^ 0x80008000u;
+            uint32_t m = bf162_min(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));  // (minimum, - maximum)
+#pragma unroll
+            for (int i = 1; i < 8; i <<= 1) m = bf162_min(m, __shfl_xor_sync(group, m, i));
+            if (g[u] == nullptr) continue;
+            const float lo = __uint_as_float(m << 16), hi = -__uint_as_float(m & 0xffff0000u);
+            // (hi - lo) / 15 correctly rounded: a product and one correction by its residual
+            const float range = hi - lo, q0 = range * (1.f / 15.f);
+            const float q = fmaf(fmaf(-15.f, q0, range), 1.f / 15.f, q0);
+            const __nv_bfloat16 scale = __float2bfloat16_rn(q);
+            uint8_t* to = g[u] + (side == 0 ? 0 : to_values);
+            *reinterpret_cast<uint32_t*>(to + code_at + tok[u] * L::kRow) = kv_quantise8(w, __bfloat162float(scale), lo);
+            if (lane8 == 0)
+              *reinterpret_cast<uint32_t*>(to + par_at + tok[u] * L::kGroups * 4) =
+                  (m << 16) | static_cast<uint32_t>(__bfloat16_as_ushort(scale));
+          }
+        }
+      }
     }
-    __nv_bfloat16* out = side == 0 ? a.k_out : a.v_out;
-    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(t) * a.heads * D + col) = o;
-    return;
-  }
-  float x[8] = {};
-  if (gran != nullptr) {
-    const __nv_bfloat16* src = side == 0 ? a.k + t * a.k_stride : a.v + t * a.v_stride;
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(src + col));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(as_bf162(w[i]));
-      x[2 * i] = f.x;
-      x[2 * i + 1] = f.y;
-    }
-  }
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-  }
-#pragma unroll
-  for (int m = 1; m < 8; m <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
-  }
-  if (gran == nullptr) return;
-  const __nv_bfloat16 scale = __float2bfloat16_rn((hi - lo) / 15.f);
-  const __nv_bfloat16 bias = __float2bfloat16_rn(lo);
-  const float s = __bfloat162float(scale), b = __bfloat162float(bias);
-  uint32_t word = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float c = s > 0.f ? fminf(fmaxf(rintf((x[i] - b) / s), 0.f), 15.f) : 0.f;
-    word |= static_cast<uint32_t>(c) << (4 * i);
-  }
-  *reinterpret_cast<uint32_t*>(gran + code_at) = word;
-  if (lane8 == 0) {
-    const __nv_bfloat162 sb = __halves2bfloat162(scale, bias);
-    *reinterpret_cast<__nv_bfloat162*>(gran + par_at) = sb;
   }
 }
 
 template <int D>
-int launch_rows(const KvRowsArgs& a, bool read, cudaStream_t st) {
-  const int64_t threads = static_cast<int64_t>(a.T) * 2 * a.heads * KvLayout<D>::kGroups * 8;
-  const int64_t blocks = (threads + 255) / 256;
-  if (blocks > 0x7fffffffLL) return fail(DFLASH2_ERR_INVALID_ARG, "T=%d rows are too many for one call", a.T);
+int launch_rows(KvRowsArgs a, bool read, cudaStream_t st) {
+  a.chunks = a.heads * (D / 8);
+  // tokens of a CTA: two to a thread, unless that leaves SMs without a CTA
+  const int most = kRowsUnroll * std::max(1, kRowsThreads / a.chunks);
+  a.per_block = std::max(1, std::min(most, a.T / (2 * sm_count())));
   const cudaError_t e = launch_pdl(read ? kv4_rows_kernel<D, true> : kv4_rows_kernel<D, false>,
-                                   dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, nullptr, 0, a);
+                                   dim3(static_cast<unsigned>((a.T + a.per_block - 1) / a.per_block)), dim3(kRowsThreads),
+                                   0, st, nullptr, 0, a);
   return e == cudaSuccess ? DFLASH2_OK : fail(DFLASH2_ERR_CUDA, "cache row launch failed: %s", cudaGetErrorString(e));
 }
 

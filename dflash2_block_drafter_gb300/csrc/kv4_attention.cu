@@ -58,6 +58,7 @@ constexpr int kBThreads = 640;
 constexpr int kBSoftRegs = 120, kBOtherRegs = 80;  // 256 x 120 + 384 x 80 = 640 x 96
 constexpr int kBJoin = 8;                  // parts that an item's last range joins itself
 constexpr float kBSlack = 8.f;              // scores may pass the reference by 2^8
+constexpr float kBSlackV = 16.f;            // and the values' power of two its reference by 2^4 (fp16 holds 2^15)
 constexpr float kBUnseen = 3e38f;           // minus the reference of a row that has seen no key: any score passes it
 constexpr float kBPadding = -1e30f;         // of a row that does not exist: no score passes it, and it counts nothing
 
@@ -202,55 +203,50 @@ struct BlockRange {
   int b;                          // the sequence of its first unit, and that unit's place among the sequence's
   long long in_seq;
 };
-// Block-wide (every thread calls it): sums the sequences' tiles and finds the range of CTA `c` of `n`.
-__device__ __forceinline__ BlockRange block_range(const BlockArgs& a, int setup, int c, int n, long long* scratch) {
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = (nt + 31) / 32;
-  const int hr = a.Hkv * a.row_tiles;
-  BlockRange r;
-  long long sum = 0;
-  for (int b = tid; b < a.B; b += nt) {
-    const int n = __ldg(a.ctx + b);
-    if (n < 0 || n > a.cap) atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_INVALID_ARG));
-    sum += block_seq(a, b).tiles + setup;
-  }
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-  if (lane == 0) scratch[warp] = sum;
-  __syncthreads();
-  sum = 0;
-  for (int w = 0; w < warps; ++w) sum += scratch[w];
-  r.total = sum * hr;
-  r.first = r.total * c / n;
-  r.count = r.total * (c + 1) / n - r.first;
-  __syncthreads();
-  long long before = 0;  // tiles of the sequences before this chunk of `nt`
-  if (tid == 0) scratch[34] = -1;
-  for (int b0 = 0; b0 < a.B; b0 += nt) {
-    const int b = b0 + tid;
-    const long long mine = b < a.B ? static_cast<long long>(block_seq(a, b).tiles + setup) * hr : 0;
-    long long inc = mine;
+// A warp's work (all lanes call it): sums the sequences' units and finds range `c` of `n`. A lane sums a run of
+// sequences; the run that holds the range's start is then walked 32 sequences at a time.
+__device__ __forceinline__ BlockRange block_range(const BlockArgs& a, int setup, int c, int n) {
+  const int lane = threadIdx.x & 31, hr = a.Hkv * a.row_tiles;
+  const int per = (a.B + 31) / 32;
+  auto prefix = [&](long long x) {  // over the lanes, this one's included
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, m);
-      if (lane >= m) inc += v;
+      const long long v = __shfl_up_sync(0xffffffffu, x, m);
+      if (lane >= m) x += v;
     }
-    if (lane == 31) scratch[warp] = inc;
-    __syncthreads();
-    long long off = before, chunk = 0;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) off += scratch[w];
-      chunk += scratch[w];
-    }
-    if (mine > 0 && r.first >= off + inc - mine && r.first < off + inc) {
-      scratch[34] = b;
-      scratch[35] = r.first - (off + inc - mine);
-    }
-    before += chunk;
-    __syncthreads();
-    if (scratch[34] >= 0) break;
+    return x;
+  };
+  long long mine = 0;
+  for (int b = lane * per; b < min(a.B, (lane + 1) * per); ++b) {
+    const int len = __ldg(a.ctx + b);
+    if (len < 0 || len > a.cap) atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_INVALID_ARG));
+    mine += block_seq(a, b).tiles + setup;
   }
-  r.b = static_cast<int>(scratch[34]);
-  r.in_seq = scratch[35];
+  mine *= hr;
+  long long inc = prefix(mine);
+  BlockRange r;
+  r.total = __shfl_sync(0xffffffffu, inc, 31);
+  r.first = r.total * c / n;
+  r.count = r.total * (c + 1) / n - r.first;
+  r.b = -1;
+  r.in_seq = 0;
+  uint32_t hit = __ballot_sync(0xffffffffu, r.first >= inc - mine && r.first < inc);
+  if (hit == 0u) return r;  // (an empty range at the end)
+  const int run = __ffs(hit) - 1;
+  long long before = __shfl_sync(0xffffffffu, inc - mine, run);
+  for (int b0 = run * per; b0 < min(a.B, (run + 1) * per); b0 += 32) {
+    const int b = b0 + lane;
+    mine = b < min(a.B, (run + 1) * per) ? static_cast<long long>(block_seq(a, b).tiles + setup) * hr : 0;
+    inc = before + prefix(mine);
+    hit = __ballot_sync(0xffffffffu, r.first >= inc - mine && r.first < inc);
+    if (hit != 0u) {
+      const int at = __ffs(hit) - 1;
+      r.b = b0 + at;
+      r.in_seq = r.first - __shfl_sync(0xffffffffu, inc - mine, at);
+      return r;
+    }
+    before = __shfl_sync(0xffffffffu, inc, 31);
+  }
   return r;
 }
 
@@ -453,7 +449,6 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
   uint32_t* vkey = tmem_slot + 3;
   uint32_t* qmax = tmem_slot + 4;
   uint32_t* came_s = tmem_slot + 5;  // [side][3]: the granules that came
-  __shared__ long long scratch[36];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -485,7 +480,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
   const uint32_t tmem = *tmem_slot;
   pdl_trigger();
   pdl_wait();
-  const BlockRange range = block_range(a, C::kSetup, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), scratch);
+  const BlockRange range = block_range(a, C::kSetup, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
 
   if (warp >= kBSoftWarps && warp < kBSoftWarps + kBDeqWarps) {
     // ------------------------------------------------------------------ dequant
@@ -849,7 +844,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
 #pragma unroll
           for (int r = 0; r < NH; ++r) top[r & 3] = fmaxf(top[r & 3], x[r]);
           top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          if (!bar_or(top[0] > kBSlack || (there && !(inf.y * vinv <= 1.f && vinv > 0.f)))) break;
+          if (!bar_or(top[0] > kBSlack || (there && !(inf.y * vinv <= kBSlackV && vinv > 0.f)))) break;
           // ---- raise the references: the rows' maxima over the tile, the values' largest power of two
           __syncwarp();
           load_s(it);
@@ -1084,10 +1079,9 @@ template <int D>
 __global__ void __launch_bounds__(256) kv4_join_kernel(const BlockArgs a, int N, int setup, int ctas) {
   pdl_trigger();
   pdl_wait();
-  __shared__ long long scratch[36];
   // the item of the first unit after range c
   const int c = static_cast<int>(blockIdx.x);
-  const BlockRange next = block_range(a, setup, c + 1, ctas, scratch);
+  const BlockRange next = block_range(a, setup, c + 1, ctas);
   if (next.b < 0) return;  // (past the end)
   const int tiles = block_seq(a, next.b).tiles;
   const int hr = static_cast<int>(next.in_seq / (tiles + setup));
@@ -1127,7 +1121,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const BlockArgs a, int N,
 // them in registers).
 struct BlockPlan {
   int row_tiles, tile_rows, nk, ctas;
-  bool many;  // an item may have more than kBJoin parts (the longest context next to the shortest ones)
+  bool many;  // an item may have more than kBJoin parts
 };
 BlockPlan block_plan(int B, int G, int Hq, int Hkv, int64_t max_ctx, int sms) {
   BlockPlan p;
@@ -1141,8 +1135,9 @@ BlockPlan block_plan(int B, int G, int Hq, int Hkv, int64_t max_ctx, int sms) {
   // parts), for less than the join kernel's cost (about five tiles), fewer
   p.ctas = static_cast<int>(std::min<int64_t>(sms, items * (longest - setup)));
   if (6 * items < p.ctas && longest / 6 - items * longest / p.ctas < 5) p.ctas = static_cast<int>(6 * items);
-  const int64_t share = std::max<int64_t>(1, ((items - 1) * (setup + 1) + longest) / p.ctas);
-  p.many = longest / share + 2 > kBJoin;
+  // most parts of an item: the longest sequence's, when all others are empty
+  const int64_t total = items / B * longest + (items - items / B) * (setup + 1);
+  p.many = longest * p.ctas / total + 2 > kBJoin;
   return p;
 }
 
