@@ -695,6 +695,7 @@ def dflash2_gated_ffn(x, w_gate, w_up, act="silu", out=None, pre=None, want_pre=
     if x.dim() != 2:
         raise ValueError(f"x must be [M, H], got shape {tuple(x.shape)}")
     M, H = x.shape
+    code = _act(act)
     F = _ffn_weights(w_gate, w_up, H)
     out = _sized(out, M * F, "out", (M, F), x.device)
     if want_pre and pre is None:
@@ -704,7 +705,7 @@ def dflash2_gated_ffn(x, w_gate, w_up, act="silu", out=None, pre=None, want_pre=
     wp, wn, _keep = _ffn_ws(M, H, F, 0, x.device, workspace)
     bf = torch.bfloat16
     _check(library().dflash2_gated_ffn(_dev(x, "x", bf), M, H, _dev(w_gate, "w_gate", bf), _dev(w_up, "w_up", bf), F,
-                                       _act(act), BF16, _dev(out, "out", bf), _dev(pre, "pre", None, True), wp, wn,
+                                       code, BF16, _dev(out, "out", bf), _dev(pre, "pre", None, True), wp, wn,
                                        _stream(stream)))
     return (out, pre) if want_pre else out
 
@@ -713,7 +714,10 @@ def dflash2_gated_ffn_backward(dh, pre, x, w_gate, w_up, act="silu", want_dx=Tru
                                dw_up=None, workspace=None, stream=None):
     """Gradients of dflash2_gated_ffn from dh [M, F] and the pre that call kept: (dx [M, H], dw_gate,
     dw_up [F, H]); None for what is not wanted."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M, H], got shape {tuple(x.shape)}")
     M, H = x.shape
+    code = _act(act)
     F = _ffn_weights(w_gate, w_up, H)
     if tuple(dh.shape) != (M, F) or pre.numel() * pre.element_size() < 4 * M * F:
         raise ValueError(f"dh must be [{M}, {F}] and pre hold {4 * M * F} bytes, got {tuple(dh.shape)} and "
@@ -727,6 +731,6 @@ def dflash2_gated_ffn_backward(dh, pre, x, w_gate, w_up, act="silu", want_dx=Tru
     bf = torch.bfloat16
     _check(library().dflash2_gated_ffn_backward(
         _dev(dh, "dh", bf), _dev(pre, "pre"), _dev(x, "x", bf), _dev(w_gate, "w_gate", bf), _dev(w_up, "w_up", bf),
-        M, H, F, _act(act), BF16, _dev(dx, "dx", bf, True), _dev(dw_gate, "dw_gate", bf, True),
+        M, H, F, code, BF16, _dev(dx, "dx", bf, True), _dev(dw_gate, "dw_gate", bf, True),
         _dev(dw_up, "dw_up", bf, True), wp, wn, _stream(stream)))
     return dx, dw_gate, dw_up

@@ -266,19 +266,24 @@ class TailRunner:
 
     def capture(self, fn, *args, **kwargs) -> "torch.cuda.CUDAGraph":
         """Record one pass of ``fn`` (e.g. ``self.full``) into a CUDA graph over the runner's fixed
-        buffers; ``graph.replay()`` then re-launches every kernel of the pass with one call.
+        buffers; ``graph.replay()`` then re-launches every kernel of the pass with one call."""
+        return capture(fn, *args, **kwargs)
 
-        The pass runs once eagerly first, so that every kernel's attributes are set outside the
-        capture. Inputs are read from the tensors passed here at replay time: refresh them in place.
-        """
-        fn(*args, **kwargs)
-        torch.cuda.synchronize()
-        graph = torch.cuda.CUDAGraph()
-        side = torch.cuda.Stream()
-        side.wait_stream(torch.cuda.current_stream())
-        with torch.cuda.stream(side):
-            with torch.cuda.graph(graph, stream=side):
-                fn(*args, **kwargs)
-        torch.cuda.current_stream().wait_stream(side)
-        torch.cuda.synchronize()
-        return graph
+
+def capture(fn, *args, **kwargs) -> "torch.cuda.CUDAGraph":
+    """Record one call of ``fn`` into a CUDA graph.
+
+    The call runs once eagerly first, so that every kernel's attributes are set outside the
+    capture. Inputs are read from the tensors passed here at replay time: refresh them in place.
+    """
+    fn(*args, **kwargs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            fn(*args, **kwargs)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    return graph
