@@ -197,15 +197,35 @@ __device__ __forceinline__ BlockSeq block_seq(const BlockArgs& a, int b) {
   return s;
 }
 
-// A CTA's range of the line of all tiles: where it starts and how many tiles it has.
+// The line of all units (a tile, or a part of an item's setup), cut into n ranges that differ by one unit at
+// most and of which none is empty: range c starts at floor(c total / n). (Kept as quotient and rest: 64-bit
+// divisions are some hundred instructions each.)
+struct BlockLine {
+  long long total, q;
+  int rem, n;
+  __device__ __forceinline__ void set(long long total_, int ctas) {
+    total = total_;
+    n = total < ctas ? static_cast<int>(total) : ctas;
+    q = total / n;
+    rem = static_cast<int>(total - q * n);
+  }
+  __device__ __forceinline__ long long start(int c) const { return q * c + rem * c / n; }
+  // the range that holds unit g: the smallest c with start(c + 1) > g
+  __device__ __forceinline__ int range_of(long long g) const {
+    return static_cast<int>(((g + 1) * n + total - 1) / total) - 1;
+  }
+};
+
+// A CTA's range of the line.
 struct BlockRange {
-  long long total, first, count;  // in units: a tile, or a part of an item's setup
+  BlockLine line;
+  long long first, count;         // in units
   int b;                          // the sequence of its first unit, and that unit's place among the sequence's
   long long in_seq;
 };
-// A warp's work (all lanes call it): sums the sequences' units and finds range `c` of `n`. A lane sums a run of
+// A warp's work (all lanes call it): sums the sequences' units and finds range `c` of `ctas`. A lane sums a run of
 // sequences; the run that holds the range's start is then walked 32 sequences at a time.
-__device__ __forceinline__ BlockRange block_range(const BlockArgs& a, int setup, int c, int n) {
+__device__ __forceinline__ BlockRange block_range(const BlockArgs& a, int setup, int c, int ctas) {
   const int lane = threadIdx.x & 31, hr = a.Hkv * a.row_tiles;
   const int per = (a.B + 31) / 32;
   auto prefix = [&](long long x) {  // over the lanes, this one's included
@@ -225,13 +245,13 @@ __device__ __forceinline__ BlockRange block_range(const BlockArgs& a, int setup,
   mine *= hr;
   long long inc = prefix(mine);
   BlockRange r;
-  r.total = __shfl_sync(0xffffffffu, inc, 31);
-  r.first = r.total * c / n;
-  r.count = r.total * (c + 1) / n - r.first;
+  r.line.set(__shfl_sync(0xffffffffu, inc, 31), ctas);
+  r.first = r.line.start(c);
+  r.count = c < r.line.n ? r.line.start(c + 1) - r.first : 0;
   r.b = -1;
   r.in_seq = 0;
   uint32_t hit = __ballot_sync(0xffffffffu, r.first >= inc - mine && r.first < inc);
-  if (hit == 0u) return r;  // (an empty range at the end)
+  if (hit == 0u) return r;  // (more CTAs than units)
   const int run = __ffs(hit) - 1;
   long long before = __shfl_sync(0xffffffffu, inc - mine, run);
   for (int b0 = run * per; b0 < min(a.B, (run + 1) * per); b0 += 32) {
@@ -248,11 +268,6 @@ __device__ __forceinline__ BlockRange block_range(const BlockArgs& a, int setup,
     before = __shfl_sync(0xffffffffu, inc, 31);
   }
   return r;
-}
-
-// The range that holds unit g: the smallest c with floor((c + 1) total / n) > g.
-__device__ __forceinline__ int range_of(long long g, long long total, int n) {
-  return static_cast<int>(((g + 1) * n + total - 1) / total) - 1;
 }
 
 // Walks a range piece by piece: piece = consecutive tiles [j0, j1) of one item (sequence b, head and row tile
@@ -300,14 +315,8 @@ struct BlockWalk {
 // The ranges [c0, c1] that hold the tiles of the item that starts at unit `start`.
 struct BlockParts {
   int c0, c1;
-  long long total;
-  int n;
-  __device__ __forceinline__ BlockParts(long long start, int setup, int tiles, long long total_, int n_) : total(total_), n(n_) {
-    c0 = range_of(start + setup, total, n);
-    c1 = range_of(start + setup + tiles - 1, total, n);
-  }
-  // (with fewer units than CTAs some ranges between are empty)
-  __device__ __forceinline__ bool empty(int c) const { return total * (c + 1) / n == total * c / n; }
+  __device__ __forceinline__ BlockParts(const BlockLine& line, long long start, int setup, int tiles)
+      : c0(line.range_of(start + setup)), c1(line.range_of(start + setup + tiles - 1)) {}
   // where the part of range c lies: the first part is a range's last piece, the others a range's first
   __device__ __forceinline__ int64_t slot(int c) const { return c * 2LL + (c == c0 ? 1 : 0); }
 };
@@ -947,7 +956,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
       }
       const bool complete = w.j0 == 0 && w.j1 == w.seq.tiles;
       if (w.j1 < w.seq.tiles) {  // the last piece goes on in the next range: does that range join it?
-        const BlockParts parts(w.start, C::kSetup, w.seq.tiles, range.total, static_cast<int>(gridDim.x));
+        const BlockParts parts(range.line, w.start, C::kSetup, w.seq.tiles);
         gave = parts.c1 - parts.c0 < kBJoin;
       }
       Walk next = w;
@@ -1004,10 +1013,10 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
       if (threadIdx.x == 0) st_release_u64(a.flags + blockIdx.x, a.call);
     }
     if (joins) {
-      const BlockParts parts(join_start, C::kSetup, join_tiles, range.total, static_cast<int>(gridDim.x));
+      const BlockParts parts(range.line, join_start, C::kSetup, join_tiles);
       const int c0 = parts.c0, me = parts.c1;
       if (me - c0 < kBJoin) {
-        if (threadIdx.x < me - c0 && !parts.empty(c0 + threadIdx.x)) {
+        if (threadIdx.x < me - c0) {
           unsigned long long* flag = a.flags + c0 + threadIdx.x;
           const uint64_t t0 = globaltimer_ns();
           while (ld_acquire_u64(flag) != a.call) {
@@ -1030,7 +1039,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
           float mm = -INFINITY, sum = 0.f;
 #pragma unroll
           for (int p = 0; p < kBJoin; ++p) {
-            const bool in = c0 + p <= me && !parts.empty(c0 + p);
+            const bool in = c0 + p <= me;
             ml[p] = in ? __ldcg(a.part_ml + parts.slot(c0 + p) * N + threadIdx.x) : make_float2(-INFINITY, 0.f);
             mm = fmaxf(mm, ml[p].x);
           }
@@ -1085,7 +1094,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const BlockArgs a, int N,
   if (next.b < 0) return;  // (past the end)
   const int tiles = block_seq(a, next.b).tiles;
   const int hr = static_cast<int>(next.in_seq / (tiles + setup));
-  const BlockParts parts(next.first - (next.in_seq - static_cast<long long>(hr) * (tiles + setup)), setup, tiles, next.total, ctas);
+  const BlockParts parts(next.line, next.first - (next.in_seq - static_cast<long long>(hr) * (tiles + setup)), setup, tiles);
   if (parts.c0 != c || parts.c1 - c < kBJoin) return;
   const int head = hr / a.row_tiles, row_first = (hr % a.row_tiles) * a.tile_rows;
   const int r = static_cast<int>(blockIdx.y) * (1024 / D) + static_cast<int>(threadIdx.x) / (D / 4);
@@ -1094,12 +1103,11 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(const BlockArgs a, int N,
   float mm = -INFINITY;
 #pragma unroll 4
   for (int p = c; p <= parts.c1; ++p)
-    if (!parts.empty(p)) mm = fmaxf(mm, a.part_ml[parts.slot(p) * N + r].x);
+    mm = fmaxf(mm, a.part_ml[parts.slot(p) * N + r].x);
   float sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int p = c; p <= parts.c1; ++p) {
-    if (parts.empty(p)) continue;
     const float2 ml = a.part_ml[parts.slot(p) * N + r];
     const float4 v = *reinterpret_cast<const float4*>(a.part_o + (parts.slot(p) * N + r) * D + col);
     const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
