@@ -56,7 +56,6 @@ constexpr int kBSoftWarps = 8, kBDeqWarps = 8, kBMmaWarp = 16, kBCopyWarp = 18; 
 constexpr int kBSoft = 32 * kBSoftWarps;    // softmax threads
 constexpr int kBThreads = 640;
 constexpr int kBSoftRegs = 120, kBOtherRegs = 80;  // 256 x 120 + 384 x 80 = 640 x 96
-constexpr int kBJoin = 8;                  // parts that an item's last range joins itself
 constexpr float kBSlack = 8.f;              // scores may pass the reference by 2^8
 constexpr float kBSlackV = 16.f;            // and the values' power of two its reference by 2^4 (fp16 holds 2^15)
 constexpr float kBUnseen = 3e38f;           // minus the reference of a row that has seen no key: any score passes it
@@ -99,7 +98,7 @@ struct BlockArgs {
   float* part_o;    // [CTA][2][N][D]
   float2* part_ml;  // [CTA][2][N]
   unsigned long long* flags;  // [CTA]
-  unsigned long long call;
+  unsigned long long call, ctas_inverse;  // (the latter floor((2^64 - 1) / CTAs))
   int* err;
 };
 
@@ -197,22 +196,37 @@ __device__ __forceinline__ BlockSeq block_seq(const BlockArgs& a, int b) {
   return s;
 }
 
+// floor(x / d) for a quotient below 2^22: the float estimate is off by one at most. (A 64-bit division is some
+// hundred instructions.)
+__device__ __forceinline__ int small_quotient(long long x, long long d) {
+  int q = static_cast<int>(static_cast<float>(x) / static_cast<float>(d));
+  if (q * d > x) --q;
+  if ((q + 1) * d <= x) ++q;
+  return q;
+}
+
 // The line of all units (a tile, or a part of an item's setup), cut into n ranges that differ by one unit at
-// most and of which none is empty: range c starts at floor(c total / n). (Kept as quotient and rest: 64-bit
-// divisions are some hundred instructions each.)
+// most and of which none is empty: range c starts at floor(c total / n).
 struct BlockLine {
-  long long total, q;
+  long long total, q;  // q, rem: total over n
   int rem, n;
-  __device__ __forceinline__ void set(long long total_, int ctas) {
+  __device__ __forceinline__ void set(long long total_, int ctas, unsigned long long ctas_inverse) {
     total = total_;
     n = total < ctas ? static_cast<int>(total) : ctas;
-    q = total / n;
+    q = n < ctas ? 1 : static_cast<long long>(__umul64hi(total, ctas_inverse));  // (one too small at most)
+    if (total - q * n >= n) ++q;
     rem = static_cast<int>(total - q * n);
   }
   __device__ __forceinline__ long long start(int c) const { return q * c + rem * c / n; }
-  // the range that holds unit g: the smallest c with start(c + 1) > g
+  // the range that holds unit g: the one c with start(c) <= g < start(c + 1)
   __device__ __forceinline__ int range_of(long long g) const {
-    return static_cast<int>(((g + 1) * n + total - 1) / total) - 1;
+    int c = small_quotient(g, q);  // at least the range: no range is shorter than q
+    c = min(c, n - 1);
+    if (rem > 0) {
+      c = min(c, static_cast<int>(static_cast<float>(g) * static_cast<float>(n) / static_cast<float>(total)) + 1);
+      while (start(c) > g) --c;
+    }
+    return c;
   }
 };
 
@@ -245,7 +259,7 @@ __device__ __forceinline__ BlockRange block_range(const BlockArgs& a, int setup,
   mine *= hr;
   long long inc = prefix(mine);
   BlockRange r;
-  r.line.set(__shfl_sync(0xffffffffu, inc, 31), ctas);
+  r.line.set(__shfl_sync(0xffffffffu, inc, 31), ctas, a.ctas_inverse);
   r.first = r.line.start(c);
   r.count = c < r.line.n ? r.line.start(c + 1) - r.first : 0;
   r.b = -1;
@@ -254,6 +268,11 @@ __device__ __forceinline__ BlockRange block_range(const BlockArgs& a, int setup,
   if (hit == 0u) return r;  // (more CTAs than units)
   const int run = __ffs(hit) - 1;
   long long before = __shfl_sync(0xffffffffu, inc - mine, run);
+  if (per == 1) {
+    r.b = run;
+    r.in_seq = r.first - before;
+    return r;
+  }
   for (int b0 = run * per; b0 < min(a.B, (run + 1) * per); b0 += 32) {
     const int b = b0 + lane;
     mine = b < min(a.B, (run + 1) * per) ? static_cast<long long>(block_seq(a, b).tiles + setup) * hr : 0;
@@ -285,7 +304,7 @@ struct BlockWalk {
     j1 = -1;
     if (left <= 0) return;
     seq = block_seq(a, b);
-    hr = static_cast<int>(r.in_seq / (seq.tiles + kSetup));
+    hr = small_quotient(r.in_seq, seq.tiles + kSetup);
     const int u = static_cast<int>(r.in_seq - static_cast<long long>(hr) * (seq.tiles + kSetup));
     start = r.first - u;
     enter(u);
@@ -315,10 +334,23 @@ struct BlockWalk {
 // The ranges [c0, c1] that hold the tiles of the item that starts at unit `start`.
 struct BlockParts {
   int c0, c1;
+  int group;  // parts that are joined first: the smallest number whose square is at least all
   __device__ __forceinline__ BlockParts(const BlockLine& line, long long start, int setup, int tiles)
-      : c0(line.range_of(start + setup)), c1(line.range_of(start + setup + tiles - 1)) {}
+      : c0(line.range_of(start + setup)), c1(line.range_of(start + setup + tiles - 1)), group(1) {
+    while (group * group < c1 - c0 + 1) ++group;
+  }
+  // range c ends a group of parts, and not the item
+  __device__ __forceinline__ bool leads(int c) const { return c < c1 && group > 1 && (c - c0) % group == group - 1; }
+  // what range c joins, c itself the last: if it leads, its group; if it ends the item, the groups before
+  // its own and then its own group's parts
+  __device__ __forceinline__ int inputs(int c) const { return c < c1 ? group : (c - c0) / group + (c - c0) % group + 1; }
+  __device__ __forceinline__ int input(int c, int p) const {
+    if (c < c1) return c - (group - 1) + p;
+    const int groups = (c - c0) / group;
+    return p < groups ? c0 + (p + 1) * group - 1 : c0 + groups * group + (p - groups);
+  }
   // where the part of range c lies: the first part is a range's last piece, the others a range's first
-  __device__ __forceinline__ int64_t slot(int c) const { return c * 2LL + (c == c0 ? 1 : 0); }
+  __device__ __forceinline__ int slot(int c) const { return c * 2 + (c == c0 ? 1 : 0); }
 };
 
 // 2^floor(log2 x) of a positive float (bits below the exponent dropped), kept inside [2^-118, 2^118].
@@ -431,6 +463,118 @@ __device__ __forceinline__ uint64_t desc_keys_sw128(uint32_t saddr) {
          (static_cast<uint64_t>(2) << 61);
 }
 
+// The item of a range's first piece, if earlier ranges began it, and what the range does for it.
+struct BlockJoin {
+  long long start;
+  int b, hr, tiles;
+  bool ends, leads;  // its last tile lies here; a group of its parts ends here
+};
+
+// Joins the parts of an item, or of a group: the softmax threads. The parts come into the operands' place (the
+// products are done) by bulk copies, three in flight: an SM reads 64 bytes a clock from L2.
+template <int D, int NK>
+__device__ __forceinline__ void block_join(const BlockArgs& a, const BlockLine& line, const BlockJoin& j, uint8_t* smem,
+                                           uint32_t full, volatile int* abort_flag) {
+  using C = BlockCfg<D, NK>;
+  constexpr int N = C::N, kSlot = N * D * 4, kItems = N * D / 4 / kBSoft;
+  static_assert(3 * kSlot <= 4 * C::kTileBytes, "the parts' place");
+  const int me = static_cast<int>(blockIdx.x);
+  const BlockParts parts(line, j.start, C::kSetup, j.tiles);
+  const int head = j.hr / a.row_tiles, row_first = (j.hr % a.row_tiles) * a.tile_rows;
+  const int nrows = min(a.tile_rows, a.rows - row_first), count = parts.inputs(me);
+  // the parts' maxima and sums, then their weights, per row; at most 25 of 169 CTAs
+  float2* ml = reinterpret_cast<float2*>(smem + C::kOffP);       // [count][N]
+  int* place = reinterpret_cast<int*>(smem + C::kOffInfo);       // [count]: the parts' slots
+  float* row_f = reinterpret_cast<float*>(smem + C::kOffRow);    // [N]
+  static_assert(25 * N * 8 <= C::kPBytes, "the parts' weights");
+  if (threadIdx.x < count) {
+    const int c = parts.input(me, threadIdx.x);
+    place[threadIdx.x] = parts.slot(c);
+    if (c != me) {
+      unsigned long long* flag = a.flags + c;
+      const uint64_t t0 = globaltimer_ns();
+      while (ld_acquire_u64(flag) != a.call) {
+        __nanosleep(64);
+        if (*abort_flag != 0 || globaltimer_ns() - t0 > kWaitLimitNs) {
+          *abort_flag = 1;
+          atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_TIMEOUT));
+          break;
+        }
+      }
+      *flag = 0ull;  // read: ready for a replay
+    }
+  }
+  bar_soft();
+  const uint32_t bytes = static_cast<uint32_t>(nrows * D * 4);
+  auto fetch = [&](int p) {  // part p into its place
+    const uint32_t bar = full + 8 * (p % 3);
+    mbar_arrive_expect_tx(bar, bytes);
+    bulk_load(smem_u32(smem) + (p % 3) * kSlot, a.part_o + static_cast<int64_t>(place[p]) * N * D, bytes, bar);
+  };
+  if (threadIdx.x == 0) {
+    fence_proxy_async_all();  // (written by other CTAs' plain stores, read by the copy engine)
+    for (int p = 0; p < min(3, count); ++p) fetch(p);
+  }
+  for (int p = threadIdx.x >> 5; p < count; p += kBSoftWarps)
+    for (int r = threadIdx.x & 31; r < nrows; r += 32)
+      ml[p * N + r] = __ldcg(a.part_ml + static_cast<int64_t>(place[p]) * N + r);
+  bar_soft();
+  if (threadIdx.x < nrows) {
+    float2* mine = ml + threadIdx.x;
+    float mm = -INFINITY, sum = 0.f;
+    for (int p = 0; p < count; ++p) mm = fmaxf(mm, mine[p * N].x);
+    for (int p = 0; p < count; ++p) {
+      const float2 v = mine[p * N];
+      const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - mm);
+      sum += f * v.y;
+      mine[p * N].x = f;
+    }
+    if (j.leads) __stcg(a.part_ml + static_cast<int64_t>(place[count - 1]) * N + threadIdx.x, make_float2(mm, sum));
+    row_f[threadIdx.x] = j.leads ? 1.f : (sum > 0.f ? 1.f / sum : 0.f);
+  }
+  bar_soft();
+  float4 acc[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kRowStep = kBSoft / (D / 4);
+  const int r0 = threadIdx.x / (D / 4), col = threadIdx.x % (D / 4) * 4;
+#pragma unroll 1
+  for (int p = 0; p < count; ++p) {
+    wait_on(full + 8 * (p % 3), static_cast<uint32_t>(p / 3) & 1u, abort_flag, a.err);
+    const float* from = reinterpret_cast<const float*>(smem + (p % 3) * kSlot) + r0 * D + col;
+    const float2* weight = ml + p * N + r0;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const float f = weight[k * kRowStep].x;
+      const float4 v = *reinterpret_cast<const float4*>(from + k * kRowStep * D);
+      if (r0 + k * kRowStep < nrows && f != 0.f) {  // (0: nothing of the row there)
+        acc[k].x += f * v.x; acc[k].y += f * v.y; acc[k].z += f * v.z; acc[k].w += f * v.w;
+      }
+    }
+    bar_soft();
+    if (threadIdx.x == 0 && p + 3 < count) fetch(p + 3);
+  }
+  float* part = a.part_o + static_cast<int64_t>(place[count - 1]) * N * D;
+  __nv_bfloat16* out = a.out + static_cast<int64_t>(j.b) * a.G * a.Hq * D + head * a.R * D + col;
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int r = r0 + k * kRowStep;
+    if (r >= nrows) break;
+    if (j.leads) {
+      __stcg(reinterpret_cast<float4*>(part + r * D + col), acc[k]);
+    } else {
+      const float inv = row_f[r];
+      const int rr = row_first + r, t = row_token(a, rr);
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv);
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[k].z * inv, acc[k].w * inv);
+      uint2 u;
+      u.x = *reinterpret_cast<const uint32_t*>(&lo);
+      u.y = *reinterpret_cast<const uint32_t*>(&hi);
+      *reinterpret_cast<uint2*>(out + static_cast<int64_t>(t * a.Hq + rr - t * a.R) * D) = u;
+    }
+  }
+}
+
 template <int D, int NK>
 __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const BlockArgs a) {
   using C = BlockCfg<D, NK>;
@@ -458,6 +602,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
   uint32_t* vkey = tmem_slot + 3;
   uint32_t* qmax = tmem_slot + 4;
   uint32_t* came_s = tmem_slot + 5;  // [side][3]: the granules that came
+  const uint32_t join_full = bars + 264;  // [3]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -471,6 +616,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     }
     mbar_init(pfull, kBSoftWarps);
     mbar_init(odone, 1);
+    for (int i = 0; i < 3; ++i) mbar_init(join_full + 8 * i, 1);
     mbar_init(qfull, kBSoftWarps);
     for (int i = 0; i < 6; ++i) {
       mbar_init(raw_full + 8 * i, 1);
@@ -770,11 +916,8 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     };
     uint32_t it = 0;
     Walk w(a, range);
-    // the first piece may end an item that earlier ranges began: joined with their parts at the end
-    const bool joins = w.valid() && w.j0 > 0 && w.j1 == w.seq.tiles;
-    const int join_b = w.b, join_hr = w.hr, join_tiles = w.seq.tiles;
-    const long long join_start = w.start;
-    bool gave = false;
+    bool gave = false;  // the last piece goes on in the next range
+    BlockJoin join{w.start, w.b, w.hr, w.seq.tiles, w.valid() && w.j0 > 0 && w.j1 == w.seq.tiles, false};
     float qf = 1.f;
     for (bool start = true; w.valid(); start = false) {
       if (start) qf = load_q(w);
@@ -955,10 +1098,9 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         if ((lane & 3) == 0) row_red[quad * N + r0 + c + warp_reduce8_row(lane)] = v;
       }
       const bool complete = w.j0 == 0 && w.j1 == w.seq.tiles;
-      if (w.j1 < w.seq.tiles) {  // the last piece goes on in the next range: does that range join it?
-        const BlockParts parts(range.line, w.start, C::kSetup, w.seq.tiles);
-        gave = parts.c1 - parts.c0 < kBJoin;
-      }
+      gave = w.j1 < w.seq.tiles;
+      if (gave && w.j0 > 0)  // (the range lies inside the item)
+        join.leads = BlockParts(range.line, w.start, C::kSetup, w.seq.tiles).leads(static_cast<int>(blockIdx.x));
       Walk next = w;
       next.next(a);
       if (next.valid()) qf = load_q(next);  // (every S of this piece is done): its scores start meanwhile
@@ -1007,71 +1149,15 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
       bar_soft();  // the rows' data are read before the next piece sets them
       w = next;
     }
-    if (gave) {  // the last piece goes on in the next range
+    auto give = [&]() {  // this range's part is complete
       __threadfence();
       bar_soft();
       if (threadIdx.x == 0) st_release_u64(a.flags + blockIdx.x, a.call);
-    }
-    if (joins) {
-      const BlockParts parts(range.line, join_start, C::kSetup, join_tiles);
-      const int c0 = parts.c0, me = parts.c1;
-      if (me - c0 < kBJoin) {
-        if (threadIdx.x < me - c0) {
-          unsigned long long* flag = a.flags + c0 + threadIdx.x;
-          const uint64_t t0 = globaltimer_ns();
-          while (ld_acquire_u64(flag) != a.call) {
-            __nanosleep(64);
-            if (*abort_flag != 0 || globaltimer_ns() - t0 > kWaitLimitNs) {
-              *abort_flag = 1;
-              atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_TIMEOUT));
-              break;
-            }
-          }
-          *flag = 0ull;  // read: ready for a replay
-        }
-        bar_soft();
-        const int head = join_hr / a.row_tiles, row_first = (join_hr % a.row_tiles) * a.tile_rows;
-        const int nrows = min(a.tile_rows, a.rows - row_first);
-        // the parts' weights per row (over the sum of all), in the keys' factors' place
-        float* weight = reinterpret_cast<float*>(info);  // [kBJoin][N]
-        if (threadIdx.x < nrows) {
-          float2 ml[kBJoin];
-          float mm = -INFINITY, sum = 0.f;
-#pragma unroll
-          for (int p = 0; p < kBJoin; ++p) {
-            const bool in = c0 + p <= me;
-            ml[p] = in ? __ldcg(a.part_ml + parts.slot(c0 + p) * N + threadIdx.x) : make_float2(-INFINITY, 0.f);
-            mm = fmaxf(mm, ml[p].x);
-          }
-#pragma unroll
-          for (int p = 0; p < kBJoin; ++p) {
-            ml[p].x = ml[p].x == -INFINITY ? 0.f : ex2_approx(ml[p].x - mm);
-            sum += ml[p].x * ml[p].y;
-          }
-#pragma unroll
-          for (int p = 0; p < kBJoin; ++p) weight[p * N + threadIdx.x] = sum > 0.f ? ml[p].x / sum : 0.f;
-        }
-        bar_soft();
-#pragma unroll 2
-        for (int i = threadIdx.x; i < nrows * (D / 4); i += kBSoft) {
-          const int r = i / (D / 4), col = i % (D / 4) * 4;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-          for (int p = 0; p < kBJoin; ++p) {
-            const float f = c0 + p <= me ? weight[p * N + r] : 0.f;  // 0: nothing of the row there
-            if (f == 0.f) continue;
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + (parts.slot(c0 + p) * N + r) * D + col));
-            acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
-          }
-          const int rr = row_first + r, t = row_token(a, rr);
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
-          uint2 u;
-          u.x = *reinterpret_cast<const uint32_t*>(&lo);
-          u.y = *reinterpret_cast<const uint32_t*>(&hi);
-          *reinterpret_cast<uint2*>(
-              a.out + ((static_cast<int64_t>(join_b) * a.G + t) * a.Hq + head * a.R + rr - t * a.R) * D + col) = u;
-        }
-      }
+    };
+    if (gave && !join.leads) give();
+    if (join.ends || join.leads) {
+      block_join<D, NK>(a, range.line, join, smem, join_full, abort_flag);
+      if (join.leads) give();
     }
   }
   tc_fence_before();
@@ -1082,54 +1168,10 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
   }
 }
 
-// Joins the items of more than kBJoin parts. CTA (c, 1024 / D rows): the item that goes from range c, where it
-// starts, into the next; a thread per 4 channels of a row.
-template <int D>
-__global__ void __launch_bounds__(256) kv4_join_kernel(const BlockArgs a, int N, int setup, int ctas) {
-  pdl_trigger();
-  pdl_wait();
-  // the item of the first unit after range c
-  const int c = static_cast<int>(blockIdx.x);
-  const BlockRange next = block_range(a, setup, c + 1, ctas);
-  if (next.b < 0) return;  // (past the end)
-  const int tiles = block_seq(a, next.b).tiles;
-  const int hr = static_cast<int>(next.in_seq / (tiles + setup));
-  const BlockParts parts(next.line, next.first - (next.in_seq - static_cast<long long>(hr) * (tiles + setup)), setup, tiles);
-  if (parts.c0 != c || parts.c1 - c < kBJoin) return;
-  const int head = hr / a.row_tiles, row_first = (hr % a.row_tiles) * a.tile_rows;
-  const int r = static_cast<int>(blockIdx.y) * (1024 / D) + static_cast<int>(threadIdx.x) / (D / 4);
-  const int col = static_cast<int>(threadIdx.x) % (D / 4) * 4;
-  if (r >= min(a.tile_rows, a.rows - row_first)) return;
-  float mm = -INFINITY;
-#pragma unroll 4
-  for (int p = c; p <= parts.c1; ++p)
-    mm = fmaxf(mm, a.part_ml[parts.slot(p) * N + r].x);
-  float sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int p = c; p <= parts.c1; ++p) {
-    const float2 ml = a.part_ml[parts.slot(p) * N + r];
-    const float4 v = *reinterpret_cast<const float4*>(a.part_o + (parts.slot(p) * N + r) * D + col);
-    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - mm);
-    sum += f * ml.y;
-    acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const int rr = row_first + r, t = row_token(a, rr);
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  uint2 u;
-  u.x = *reinterpret_cast<const uint32_t*>(&lo);
-  u.y = *reinterpret_cast<const uint32_t*>(&hi);
-  *reinterpret_cast<uint2*>(
-      a.out + ((static_cast<int64_t>(next.b) * a.G + t) * a.Hq + head * a.R + rr - t * a.R) * D + col) = u;
-}
-
 // Row tiles of equal size, at most 80 rows each (the softmax threads keep a sum and a score of half of
 // them in registers).
 struct BlockPlan {
   int row_tiles, tile_rows, nk, ctas;
-  bool many;  // an item may have more than kBJoin parts
 };
 BlockPlan block_plan(int B, int G, int Hq, int Hkv, int64_t max_ctx, int sms) {
   BlockPlan p;
@@ -1138,14 +1180,8 @@ BlockPlan block_plan(int B, int G, int Hq, int Hkv, int64_t max_ctx, int sms) {
   p.tile_rows = (rows + p.row_tiles - 1) / p.row_tiles;
   p.nk = p.tile_rows <= 16 ? 1 : (p.tile_rows <= 32 ? 2 : (p.tile_rows <= 64 ? 4 : 5));
   const int64_t items = static_cast<int64_t>(B) * Hkv * p.row_tiles;
-  const int64_t setup = p.nk <= 2 ? 3 : p.nk, longest = (max_ctx + kBTile - 1) / kBTile + 1 + setup;
-  // CTAs: every SM; but where the ranges would only be cut finer than an item's last range joins (six
-  // parts), for less than the join kernel's cost (about five tiles), fewer
-  p.ctas = static_cast<int>(std::min<int64_t>(sms, items * (longest - setup)));
-  if (6 * items < p.ctas && longest / 6 - items * longest / p.ctas < 5) p.ctas = static_cast<int>(6 * items);
-  // most parts of an item: the longest sequence's, when all others are empty
-  const int64_t total = items / B * longest + (items - items / B) * (setup + 1);
-  p.many = longest * p.ctas / total + 2 > kBJoin;
+  // an SM each, as far as there can be tiles
+  p.ctas = static_cast<int>(std::min<int64_t>(sms, items * ((max_ctx + kBTile - 1) / kBTile + 1)));
   return p;
 }
 
@@ -1156,11 +1192,8 @@ int launch_block_t(const BlockArgs& a, const BlockPlan& p, cudaStream_t st) {
   static unsigned done = 0;
   auto kern = kv4_attention_kernel<D, NK>;
   if (!ensure_smem_attr(kern, C::kSmem, &done)) return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (attention)");
-  cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(p.ctas)), dim3(kBThreads), C::kSmem, st, nullptr, 0, a);
-  if (e == cudaSuccess && p.many && p.ctas > 1)
-    e = launch_pdl(kv4_join_kernel<D>,
-                   dim3(static_cast<unsigned>(p.ctas - 1), static_cast<unsigned>((p.tile_rows * D + 1023) / 1024)),
-                   dim3(256), 0, st, nullptr, 0, a, C::N, C::kSetup, p.ctas);
+  const cudaError_t e =
+      launch_pdl(kern, dim3(static_cast<unsigned>(p.ctas)), dim3(kBThreads), C::kSmem, st, nullptr, 0, a);
   return e == cudaSuccess ? DFLASH2_OK : fail(DFLASH2_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
 }
 
@@ -1202,6 +1235,7 @@ int launch_kv4_attention(const Kv4Attention& r, cudaStream_t st) {
   a.part_ml = reinterpret_cast<float2*>(a.part_o + slots * r.D);
   a.flags = reinterpret_cast<unsigned long long*>(a.part_ml + slots);
   a.call = next_call_number();
+  a.ctas_inverse = ~0ull / static_cast<unsigned long long>(p.ctas);
   a.err = device_error_word();
   if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
   if (r.D == 64) {
