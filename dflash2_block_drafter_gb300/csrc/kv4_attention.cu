@@ -337,7 +337,9 @@ struct BlockParts {
   int group;  // parts that are joined first: the smallest number whose square is at least all
   __device__ __forceinline__ BlockParts(const BlockLine& line, long long start, int setup, int tiles)
       : c0(line.range_of(start + setup)), c1(line.range_of(start + setup + tiles - 1)), group(1) {
-    while (group * group < c1 - c0 + 1) ++group;
+    const int all = c1 - c0 + 1;
+    if (all <= 8) group = all;
+    while (group * group < all) ++group;
   }
   // range c ends a group of parts, and not the item
   __device__ __forceinline__ bool leads(int c) const { return c < c1 && group > 1 && (c - c0) % group == group - 1; }
@@ -515,6 +517,7 @@ __device__ __forceinline__ void block_join(const BlockArgs& a, const BlockLine& 
     fence_proxy_async_all();  // (written by other CTAs' plain stores, read by the copy engine)
     for (int p = 0; p < min(3, count); ++p) fetch(p);
   }
+#pragma unroll 1
   for (int p = threadIdx.x >> 5; p < count; p += kBSoftWarps)
     for (int r = threadIdx.x & 31; r < nrows; r += 32)
       ml[p * N + r] = __ldcg(a.part_ml + static_cast<int64_t>(place[p]) * N + r);
@@ -522,7 +525,9 @@ __device__ __forceinline__ void block_join(const BlockArgs& a, const BlockLine& 
   if (threadIdx.x < nrows) {
     float2* mine = ml + threadIdx.x;
     float mm = -INFINITY, sum = 0.f;
+#pragma unroll 1
     for (int p = 0; p < count; ++p) mm = fmaxf(mm, mine[p * N].x);
+#pragma unroll 1
     for (int p = 0; p < count; ++p) {
       const float2 v = mine[p * N];
       const float f = v.x == -INFINITY ? 0.f : ex2_approx(v.x - mm);
@@ -769,6 +774,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         const uint32_t hi = static_cast<uint32_t>(kd >> 32), k_lo = static_cast<uint32_t>(kd), q = static_cast<uint32_t>(qd);
         for (Walk w(a, range); w.valid(); w.next(a), ++piece) {
           wait_on(qfull, piece & 1u, abort_flag, a.err);
+#pragma unroll 1
           for (int j = w.j0; j < w.j1; ++j, ++it) {
             const uint32_t buf = it & 1u;
             wait_on(sempty + 8 * buf, ((it >> 1) & 1u) ^ 1u, abort_flag, a.err);
@@ -790,6 +796,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         constexpr uint32_t id = kFmt | (1u << 15) | (1u << 16);
         const uint32_t d = tmem + 2 * N;
         for (Walk w(a, range); w.valid(); w.next(a))
+#pragma unroll 1
           for (int j = w.j0; j < w.j1; ++j, ++it) {
             const uint32_t buf = it & 1u;
             wait_on(vfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
@@ -958,6 +965,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         for (int c = 0; c < NH; c += 8) tmem_ld8(tl + (i & 1u) * N + static_cast<uint32_t>(c), x + c);
       };
       bool loaded = false;  // this tile's scores were requested behind the last one's probabilities
+#pragma unroll 1
       for (int j = w.j0; j < w.j1; ++j, ++it) {
         const uint32_t buf = it & 1u;
         const int key0 = j >= w.seq.cached ? w.seq.L : (w.seq.lo / kBTile + j) * kBTile;
