@@ -51,11 +51,10 @@
 namespace dfl {
 namespace {
 
-constexpr int kBTile = 128;                 // keys per tile
+constexpr int kBTileLog = 7, kBTile = 1 << kBTileLog;  // keys per tile
 constexpr int kBSoftWarps = 8, kBDeqWarps = 8, kBMmaWarp = 16, kBCopyWarp = 18;  // two each
 constexpr int kBSoft = 32 * kBSoftWarps;    // softmax threads
 constexpr int kBThreads = 640;
-constexpr int kBSoftRegs = 120, kBOtherRegs = 80;  // 256 x 120 + 384 x 80 = 640 x 96
 constexpr float kBSlack = 8.f;              // scores may pass the reference by 2^8
 constexpr float kBSlackV = 16.f;            // and the values' power of two its reference by 2^4 (fp16 holds 2^15)
 constexpr float kBUnseen = 3e38f;           // minus the reference of a row that has seen no key: any score passes it
@@ -67,6 +66,11 @@ struct BlockCfg {
   // the change from one item to the next, in tiles (measured: 15 of 3.1 thousand cycles with 80 rows, 5 of
   // 2.0 with 16)
   static constexpr int kSetup = NK <= 2 ? 3 : NK;
+  // registers a thread: 640 x 96 at launch, then shared out. With 80 rows 136 / 64 takes 130 us for 64 blocks
+  // over 256 .. 4096 keys where 120 / 80 takes 144 (152 / 56: 132); with 16 rows, whose softmax threads need
+  // few, 120 / 80 and 136 / 64 are alike and 80 / 104 is slower.
+  static constexpr int kSoftRegs = NK >= 4 ? 136 : 120, kOtherRegs = NK >= 4 ? 64 : 80;
+  static_assert(kBSoft * kSoftRegs + (kBThreads - kBSoft) * kOtherRegs <= kBThreads * 96, "registers");
   static constexpr int kHalves = D / 64;                     // 64-channel halves of a K or V tile
   static constexpr int kTileBytes = kHalves * kBTile * 128;  // fp16 [half][key][64]
   static constexpr int kPBytes = (N > 64 ? 2 : 1) * kBTile * 128;
@@ -191,7 +195,7 @@ __device__ __forceinline__ BlockSeq block_seq(const BlockArgs& a, int b) {
   s.base = s.L + (own - 1) * a.G;
   s.lo = a.window > 0 ? max(0, min(s.L, s.base - a.window + 1)) : 0;
   s.hi = a.causal ? max(0, min(s.L, s.base + a.G)) : s.L;
-  s.cached = s.hi > s.lo ? (s.hi + kBTile - 1) / kBTile - s.lo / kBTile : 0;
+  s.cached = s.hi > s.lo ? ((s.hi - 1) >> kBTileLog) - (s.lo >> kBTileLog) + 1 : 0;
   s.tiles = max(1, s.cached + own);
   return s;
 }
@@ -289,22 +293,23 @@ __device__ __forceinline__ BlockRange block_range(const BlockArgs& a, int setup,
   return r;
 }
 
-// Walks a range piece by piece: piece = consecutive tiles [j0, j1) of one item (sequence b, head and row tile
-// hr), none empty.
+// Walks a range piece by piece: piece = consecutive tiles [j0, j1) of one item (sequence b, head, row tile rt),
+// none empty.
 template <int kSetup>
 struct BlockWalk {
   int left;  // units (a cache that fits the memory has far fewer tiles than 2^31)
-  int b, hr, j0, j1, hrs;
+  int b, head, rt, j0, j1;
   long long start;  // the item's first unit
   BlockSeq seq;
   __device__ __forceinline__ BlockWalk(const BlockArgs& a, const BlockRange& r) {
     left = static_cast<int>(r.count);
-    hrs = a.Hkv * a.row_tiles;
     b = r.b;
     j1 = -1;
     if (left <= 0) return;
     seq = block_seq(a, b);
-    hr = small_quotient(r.in_seq, seq.tiles + kSetup);
+    const int hr = small_quotient(r.in_seq, seq.tiles + kSetup);
+    head = hr / a.row_tiles;
+    rt = hr - head * a.row_tiles;
     const int u = static_cast<int>(r.in_seq - static_cast<long long>(hr) * (seq.tiles + kSetup));
     start = r.first - u;
     enter(u);
@@ -323,9 +328,12 @@ struct BlockWalk {
       return;
     }
     start += seq.tiles + kSetup;
-    if (++hr == hrs) {
-      hr = 0;
-      seq = block_seq(a, ++b);
+    if (++rt == a.row_tiles) {
+      rt = 0;
+      if (++head == a.Hkv) {
+        head = 0;
+        seq = block_seq(a, ++b);
+      }
     }
     enter(0);
   }
@@ -468,7 +476,7 @@ __device__ __forceinline__ uint64_t desc_keys_sw128(uint32_t saddr) {
 // The item of a range's first piece, if earlier ranges began it, and what the range does for it.
 struct BlockJoin {
   long long start;
-  int b, hr, tiles;
+  int b, head, rt, tiles;
   bool ends, leads;  // its last tile lies here; a group of its parts ends here
 };
 
@@ -482,7 +490,7 @@ __device__ __forceinline__ void block_join(const BlockArgs& a, const BlockLine& 
   static_assert(3 * kSlot <= 4 * C::kTileBytes, "the parts' place");
   const int me = static_cast<int>(blockIdx.x);
   const BlockParts parts(line, j.start, C::kSetup, j.tiles);
-  const int head = j.hr / a.row_tiles, row_first = (j.hr % a.row_tiles) * a.tile_rows;
+  const int head = j.head, row_first = j.rt * a.tile_rows;
   const int nrows = min(a.tile_rows, a.rows - row_first), count = parts.inputs(me);
   // the parts' maxima and sums, then their weights, per row; at most 25 of 169 CTAs
   float2* ml = reinterpret_cast<float2*>(smem + C::kOffP);       // [count][N]
@@ -644,7 +652,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
 
   if (warp >= kBSoftWarps && warp < kBSoftWarps + kBDeqWarps) {
     // ------------------------------------------------------------------ dequant
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     const int side = (warp - kBSoftWarps) >> 2, dw = warp & 3;  // K or V; keys 32 dw .. of each tile
     const int ch = lane % NCH;
     constexpr int kStep = 32 / NCH;                        // step i converts keys sub + i kStep of the warp's 32
@@ -666,13 +674,13 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     for (Walk w(a, range); w.valid(); w.next(a)) {
       const __nv_bfloat16* own_src = (side == 0 ? a.k_new : a.v_new);
       if (own_src != nullptr) {
-        own_src += static_cast<int64_t>(w.b) * a.G * a.new_stride + w.hr / a.row_tiles * D;
+        own_src += static_cast<int64_t>(w.b) * a.G * a.new_stride + w.head * D;
         if (w.j1 > w.seq.cached && dw * 32 + lane < a.G)  // the piece ends with its own rows
 #pragma unroll
           for (int x = 0; x < D; x += 64) prefetch_l1(own_src + (dw * 32 + lane) * a.new_stride + x);
       }
       // the lane's key of the piece's tile j is seen for 128 j in [seen_lo, seen_hi)
-      const int at = w.seq.lo / kBTile * kBTile + dw * 32 + lane;
+      const int at = (w.seq.lo & ~(kBTile - 1)) + dw * 32 + lane;
       const int seen_lo = w.seq.lo - at, seen_hi = w.seq.hi - at;
 #pragma unroll 1
       for (int j = w.j0; j < w.j1; ++j, ++it) {
@@ -763,7 +771,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     }
   } else if (warp == kBMmaWarp || warp == kBMmaWarp + 1) {
     // ------------------------------------------------------------------ MMA issuers: S, and O
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     if (lane == 0) {
       constexpr uint32_t kFmt = (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);  // f32 <- f16, M = 128
       uint32_t it = 0, piece = 0;
@@ -822,7 +830,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     __syncwarp();
   } else if (warp >= kBCopyWarp) {
     // ------------------------------------------------------------------ copies of one side
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBOtherRegs));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     // A lane per granule looks up its page; the first granule of each run that lies together in a page
     // (the tile, a page, or a granule) is copied with the rest of its run.
     const int side = warp - kBCopyWarp;
@@ -832,7 +840,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     for (Walk w(a, range); w.valid(); w.next(a)) {
       const int last = min(w.j1, w.seq.cached);
       for (int j0 = w.j0; j0 < last; j0 += 4) {  // pages of four tiles at a time: 32 granules
-        const int g0 = (w.seq.lo / kBTile + j0) * (kBTile / kKvGranule) + lane;  // the lane's granule of the sequence
+        const int g0 = ((w.seq.lo >> kBTileLog) + j0) * (kBTile / kKvGranule) + lane;  // the lane's granule of the sequence
         const int key = g0 * kKvGranule;
         int page = -1;
         // a granule that some row sees (a window may have left the others' pages behind)
@@ -858,7 +866,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
           const uint32_t mine = (got >> first) & ((1u << run) - 1u);
           if (lane / 8 == j - j0 && mine != 0u && g == first + __ffs(mine) - 1)
             bulk_load(smem_u32(smem + C::kOffRaw + (side * C::kRawStages + stage) * C::kRaw + g * L::kGranuleBytes),
-                      a.cache + (((static_cast<int64_t>(page) * a.Hkv + w.hr / a.row_tiles) * 2 + side) * granules +
+                      a.cache + (((static_cast<int64_t>(page) * a.Hkv + w.head) * 2 + side) * granules +
                                  (g0 & (granules - 1))) *
                                     static_cast<int64_t>(L::kGranuleBytes),
                       static_cast<uint32_t>(__popc(mine)) * L::kGranuleBytes, rfull + 8 * stage);
@@ -872,7 +880,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     }
   } else {
     // ------------------------------------------------------------------ softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     const int quad = warp & 3;                    // TMEM lanes 32 quad .., rows (warp / 4) NH ..
     const int key_in = quad * 32 + lane;          // the thread's key of each tile; at the end, its channel
     const int r0 = (warp >> 2) * NH;
@@ -885,7 +893,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     }
     // Q of a piece: its rows as fp16 over their common power of two (returned), channels in the codes' order
     auto load_q = [&](const Walk& w) {
-      const int head = w.hr / a.row_tiles, row_first = (w.hr % a.row_tiles) * a.tile_rows;
+      const int head = w.head, row_first = w.rt * a.tile_rows;
       const int nrows = min(a.tile_rows, a.rows - row_first);
       constexpr int kQItems = (N * (D / 8) + kBSoft - 1) / kBSoft;
       uint4 qv[kQItems];
@@ -924,11 +932,11 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     uint32_t it = 0;
     Walk w(a, range);
     bool gave = false;  // the last piece goes on in the next range
-    BlockJoin join{w.start, w.b, w.hr, w.seq.tiles, w.valid() && w.j0 > 0 && w.j1 == w.seq.tiles, false};
+    BlockJoin join{w.start, w.b, w.head, w.rt, w.seq.tiles, w.valid() && w.j0 > 0 && w.j1 == w.seq.tiles, false};
     float qf = 1.f;
     for (bool start = true; w.valid(); start = false) {
       if (start) qf = load_q(w);
-      const int head = w.hr / a.row_tiles, row_first = (w.hr % a.row_tiles) * a.tile_rows;
+      const int head = w.head, row_first = w.rt * a.tile_rows;
       const int nrows = min(a.tile_rows, a.rows - row_first);
       if (threadIdx.x == 0) {
         *vkey = 0u;
@@ -968,7 +976,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
 #pragma unroll 1
       for (int j = w.j0; j < w.j1; ++j, ++it) {
         const uint32_t buf = it & 1u;
-        const int key0 = j >= w.seq.cached ? w.seq.L : (w.seq.lo / kBTile + j) * kBTile;
+        const int key0 = j >= w.seq.cached ? w.seq.L : ((w.seq.lo >> kBTileLog) + j) * kBTile;
         const int key = key0 + key_in;
         if (!loaded) {
           wait_on(vfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
