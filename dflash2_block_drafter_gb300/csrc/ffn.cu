@@ -28,6 +28,11 @@
 // dispatched before it. The flags lie in the call's workspace and hold the call's own 64-bit number, so
 // the workspace needs no initialisation and calls on different streams (with their own workspaces) are
 // independent; an owner clears what it has read, so a captured call can be replayed.
+//
+// Bound: the tensor pipe, busy in 87 % of the cycles of a large product; the rest waits on operands from L2 (an
+// SM takes 64 bytes a clock, a pair's tile needs 32 KB a CTA each 512 cycles). 1024 x 5120 x 13824 forward:
+// 167 us, 1.74 PFLOP/s in a short loop (the burst rate of a library product is 1.91); forward and all gradients
+// of 4096 rows: 2.2 ms, 1.55 PFLOP/s under the power cap (library, sustained: 1.72).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -8,6 +8,8 @@
 // All tiles are resident at once (two or three CTAs an SM), so that every SM keeps copies in flight until
 // the stream ends. Few tiles (a small F) split K over the CTAs of a cluster; the parts are read through
 // distributed shared memory and added in K order.
+//
+// Bound: the weights' stream. 16 rows, 2 x 13824 x 5120 weights (283 MB): 44 us, 6.4 TB/s.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -4,6 +4,11 @@
 // Quantisation, per token, head and group of 64 channels (affine, as dflash2.ts quantizedWeight's):
 //   bias = bf16(min x), scale = bf16((max x - min x) / 15), code = clamp(round((x - bias) / scale), 0, 15)
 // in IEEE fp32 with ties to even (scale = 0: code 0).
+//
+// A thread takes the same 16-byte chunk of K and of V of two tokens, all four loads in flight; a group's minimum
+// and maximum are packed bf16 operations over eight lanes. 32768 tokens of 8 heads of 128 channels: 62 us in
+// (2.8 TB/s), bound by issue slots (some 200 instructions a chunk, most of them the exact rounding of the
+// quotients), and 32 us out (5.4 TB/s), bound by DRAM; 6 us for 16 tokens, both calls together.
 #include <algorithm>
 
 #include "internal.h"
