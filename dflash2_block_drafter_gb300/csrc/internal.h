@@ -137,7 +137,8 @@ int launch_wait_selftest(int limit_us, cudaStream_t st);
 
 // bf16 row-major [rows, cols] operand for tcgen05: box of 64 elements (128 bytes) x box_rows rows,
 // 128-byte swizzle (defined in gemm.cu).
-bool make_tmap_sw128(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows);
+bool make_tmap_sw128(CUtensorMap* m, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
+                     uint64_t pitch = 0);  // elements between rows (0: cols)
 // The same over `planes` planes of [rows, cols] (plane_stride_bytes apart): box of 64 elements x
 // box_rows rows x box_planes planes, landing as box_planes consecutive [box_rows][128 B] tiles.
 bool make_tmap_sw128_3d(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint64_t planes,
