@@ -57,6 +57,7 @@ constexpr int kFGroupM = 8;                    // tiles are walked in strips of 
 constexpr int kFSlot = 128 * kFTile;           // fp32 values of one CTA's partial tile
 constexpr int kFMaxParts = 6;                  // pairs that share a tile at most, when there are few tiles
 constexpr int kFMinPiece = 8;                  // k-blocks of a share at least
+constexpr int kFMinGain = 45;                  // k-blocks a pair that shares of the last round have to save
 constexpr int kFPitchBlocks = 32;              // k-blocks a pair from which x is copied to whole lines
 constexpr uint64_t kFDrainNs = 100000000ull;
 
@@ -538,13 +539,14 @@ int launch_ffn_gemm(const FfnMaps& maps, FfnArgs a, void* share_ws, cudaStream_t
   a.wide = a.cols % 16 == 0 && is32(a.out0) && is32(a.out1) && is32(a.pre);
   a.err = device_error_word();
   if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
-  // The last round's tiles are cut into shares unless they nearly fill it (a cut tile costs its partial
-  // sums' way through the workspace). Few tiles over all pairs would leave an owner many parts to add
+  // The last round's tiles are cut into shares where that saves each pair kFMinGain k-blocks (a cut tile costs
+  // its partial sums' way through the workspace: with 5 saved, 333 x 1352 x 3592 takes 25.0 us cut and 14.8
+  // whole; with 25, 1024 x 5120 x 13824 takes 195 and 183). Few tiles over all pairs would leave an owner many parts to add
   // (19 of them at 1024 x 5120 with K = 27648: 320 us against 142 us of MMAs), so the round before is
   // cut with them where there is one: then a share is a tile and a bit, and a tile has at most three
   // parts. Without one, at most kFMaxParts pairs share a tile. A share has at least kFMinPiece k-blocks.
   const int rest = a.n_tiles % units;
-  a.sk_tiles = 10 * rest > 9 * units ? 0 : rest;
+  a.sk_tiles = a.kblocks * (units - rest) < kFMinGain * units ? 0 : rest;
   if (a.sk_tiles > 0 && 3 * rest < units && a.n_tiles > units) a.sk_tiles += units;
   const long long total = static_cast<long long>(a.sk_tiles) * a.kblocks;
   a.sk_units = static_cast<int>(std::max<long long>(
@@ -575,7 +577,7 @@ bool ffn_map(CUtensorMap* m, const void* p, int rows, int cols, int box_rows, in
 // twice. x is copied to such rows where its own are not; the weights are read as they lie (a copy of them
 // costs what it gives at a thousand rows).
 // 1001 x 2568 x 6920, forward and gradients: 247 -> 213 us. A forward product of less than kFPitchBlocks k-blocks a
-// pair keeps x as it is: 333 x 1352 x 3592 (17 of them) takes 25.3 us so and 26.5 with the copy.
+// pair keeps x as it is: 333 x 1352 x 3592 (17 of them) is 1.2 us slower with the copy.
 int ffn_pitch(int n) { return (n + 63) / 64 * 64; }
 size_t ffn_pitch_bytes(int M, int n) { return n % 64 == 0 ? 0 : align256(static_cast<size_t>(M) * ffn_pitch(n) * 2); }
 

@@ -13,3 +13,10 @@ pytestmark = pytest.mark.gpu
 def test_rows_of_odd_pitch(torch, M, H, F, kind):
     T.test_forward(torch, M, H, F, kind)
     T.test_backward(torch, M, H, F, kind)
+
+
+@pytest.mark.parametrize("M,H,F", [(300, 3136, 5120), (3600, 264, 520)])
+def test_products_whose_last_round_is_cut_into_shares(torch, M, H, F):
+    """80 tiles of 49 k-blocks (the round before is cut with the last four), 26 tiles of 160, 12 of 57."""
+    T.test_forward(torch, M, H, F, "silu")
+    T.test_backward(torch, M, H, F, "silu")
