@@ -13,7 +13,7 @@
 //   O^T [D channels x N rows] += V tile [keys][D]^T . P^T [keys][rows]   (both MN-major: V as it lies)
 // A softmax thread holds one key's scores of all (half of the) rows. It needs no reduction over keys:
 // the rows' reference (the number subtracted before the exponential) is only raised when some score
-// passes it by 2^8, which all threads agree on by one barrier a tile; then, rarely, the rows' maxima are
+// passes it by 2^8, which all threads agree on by one barrier a tile; then, rarely and once a tile, the rows' maxima are
 // taken, and O and the sums rescaled. The sums stay per thread until the end.
 //
 // Precision: operands are fp16 (11 significant bits; with bf16 the keys', the values' and the
@@ -997,41 +997,43 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         const bool there = inf.y >= 0.f;
         const bool masked = key0 < all_lo || key0 + kBTile > all_hi || __any_sync(0xffffffffu, !there);
         tmem_ld_wait();
-        for (;;) {
-          // scores (log2 domain) relative to the rows' references
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // scores (log2 domain) relative to the rows' references
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int r = 0; r < NH; r += 4) {
+          const float4 t = *reinterpret_cast<const float4*>(row_t + r0 + r);
+          const float2 y0 = __ffma2_rn(make_float2(x[r], x[r + 1]), make_float2(f, f), make_float2(t.x, t.y));
+          const float2 y1 = __ffma2_rn(make_float2(x[r + 2], x[r + 3]), make_float2(f, f), make_float2(t.z, t.w));
+          x[r] = y0.x; x[r + 1] = y0.y; x[r + 2] = y1.x; x[r + 3] = y1.y;
+        }
+        if (masked) {
 #pragma unroll
           for (int r = 0; r < NH; r += 4) {
-            const float4 t = *reinterpret_cast<const float4*>(row_t + r0 + r);
-            const float2 y0 = __ffma2_rn(make_float2(x[r], x[r + 1]), make_float2(f, f), make_float2(t.x, t.y));
-            const float2 y1 = __ffma2_rn(make_float2(x[r + 2], x[r + 3]), make_float2(f, f), make_float2(t.z, t.w));
-            x[r] = y0.x; x[r + 1] = y0.y; x[r + 2] = y1.x; x[r + 3] = y1.y;
+            const int4 lo = *reinterpret_cast<const int4*>(row_lo + r0 + r), hi = *reinterpret_cast<const int4*>(row_hi + r0 + r);
+            if (!there || key < lo.x || key >= hi.x) x[r] = -INFINITY;
+            if (!there || key < lo.y || key >= hi.y) x[r + 1] = -INFINITY;
+            if (!there || key < lo.z || key >= hi.z) x[r + 2] = -INFINITY;
+            if (!there || key < lo.w || key >= hi.w) x[r + 3] = -INFINITY;
           }
-          if (masked) {
+        }
 #pragma unroll
-            for (int r = 0; r < NH; r += 4) {
-              const int4 lo = *reinterpret_cast<const int4*>(row_lo + r0 + r), hi = *reinterpret_cast<const int4*>(row_hi + r0 + r);
-              if (!there || key < lo.x || key >= hi.x) x[r] = -INFINITY;
-              if (!there || key < lo.y || key >= hi.y) x[r + 1] = -INFINITY;
-              if (!there || key < lo.z || key >= hi.z) x[r + 2] = -INFINITY;
-              if (!there || key < lo.w || key >= hi.w) x[r + 3] = -INFINITY;
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < NH; ++r) top[r & 3] = fmaxf(top[r & 3], x[r]);
-          top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          if (!bar_or(top[0] > kBSlack || (there && !(inf.y * vinv <= kBSlackV && vinv > 0.f)))) break;
-          // ---- raise the references: the rows' maxima over the tile, the values' largest power of two
+        for (int r = 0; r < NH; ++r) top[r & 3] = fmaxf(top[r & 3], x[r]);
+        top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        if (bar_or(top[0] > kBSlack || (there && !(inf.y * vinv <= kBSlackV && vinv > 0.f)))) {
+          // ---- raise the references: the rows' maxima over the tile, the values' largest power of two. Once a
+          // tile: a row's scores are then its rounded products less at least their maximum, so none is above
+          // 0. (The check's FMA does not round the product: from 2^27 on its largest may pass the slack by the
+          // maximum's own rounding, again and again.)
           __syncwarp();
           load_s(it);
           tmem_ld_wait();
 #pragma unroll
           for (int r = 0; r < NH; r += 4) {
             const int4 lo = *reinterpret_cast<const int4*>(row_lo + r0 + r), hi = *reinterpret_cast<const int4*>(row_hi + r0 + r);
-            x[r] = there && key >= lo.x && key < hi.x ? x[r] * f : -INFINITY;
-            x[r + 1] = there && key >= lo.y && key < hi.y ? x[r + 1] * f : -INFINITY;
-            x[r + 2] = there && key >= lo.z && key < hi.z ? x[r + 2] * f : -INFINITY;
-            x[r + 3] = there && key >= lo.w && key < hi.w ? x[r + 3] * f : -INFINITY;
+            x[r] = there && key >= lo.x && key < hi.x ? __fmul_rn(x[r], f) : -INFINITY;
+            x[r + 1] = there && key >= lo.y && key < hi.y ? __fmul_rn(x[r + 1], f) : -INFINITY;
+            x[r + 2] = there && key >= lo.z && key < hi.z ? __fmul_rn(x[r + 2], f) : -INFINITY;
+            x[r + 3] = there && key >= lo.w && key < hi.w ? __fmul_rn(x[r + 3], f) : -INFINITY;
           }
 #pragma unroll
           for (int c = 0; c < NH; c += 8) {
@@ -1081,9 +1083,11 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
             tmem_st_wait();
             tc_fence_before();
           }
-          __syncwarp();
-          load_s(it);
-          tmem_ld_wait();
+#pragma unroll
+          for (int r = 0; r < NH; r += 4) {
+            const float4 t = *reinterpret_cast<const float4*>(row_t + r0 + r);
+            x[r] += t.x; x[r + 1] += t.y; x[r + 2] += t.z; x[r + 3] += t.w;
+          }
         }
         tc_fence_before();
         __syncwarp();

@@ -1,0 +1,54 @@
+"""Attention over the 4-bit cache with scores and values far from one another: one call, float64 statements."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_kv4 import S, _cached, _check, _dev, _host, _rows, torch  # noqa: F401 (fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def _fill(torch, d, k, v, page):
+    """A cache of one sequence's rows k, v [n, heads, D] in pages in order: (cache, table, ctx)."""
+    n, heads, D = k.shape
+    pages = max(1, -(-n // page))
+    cache = d.dflash2_kv4_cache(pages, heads, D, page)
+    cache.fill_(255)
+    d.dflash2_kv4_append(_dev(torch, k), _dev(torch, v), torch.arange(n, device="cuda"), cache, page)
+    return (cache, torch.arange(pages, dtype=torch.int32, device="cuda")[None],
+            torch.tensor([n], dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("qm,km,scale", [(1e3, 1e3, 0.125), (1e4, 1e4, 0.125), (1e6, 1e2, 1.0), (1e8, 1e8, 0.125),
+                                         (1e15, 1e15, 0.1), (1.0, 1.0, 3e7), (1e-3, 1.0, 1e12)])
+@pytest.mark.parametrize("G,Hq,first", [(1, 2, 3), (2, 4, 600), (10, 8, 1299), (16, 5, 700)])
+def test_large_finite_scores(torch, qm, km, scale, G, Hq, first):
+    """Scores up to 2^110 (an fp32 product near 2^28 is rounded by more than the slack that scores have over their
+    row's reference). One key stands out by a factor of two for rows of either sign, so that it takes everything."""
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(first + G)
+    n, D, page = 1300, 64, 32
+    u = rng.choice([-1.0, 1.0], D)
+    size = rng.uniform(0.5, 0.9, (n, 1, 1))
+    size[first], size[(first + n // 2) % n] = 2.0, -2.0
+    k, v = S.bf16(km * size * u), _rows(rng, n, 1, D)
+    q = S.bf16(qm * rng.choice([-1.0, 1.0], (1, G, Hq, 1)) * rng.uniform(1.0, 2.0, (1, G, Hq, 1)) * u)
+    cache, table, ctx = _fill(torch, d, k, v, page)
+    out = d.dflash2_kv4_attention(_dev(torch, q), cache, table, ctx, page, scale)
+    assert d.dflash2_poll_error() == 0
+    want, sd = S.attention(q[0], S.kv4_values(k), S.kv4_values(v), np.ones((G, n), bool), scale)
+    # everything is one key's value: only its operand's and the result's roundings count
+    assert np.all(np.abs(_host(out)[0] - want) <= 2 ** -7 * np.abs(want) + 1e-5)
+
+
+def test_large_random_scores(torch):
+    """Scores of hundreds of millions with no key far ahead: finite, within the values' range, the same bits again."""
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(12)
+    cache, table, ctx, K, V = _cached(torch, d, rng, [3000, 129, 1], 2, 128, 64)
+    for size in (3e6, 1e9):
+        q = _dev(torch, size * rng.normal(size=(3, 5, 8, 128)))
+        a = d.dflash2_kv4_attention(q, cache, table, ctx, 64, 1.0)
+        assert d.dflash2_poll_error() == 0
+        top = max(np.abs(v).max() for v in V)
+        assert torch.isfinite(a.float()).all() and float(a.abs().max()) <= top * (1 + 2 ** -6) and bool(a.any(-1).all())
+        assert torch.equal(a, d.dflash2_kv4_attention(q, cache, table, ctx, 64, 1.0))
