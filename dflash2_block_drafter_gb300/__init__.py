@@ -651,7 +651,7 @@ def dflash2_kv4_attention(q, cache, page_table, ctx_len, page_size, scale, k_new
     _check(lib.dflash2_kv4_attention(
         qp, qs, _dev(cache, "cache", torch.uint8), _dev(page_table, "page_table", torch.int32),
         _dev(ctx_len, "ctx_len", torch.int32), kp, vp, ns, B, G, Hq, Hkv, D, page_size, pages, width, int(bool(causal)),
-        window, scale, BF16, _dev(out, "out", torch.bfloat16), wp, wn, _stream(stream)))
+        max(-1, min(window, 2 ** 31 - 1)), scale, BF16, _dev(out, "out", torch.bfloat16), wp, wn, _stream(stream)))
     return out
 
 

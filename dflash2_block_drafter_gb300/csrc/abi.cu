@@ -539,6 +539,8 @@ int dflash2_kv4_attention(const void* q, int64_t q_stride, const void* cache, co
                   need);
     REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, "workspace must be 256-byte aligned");
   }
+  // a window that reaches every key from every row is none (and the rows' positions less it stay above -2^31)
+  if (static_cast<int64_t>(window) >= static_cast<int64_t>(max_pages) * page_size + 2 * G) window = 0;
   const Kv4Attention r{q, q_stride, cache, page_table, ctx_len, k_new, v_new, new_stride, B, G, Hq, Hkv, D, page_size,
                        num_pages, max_pages, causal, window, scale, out, workspace};
   return launch_kv4_attention(r, static_cast<cudaStream_t>(stream));

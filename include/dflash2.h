@@ -373,7 +373,7 @@ DFLASH2_API int dflash2_proj_conv_out(const void* a, int M, int K, const void* w
  *   k_new, v_new [B, G, Hkv, D] or both NULL: rows new_stride elements apart; keys L .. L + G - 1.
  *   Row t stands at position L + N - G + t (N = G with own rows, else 0: the rows' own keys are then
  *   the last cached ones). causal = 1: it sees keys up to its position; 0: every key (the draft
- *   block is bidirectional). window > 0: only keys after its position - window.
+ *   block is bidirectional). window > 0: only keys after its position - window (the largest int: all).
  *   out        [B, G, Hq, D] dense: softmax(scale q k^T) v over the keys a row sees (fp32 scores,
  *              statistics and sums; q, dequantised values and probabilities enter the tensor cores with
  *              11 significant bits, over a power of two per row so that bf16's range is kept); a row

@@ -52,3 +52,22 @@ def test_large_random_scores(torch):
         top = max(np.abs(v).max() for v in V)
         assert torch.isfinite(a.float()).all() and float(a.abs().max()) <= top * (1 + 2 ** -6) and bool(a.any(-1).all())
         assert torch.equal(a, d.dflash2_kv4_attention(q, cache, table, ctx, 64, 1.0))
+
+
+@pytest.mark.parametrize("new", [False, True])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 60, 2 ** 31, 2 ** 40])
+def test_windows_that_leave_nothing_out(torch, new, causal, window):
+    """Also where rows stand before the first key (contexts shorter than the rows, no own rows)."""
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(21)
+    lens, G, Hq, Hkv, D, page = [0, 2, 3, 5, 150, 1], 9, 4, 2, 64, 16
+    cache, table, ctx, K, V = _cached(torch, d, rng, lens, Hkv, D, page)
+    q = _dev(torch, _rows(rng, len(lens), G, Hq, D))
+    kw = dict(causal=causal)
+    if new:
+        kw.update(k_new=_dev(torch, _rows(rng, len(lens), G, Hkv, D)), v_new=_dev(torch, _rows(rng, len(lens), G, Hkv, D)))
+    want = d.dflash2_kv4_attention(q, cache, table, ctx, page, 0.125, **kw)
+    got = d.dflash2_kv4_attention(q, cache, table, ctx, page, 0.125, window=window, **kw)
+    assert d.dflash2_poll_error() == 0 and torch.equal(got, want)
+    assert bool(want[1].any()) and bool(want[2].any())
