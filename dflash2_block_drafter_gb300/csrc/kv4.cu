@@ -33,12 +33,13 @@ struct KvRowsArgs {
 constexpr int kRowsThreads = 256;
 constexpr int kRowsUnroll = 2;  // tokens of a thread in flight
 
+// (A NaN is kept: it ends in its group's scale and bias, which then read as NaN.)
 __device__ __forceinline__ uint32_t bf162_min(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 m = __hmin2(as_bf162(a), as_bf162(b));
+  const __nv_bfloat162 m = __hmin2_nan(as_bf162(a), as_bf162(b));
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 __device__ __forceinline__ uint32_t bf162_max(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 m = __hmax2(as_bf162(a), as_bf162(b));
+  const __nv_bfloat162 m = __hmax2_nan(as_bf162(a), as_bf162(b));
   return *reinterpret_cast<const uint32_t*>(&m);
 }
 
@@ -48,6 +49,7 @@ __device__ __forceinline__ uint32_t bf162_max(uint32_t a, uint32_t b) {
 // half a step (or half a step, and n odd): ties to even, as rounding the quotient gives. The values are
 // bf16, so b is their exact minimum and n ends in [0, 15] (15 steps fall short of the range by less than
 // half a step). The word is summed with the rounding constant still in every n, taken off at the end.
+// A group with a NaN or an infinity, or a range past fp32, has s = NaN: word 0.
 __device__ __forceinline__ uint32_t kv_quantise8(const uint32_t (&w)[4], float s, float b) {
   constexpr float kRound = 12582912.f;
   constexpr uint32_t kBits = 0x4b400000u;
@@ -169,7 +171,8 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_rows_kernel(const KvRowsArgs
             for (int i = 1; i < 8; i <<= 1) m = bf162_min(m, __shfl_xor_sync(group, m, i));
             if (g[u] == nullptr) continue;
             const float lo = __uint_as_float(m << 16), hi = -__uint_as_float(m & 0xffff0000u);
-            // (hi - lo) / 15 correctly rounded: a product and one correction by its residual
+            // (hi - lo) / 15 correctly rounded: a product and one correction by its residual (P. Markstein's
+            // method); NaN for a range that is not finite
             const float range = hi - lo, q0 = range * (1.f / 15.f);
             const float q = fmaf(fmaf(-15.f, q0, range), 1.f / 15.f, q0);
             const __nv_bfloat16 scale = __float2bfloat16_rn(q);

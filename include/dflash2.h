@@ -350,7 +350,8 @@ DFLASH2_API int dflash2_proj_conv_out(const void* a, int M, int K, const void* w
  *   4 (d % 8) .. 4 (d % 8) + 3 of the token's little-endian 32-bit word d / 8), then [16][D / 64]
  *   pairs of bf16 (scale, bias). Per token, head and group of 64 channels:
  *   bias = bf16(min x), scale = bf16((max x - min x) / 15), code = clamp(round((x - bias) / scale), 0, 15)
- *   (fp32, ties to even; scale = 0 gives code 0). A code stands for scale * code + bias.
+ *   (fp32, ties to even; scale = 0 gives code 0). A code stands for scale * code + bias. A group that
+ *   holds a NaN or an infinity, or whose range passes fp32's, reads as NaN.
  *   Slot s of the cache is token s % page_size of page s / page_size.
  *
  * dflash2_kv4_append: writes T rows (T >= 0) of keys and values into slots.
