@@ -407,7 +407,8 @@ DFLASH2_API int dflash2_kv4_attention(const void* q, int64_t q_stride, const voi
  *   zeroed weight gradients).
  *   forward:  g = x w_gate^T, u = x w_up^T (fp32), h [M, F] = act(g) * u, rounded once.
  *             pre [M, F] 32-bit words or NULL: g (low half) and u for the backward call, in 16 bits
- *             each (sign, 6 exponent bits of bias 31, 9 mantissa bits; |values| above 2^32 saturate).
+ *             each (sign, 6 exponent bits of bias 31, 9 mantissa bits; |values| above 2^32 saturate;
+ *             exponent 63: infinity or NaN, which the backward call reads as NaN).
  *   backward: from dh [M, F] and pre: dg = dh * u * act'(g), du = dh * act(g) (each rounded once to
  *             dtype, the operands of the products), then dx [M, H] = dg w_gate + du w_up (NULL: not
  *             wanted; the weights may then be NULL) and dw_gate, dw_up [F, H] = dg^T x, du^T x (both
