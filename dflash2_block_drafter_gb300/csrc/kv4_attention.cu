@@ -12,15 +12,18 @@
 //   S^T [128 keys x N rows]   = K tile [keys][D] . Q [rows][D]^T         (K-major operands)
 //   O^T [D channels x N rows] += V tile [keys][D]^T . P^T [keys][rows]   (both MN-major: V as it lies)
 // A softmax thread holds one key's scores of all (half of the) rows. It needs no reduction over keys:
-// the rows' reference (the number subtracted before the exponential) is only raised when some score
+// the rows' reference (the number subtracted before the exponential) is only raised when some number
 // passes it by 2^8, which all threads agree on by one barrier a tile; then, rarely and once a tile, the rows' maxima are
 // taken, and O and the sums rescaled. The sums stay per thread until the end.
 //
 // Precision: operands are fp16 (11 significant bits; with bf16 the keys', the values' and the
 // probabilities' roundings add up to twice the rounding of the bf16 result). fp16's range does not hold
 // every bf16 value, so each key row and each value row is divided by a power of two that brings its
-// largest value to [1, 2), and Q by one for all rows. The keys' factor multiplies the thread's scores (an
-// FMA that is there anyway), the values' the thread's probabilities, relative to the largest so far.
+// largest value to [1, 2), and Q by one for all rows. The keys' factor multiplies the thread's scores, and the
+// values' is added to them as its logarithm (one FMA): the operand P holds probabilities times values'
+// factors over the row's own largest such product, so that a value row far larger than the rest counts in
+// the rows that give it weight and is not felt by those that do not, to which a mask may hide it. The sums
+// take the factor off again, in fp32.
 //
 // Warps: 8 softmax (two per 32 TMEM lanes, half of the rows each), 8 dequant (four for K, four for V, 32
 // keys of a tile each: codes -> fp16 operand tiles in shared memory, 128-byte swizzle), 2 MMA (one thread
@@ -63,9 +66,12 @@ constexpr int kBTileLog = 7, kBTile = 1 << kBTileLog;  // keys per tile
 constexpr int kBSoftWarps = 8, kBDeqWarps = 8, kBMmaWarp = 16, kBCopyWarp = 18;  // two each
 constexpr int kBSoft = 32 * kBSoftWarps;    // softmax threads
 constexpr int kBThreads = 640;
-constexpr float kBSlack = 8.f;              // scores may pass the reference by 2^8
-constexpr float kBSlackV = 16.f;            // and the values' power of two its reference by 2^4 (fp16 holds 2^15)
+constexpr float kBLift = 7.f;               // a row's largest probability is 2^7 when its reference is set, and may
+constexpr float kBSlack = 15.f;             // grow to 2^15 (fp16 holds 2^15, and steps of 2^-24)
+constexpr float kBSumUnit = 0x1p-12f;       // of the sums: 2^31 keys of the smallest values' factor, 2^-93, stay finite
 constexpr float kBUnseen = 3e38f;           // minus the reference of a row that has seen no key: any score passes it
+constexpr uint32_t kBPow2Low = 9u << 23;    // 2^-118: powers of two of keys and queries go no lower
+constexpr uint32_t kBPow2LowV = 27u << 23;  // 2^-100: nor values'
 constexpr float kBPadding = -1e30f;         // of a row that does not exist: no score passes it, and it counts nothing
 
 template <int D, int NK>                    // N = 16 NK rows
@@ -371,10 +377,10 @@ struct BlockParts {
   __device__ __forceinline__ int slot(int c) const { return c * 2 + (c == c0 ? 1 : 0); }
 };
 
-// 2^floor(log2 x) of a positive float (bits below the exponent dropped), kept inside [2^-118, 2^118].
-__device__ __forceinline__ float pow2_of(float x) {
+// 2^floor(log2 x) of a positive float (bits below the exponent dropped), kept inside [low, 2^118].
+__device__ __forceinline__ float pow2_of(float x, uint32_t low = kBPow2Low) {
   const uint32_t u = __float_as_uint(x) & 0x7f800000u;
-  return __uint_as_float(min(max(u, 0x04800000u), 0x7a800000u));
+  return __uint_as_float(min(max(u, low), 0x7a800000u));
 }
 __device__ __forceinline__ float pow2_inverse(float p) { return __uint_as_float(0x7f000000u - __float_as_uint(p)); }
 
@@ -420,7 +426,7 @@ __device__ __forceinline__ float max_abs8(const uint4& u) {
 // A row's (scale, bias) pairs as operands of dequant_word: half2 (scale 2^24, bias) over the row's power
 // of two, and that power times 2^7 (the factor to undo it).
 template <int kGroups>
-__device__ __forceinline__ float row_params(const uint32_t (&par)[2], uint32_t (&out)[2]) {
+__device__ __forceinline__ float row_params(const uint32_t (&par)[2], uint32_t (&out)[2], uint32_t low) {
   float2 p[2];
   float m = 0.f;
 #pragma unroll
@@ -428,7 +434,7 @@ __device__ __forceinline__ float row_params(const uint32_t (&par)[2], uint32_t (
     p[g] = __bfloat1622float2(as_bf162(par[g]));
     m = fmaxf(m, fmaxf(fabsf(p[g].y), fabsf(fmaf(15.f, p[g].x, p[g].y))));
   }
-  const float f = pow2_of(m), inv = pow2_inverse(f) * 0.0078125f;
+  const float f = pow2_of(m, low), inv = pow2_inverse(f) * 0.0078125f;
 #pragma unroll
   for (int g = 0; g < kGroups; ++g) {
     const __half2 h = __floats2half2_rn(p[g].x * inv * 16777216.f, p[g].y * inv);
@@ -551,7 +557,7 @@ __device__ __forceinline__ void block_join(const BlockArgs& a, const BlockLine& 
       mine[p * N].x = f;
     }
     if (j.leads) __stcg(a.part_ml + static_cast<int64_t>(place[count - 1]) * N + threadIdx.x, make_float2(mm, sum));
-    row_f[threadIdx.x] = j.leads ? 1.f : (sum > 0.f ? 1.f / sum : 0.f);
+    row_f[threadIdx.x] = j.leads ? 1.f : (sum > 0.f ? kBSumUnit / sum : 0.f);
   }
   bar_soft();
   float4 acc[kItems];
@@ -619,10 +625,8 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
   const uint32_t raw_full = bars + 120, raw_empty = bars + 168;                               // [side][3]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 216);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* vref_s = reinterpret_cast<float*>(tmem_slot + 2);
-  uint32_t* vkey = tmem_slot + 3;
-  uint32_t* qmax = tmem_slot + 4;
-  uint32_t* came_s = tmem_slot + 5;  // [side][3]: the granules that came
+  uint32_t* qmax = tmem_slot + 2;
+  uint32_t* came_s = tmem_slot + 3;  // [side][3]: the granules that came
   const uint32_t join_full = bars + 264;  // [3]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -662,6 +666,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     // ------------------------------------------------------------------ dequant
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     const int side = (warp - kBSoftWarps) >> 2, dw = warp & 3;  // K or V; keys 32 dw .. of each tile
+    const uint32_t low = side == 0 ? kBPow2Low : kBPow2LowV;
     const int ch = lane % NCH;
     constexpr int kStep = 32 / NCH;                        // step i converts keys sub + i kStep of the warp's 32
     const int sub = lane / NCH;
@@ -717,7 +722,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
             pr[0] = *reinterpret_cast<const uint32_t*>(par0 + raw);
             if (L::kGroups == 2) pr[1] = *reinterpret_cast<const uint32_t*>(par0 + raw + 4);
           }
-          const float f = row_params<L::kGroups>(pr, po);
+          const float f = row_params<L::kGroups>(pr, po, low);
           uint32_t sb_bits[NCH];
 #pragma unroll
           for (int i = 0; i < NCH; ++i) {
@@ -762,8 +767,8 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
               for (int k = 0; k < 4; ++k) m = fmaxf(m, max_abs8(u[k]));
 #pragma unroll
               for (int x = 1; x < NCH; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-              f = pow2_of(m) * 128.f;
-              const float inv = pow2_inverse(pow2_of(m)) * 0.0078125f;
+              f = pow2_of(m, low) * 128.f;
+              const float inv = pow2_inverse(pow2_of(m, low)) * 0.0078125f;
 #pragma unroll
               for (int k = 0; k < 4; ++k) u[k] = convert_word(u[k], inv);
             }
@@ -946,10 +951,6 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
       if (start) qf = load_q(w);
       const int head = w.head, row_first = w.rt * a.tile_rows;
       const int nrows = min(a.tile_rows, a.rows - row_first);
-      if (threadIdx.x == 0) {
-        *vkey = 0u;
-        *vref_s = 0.f;
-      }
       if (threadIdx.x < N) {
         const int r = threadIdx.x, rr = row_first + r, t = row_token(a, rr), pos = w.seq.base + t;
         const int all = w.seq.L + (a.k_new != nullptr ? a.G : 0);
@@ -968,8 +969,6 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
       float l[NH];
 #pragma unroll
       for (int r = 0; r < NH; ++r) l[r] = 0.f;
-      float vinv = 0.f;  // 1 / the values' reference (0: none yet)
-
       float x[NH];
       auto ready = [&](uint32_t i) {  // S of tile i and its values' factors, without waiting
         return __all_sync(0xffffffffu, mbar_test(vfull + 8 * (i & 1u), (i >> 1) & 1u) &&
@@ -995,15 +994,20 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         const float2 inf = info[(it & 3) * kBTile + key_in];
         const float f = inf.x * qscale;
         const bool there = inf.y >= 0.f;
+        const float vlog = static_cast<float>(static_cast<int>(__float_as_uint(inf.y) >> 23) - 127);  // the values' factor
+        const float vinv = pow2_inverse(inf.y) * kBSumUnit;
         const bool masked = key0 < all_lo || key0 + kBTile > all_hi || __any_sync(0xffffffffu, !there);
         tmem_ld_wait();
-        // scores (log2 domain) relative to the rows' references
+        // scores and values' factors (log2 domain) relative to the rows' references
+        auto weigh = [&](float a, float b) {
+          return __ffma2_rn(make_float2(a, b), make_float2(f, f), make_float2(vlog, vlog));
+        };
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int r = 0; r < NH; r += 4) {
           const float4 t = *reinterpret_cast<const float4*>(row_t + r0 + r);
-          const float2 y0 = __ffma2_rn(make_float2(x[r], x[r + 1]), make_float2(f, f), make_float2(t.x, t.y));
-          const float2 y1 = __ffma2_rn(make_float2(x[r + 2], x[r + 3]), make_float2(f, f), make_float2(t.z, t.w));
+          const float2 y0 = __fadd2_rn(weigh(x[r], x[r + 1]), make_float2(t.x, t.y));
+          const float2 y1 = __fadd2_rn(weigh(x[r + 2], x[r + 3]), make_float2(t.z, t.w));
           x[r] = y0.x; x[r + 1] = y0.y; x[r + 2] = y1.x; x[r + 3] = y1.y;
         }
         if (masked) {
@@ -1019,55 +1023,48 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
 #pragma unroll
         for (int r = 0; r < NH; ++r) top[r & 3] = fmaxf(top[r & 3], x[r]);
         top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        if (bar_or(top[0] > kBSlack || (there && !(inf.y * vinv <= kBSlackV && vinv > 0.f)))) {
-          // ---- raise the references: the rows' maxima over the tile, the values' largest power of two. Once a
-          // tile: a row's scores are then its rounded products less at least their maximum, so none is above
-          // 0. (The check's FMA does not round the product: from 2^27 on its largest may pass the slack by the
-          // maximum's own rounding, again and again.)
+        if (bar_or(top[0] > kBSlack)) {
+          // ---- raise the references to the rows' maxima over the tile. Once a tile: a row's weights are then
+          // numbers less at least their maximum, and a lift, so that none passes the slack. (The maximum is
+          // taken over the same rounded numbers: were the reference subtracted inside the FMA, from 2^27
+          // on the largest would pass any slack by its own rounding.)
           __syncwarp();
           load_s(it);
           tmem_ld_wait();
 #pragma unroll
           for (int r = 0; r < NH; r += 4) {
             const int4 lo = *reinterpret_cast<const int4*>(row_lo + r0 + r), hi = *reinterpret_cast<const int4*>(row_hi + r0 + r);
-            x[r] = there && key >= lo.x && key < hi.x ? __fmul_rn(x[r], f) : -INFINITY;
-            x[r + 1] = there && key >= lo.y && key < hi.y ? __fmul_rn(x[r + 1], f) : -INFINITY;
-            x[r + 2] = there && key >= lo.z && key < hi.z ? __fmul_rn(x[r + 2], f) : -INFINITY;
-            x[r + 3] = there && key >= lo.w && key < hi.w ? __fmul_rn(x[r + 3], f) : -INFINITY;
+            const float2 y0 = weigh(x[r], x[r + 1]), y1 = weigh(x[r + 2], x[r + 3]);
+            x[r] = there && key >= lo.x && key < hi.x ? y0.x : -INFINITY;
+            x[r + 1] = there && key >= lo.y && key < hi.y ? y0.y : -INFINITY;
+            x[r + 2] = there && key >= lo.z && key < hi.z ? y1.x : -INFINITY;
+            x[r + 3] = there && key >= lo.w && key < hi.w ? y1.y : -INFINITY;
           }
 #pragma unroll
           for (int c = 0; c < NH; c += 8) {
             const float v = warp_reduce8(x + c, lane, [](float p, float q) { return fmaxf(p, q); });
             if ((lane & 3) == 0) row_red[quad * N + r0 + c + warp_reduce8_row(lane)] = v;
           }
-          const uint32_t vk = __reduce_max_sync(0xffffffffu, there ? __float_as_uint(inf.y) : 0u);
-          if (lane == 0) atomicMax(vkey, vk);
           bar_soft();
-          const float vold = *vref_s, vnew = fmaxf(vold, __uint_as_float(*vkey));
           if (threadIdx.x < N) {
             const int r = threadIdx.x;
             const float told = row_t[r];
             const float mx = fmaxf(fmaxf(row_red[r], row_red[N + r]), fmaxf(row_red[2 * N + r], row_red[3 * N + r]));
+            const float t = kBLift - mx;
             float shrink = 1.f;
-            if (told != kBPadding && mx > -INFINITY && mx > -told) {
-              shrink = told == kBUnseen ? 0.f : ex2_approx(-told - mx);
-              row_t[r] = -mx;
+            if (told != kBPadding && mx > -INFINITY && t < told) {
+              shrink = told == kBUnseen ? 0.f : ex2_approx(t - told);
+              row_t[r] = t;
             }
             row_f[r] = shrink;
           }
           bar_soft();
-          if (threadIdx.x == 0) {
-            *vref_s = vnew;
-            *vkey = 0u;
-          }
-          vinv = vnew > 0.f ? pow2_inverse(vnew) : 0.f;
 #pragma unroll
           for (int r = 0; r < NH; r += 4) {
             const float4 g = *reinterpret_cast<const float4*>(row_f + r0 + r);
             l[r] *= g.x; l[r + 1] *= g.y; l[r + 2] *= g.z; l[r + 3] *= g.w;
           }
           if (j > w.j0) {
-            const float vscale = vold > 0.f ? vold * pow2_inverse(vnew) : 0.f;
             wait_on(odone, (it - 1) & 1u, abort_flag, a.err);
             tc_fence_after();
             __syncwarp();
@@ -1077,7 +1074,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
               tmem_ld8(tl + static_cast<uint32_t>(2 * N + c), o);
               tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) o[i] *= row_f[r0 + c + i] * vscale;
+              for (int i = 0; i < 8; ++i) o[i] *= row_f[r0 + c + i];
               tmem_st8(tl + static_cast<uint32_t>(2 * N + c), o);
             }
             tmem_st_wait();
@@ -1092,8 +1089,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(sempty + 8 * buf);
-        // ---- probabilities: fp32 sums, fp16 operand
-        const __half2 w2 = __float2half2_rn(there ? inf.y * vinv : 0.f);
+        // ---- probabilities times the values' factors: fp16 operand; without those: fp32 sums
         if (it > 0) wait_on(odone, (it - 1) & 1u, abort_flag, a.err);  // the operand tile is free
 #pragma unroll
         for (int c = 0; c < NK; ++c) {
@@ -1102,10 +1098,10 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
           for (int i = 0; i < 4; ++i) {
             const int r = 8 * c + 2 * i;
             const float2 e = make_float2(ex2_approx(x[r]), ex2_approx(x[r + 1]));
-            const float2 sum = __fadd2_rn(make_float2(l[r], l[r + 1]), e);
+            const float2 sum = __ffma2_rn(e, make_float2(vinv, vinv), make_float2(l[r], l[r + 1]));
             l[r] = sum.x;
             l[r + 1] = sum.y;
-            const __half2 h = __hmul2(__floats2half2_rn(e.x, e.y), w2);
+            const __half2 h = __floats2half2_rn(e.x, e.y);
             p[i] = *reinterpret_cast<const uint32_t*>(&h);
           }
           st_shared_v4(to[c], make_uint4(p[0], p[1], p[2], p[3]));
@@ -1138,7 +1134,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         const int r = threadIdx.x;
         const float sum = row_red[r] + row_red[N + r] + row_red[2 * N + r] + row_red[3 * N + r];
         const bool some = row_t[r] != kBUnseen;
-        row_f[r] = some ? (complete ? (sum > 0.f ? *vref_s / sum : 0.f) : *vref_s) : 0.f;
+        row_f[r] = some ? (complete ? (sum > 0.f ? kBSumUnit / sum : 0.f) : 1.f) : 0.f;
         if (!complete && r < nrows) a.part_ml[slot + r] = make_float2(some ? -row_t[r] : -INFINITY, sum);
       }
       bar_soft();

@@ -71,3 +71,73 @@ def test_windows_that_leave_nothing_out(torch, new, causal, window):
     got = d.dflash2_kv4_attention(q, cache, table, ctx, page, 0.125, window=window, **kw)
     assert d.dflash2_poll_error() == 0 and torch.equal(got, want)
     assert bool(want[1].any()) and bool(want[2].any())
+
+
+def _check_rows(got, want, sd, unit, what):
+    """Row by row (rows differ in size): `unit` is what 1 stands for in the row's absolute allowance."""
+    for t in np.ndindex(got.shape[:2]):
+        _check(got[t] / unit[t], want[t] / unit[t], sd[t] / unit[t], f"{what} row {t}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("e", [12, 16, 24, 60])
+def test_one_value_row_far_larger(torch, D, e):
+    """A value row 2^e above the rest is felt by the rows that give it weight, and by no other: rows to which causal
+    order or the window hides it, and rows whose score for it is far below, give what the rest gives."""
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(e)
+    n, G, R, page = 300, 4, 3, 16
+    for place in ("own row", "window's edge", "low score"):
+        k, v = _rows(rng, n, 1, D), _rows(rng, n, 1, D)
+        kn, vn = _rows(rng, 1, G, 1, D), _rows(rng, 1, G, 1, D)
+        q = _rows(rng, 1, G, R, D)
+        causal, window = place == "own row", 50 if place == "window's edge" else 0
+        if place == "own row":
+            vn[0, 2] *= 2.0 ** e
+        elif place == "window's edge":
+            v[n - window + 1] *= 2.0 ** e  # (the last key of row 0 and of no other; own rows follow at n)
+        else:
+            q = np.abs(q)
+            k[40], v[40] = -30.0, v[40] * 2.0 ** e
+        cache, table, ctx = _fill(torch, d, k, v, page)
+        out = d.dflash2_kv4_attention(_dev(torch, q), cache, table, ctx, page, D ** -0.5, k_new=_dev(torch, kn),
+                                      v_new=_dev(torch, vn), causal=causal, window=window)
+        assert d.dflash2_poll_error() == 0
+        K, V = np.concatenate([S.kv4_values(k), kn[0]]), np.concatenate([S.kv4_values(v), vn[0]])
+        want, sd = S.attention(q[0], K, V, S.seen(G, n, G, causal, window), D ** -0.5)
+        unit = np.maximum(1.0, np.abs(want).max(-1))
+        _check_rows(_host(out)[0], want, sd, unit, f"{place} 2^{e}")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_value_rows_of_every_size(torch, D):
+    """Value rows from 2^-60 to 2^60, in an order that meets the largest late, over many tiles and parts."""
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(D)
+    n, G, R, page = 5000, 2, 2, 64
+    k, v = _rows(rng, n, 1, D), _rows(rng, n, 1, D) * 2.0 ** np.round(np.linspace(-60, 60, n))[:, None, None]
+    q = _rows(rng, 1, G, R, D)
+    cache, table, ctx = _fill(torch, d, k, v, page)
+    out = d.dflash2_kv4_attention(_dev(torch, q), cache, table, ctx, page, D ** -0.5)
+    assert d.dflash2_poll_error() == 0
+    want, sd = S.attention(q[0], S.kv4_values(k), S.kv4_values(v), np.ones((G, n), bool), D ** -0.5)
+    _check_rows(_host(out)[0], want, sd, np.abs(want).max(-1), "sizes")
+
+
+@pytest.mark.parametrize("sink", [0.0, 2.0 ** -8, 1.0])
+@pytest.mark.parametrize("gap", [8.0, 14.0])
+def test_a_key_that_takes_nearly_everything(torch, gap, sink):
+    """The first key's score stands `gap` above the rest; its value is small. What is left of the output is the
+    rest's, each of them a small probability."""
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(int(gap))
+    n, D, page, G, R = 6000, 64, 64, 1, 4
+    k, v = 0.02 * _rows(rng, n, 1, D), _rows(rng, n, 1, D) + 1.0
+    q = np.ones((1, G, R, D))
+    k[0], v[0] = gap / 8.0, v[0] * sink
+    k, v = S.bf16(k), S.bf16(v)
+    cache, table, ctx = _fill(torch, d, k, v, page)
+    out = d.dflash2_kv4_attention(_dev(torch, q), cache, table, ctx, page, 0.125)
+    assert d.dflash2_poll_error() == 0
+    want, sd = S.attention(q[0], S.kv4_values(k), S.kv4_values(v), np.ones((G, n), bool), 0.125)
+    _check_rows(_host(out)[0], want, sd, np.abs(want).max(-1), f"gap {gap}")
