@@ -415,12 +415,18 @@ __device__ __forceinline__ uint4 convert_word(const uint4& u, float f) {
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-__device__ __forceinline__ float max_abs8(const uint4& u) {
+// The largest magnitude as the bits of an fp32 number (they compare as integers, NaN above infinity).
+__device__ __forceinline__ uint32_t max_abs8(const uint4& u) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint32_t m = 0;  // magnitudes of bf16 compare as integers
+  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-  return __uint_as_float(m << 16);
+  return m << 16;
+}
+constexpr uint32_t kBInfinity = 0x7f800000u;
+// one of a pair of bf16 is infinite or NaN
+__device__ __forceinline__ bool pair_not_finite(uint32_t p) {
+  return (p & 0x7f80u) == 0x7f80u || (p & 0x7f800000u) == 0x7f800000u;
 }
 
 // A row's (scale, bias) pairs as operands of dequant_word: half2 (scale 2^24, bias) over the row's power
@@ -557,7 +563,7 @@ __device__ __forceinline__ void block_join(const BlockArgs& a, const BlockLine& 
       mine[p * N].x = f;
     }
     if (j.leads) __stcg(a.part_ml + static_cast<int64_t>(place[count - 1]) * N + threadIdx.x, make_float2(mm, sum));
-    row_f[threadIdx.x] = j.leads ? 1.f : (sum > 0.f ? kBSumUnit / sum : 0.f);
+    row_f[threadIdx.x] = j.leads ? 1.f : (sum == 0.f ? 0.f : kBSumUnit / sum);  // (NaN stays)
   }
   bar_soft();
   float4 acc[kItems];
@@ -722,7 +728,10 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
             pr[0] = *reinterpret_cast<const uint32_t*>(par0 + raw);
             if (L::kGroups == 2) pr[1] = *reinterpret_cast<const uint32_t*>(par0 + raw + 4);
           }
-          const float f = row_params<L::kGroups>(pr, po, low);
+          // (a value row that is not finite counts as zeros, with a factor of NaN: only rows that see it become NaN)
+          const bool odd = side == 1 && (pair_not_finite(pr[0]) || (L::kGroups == 2 && pair_not_finite(pr[1])));
+          if (odd) pr[0] = pr[1] = 0u;
+          const float f = odd ? __uint_as_float(0x7fffffffu) : row_params<L::kGroups>(pr, po, low);
           uint32_t sb_bits[NCH];
 #pragma unroll
           for (int i = 0; i < NCH; ++i) {
@@ -759,18 +768,20 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
 #pragma unroll
             for (int k = 0; k < 4; ++k) u[k] = make_uint4(0u, 0u, 0u, 0u);
             if (dw * 32 + i * kStep < a.G) {
-              float m = 0.f;
+              uint32_t m = 0;
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 if (key < a.G) u[k] = __ldg(reinterpret_cast<const uint4*>(own_src + key * a.new_stride + ch * 32 + 8 * k));
 #pragma unroll
-              for (int k = 0; k < 4; ++k) m = fmaxf(m, max_abs8(u[k]));
+              for (int k = 0; k < 4; ++k) m = max(m, max_abs8(u[k]));
 #pragma unroll
-              for (int x = 1; x < NCH; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-              f = pow2_of(m, low) * 128.f;
-              const float inv = pow2_inverse(pow2_of(m, low)) * 0.0078125f;
+              for (int x = 1; x < NCH; x <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
+              const float p2 = pow2_of(__uint_as_float(m), low);
+              const bool odd = side == 1 && m >= kBInfinity;  // (as for cached rows)
+              f = odd ? __uint_as_float(0x7fffffffu) : p2 * 128.f;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) u[k] = convert_word(u[k], inv);
+              for (int k = 0; k < 4; ++k)
+                u[k] = odd ? make_uint4(0u, 0u, 0u, 0u) : convert_word(u[k], pow2_inverse(p2) * 0.0078125f);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) st_shared_v4(to[k] + tile + i * kStep * 128, u[k]);
@@ -910,7 +921,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
       const int nrows = min(a.tile_rows, a.rows - row_first);
       constexpr int kQItems = (N * (D / 8) + kBSoft - 1) / kBSoft;
       uint4 qv[kQItems];
-      float qm = 0.f;
+      uint32_t qm = 0;
 #pragma unroll
       for (int i = 0; i < kQItems; ++i) {
         const int x = threadIdx.x + i * kBSoft, r = x / (D / 8), c = x % (D / 8);
@@ -924,8 +935,11 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
       if (threadIdx.x == 0) *qmax = 0u;
       bar_soft();
 #pragma unroll
-      for (int i = 0; i < kQItems; ++i) qm = fmaxf(qm, max_abs8(qv[i]));
-      const uint32_t qk = __reduce_max_sync(0xffffffffu, __float_as_uint(qm));
+      for (int i = 0; i < kQItems; ++i) {
+        const uint32_t m = max_abs8(qv[i]);
+        qm = max(qm, m <= kBInfinity ? m : 0u);
+      }
+      const uint32_t qk = __reduce_max_sync(0xffffffffu, qm);
       if (lane == 0) atomicMax(qmax, qk);
       bar_soft();
       const float qf = pow2_of(__uint_as_float(*qmax));
@@ -993,8 +1007,9 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         }
         const float2 inf = info[(it & 3) * kBTile + key_in];
         const float f = inf.x * qscale;
-        const bool there = inf.y >= 0.f;
-        const float vlog = static_cast<float>(static_cast<int>(__float_as_uint(inf.y) >> 23) - 127);  // the values' factor
+        const bool there = !(inf.y < 0.f);
+        // the values' factor (NaN if it is)
+        const float vlog = fmaf(inf.y, 0.f, static_cast<float>(static_cast<int>(__float_as_uint(inf.y) >> 23) - 127));
         const float vinv = pow2_inverse(inf.y) * kBSumUnit;
         const bool masked = key0 < all_lo || key0 + kBTile > all_hi || __any_sync(0xffffffffu, !there);
         tmem_ld_wait();
@@ -1133,9 +1148,9 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
       if (threadIdx.x < N) {
         const int r = threadIdx.x;
         const float sum = row_red[r] + row_red[N + r] + row_red[2 * N + r] + row_red[3 * N + r];
-        const bool some = row_t[r] != kBUnseen;
-        row_f[r] = some ? (complete ? (sum > 0.f ? kBSumUnit / sum : 0.f) : 1.f) : 0.f;
-        if (!complete && r < nrows) a.part_ml[slot + r] = make_float2(some ? -row_t[r] : -INFINITY, sum);
+        // (a row that saw something that is not finite has a sum, and an O, of NaN)
+        row_f[r] = sum == 0.f ? 0.f : (complete ? kBSumUnit / sum : 1.f);
+        if (!complete && r < nrows) a.part_ml[slot + r] = make_float2(row_t[r] != kBUnseen ? -row_t[r] : -INFINITY, sum);
       }
       bar_soft();
       // the thread's channel: operand position p of each eight holds channel p / 2 + 4 (p % 2) of its word

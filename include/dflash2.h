@@ -378,7 +378,8 @@ DFLASH2_API int dflash2_proj_conv_out(const void* a, int M, int K, const void* w
  *   out        [B, G, Hq, D] dense: softmax(scale q k^T) v over the keys a row sees (fp32 scores,
  *              statistics and sums; q, dequantised values and probabilities enter the tensor cores with
  *              11 significant bits, over a power of two per row so that bf16's range is kept); a row
- *              that sees no key gives zeros. Magnitudes below 2^118.
+ *              that sees no key gives zeros. Magnitudes below 2^118. A row whose query is not finite, or
+ *              that sees a key or value row which is not, gives NaN; other rows do not feel it.
  *   workspace  at least dflash2_kv4_attention_workspace_bytes(...) bytes, 256-byte aligned (NULL
  *              when that is 0): partial results of contexts that several CTAs share. Needs no
  *              initialisation. Results do not depend on timing: the same call gives the same bits.

@@ -141,3 +141,45 @@ def test_a_key_that_takes_nearly_everything(torch, gap, sink):
     assert d.dflash2_poll_error() == 0
     want, sd = S.attention(q[0], S.kv4_values(k), S.kv4_values(v), np.ones((G, n), bool), 0.125)
     _check_rows(_host(out)[0], want, sd, np.abs(want).max(-1), f"gap {gap}")
+
+
+def _sizes_case(torch, d, rng, n, G, R, D, page, causal=False, window=0):
+    k, v = _rows(rng, n, 1, D), _rows(rng, n, 1, D)
+    kn, vn, q = _rows(rng, 1, G, 1, D), _rows(rng, 1, G, 1, D), _rows(rng, 1, G, R, D)
+    return k, v, kn, vn, q, S.seen(G, n, G, causal, window)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("what", ["own key", "own value", "cached"])
+@pytest.mark.parametrize("n,G,R", [(300, 4, 2), (5000, 16, 5), (40, 1, 1)])
+def test_keys_and_values_that_are_not_finite(torch, D, bad, what, n, G, R):
+    """They give NaN to the rows that see them, and nothing to the others (hidden by causal order, or by the window)."""
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(n + D)
+    window = 30 if what == "cached" else 0
+    causal = True
+    k, v, kn, vn, q, see = _sizes_case(torch, d, rng, n, G, R, D, 16, causal, window)
+    cache, table, ctx = _fill(torch, d, k, v, 16)
+    if what == "cached":  # (its parameters, in one granule, of the first key that row 0's window holds)
+        at = n - window + 1
+        par = cache[at // 16, 0, :, at % 16 // 16, 16 * D // 2:].reshape(2, 16, -1)
+        par[:, at % 16] = torch.tensor([0xC0, 0x7F] if np.isnan(bad) else [0x80, 0x7F], dtype=torch.uint8).repeat(
+            D // 32).cuda()
+        cache[at // 16, 0, :, 0, 16 * D // 2:] = par.reshape(2, -1)
+        sees = see[:, at]
+    else:
+        (kn if what == "own key" else vn)[0, G // 2, 0, 7] = bad
+        if what == "own key":
+            q[..., 7] = np.abs(q[..., 7]) + 0.5  # (an infinite score above, not below)
+        sees = see[:, n + G // 2]
+    out = _host(d.dflash2_kv4_attention(_dev(torch, q), cache, table, ctx, 16, D ** -0.5, k_new=_dev(torch, kn),
+                                        v_new=_dev(torch, vn), causal=causal, window=window))[0]
+    assert d.dflash2_poll_error() == 0
+    assert sees.any() and np.isnan(out[sees]).all()
+    see = see & ~sees[:, None]
+    fine = lambda x: np.where(np.isfinite(x), x, 0.0)
+    want, sd = S.attention(q[0], np.concatenate([S.kv4_values(k), fine(kn[0])]),
+                           np.concatenate([S.kv4_values(v), fine(vn[0])]), see, D ** -0.5)
+    if not sees.all():
+        _check(out[~sees], want[~sees], sd[~sees], "rows that do not see it")
