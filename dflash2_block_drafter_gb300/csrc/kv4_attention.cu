@@ -13,17 +13,17 @@
 //   O^T [D channels x N rows] += V tile [keys][D]^T . P^T [keys][rows]   (both MN-major: V as it lies)
 // A softmax thread holds one key's scores of all (half of the) rows. It needs no reduction over keys:
 // the rows' reference (the number subtracted before the exponential) is only raised when some number
-// passes it by 2^8, which all threads agree on by one barrier a tile; then, rarely and once a tile, the rows' maxima are
-// taken, and O and the sums rescaled. The sums stay per thread until the end.
+// passes it by 2^8, which all threads agree on by one barrier a tile; then, rarely and once a tile, the
+// rows' maxima are taken, and O and the sums rescaled. The sums stay per thread until the end.
 //
 // Precision: operands are fp16 (11 significant bits; with bf16 the keys', the values' and the
 // probabilities' roundings add up to twice the rounding of the bf16 result). fp16's range does not hold
 // every bf16 value, so each key row and each value row is divided by a power of two that brings its
-// largest value to [1, 2), and Q by one for all rows. The keys' factor multiplies the thread's scores, and the
-// values' is added to them as its logarithm (one FMA): the operand P holds probabilities times values'
-// factors over the row's own largest such product, so that a value row far larger than the rest counts in
-// the rows that give it weight and is not felt by those that do not, to which a mask may hide it. The sums
-// take the factor off again, in fp32.
+// largest value to [1, 2), and Q by one for all rows (one a row where rows differ by more than 2^14). The
+// keys' factor multiplies the thread's scores, and the values' is added to them as its logarithm (one FMA):
+// the operand P holds probabilities times values' factors over the row's own largest such product, so that
+// a value row far larger than the rest counts in the rows that give it weight and is not felt by those that
+// do not, to which a mask may hide it. The sums take the factor off again, in fp32.
 //
 // Warps: 8 softmax (two per 32 TMEM lanes, half of the rows each), 8 dequant (four for K, four for V, 32
 // keys of a tile each: codes -> fp16 operand tiles in shared memory, 128-byte swizzle), 2 MMA (one thread
@@ -70,8 +70,9 @@ constexpr float kBLift = 7.f;               // a row's largest probability is 2^
 constexpr float kBSlack = 15.f;             // grow to 2^15 (fp16 holds 2^15, and steps of 2^-24)
 constexpr float kBSumUnit = 0x1p-12f;       // of the sums: 2^31 keys of the smallest values' factor, 2^-93, stay finite
 constexpr float kBUnseen = 3e38f;           // minus the reference of a row that has seen no key: any score passes it
-constexpr uint32_t kBPow2Low = 9u << 23;    // 2^-118: powers of two of keys and queries go no lower
-constexpr uint32_t kBPow2LowV = 27u << 23;  // 2^-100: nor values'
+constexpr uint32_t kBPow2Low = 9u << 23;     // 2^-118: powers of two of keys go no lower
+constexpr uint32_t kBPow2LowQV = 27u << 23;  // 2^-100: nor those of queries and values
+constexpr float kBLiftQ = 16384.f;           // a query row's largest value is in [2^14, 2^15)
 constexpr float kBPadding = -1e30f;         // of a row that does not exist: no score passes it, and it counts nothing
 
 template <int D, int NK>                    // N = 16 NK rows
@@ -80,10 +81,10 @@ struct BlockCfg {
   // the change from one item to the next, in tiles (measured: 15 of 3.1 thousand cycles with 80 rows, 5 of
   // 2.0 with 16)
   static constexpr int kSetup = NK <= 2 ? 3 : NK;
-  // registers a thread: 640 x 96 at launch, then shared out. With 80 rows 136 / 64 takes 130 us for 64 blocks
-  // over 256 .. 4096 keys where 120 / 80 takes 144 (152 / 56: 132); with 16 rows, whose softmax threads need
-  // few, 120 / 80 and 136 / 64 are alike and 80 / 104 is slower.
-  static constexpr int kSoftRegs = NK >= 4 ? 136 : 120, kOtherRegs = NK >= 4 ? 64 : 80;
+  // registers a thread: 640 x 96 at launch, then shared out. With 80 rows 144 / 64 takes 128 to 130 us for 64
+  // blocks over 256 .. 4096 keys where 120 / 80 takes 147, 136 / 64 133 and 152 / 56 132; with 16 rows, whose softmax
+  // threads need few, 120 / 80 takes 111 us for 64 tokens over 1 .. 8192 keys and 152 / 56 128.
+  static constexpr int kSoftRegs = NK >= 4 ? 144 : 120, kOtherRegs = NK >= 4 ? 64 : 80;
   static_assert(kBSoft * kSoftRegs + (kBThreads - kBSoft) * kOtherRegs <= kBThreads * 96, "registers");
   static constexpr int kHalves = D / 64;                     // 64-channel halves of a K or V tile
   static constexpr int kTileBytes = kHalves * kBTile * 128;  // fp16 [half][key][64]
@@ -96,8 +97,8 @@ struct BlockCfg {
   static constexpr int kRawStages = NK == 5 ? 2 : 3;
   static constexpr int kOffRaw = kOffQ + kQBytes;            // [side][stage]
   static constexpr int kOffInfo = kOffRaw + 2 * kRawStages * kRaw;           // float2 [4][128]: key factor, value factor
-  static constexpr int kOffRow = kOffInfo + 4 * kBTile * 8;  // per row: t, lo, hi, factor, offset
-  static constexpr int kOffSum = kOffRow + 5 * N * 4;        // float [4][N]
+  static constexpr int kOffRow = kOffInfo + 4 * kBTile * 8;  // per row: t, lo, hi, factor, offset, query factor
+  static constexpr int kOffSum = kOffRow + 6 * N * 4;        // float [4][N]
   static constexpr int kOffBar = (kOffSum + 4 * N * 4 + 15) / 16 * 16;
   static constexpr int kSmem = 1024 + kOffBar + 384;
   static constexpr uint32_t kTmemCols = 3 * N <= 64 ? 64 : (3 * N <= 128 ? 128 : (3 * N <= 256 ? 256 : 512));
@@ -623,6 +624,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
   int* row_hi = row_lo + N;
   float* row_f = reinterpret_cast<float*>(row_hi + N);               // what the row's sum and O shrink by; at the end, O's factor
   int* row_off = reinterpret_cast<int*>(row_f + N);                  // where the row starts in the sequence's out
+  float* row_q = reinterpret_cast<float*>(row_off + N);              // what the query row's scores are multiplied by
   float* row_red = reinterpret_cast<float*>(smem + C::kOffSum);      // [4][N] the TMEM quarters' maxima or sums
   // barriers, as shared addresses
   const uint32_t bars = smem_u32(smem + C::kOffBar);
@@ -632,7 +634,9 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 216);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* qmax = tmem_slot + 2;
-  uint32_t* came_s = tmem_slot + 3;  // [side][3]: the granules that came
+  uint32_t* qmin = tmem_slot + 3;
+  volatile int* mixed = reinterpret_cast<volatile int*>(tmem_slot + 4);
+  uint32_t* came_s = tmem_slot + 5;  // [side][3]: the granules that came
   const uint32_t join_full = bars + 264;  // [3]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -672,7 +676,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     // ------------------------------------------------------------------ dequant
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     const int side = (warp - kBSoftWarps) >> 2, dw = warp & 3;  // K or V; keys 32 dw .. of each tile
-    const uint32_t low = side == 0 ? kBPow2Low : kBPow2LowV;
+    const uint32_t low = side == 0 ? kBPow2Low : kBPow2LowQV;
     const int ch = lane % NCH;
     constexpr int kStep = 32 / NCH;                        // step i converts keys sub + i kStep of the warp's 32
     const int sub = lane / NCH;
@@ -915,54 +919,144 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
       const int r8 = r0 / 8 + c;
       to[c] = smem_u32(smem + C::kOffP) + key_in * 128 + (r8 >> 3) * (kBTile * 128) + (((r8 & 7) ^ (key_in & 7)) << 4);
     }
-    // Q of a piece: its rows as fp16 over their common power of two (returned), channels in the codes' order
+    // Q of a piece: its rows as fp16, channels in the codes' order, over a power of two common to all (returned),
+    // with which rows 2^14 smaller than the largest still have 11 significant bits. Where some channels lie
+    // further below it, or are not finite, each row goes over its own power (`mixed`), and row_q multiplies its
+    // scores: where references are raised, so that the piece's every tile goes there. A row that is not finite
+    // becomes NaN, and does not count for the others.
     auto load_q = [&](const Walk& w) {
       const int head = w.head, row_first = w.rt * a.tile_rows;
       const int nrows = min(a.tile_rows, a.rows - row_first);
       constexpr int kQItems = (N * (D / 8) + kBSoft - 1) / kBSoft;
-      uint4 qv[kQItems];
-      uint32_t qm = 0;
-#pragma unroll
-      for (int i = 0; i < kQItems; ++i) {
-        const int x = threadIdx.x + i * kBSoft, r = x / (D / 8), c = x % (D / 8);
-        qv[i] = make_uint4(0u, 0u, 0u, 0u);
+      auto fetch = [&](int r, int c) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
         if (r < nrows) {
           const int rr = row_first + r, t = row_token(a, rr);
-          qv[i] = __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(w.b) * a.G + t) * a.q_stride +
-                                                       (head * a.R + rr - t * a.R) * D + 8 * c));
+          v = __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(w.b) * a.G + t) * a.q_stride +
+                                                   (head * a.R + rr - t * a.R) * D + 8 * c));
         }
+        return v;
+      };
+      auto store = [&](int r, int c, const uint4& v) {
+        const int pc = piece_of_word<D>(c);
+        *reinterpret_cast<uint4*>(smem + C::kOffQ + (pc >> 3) * (N * 128) + r * 128 + (((pc & 7) ^ (r & 7)) << 4)) = v;
+      };
+      uint4 qv[kQItems];
+#pragma unroll
+      for (int i = 0; i < kQItems; ++i) {
+        const int x = threadIdx.x + i * kBSoft;
+        qv[i] = fetch(x / (D / 8), x % (D / 8));
       }
-      if (threadIdx.x == 0) *qmax = 0u;
+      if (threadIdx.x == 0) {
+        *qmax = 0u;
+        *qmin = kBInfinity;
+      }
       bar_soft();
+      uint32_t most = 0, least = kBInfinity;
 #pragma unroll
       for (int i = 0; i < kQItems; ++i) {
         const uint32_t m = max_abs8(qv[i]);
-        qm = max(qm, m <= kBInfinity ? m : 0u);
+        most = max(most, m);
+        least = min(least, m - 1u);  // (zeros do not count)
       }
-      const uint32_t qk = __reduce_max_sync(0xffffffffu, qm);
-      if (lane == 0) atomicMax(qmax, qk);
+      most = __reduce_max_sync(0xffffffffu, most);
+      least = __reduce_min_sync(0xffffffffu, least);
+      if (lane == 0) {
+        atomicMax(qmax, most);
+        atomicMin(qmin, least);
+      }
+      if (threadIdx.x < N) row_q[threadIdx.x] = 1.f;
       bar_soft();
-      const float qf = pow2_of(__uint_as_float(*qmax));
+      most = *qmax;
+      const float common = pow2_of(__uint_as_float(most), kBPow2LowQV);
+      const bool mix = most >= kBInfinity || pow2_of(__uint_as_float(*qmin), kBPow2LowQV) * kBLiftQ < common;
+      if (threadIdx.x == 0) *mixed = mix ? 1 : 0;
+      if (!mix) {
 #pragma unroll
-      for (int i = 0; i < kQItems; ++i) {
-        const int x = threadIdx.x + i * kBSoft, r = x / (D / 8), c = x % (D / 8);
-        const int pc = piece_of_word<D>(c);
-        if (r < N)
-          *reinterpret_cast<uint4*>(smem + C::kOffQ + (pc >> 3) * (N * 128) + r * 128 + (((pc & 7) ^ (r & 7)) << 4)) =
-              convert_word(qv[i], pow2_inverse(qf));
+        for (int i = 0; i < kQItems; ++i) {
+          const int x = threadIdx.x + i * kBSoft;
+          if (x / (D / 8) < N) store(x / (D / 8), x % (D / 8), convert_word(qv[i], pow2_inverse(common) * kBLiftQ));
+        }
+      } else {
+#pragma unroll 1
+        for (int x = threadIdx.x; x < (N * (D / 8) + 31) / 32 * 32; x += kBSoft) {  // whole warps
+          const int r = x / (D / 8), c = x % (D / 8);
+          const uint4 v = fetch(r, c);
+          uint32_t m = max_abs8(v);
+#pragma unroll 1
+          for (int k = 1; k < D / 8; k <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
+          const float own = pow2_of(__uint_as_float(m), kBPow2LowQV);
+          if (r < N) {
+            store(r, c, m < kBInfinity ? convert_word(v, pow2_inverse(own) * kBLiftQ)
+                                       : make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu));
+            if (c == 0) row_q[r] = own * (1.f / kBLiftQ);
+          }
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(qfull);
-      return qf;
+      return mix ? 1.f : common * (1.f / kBLiftQ);
     };
     uint32_t it = 0;
     Walk w(a, range);
     bool gave = false;  // the last piece goes on in the next range
     BlockJoin join{w.start, w.b, w.head, w.rt, w.seq.tiles, w.valid() && w.j0 > 0 && w.j1 == w.seq.tiles, false};
-    float qf = 1.f;
-    for (bool start = true; w.valid(); start = false) {
-      if (start) qf = load_q(w);
+    Walk next = w;
+    for (bool first = true;; first = false) {
+      float qf = 1.f;
+      if (next.valid()) qf = load_q(next);  // (every S of the piece before is done): its scores start meanwhile
+      if (!first) {
+        // ---- the result of the item before (or of its part)
+        const int row_first = w.rt * a.tile_rows, nrows = min(a.tile_rows, a.rows - row_first);
+        const bool complete = w.j0 == 0 && w.j1 == w.seq.tiles;
+        bar_soft();
+        const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (w.j0 > 0 ? 0 : 1)) * N;
+        if (threadIdx.x < N) {
+          const int r = threadIdx.x;
+          const float sum = row_red[r] + row_red[N + r] + row_red[2 * N + r] + row_red[3 * N + r];
+          // (a row that saw something that is not finite has a sum, and an O, of NaN)
+          row_f[r] = sum == 0.f ? 0.f : (complete ? kBSumUnit / sum : 1.f);
+          if (!complete && r < nrows) a.part_ml[slot + r] = make_float2(row_t[r] != kBUnseen ? -row_t[r] : -INFINITY, sum);
+        }
+        bar_soft();
+        // the thread's channel: operand position p of each eight holds channel p / 2 + 4 (p % 2) of its word
+        const int ch = word_of_piece<D>(key_in >> 3) * 8 + ((key_in & 7) >> 1) + 4 * (key_in & 1);
+        wait_on(odone, (it - 1) & 1u, abort_flag, a.err);
+        tc_fence_after();
+        __syncwarp();
+        __nv_bfloat16* out = a.out + static_cast<int64_t>(w.b) * a.G * a.Hq * D + ch;
+        float* part = a.part_o + (slot + r0) * D + ch;
+        float o[NH];
+#pragma unroll
+        for (int c = 0; c < NH; c += 8) tmem_ld8(tl + static_cast<uint32_t>(2 * N + c), o + c);
+        tmem_ld_wait();
+        if (key_in < D) {
+          const int n = nrows - r0;
+#pragma unroll
+          for (int r = 0; r < NH; r += 4) {
+            const float4 g4 = *reinterpret_cast<const float4*>(row_f + r0 + r);
+            const int4 o4 = *reinterpret_cast<const int4*>(row_off + r0 + r);
+            const float g[4] = {g4.x, g4.y, g4.z, g4.w};
+            const int off[4] = {o4.x, o4.y, o4.z, o4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float v = g[i] != 0.f ? o[r + i] * g[i] : 0.f;  // (O of a row that saw nothing is not looked at)
+              if (r + i < n) {
+                if (complete)
+                  out[off[i]] = __float2bfloat16_rn(v);
+                else
+                  part[(r + i) * D] = v;
+              }
+            }
+          }
+        }
+        __syncwarp();
+        tc_fence_before();
+        bar_soft();  // the rows' data are read before the next piece sets them
+      }
+      if (!next.valid()) break;
+      w = next;
       const int head = w.head, row_first = w.rt * a.tile_rows;
       const int nrows = min(a.tile_rows, a.rows - row_first);
       if (threadIdx.x < N) {
@@ -1038,7 +1132,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
 #pragma unroll
         for (int r = 0; r < NH; ++r) top[r & 3] = fmaxf(top[r & 3], x[r]);
         top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        if (bar_or(top[0] > kBSlack)) {
+        if (bar_or(top[0] > kBSlack || *mixed != 0)) {
           // ---- raise the references to the rows' maxima over the tile. Once a tile: a row's weights are then
           // numbers less at least their maximum, and a lift, so that none passes the slack. (The maximum is
           // taken over the same rounded numbers: were the reference subtracted inside the FMA, from 2^27
@@ -1048,8 +1142,11 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
           tmem_ld_wait();
 #pragma unroll
           for (int r = 0; r < NH; r += 4) {
+            const float4 g = *reinterpret_cast<const float4*>(row_q + r0 + r);
+            const float2 g0 = __fmul2_rn(make_float2(x[r], x[r + 1]), make_float2(g.x, g.y));
+            const float2 g1 = __fmul2_rn(make_float2(x[r + 2], x[r + 3]), make_float2(g.z, g.w));
             const int4 lo = *reinterpret_cast<const int4*>(row_lo + r0 + r), hi = *reinterpret_cast<const int4*>(row_hi + r0 + r);
-            const float2 y0 = weigh(x[r], x[r + 1]), y1 = weigh(x[r + 2], x[r + 3]);
+            const float2 y0 = weigh(g0.x, g0.y), y1 = weigh(g1.x, g1.y);
             x[r] = there && key >= lo.x && key < hi.x ? y0.x : -INFINITY;
             x[r + 1] = there && key >= lo.y && key < hi.y ? y0.y : -INFINITY;
             x[r + 2] = there && key >= lo.z && key < hi.z ? y1.x : -INFINITY;
@@ -1130,63 +1227,15 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         if (lane == 0) mbar_arrive(pfull);
       }
 
-      // ---- the item's (or its part's) result
 #pragma unroll
       for (int c = 0; c < NH; c += 8) {
         const float v = warp_reduce8(l + c, lane, [](float p, float q) { return p + q; });
         if ((lane & 3) == 0) row_red[quad * N + r0 + c + warp_reduce8_row(lane)] = v;
       }
-      const bool complete = w.j0 == 0 && w.j1 == w.seq.tiles;
       gave = w.j1 < w.seq.tiles;
       if (gave && w.j0 > 0)  // (the range lies inside the item)
         join.leads = BlockParts(range.line, w.start, C::kSetup, w.seq.tiles).leads(static_cast<int>(blockIdx.x));
-      Walk next = w;
       next.next(a);
-      if (next.valid()) qf = load_q(next);  // (every S of this piece is done): its scores start meanwhile
-      bar_soft();
-      const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (w.j0 > 0 ? 0 : 1)) * N;
-      if (threadIdx.x < N) {
-        const int r = threadIdx.x;
-        const float sum = row_red[r] + row_red[N + r] + row_red[2 * N + r] + row_red[3 * N + r];
-        // (a row that saw something that is not finite has a sum, and an O, of NaN)
-        row_f[r] = sum == 0.f ? 0.f : (complete ? kBSumUnit / sum : 1.f);
-        if (!complete && r < nrows) a.part_ml[slot + r] = make_float2(row_t[r] != kBUnseen ? -row_t[r] : -INFINITY, sum);
-      }
-      bar_soft();
-      // the thread's channel: operand position p of each eight holds channel p / 2 + 4 (p % 2) of its word
-      const int ch = word_of_piece<D>(key_in >> 3) * 8 + ((key_in & 7) >> 1) + 4 * (key_in & 1);
-      wait_on(odone, (it - 1) & 1u, abort_flag, a.err);
-      tc_fence_after();
-      __syncwarp();
-      __nv_bfloat16* out = a.out + static_cast<int64_t>(w.b) * a.G * a.Hq * D + ch;
-      float* part = a.part_o + (slot + r0) * D + ch;
-#pragma unroll
-      for (int c = 0; c < NH; c += 8) tmem_ld8(tl + static_cast<uint32_t>(2 * N + c), x + c);
-      tmem_ld_wait();
-      if (key_in < D) {
-        const int n = nrows - r0;
-#pragma unroll
-        for (int r = 0; r < NH; r += 4) {
-          const float4 g4 = *reinterpret_cast<const float4*>(row_f + r0 + r);
-          const int4 o4 = *reinterpret_cast<const int4*>(row_off + r0 + r);
-          const float g[4] = {g4.x, g4.y, g4.z, g4.w};
-          const int off[4] = {o4.x, o4.y, o4.z, o4.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float v = g[i] != 0.f ? x[r + i] * g[i] : 0.f;  // (O of a row that saw nothing is not looked at)
-            if (r + i < n) {
-              if (complete)
-                out[off[i]] = __float2bfloat16_rn(v);
-              else
-                part[(r + i) * D] = v;
-            }
-          }
-        }
-      }
-      __syncwarp();
-      tc_fence_before();
-      bar_soft();  // the rows' data are read before the next piece sets them
-      w = next;
     }
     auto give = [&]() {  // this range's part is complete
       __threadfence();

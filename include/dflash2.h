@@ -376,8 +376,9 @@ DFLASH2_API int dflash2_proj_conv_out(const void* a, int M, int K, const void* w
  *   the last cached ones). causal = 1: it sees keys up to its position; 0: every key (the draft
  *   block is bidirectional). window > 0: only keys after its position - window (the largest int: all).
  *   out        [B, G, Hq, D] dense: softmax(scale q k^T) v over the keys a row sees (fp32 scores,
- *              statistics and sums; q, dequantised values and probabilities enter the tensor cores with
- *              11 significant bits, over a power of two per row so that bf16's range is kept); a row
+ *              statistics and sums; q, keys, values and probabilities enter the tensor cores in fp16, 11
+ *              significant bits, over powers of two that keep bf16's range: one per key row, per value
+ *              row, and of each query row's own probabilities); a row
  *              that sees no key gives zeros. Magnitudes below 2^118. A row whose query is not finite, or
  *              that sees a key or value row which is not, gives NaN; other rows do not feel it.
  *   workspace  at least dflash2_kv4_attention_workspace_bytes(...) bytes, 256-byte aligned (NULL

@@ -183,3 +183,54 @@ def test_keys_and_values_that_are_not_finite(torch, D, bad, what, n, G, R):
                            np.concatenate([S.kv4_values(v), fine(vn[0])]), see, D ** -0.5)
     if not sees.all():
         _check(out[~sees], want[~sees], sd[~sees], "rows that do not see it")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 1e30, 2.0 ** -100])
+def test_one_query_row_unlike_the_others(torch, D, bad):
+    """A query row that is not finite gives NaN, one of another size what it should, and neither touches the rest."""
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(5)
+    for n, G, R in ((300, 3, 2), (4000, 16, 5), (0, 2, 1)):
+        k, v, kn, vn, q, see = _sizes_case(torch, d, rng, n, G, R, D, 16)
+        at = (0, G - 1, R - 1)
+        q[at] = S.bf16(q[at] * bad) if np.isfinite(bad) else q[at]
+        if not np.isfinite(bad):
+            q[at][1] = bad
+        cache, table, ctx = _fill(torch, d, k if n else _rows(rng, 1, 1, D), v if n else _rows(rng, 1, 1, D), 16)
+        if n == 0:
+            ctx.zero_()
+        out = _host(d.dflash2_kv4_attention(_dev(torch, q), cache, table, ctx, 16, D ** -0.5, k_new=_dev(torch, kn),
+                                            v_new=_dev(torch, vn)))[0]
+        assert d.dflash2_poll_error() == 0
+        K, V = np.concatenate([S.kv4_values(k), kn[0]]), np.concatenate([S.kv4_values(v), vn[0]])
+        mask = np.ones((G, R), bool)
+        if abs(bad) != 2.0 ** -100:
+            mask[at[1:]] = False
+            got = out[at[1:]]
+            assert np.isfinite(got).all() if np.isfinite(bad) else np.isnan(got).all()
+        q[at] = q[at] if np.isfinite(bad) else 0.0
+        want, sd = S.attention(q[0], K, V, see, D ** -0.5)
+        _check(out[mask], want[mask], sd[mask], f"rows beside {bad}")
+
+
+@pytest.mark.parametrize("n", [0, 100, 5000])
+def test_query_rows_of_every_size(torch, n):
+    """Rows from 2^-30 to 2^30 over keys of 2^28: the small rows' scores are moderate, the large rows take one key."""
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(n)
+    G, R, D = 8, 2, 64
+    k, v, kn, vn, q, see = _sizes_case(torch, d, rng, max(n, 1), G, R, D, 16)
+    size = 2.0 ** np.array([-30, -28, -26, -40, 30, -27, -29, 10])
+    q *= size[None, :, None, None]
+    k, kn = k * 2.0 ** 28, kn * 2.0 ** 28
+    cache, table, ctx = _fill(torch, d, k, v, 16)
+    ctx.fill_(n)
+    out = _host(d.dflash2_kv4_attention(_dev(torch, q), cache, table, ctx, 16, D ** -0.5, k_new=_dev(torch, kn),
+                                        v_new=_dev(torch, vn)))[0]
+    assert d.dflash2_poll_error() == 0
+    K, V = np.concatenate([S.kv4_values(k)[:n], kn[0]]), np.concatenate([S.kv4_values(v)[:n], vn[0]])
+    want, sd = S.attention(q[0], K, V, np.ones((G, n + G), bool), D ** -0.5)
+    small = size < 2.0 ** -20
+    _check(out[small], want[small], sd[small], "small rows")
+    assert np.isfinite(out).all()
