@@ -19,11 +19,13 @@
 // Precision: operands are fp16 (11 significant bits; with bf16 the keys', the values' and the
 // probabilities' roundings add up to twice the rounding of the bf16 result). fp16's range does not hold
 // every bf16 value, so each key row and each value row is divided by a power of two that brings its
-// largest value to [1, 2), and Q by one for all rows (one a row where rows differ by more than 2^14). The
-// keys' factor multiplies the thread's scores, and the values' is added to them as its logarithm (one FMA):
-// the operand P holds probabilities times values' factors over the row's own largest such product, so that
-// a value row far larger than the rest counts in the rows that give it weight and is not felt by those that
-// do not, to which a mask may hide it. The sums take the factor off again, in fp32.
+// largest value to [1, 2), and Q by one for all rows (one a row where rows differ by more than 2^14). Cached
+// rows go to 2^-7 of that, for scale 2^24 to fit (dequant_word): their channels more than 2^7 below the row's
+// largest have steps of 2^-17 of it (6 bits are left of a group 2^12 below the row's other). The keys'
+// factor multiplies the thread's scores, and the values' is added to them as its logarithm (one FMA): the
+// operand P holds probabilities times values' factors over the row's own largest such product, so that a
+// value row far larger than the rest counts in the rows that give it weight and is not felt by those that do
+// not, to which a mask may hide it. The sums take the factor off again, in fp32.
 //
 // Warps: 8 softmax (two per 32 TMEM lanes, half of the rows each), 8 dequant (four for K, four for V, 32
 // keys of a tile each: codes -> fp16 operand tiles in shared memory, 128-byte swizzle), 2 MMA (one thread
@@ -782,10 +784,10 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
               for (int x = 1; x < NCH; x <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
               const float p2 = pow2_of(__uint_as_float(m), low);
               const bool odd = side == 1 && m >= kBInfinity;  // (as for cached rows)
-              f = odd ? __uint_as_float(0x7fffffffu) : p2 * 128.f;
+              f = odd ? __uint_as_float(0x7fffffffu) : p2;
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                u[k] = odd ? make_uint4(0u, 0u, 0u, 0u) : convert_word(u[k], pow2_inverse(p2) * 0.0078125f);
+                u[k] = odd ? make_uint4(0u, 0u, 0u, 0u) : convert_word(u[k], pow2_inverse(p2));
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) st_shared_v4(to[k] + tile + i * kStep * 128, u[k]);

@@ -378,8 +378,9 @@ DFLASH2_API int dflash2_proj_conv_out(const void* a, int M, int K, const void* w
  *   out        [B, G, Hq, D] dense: softmax(scale q k^T) v over the keys a row sees (fp32 scores,
  *              statistics and sums; q, keys, values and probabilities enter the tensor cores in fp16, 11
  *              significant bits, over powers of two that keep bf16's range: one per key row, per value
- *              row, and of each query row's own probabilities); a row
- *              that sees no key gives zeros. Magnitudes below 2^118. A row whose query is not finite, or
+ *              row, and of each query row's own probabilities; channels of a cached row more than 2^7
+ *              below its largest have steps of 2^-17 of that); a row that sees no key gives zeros.
+ *              Magnitudes below 2^118. A row whose query is not finite, or
  *              that sees a key or value row which is not, gives NaN; other rows do not feel it.
  *   workspace  at least dflash2_kv4_attention_workspace_bytes(...) bytes, 256-byte aligned (NULL
  *              when that is 0): partial results of contexts that several CTAs share. Needs no

@@ -234,3 +234,29 @@ def test_query_rows_of_every_size(torch, n):
     small = size < 2.0 ** -20
     _check(out[small], want[small], sd[small], "small rows")
     assert np.isfinite(out).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_own_rows_with_strong_channels(torch, D):
+    """Own rows whose channels differ by 2^8 to 2^12 keep the small ones to 11 significant bits, as the bound's."""
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(D + 1)
+    G, R, page = 16, 2, 16
+    for e in (8, 12):
+        kn, vn, q = _rows(rng, 1, G, 1, D), _rows(rng, 1, G, 1, D), _rows(rng, 1, G, R, D)
+        vn[..., 3] *= 2.0 ** e
+        kn[..., 5] *= 2.0 ** e
+        q[..., 5] = 0.0
+        cache, table, _ = _fill(torch, d, _rows(rng, 1, 1, D), _rows(rng, 1, 1, D), page)
+        ctx = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = d.dflash2_kv4_attention(_dev(torch, q), cache, table, ctx, page, D ** -0.5, k_new=_dev(torch, kn),
+                                      v_new=_dev(torch, vn))
+        assert d.dflash2_poll_error() == 0
+        want, _ = S.attention(q[0], kn[0], vn[0], np.ones((G, G), bool), D ** -0.5)
+        # the channels apart from the strong one: bf16's half step of the result; 2^-11 of the weighted values for each
+        # of the probability's, the value's and (through a score below 2 in size) the key's rounding
+        big = np.abs(vn[0, :, 0]).copy()
+        big[:, 3] = 0
+        keep = np.arange(D) != 3
+        err = np.abs(_host(out)[0] - want)[..., keep]
+        assert np.all(err <= 2.0 ** -8 * np.abs(want[..., keep]) + 4 * 2.0 ** -11 * big.max()), e
