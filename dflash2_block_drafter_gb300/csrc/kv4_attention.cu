@@ -745,7 +745,8 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
             const uint32_t w1 = L::kGroups == 2 ? __shfl_sync(0xffffffffu, po[1], sub + i * kStep) : w0;
             sb_bits[i] = ch >= 2 ? w1 : w0;
           }
-          if (cached) {  // read out (the shuffles joined the lanes)
+          if (cached) {  // read out: every lane's loads come before the arrival
+            __syncwarp();
             if (lane == 0) mbar_arrive(rempty + 8 * stage);
             if (++stage == C::kRawStages) {
               stage = 0;
