@@ -558,10 +558,14 @@ def _kv4_cache_shape(cache, head_dim, page_size):
     return cache.shape[0], cache.shape[1]
 
 
-def _kv4_rows(t, name, rows, heads, head_dim):
-    """(pointer, row stride) of a [..., heads, head_dim] bf16 tensor whose leading dimensions walk
-    `rows` equally spaced rows; the last two are dense."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16:
+def _kv4_rows(t, name, rows, heads, head_dim, lead=None):
+    """(pointer, row stride) of a [rows, heads, head_dim] or [B, G, heads, head_dim] (`lead`: B, G) bf16 tensor
+    whose leading dimensions walk `rows` equally spaced rows; the last two are dense."""
+    if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4) or (t.dim() == 4 and lead and tuple(t.shape[:2]) != lead):
+        raise ValueError(f"{name} must be a tensor of {rows} rows of [{heads}, {head_dim}]"
+                         f"{f' or [{lead[0]}, {lead[1]}] of them' if lead else ''}, got "
+                         f"{tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__}")
+    if not t.is_cuda or t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be a bf16 CUDA tensor")
     shape, stride = t.shape, t.stride()
     if shape[-2:] != (heads, head_dim) or t.numel() != rows * heads * head_dim:
@@ -634,8 +638,8 @@ def dflash2_kv4_attention(q, cache, page_table, ctx_len, page_size, scale, k_new
     kp = vp = None
     ns = 0
     if k_new is not None:
-        kp, ns = _kv4_rows(k_new, "k_new", B * G, Hkv, D)
-        vp, vs = _kv4_rows(v_new, "v_new", B * G, Hkv, D)
+        kp, ns = _kv4_rows(k_new, "k_new", B * G, Hkv, D, (B, G))
+        vp, vs = _kv4_rows(v_new, "v_new", B * G, Hkv, D, (B, G))
         if vs != ns:
             raise ValueError(f"k_new and v_new must have the same row stride, got {ns} and {vs}")
     if out is None:
