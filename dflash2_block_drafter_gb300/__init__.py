@@ -651,7 +651,8 @@ def dflash2_kv4_attention(q, cache, page_table, ctx_len, page_size, scale, k_new
     if workspace is None:
         need = lib.dflash2_kv4_attention_workspace_bytes(B, G, Hq, Hkv, D, page_size, width)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-    wp, wn = (None, 0) if workspace is None else (_dev(workspace, "workspace"), workspace.numel())
+    wp, wn = (None, 0) if workspace is None else (_dev(workspace, "workspace"),
+                                                     workspace.numel() * workspace.element_size())
     _check(lib.dflash2_kv4_attention(
         qp, qs, _dev(cache, "cache", torch.uint8), _dev(page_table, "page_table", torch.int32),
         _dev(ctx_len, "ctx_len", torch.int32), kp, vp, ns, B, G, Hq, Hkv, D, page_size, pages, width, int(bool(causal)),
