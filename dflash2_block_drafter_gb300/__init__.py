@@ -535,6 +535,19 @@ def dflash2_proj_conv_out(a, w, coef1, base, G, group_size, residual=None, w_sca
     return out
 
 
+def _new(shape, dtype, device, stream):
+    """A tensor that a call makes for itself or its caller. On a stream that the caller named it is that stream's: its
+    memory waits for nothing that the current stream still does, and serves nothing else before either is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream).value or 0)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def dflash2_kv4_page_bytes(heads, head_dim, page_size) -> int:
     return library().dflash2_kv4_page_bytes(heads, head_dim, page_size)
 
@@ -606,10 +619,10 @@ def dflash2_kv4_read(cache, slots, head_dim, page_size, k=None, v=None, stream=N
     T = slots.numel()
     n = T * heads * head_dim
     if k is None and v is None:
-        k, v = torch.empty((2, T, heads, head_dim), dtype=torch.bfloat16, device=cache.device).unbind(0)
+        k, v = _new((2, T, heads, head_dim), torch.bfloat16, cache.device, stream).unbind(0)
     else:
-        k = _sized(k, n, "k", (T, heads, head_dim), cache.device)
-        v = _sized(v, n, "v", (T, heads, head_dim), cache.device)
+        k = _sized(k, n, "k", (T, heads, head_dim), cache.device, stream)
+        v = _sized(v, n, "v", (T, heads, head_dim), cache.device, stream)
     _check(library().dflash2_kv4_read(_dev(cache, "cache", torch.uint8), _dev(slots, "slots", torch.int64), T, heads,
                                       head_dim, page_size, pages, BF16, _dev(k, "k", torch.bfloat16),
                                       _dev(v, "v", torch.bfloat16), _stream(stream)))
@@ -643,14 +656,14 @@ def dflash2_kv4_attention(q, cache, page_table, ctx_len, page_size, scale, k_new
         if vs != ns:
             raise ValueError(f"k_new and v_new must have the same row stride, got {ns} and {vs}")
     if out is None:
-        out = torch.empty((B, G, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = _new((B, G, Hq, D), torch.bfloat16, q.device, stream)
     if out.numel() < B * G * Hq * D:
         raise ValueError(f"out holds {out.numel()} elements, fewer than the {B * G * Hq * D} the call writes")
     width = page_table.shape[1]
     lib = library()
     if workspace is None:
         need = lib.dflash2_kv4_attention_workspace_bytes(B, G, Hq, Hkv, D, page_size, width)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        workspace = _new(need, torch.uint8, q.device, stream) if need else None
     wp, wn = (None, 0) if workspace is None else (_dev(workspace, "workspace"),
                                                      workspace.numel() * workspace.element_size())
     _check(lib.dflash2_kv4_attention(
@@ -677,19 +690,19 @@ def _ffn_weights(w_gate, w_up, H):
     return w_gate.shape[0]
 
 
-def _sized(t, n, name, shape, device):
+def _sized(t, n, name, shape, device, stream):
     """The output tensor `name` of n elements: allocated when not given, else checked for size."""
     if t is None:
-        return torch.empty(shape, dtype=torch.bfloat16, device=device)
+        return _new(shape, torch.bfloat16, device, stream)
     if t.numel() < n:
         raise ValueError(f"{name} holds {t.numel()} elements, fewer than the {n} the call writes")
     return t
 
 
-def _ffn_ws(M, H, F, backward, device, workspace):
+def _ffn_ws(M, H, F, backward, device, workspace, stream):
     if workspace is None:
         need = library().dflash2_gated_ffn_workspace_bytes(M, H, F, backward)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        workspace = _new(max(need, 256), torch.uint8, device, stream)
     return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), workspace
 
 
@@ -702,12 +715,12 @@ def dflash2_gated_ffn(x, w_gate, w_up, act="silu", out=None, pre=None, want_pre=
     M, H = x.shape
     code = _act(act)
     F = _ffn_weights(w_gate, w_up, H)
-    out = _sized(out, M * F, "out", (M, F), x.device)
+    out = _sized(out, M * F, "out", (M, F), x.device, stream)
     if want_pre and pre is None:
-        pre = torch.empty((M, F), dtype=torch.int32, device=x.device)
+        pre = _new((M, F), torch.int32, x.device, stream)
     if pre is not None and pre.numel() * pre.element_size() < 4 * M * F:
         raise ValueError(f"pre holds {pre.numel() * pre.element_size()} bytes, fewer than the {4 * M * F} the call writes")
-    wp, wn, _keep = _ffn_ws(M, H, F, 0, x.device, workspace)
+    wp, wn, _keep = _ffn_ws(M, H, F, 0, x.device, workspace, stream)
     bf = torch.bfloat16
     _check(library().dflash2_gated_ffn(_dev(x, "x", bf), M, H, _dev(w_gate, "w_gate", bf), _dev(w_up, "w_up", bf), F,
                                        code, BF16, _dev(out, "out", bf), _dev(pre, "pre", None, True), wp, wn,
@@ -729,10 +742,10 @@ def dflash2_gated_ffn_backward(dh, pre, x, w_gate, w_up, act="silu", want_dx=Tru
                          f"{pre.numel() * pre.element_size()} bytes")
     if (dw_gate is None) != (dw_up is None):
         raise ValueError("dw_gate and dw_up go together")
-    dx = _sized(dx, M * H, "dx", (M, H), x.device) if want_dx else None
-    dw_gate = _sized(dw_gate, F * H, "dw_gate", (F, H), x.device) if want_dw else None
-    dw_up = _sized(dw_up, F * H, "dw_up", (F, H), x.device) if want_dw else None
-    wp, wn, _keep = _ffn_ws(M, H, F, 1, x.device, workspace)
+    dx = _sized(dx, M * H, "dx", (M, H), x.device, stream) if want_dx else None
+    dw_gate = _sized(dw_gate, F * H, "dw_gate", (F, H), x.device, stream) if want_dw else None
+    dw_up = _sized(dw_up, F * H, "dw_up", (F, H), x.device, stream) if want_dw else None
+    wp, wn, _keep = _ffn_ws(M, H, F, 1, x.device, workspace, stream)
     bf = torch.bfloat16
     _check(library().dflash2_gated_ffn_backward(
         _dev(dh, "dh", bf), _dev(pre, "pre"), _dev(x, "x", bf), _dev(w_gate, "w_gate", bf), _dev(w_up, "w_up", bf),
