@@ -553,7 +553,8 @@ static int check_ffn(int M, int H, int F, int act, int dtype) {
   REQUIRE(act == DFLASH2_ACT_SILU || act == DFLASH2_ACT_GELU_TANH, "act=%d is not a dflash2_act", act);
   // tiles of 256 rows by 128 columns (and twice 256 by 256 for the weights' gradients) are counted in int
   const int64_t m = (M + 255LL) / 256, h = (H + 127LL) / 128, f = (F + 127LL) / 128;
-  REQUIRE(m * f <= 0x3fffffff && m * h <= 0x3fffffff && f * h <= 0x3fffffff, "M=%d, H=%d, F=%d are too large", M, H, F);
+  // (and H and F rounded up to 64 columns are ints)
+  REQUIRE(H <= 0x7fffffc0 && F <= 0x7fffffc0 && m * f <= 0x3fffffff && m * h <= 0x3fffffff && f * h <= 0x3fffffff, "M=%d, H=%d, F=%d are too large", M, H, F);
   return DFLASH2_OK;
 }
 

@@ -546,7 +546,7 @@ int launch_ffn_gemm(const FfnMaps& maps, FfnArgs a, void* share_ws, cudaStream_t
   // cut with them where there is one: then a share is a tile and a bit, and a tile has at most three
   // parts. Without one, at most kFMaxParts pairs share a tile. A share has at least kFMinPiece k-blocks.
   const int rest = a.n_tiles % units;
-  a.sk_tiles = a.kblocks * (units - rest) < kFMinGain * units ? 0 : rest;
+  a.sk_tiles = static_cast<long long>(a.kblocks) * (units - rest) < kFMinGain * units ? 0 : rest;
   if (a.sk_tiles > 0 && 3 * rest < units && a.n_tiles > units) a.sk_tiles += units;
   const long long total = static_cast<long long>(a.sk_tiles) * a.kblocks;
   a.sk_units = static_cast<int>(std::max<long long>(
@@ -565,7 +565,7 @@ int launch_ffn_gemm(const FfnMaps& maps, FfnArgs a, void* share_ws, cudaStream_t
   return e == cudaSuccess ? DFLASH2_OK : fail(DFLASH2_ERR_CUDA, "gated FFN launch failed: %s", cudaGetErrorString(e));
 }
 
-int tiles_of(int n, int tile) { return (n + tile - 1) / tile; }
+int tiles_of(int n, int tile) { return static_cast<int>((static_cast<long long>(n) + tile - 1) / tile); }
 
 bool ffn_map(CUtensorMap* m, const void* p, int rows, int cols, int box_rows, int pitch = 0) {
   return make_tmap_sw128(m, p, static_cast<uint64_t>(rows), static_cast<uint64_t>(cols), static_cast<uint32_t>(box_rows),
@@ -598,7 +598,7 @@ size_t gated_ffn_workspace(int M, int H, int F, bool backward, int sms) {
 int launch_gated_ffn(const GatedFfn& r, cudaStream_t st) {
   if (r.M <= kFfnSmallRows) return launch_gated_ffn_small(r, st);
   FfnMaps maps;
-  const int a_rows = std::min(128, (r.M + 7) / 8 * 8);
+  const int a_rows = (std::min(128, r.M) + 7) / 8 * 8;
   const void* x = r.x;
   int pitch = r.H;
   const long long blocks = static_cast<long long>(tiles_of(r.M, kFTile)) * tiles_of(r.F, 128) * tiles_of(r.H, kFK);
@@ -645,7 +645,7 @@ int launch_gated_ffn_backward(const GatedFfn& r, cudaStream_t st) {
   a.tiles_n = tiles_of(r.H, kFTile);
   FfnMaps maps;
   if (r.dx != nullptr) {
-    a.a_rows = std::min(128, (r.M + 7) / 8 * 8);
+    a.a_rows = (std::min(128, r.M) + 7) / 8 * 8;
     if (!ffn_map(&maps.a0, dgu, r.M, r.F, a.a_rows, pitch) || !ffn_map(&maps.a1, dgu + plane, r.M, r.F, a.a_rows, pitch) ||
         !ffn_map(&maps.b0, r.w_gate, r.F, r.H, kFK) || !ffn_map(&maps.b1, r.w_up, r.F, r.H, kFK))
       return fail(DFLASH2_ERR_CUDA, "tensor map encode failed (gated FFN dx)");
