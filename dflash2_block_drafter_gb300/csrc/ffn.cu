@@ -29,10 +29,11 @@
 // the workspace needs no initialisation and calls on different streams (with their own workspaces) are
 // independent; an owner clears what it has read, so a captured call can be replayed.
 //
-// Bound: the tensor pipe, busy in 87 % of the cycles of a large product; the rest waits on operands from L2 (an
+// Bound: the tensor pipe, busy in 80 % of the cycles of a large product; the rest waits on operands from L2 (an
 // SM takes 64 bytes a clock, a pair's tile needs 32 KB a CTA each 512 cycles). 1024 x 5120 x 13824 forward:
-// 167 us, 1.74 PFLOP/s in a short loop (the burst rate of a library product is 1.91); forward and all gradients
-// of 4096 rows: 2.2 ms, 1.55 PFLOP/s under the power cap (library, sustained: 1.72).
+// 162 us, 1.80 PFLOP/s in a loop of 400 (a library product of the two weights at once: 151), 180 us among other
+// passes; forward and all gradients of 4096 rows: 2.25 ms, 1.55 PFLOP/s under the power cap (library, sustained:
+// 1.72).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -541,8 +542,8 @@ int launch_ffn_gemm(const FfnMaps& maps, FfnArgs a, void* share_ws, cudaStream_t
   if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
   // The last round's tiles are cut into shares where that saves each pair kFMinGain k-blocks (a cut tile costs
   // its partial sums' way through the workspace: with 5 saved, 333 x 1352 x 3592 takes 25.0 us cut and 14.8
-  // whole; with 25, 1024 x 5120 x 13824 takes 195 and 183). Few tiles over all pairs would leave an owner many parts to add
-  // (19 of them at 1024 x 5120 with K = 27648: 320 us against 142 us of MMAs), so the round before is
+  // whole; with 25, 1024 x 5120 x 13824 takes 195 and 183; a third size, 1001 x 2568 x 6920, agrees). Few
+  // tiles over all pairs would leave an owner many parts to add (19 of them at 1024 x 5120 with K = 27648: 320 us against 142 us of MMAs), so the round before is
   // cut with them where there is one: then a share is a tile and a bit, and a tile has at most three
   // parts. Without one, at most kFMaxParts pairs share a tile. A share has at least kFMinPiece k-blocks.
   const int rest = a.n_tiles % units;

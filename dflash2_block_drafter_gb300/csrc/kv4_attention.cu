@@ -35,9 +35,9 @@
 //
 // What a tile takes: about 3.0 thousand cycles with 80 rows, where the softmax warps' chain (scores from TMEM,
 // the check, exponentials, the operand's stores and their fence) is the longest, and 1.9 with 16, where the
-// conversion of codes is; each scheduler issues in 43 % and 56 % of the cycles. 64 blocks of 16 rows and five
-// query heads a key head over 256 to 4096 keys of 128 channels take 128 us, 64 single tokens over 1 to 8192 keys 110 us
-// (2.7 TB/s of the cache). What was slower: sixteen softmax warps; two sets of dequant warps taking tiles in
+// conversion of codes is; each scheduler issues in 49 % and 57 % of the cycles. 64 blocks of 16 rows and five
+// query heads a key head over 256 to 4096 keys of 128 channels take 128 us, 64 single tokens over 1 to 8192 keys 112 us
+// (2.7 TB/s of the cache). What was slower (each against the code of its time): sixteen softmax warps; two sets of dequant warps taking tiles in
 // turn (118 us for the tokens); K converted into TMEM (155 us: the loops then miss the instruction cache); the
 // check split into an arrival and a later wait (172 us for the blocks); the next tile's codes read ahead (126 us).
 //
@@ -51,8 +51,8 @@
 // for a replay. A block over 32768 keys, 19 parts a head, takes 42 us of which the joins are 12; a kernel of
 // its own for them took 20.
 //
-// No wait blocks for ever, and none is skipped: after a timeout the roles run on (their results are void
-// and the error word says so), so that every barrier stays balanced.
+// No wait blocks for ever, no loop but over tiles, parts and rows, and no wait is skipped: after a timeout the
+// roles run on (their results are void and the error word says so), so that every barrier stays balanced.
 #include <algorithm>
 
 #include <cuda_fp16.h>

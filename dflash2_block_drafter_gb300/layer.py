@@ -1,18 +1,19 @@
-"""One drafter layer with its sublayers, as a sequence of library calls over preallocated buffers.
+"""A drafter layer around its sublayers, as a sequence of library calls over preallocated buffers.
 
 ``LayerRunner`` is the layer that ``TailRunner`` leaves open (there the sublayers' outputs are given):
 attention over a 4-bit context cache and the gated feed-forward block, each between its conv site's
 prepare and finish (MAX DFlash2TransformerBlock; dflash2.ts #block):
 
-    a, coef = conv_prepare(norm(x));  q, k, v = a Wqkv^T           # the block's own rows
+    a, coef = conv_prepare(norm(x));  q, k, v = a Wqkv^T           # the block's own rows; positions(q, k)
     o = attention(q; the context's cached rows, k, v)              # bidirectional inside the block
     x = x + conv_finish(o Wo^T, coef)                              # and the MLP site's RMSNorm
     a, coef = conv_prepare(n);  h = act(a Wg^T) * (a Wu^T)
     x = x + conv_finish(h Wd^T, coef)
 
 The context's rows enter the cache with ``append_context`` once their tokens are verified (the pages
-project them from the target's hidden states; here they are given). Rotary positions are the caller's:
-``positions(q, k)`` may rotate both in place between the projection and the attention.
+project them from the target's hidden states; here they are given). The RMSNorm of each head of q and k and the
+rotary positions, which the pages put between projection and attention, are the caller's: ``positions(q, k)``
+may change both in place there; without it neither is applied.
 """
 from __future__ import annotations
 

@@ -384,7 +384,8 @@ DFLASH2_API int dflash2_proj_conv_out(const void* a, int M, int K, const void* w
  *              that sees a key or value row which is not, gives NaN; other rows do not feel it.
  *   workspace  at least dflash2_kv4_attention_workspace_bytes(...) bytes, 256-byte aligned (NULL
  *              when that is 0): partial results of contexts that several CTAs share. Needs no
- *              initialisation. Results do not depend on timing: the same call gives the same bits.
+ *              initialisation (but a captured call that recorded DFLASH2_ERR_TIMEOUT needs it
+ *              cleared before the next replay). Results do not depend on timing: the same call gives the same bits.
  * ---------------------------------------------------------------------------------- */
 DFLASH2_API size_t dflash2_kv4_page_bytes(int heads, int D, int page_size);
 DFLASH2_API int dflash2_kv4_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
@@ -417,7 +418,8 @@ DFLASH2_API int dflash2_kv4_attention(const void* q, int64_t q_stride, const voi
  *             wanted; the weights may then be NULL) and dw_gate, dw_up [F, H] = dg^T x, du^T x (both
  *             NULL: not wanted; x may then be NULL).
  *   workspace at least dflash2_gated_ffn_workspace_bytes(M, H, F, backward) bytes, 256-byte aligned,
- *             no initialisation (the backward size serves both). Calls that can run at the same time
+ *             no initialisation (the backward size serves both; a captured call that recorded
+ *             DFLASH2_ERR_TIMEOUT needs it cleared before the next replay). Calls that can run at the same time
  *             need workspaces of their own. The same call gives the same bits.
  * ---------------------------------------------------------------------------------- */
 typedef enum { DFLASH2_ACT_SILU = 0, DFLASH2_ACT_GELU_TANH = 1 } dflash2_act;
