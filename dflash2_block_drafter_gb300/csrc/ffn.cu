@@ -543,9 +543,10 @@ int launch_ffn_gemm(const FfnMaps& maps, FfnArgs a, void* share_ws, cudaStream_t
   // The last round's tiles are cut into shares where that saves each pair kFMinGain k-blocks (a cut tile costs
   // its partial sums' way through the workspace: with 5 saved, 333 x 1352 x 3592 takes 25.0 us cut and 14.8
   // whole; with 25, 1024 x 5120 x 13824 takes 195 and 183; a third size, 1001 x 2568 x 6920, agrees). Few
-  // tiles over all pairs would leave an owner many parts to add (19 of them at 1024 x 5120 with K = 27648: 320 us against 142 us of MMAs), so the round before is
-  // cut with them where there is one: then a share is a tile and a bit, and a tile has at most three
-  // parts. Without one, at most kFMaxParts pairs share a tile. A share has at least kFMinPiece k-blocks.
+  // tiles over all pairs would leave an owner many parts to add (19 of them at 1024 x 5120 with K = 27648:
+  // 320 us against 142 us of MMAs), so the round before is cut with them where there is one: then a share is a
+  // tile and a bit, and a tile has at most three parts. Without one, at most kFMaxParts pairs share a tile. A
+  // share has at least kFMinPiece k-blocks.
   const int rest = a.n_tiles % units;
   a.sk_tiles = static_cast<long long>(a.kblocks) * (units - rest) < kFMinGain * units ? 0 : rest;
   if (a.sk_tiles > 0 && 3 * rest < units && a.n_tiles > units) a.sk_tiles += units;

@@ -380,12 +380,13 @@ DFLASH2_API int dflash2_proj_conv_out(const void* a, int M, int K, const void* w
  *              significant bits, over powers of two that keep bf16's range: one per key row, per value
  *              row, and of each query row's own probabilities; channels of a cached row more than 2^7
  *              below its largest have steps of 2^-17 of that); a row that sees no key gives zeros.
- *              Magnitudes below 2^118. A row whose query is not finite, or
- *              that sees a key or value row which is not, gives NaN; other rows do not feel it.
+ *              Magnitudes below 2^118. A row whose query is not finite, or that sees a key or value row
+ *              which is not, gives NaN; other rows do not feel it.
  *   workspace  at least dflash2_kv4_attention_workspace_bytes(...) bytes, 256-byte aligned (NULL
  *              when that is 0): partial results of contexts that several CTAs share. Needs no
  *              initialisation (but a captured call that recorded DFLASH2_ERR_TIMEOUT needs it
- *              cleared before the next replay). Results do not depend on timing: the same call gives the same bits.
+ *              cleared before the next replay). Results do not depend on timing: the same call gives
+ *              the same bits.
  * ---------------------------------------------------------------------------------- */
 DFLASH2_API size_t dflash2_kv4_page_bytes(int heads, int D, int page_size);
 DFLASH2_API int dflash2_kv4_append(const void* k, const void* v, int64_t k_stride, int64_t v_stride,
