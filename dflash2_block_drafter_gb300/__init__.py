@@ -27,6 +27,7 @@ __all__ = [
     "dflash2_proj_workspace_bytes",
     "dflash2_kv4_page_bytes", "dflash2_kv4_cache", "dflash2_kv4_append", "dflash2_kv4_read",
     "dflash2_kv4_attention_workspace_bytes", "dflash2_kv4_attention",
+    "dflash2_kv4_attention_tree", "dflash2_kv4_plan", "dflash2_logits_topk",
     "dflash2_gated_ffn_workspace_bytes", "dflash2_gated_ffn", "dflash2_gated_ffn_backward", "ACT_CODES",
     "DTYPE_CODES",
 ]
@@ -80,6 +81,11 @@ _SIGNATURES = {
     "dflash2_kv4_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "dflash2_kv4_attention": (_i, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                                    _i, _vp, _vp, _sz, _vp]),
+    "dflash2_kv4_attention_tree": (_i, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i,
+                                        _f, _i, _vp, _vp, _sz, _vp]),
+    "dflash2_kv4_plan": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "dflash2_logits_topk": (_i, [_vp, _i64, _i, _i, _i, _i, _vp, _vp, _i64, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                 _i, _vp, _i64, _i, _vp, _vp, _vp, _i64, _vp]),
     "dflash2_gated_ffn_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "dflash2_gated_ffn": (_i, [_vp, _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "dflash2_gated_ffn_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -633,12 +639,8 @@ def dflash2_kv4_attention_workspace_bytes(B, G, q_heads, kv_heads, head_dim, pag
     return library().dflash2_kv4_attention_workspace_bytes(B, G, q_heads, kv_heads, head_dim, page_size, max_pages)
 
 
-def dflash2_kv4_attention(q, cache, page_table, ctx_len, page_size, scale, k_new=None, v_new=None, causal=False,
-                          window=0, out=None, workspace=None, stream=None):
-    """Attention of q [B, G, q_heads, head_dim] (bf16, rows may be strided) over each sequence's cached
-    rows (page_table [B, max_pages], ctx_len [B], int32) and its own rows k_new, v_new
-    [B, G, kv_heads, head_dim] when given; see dflash2.h for what a row sees. Returns out
-    [B, G, q_heads, head_dim] bf16."""
+def _kv4_attention_args(q, cache, page_table, ctx_len, page_size, k_new, v_new, out, workspace, stream):
+    """Checks and pointers that the attention calls share: (sizes, rows, out, workspace pointer and bytes)."""
     if q.dim() != 4:
         raise ValueError(f"q must be [B, G, q_heads, head_dim], got shape {tuple(q.shape)}")
     B, G, Hq, D = q.shape
@@ -660,17 +662,151 @@ def dflash2_kv4_attention(q, cache, page_table, ctx_len, page_size, scale, k_new
     if out.numel() < B * G * Hq * D:
         raise ValueError(f"out holds {out.numel()} elements, fewer than the {B * G * Hq * D} the call writes")
     width = page_table.shape[1]
-    lib = library()
     if workspace is None:
-        need = lib.dflash2_kv4_attention_workspace_bytes(B, G, Hq, Hkv, D, page_size, width)
+        need = library().dflash2_kv4_attention_workspace_bytes(B, G, Hq, Hkv, D, page_size, width)
         workspace = _new(need, torch.uint8, q.device, stream) if need else None
-    wp, wn = (None, 0) if workspace is None else (_dev(workspace, "workspace"),
-                                                     workspace.numel() * workspace.element_size())
-    _check(lib.dflash2_kv4_attention(
-        qp, qs, _dev(cache, "cache", torch.uint8), _dev(page_table, "page_table", torch.int32),
-        _dev(ctx_len, "ctx_len", torch.int32), kp, vp, ns, B, G, Hq, Hkv, D, page_size, pages, width, int(bool(causal)),
-        max(-1, min(window, 2 ** 31 - 1)), scale, BF16, _dev(out, "out", torch.bfloat16), wp, wn, _stream(stream)))
+    ws = (None, 0, None) if workspace is None else (_dev(workspace, "workspace"),
+                                                    workspace.numel() * workspace.element_size(), workspace)
+    rows = (qp, qs, _dev(cache, "cache", torch.uint8), _dev(page_table, "page_table", torch.int32),
+            _dev(ctx_len, "ctx_len", torch.int32), kp, vp, ns)
+    return (B, G, Hq, Hkv, D, page_size, pages, width), rows, out, ws
+
+
+def dflash2_kv4_attention(q, cache, page_table, ctx_len, page_size, scale, k_new=None, v_new=None, causal=False,
+                          window=0, out=None, workspace=None, stream=None):
+    """Attention of q [B, G, q_heads, head_dim] (bf16, rows may be strided) over each sequence's cached
+    rows (page_table [B, max_pages], ctx_len [B], int32) and its own rows k_new, v_new
+    [B, G, kv_heads, head_dim] when given; see dflash2.h for what a row sees. Returns out
+    [B, G, q_heads, head_dim] bf16."""
+    sizes, rows, out, (wp, wn, _keep) = _kv4_attention_args(q, cache, page_table, ctx_len, page_size, k_new, v_new, out,
+                                                            workspace, stream)
+    _check(library().dflash2_kv4_attention(*rows, *sizes, int(bool(causal)), max(-1, min(window, 2 ** 31 - 1)), scale, BF16,
+                                           _dev(out, "out", torch.bfloat16), wp, wn, _stream(stream)))
     return out
+
+
+def dflash2_kv4_attention_tree(q, cache, page_table, ctx_len, page_size, scale, k_new, v_new, parents, window=0, out=None,
+                               workspace=None, stream=None):
+    """dflash2_kv4_attention for a tree of drafted tokens: row t of a sequence continues row parents[b, t] (int32 [B, G]; -1:
+    the context; less: not there) and sees the cached rows, its ancestors' own rows and its own. Returns out
+    [B, G, q_heads, head_dim] bf16."""
+    if k_new is None or v_new is None or parents is None:
+        raise ValueError("a tree needs k_new, v_new and parents")
+    sizes, rows, out, (wp, wn, _keep) = _kv4_attention_args(q, cache, page_table, ctx_len, page_size, k_new, v_new, out,
+                                                            workspace, stream)
+    if tuple(parents.shape) != sizes[:2]:
+        raise ValueError(f"parents must be [{sizes[0]}, {sizes[1]}], got {tuple(parents.shape)}")
+    _check(library().dflash2_kv4_attention_tree(*rows, _dev(parents, "parents", torch.int32), *sizes,
+                                                max(-1, min(window, 2 ** 31 - 1)), scale, BF16,
+                                                _dev(out, "out", torch.bfloat16), wp, wn, _stream(stream)))
+    return out
+
+
+def _output(t, name, shape, dtype, device, stream):
+    """The output tensor `name`: allocated when not given, else checked for its size (_dev checks the rest)."""
+    n = 1
+    for x in shape:
+        n *= x
+    if t is None:
+        return _new(shape, dtype, device, stream)
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} elements, fewer than the {n} the call writes")
+    return t
+
+
+def dflash2_kv4_plan(ctx_len, change, page_table, free_pages, free_state, page_size, num_pages, rows=0, place=None,
+                     ctx_out=None, state_out=None, offsets=None, slots=None, positions=None, stream=None):
+    """Pages and slots for what each sequence gains (change > 0) or drops from its end (< 0): ctx_len, change [B],
+    page_table [B, max_pages] (in place), free_pages [capacity] with free_state [2] (a ring: its first place, its count;
+    free_pages in place), all int32. New rows are packed, `rows` of them in all, or place [B, G] says which new token each
+    row is. Returns (ctx_out [B], state_out [2], offsets [B + 1], slots int64, positions); see dflash2.h."""
+    if ctx_len.dim() != 1 or change.shape != ctx_len.shape:
+        raise ValueError(f"ctx_len and change must both be [B], got {tuple(ctx_len.shape)} and {tuple(change.shape)}")
+    B = ctx_len.shape[0]
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be [{B}, max_pages], got {tuple(page_table.shape)}")
+    if free_pages.dim() != 1 or free_state.numel() != 2:
+        raise ValueError("free_pages must be [capacity] and free_state hold its first place and its count")
+    if place is not None and (place.dim() != 2 or place.shape[0] != B):
+        raise ValueError(f"place must be [{B}, G], got {tuple(place.shape)}")
+    i32, dev = torch.int32, ctx_len.device
+    shape = (max(0, rows),) if place is None else tuple(place.shape)
+    ctx_out = _output(ctx_out, "ctx_out", (B,), i32, dev, stream)
+    state_out = _output(state_out, "state_out", (2,), i32, dev, stream)
+    offsets = _output(offsets, "offsets", (B + 1,), i32, dev, stream)
+    slots = _output(slots, "slots", shape, torch.int64, dev, stream)
+    positions = _output(positions, "positions", shape, i32, dev, stream)
+    _check(library().dflash2_kv4_plan(
+        _dev(ctx_len, "ctx_len", i32), _dev(change, "change", i32), _dev(page_table, "page_table", i32),
+        _dev(free_pages, "free_pages", i32), _dev(free_state, "free_state", i32), _dev(place, "place", i32, True), B,
+        0 if place is None else shape[1], rows, page_table.shape[1], page_size, num_pages, free_pages.shape[0],
+        _dev(ctx_out, "ctx_out", i32), _dev(state_out, "state_out", i32), _dev(offsets, "offsets", i32),
+        _dev(slots, "slots", torch.int64), _dev(positions, "positions", i32), _stream(stream)))
+    return ctx_out, state_out, offsets, slots, positions
+
+
+def _matrix(t, name, rows, width, dtypes):
+    """(pointer, row stride) of a [rows, >= width] tensor whose rows are dense and may lie apart."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < width:
+        raise ValueError(f"{name} must be [{rows}, {width}], got "
+                         f"{tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__}")
+    if not t.is_cuda or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a CUDA tensor of {' or '.join(str(x) for x in dtypes)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: each row must be dense")
+    return _vp(t.data_ptr()), t.stride(0) if rows > 1 else max(t.shape[1], 1)
+
+
+def dflash2_logits_topk(logits, K, requests=None, row_offsets=None, history=None, prompt_len=None, history_len=None,
+                        repetition=None, frequency=None, presence=None, tokens=None, parents=None, bias_ids=None, bias=None,
+                        mask=None, cand=None, unary=None, out=None, want_out=False, stream=None):
+    """The K best tokens of each row of logits [M, V] (bf16 or fp32, rows may be strided) after penalties for repeated
+    tokens, biases and a grammar mask; see dflash2.h. B = `requests` requests with M / B rows each, or row_offsets
+    [B + 1]; history [B, max_len] with prompt_len, history_len [B]; repetition, frequency, presence [B] fp32; tokens,
+    parents [M]: drafted rows; bias_ids, bias [B, n]; mask int32 [M, >= V / 32] bits. Returns (cand [M, K] int32,
+    unary [M, K] fp32, out [M, V] or None); cand and unary are None for K = 0."""
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [M, V], got shape {tuple(logits.shape)}")
+    M, V = logits.shape
+    if requests is None:
+        requests = row_offsets.numel() - 1 if row_offsets is not None else M
+    B = requests
+    if row_offsets is not None and row_offsets.numel() != B + 1:
+        raise ValueError(f"row_offsets holds {row_offsets.numel()} entries, expected B + 1 = {B + 1}")
+    i32, f32, types = torch.int32, torch.float32, (torch.bfloat16, torch.float32)
+    code = _code(logits)
+    lp, ls = _matrix(logits, "logits", M, V, types)
+    hp, hs, max_len = None, 0, 0
+    if history is not None:
+        max_len = history.shape[-1]
+        if history_len is None:
+            raise ValueError("history needs history_len")
+        hp, hs = _matrix(history, "history", B, 0, (i32,))
+    for t, n, name in ((prompt_len, B, "prompt_len"), (history_len, B, "history_len"), (repetition, B, "repetition"),
+                       (frequency, B, "frequency"), (presence, B, "presence"), (tokens, M, "tokens"), (parents, M, "parents")):
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{name} holds {t.numel()} elements, expected {n}")
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    if bias is not None and (bias_ids.dim() != 2 or bias_ids.shape[0] != B or bias.shape != bias_ids.shape):
+        raise ValueError(f"bias_ids and bias must both be [{B}, n], got {tuple(bias_ids.shape)} and {tuple(bias.shape)}")
+    mp, ms = (None, 0) if mask is None else _matrix(mask, "mask", M, (V + 31) // 32, (i32,))
+    if K > 0:
+        cand = _output(cand, "cand", (M, K), i32, logits.device, stream)
+        unary = _output(unary, "unary", (M, K), f32, logits.device, stream)
+    else:
+        cand = unary = None
+    if out is None and want_out:
+        out = _new((M, V), logits.dtype, logits.device, stream)
+    op, os_ = (None, 0) if out is None else _matrix(out, "out", M, V, (logits.dtype,))
+    _check(library().dflash2_logits_topk(
+        lp, ls, M, V, code, B, _dev(row_offsets, "row_offsets", i32, True), hp, hs, _dev(prompt_len, "prompt_len", i32, True),
+        _dev(history_len, "history_len", i32, True), max_len, _dev(repetition, "repetition", f32, True),
+        _dev(frequency, "frequency", f32, True), _dev(presence, "presence", f32, True), _dev(tokens, "tokens", i32, True),
+        _dev(parents, "parents", i32, True), _dev(bias_ids, "bias_ids", i32, True), _dev(bias, "bias", f32, True),
+        0 if bias is None else bias.shape[1], mp, ms, K, _dev(cand, "cand", i32, True), _dev(unary, "unary", f32, True), op,
+        os_, _stream(stream)))
+    return cand, unary, out
 
 
 def dflash2_gated_ffn_workspace_bytes(M, H, F, backward) -> int:

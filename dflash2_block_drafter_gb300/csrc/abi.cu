@@ -514,36 +514,113 @@ size_t dflash2_kv4_attention_workspace_bytes(int B, int G, int Hq, int Hkv, int 
   return kv4_attention_workspace(B, G, Hq, Hkv, D, page_size, max_pages, sm_count());
 }
 
+static int kv4_attention_call(Kv4Attention r, int dtype, size_t workspace_bytes, void* stream) {
+  int rc = check_kv4_attention(r.B, r.G, r.Hq, r.Hkv, r.D, r.page_size, r.num_pages, r.max_pages, dtype);
+  if (rc != DFLASH2_OK) return rc;
+  REQUIRE(r.q && r.cache && r.table && r.ctx && r.out, "a required pointer is NULL");
+  REQUIRE((r.k_new == nullptr) == (r.v_new == nullptr), "k_new and v_new must be both set or both NULL");
+  REQUIRE(aligned16(r.q) && aligned16(r.cache) && aligned16(r.out) && aligned16(r.k_new) && aligned16(r.v_new),
+          "q, cache, k_new, v_new and out must be 16-byte aligned");
+  REQUIRE(r.q_stride >= static_cast<int64_t>(r.Hq) * r.D && r.q_stride % 8 == 0,
+          "q_stride=%lld must be a multiple of 8 and at least Hq * head_dim", static_cast<long long>(r.q_stride));
+  if (r.k_new != nullptr)
+    REQUIRE(r.new_stride >= static_cast<int64_t>(r.Hkv) * r.D && r.new_stride % 8 == 0,
+            "new_stride=%lld must be a multiple of 8 and at least Hkv * head_dim", static_cast<long long>(r.new_stride));
+  REQUIRE(r.window >= 0, "window=%d must be >= 0 (0: none)", r.window);
+  REQUIRE(r.causal == 0 || r.causal == 1, "causal=%d must be 0 or 1", r.causal);
+  REQUIRE(r.scale == r.scale && r.scale - r.scale == 0.f, "scale must be finite");
+  const size_t need = kv4_attention_workspace(r.B, r.G, r.Hq, r.Hkv, r.D, r.page_size, r.max_pages, sm_count());
+  if (need > 0) {
+    if (r.workspace == nullptr || workspace_bytes < need)
+      return fail(DFLASH2_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes,
+                  need);
+    REQUIRE((reinterpret_cast<uintptr_t>(r.workspace) & 255u) == 0, "workspace must be 256-byte aligned");
+  }
+  // a window that reaches every key from every row is none (and the rows' positions less it stay above -2^31)
+  if (static_cast<int64_t>(r.window) >= static_cast<int64_t>(r.max_pages) * r.page_size + 2 * r.G) r.window = 0;
+  return launch_kv4_attention(r, static_cast<cudaStream_t>(stream));
+}
+
 int dflash2_kv4_attention(const void* q, int64_t q_stride, const void* cache, const int32_t* page_table,
                           const int32_t* ctx_len, const void* k_new, const void* v_new, int64_t new_stride, int B, int G,
                           int Hq, int Hkv, int D, int page_size, int num_pages, int max_pages, int causal, int window,
                           float scale, int dtype, void* out, void* workspace, size_t workspace_bytes, void* stream) {
-  int rc = check_kv4_attention(B, G, Hq, Hkv, D, page_size, num_pages, max_pages, dtype);
-  if (rc != DFLASH2_OK) return rc;
-  REQUIRE(q && cache && page_table && ctx_len && out, "a required pointer is NULL");
-  REQUIRE((k_new == nullptr) == (v_new == nullptr), "k_new and v_new must be both set or both NULL");
-  REQUIRE(aligned16(q) && aligned16(cache) && aligned16(out) && aligned16(k_new) && aligned16(v_new),
-          "q, cache, k_new, v_new and out must be 16-byte aligned");
-  REQUIRE(q_stride >= static_cast<int64_t>(Hq) * D && q_stride % 8 == 0,
-          "q_stride=%lld must be a multiple of 8 and at least Hq * head_dim", static_cast<long long>(q_stride));
-  if (k_new != nullptr)
-    REQUIRE(new_stride >= static_cast<int64_t>(Hkv) * D && new_stride % 8 == 0,
-            "new_stride=%lld must be a multiple of 8 and at least Hkv * head_dim", static_cast<long long>(new_stride));
-  REQUIRE(window >= 0, "window=%d must be >= 0 (0: none)", window);
-  REQUIRE(causal == 0 || causal == 1, "causal=%d must be 0 or 1", causal);
-  REQUIRE(scale == scale && scale - scale == 0.f, "scale must be finite");
-  const size_t need = kv4_attention_workspace(B, G, Hq, Hkv, D, page_size, max_pages, sm_count());
-  if (need > 0) {
-    if (workspace == nullptr || workspace_bytes < need)
-      return fail(DFLASH2_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes,
-                  need);
-    REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, "workspace must be 256-byte aligned");
+  return kv4_attention_call(Kv4Attention{q, q_stride, cache, page_table, ctx_len, k_new, v_new, new_stride, B, G, Hq, Hkv,
+                                         D, page_size, num_pages, max_pages, causal, window, scale, out, workspace, nullptr},
+                            dtype, workspace_bytes, stream);
+}
+
+int dflash2_kv4_attention_tree(const void* q, int64_t q_stride, const void* cache, const int32_t* page_table,
+                               const int32_t* ctx_len, const void* k_new, const void* v_new, int64_t new_stride,
+                               const int32_t* parents, int B, int G, int Hq, int Hkv, int D, int page_size, int num_pages,
+                               int max_pages, int window, float scale, int dtype, void* out, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  if (dtype == DFLASH2_BF16)  // (any other is refused as such)
+    REQUIRE(parents && k_new && v_new, "a tree needs parents, k_new and v_new");
+  return kv4_attention_call(Kv4Attention{q, q_stride, cache, page_table, ctx_len, k_new, v_new, new_stride, B, G, Hq, Hkv,
+                                         D, page_size, num_pages, max_pages, 0, window, scale, out, workspace, parents},
+                            dtype, workspace_bytes, stream);
+}
+
+int dflash2_kv4_plan(const int32_t* ctx_len, const int32_t* change, int32_t* page_table, int32_t* free_pages,
+                     const int32_t* free_state, const int32_t* place, int B, int G, int rows, int max_pages, int page_size,
+                     int num_pages, int capacity, int32_t* ctx_out, int32_t* state_out, int32_t* row_offsets,
+                     int64_t* slots, int32_t* positions, void* stream) {
+  REQUIRE(B >= 1 && B <= kPlanMaxSequences, "B=%d must be in [1, %d]", B, kPlanMaxSequences);
+  REQUIRE(page_size >= 16 && page_size <= 4096 && (page_size & (page_size - 1)) == 0,
+          "page_size=%d must be a power of two in [16, 4096]", page_size);
+  REQUIRE(num_pages >= 1 && capacity >= 1, "num_pages=%d and capacity=%d must be >= 1", num_pages, capacity);
+  REQUIRE(max_pages >= 1 && static_cast<int64_t>(max_pages) * page_size <= 0x7fffff00LL,
+          "max_pages=%d must be >= 1, and a sequence's pages hold less than 2^31 tokens", max_pages);
+  REQUIRE(ctx_len && change && page_table && free_pages && free_state && ctx_out && state_out && row_offsets,
+          "a required pointer is NULL");
+  if (place != nullptr)
+    REQUIRE(G >= 1 && static_cast<int64_t>(B) * G <= 0x7fffff00LL, "G=%d must be >= 1 and B * G below 2^31", G);
+  else
+    REQUIRE(rows >= 0 && rows <= 0x7fffff00, "rows=%d must be in [0, 2^31 - 256]", rows);
+  REQUIRE((place == nullptr && rows == 0) || (slots && positions), "slots and positions are required");
+  const Kv4Plan r{ctx_len, change, free_state, place, page_table, free_pages, ctx_out, state_out, row_offsets, positions,
+                  slots, B, max_pages, page_size, num_pages, capacity, G, place != nullptr ? 0x7fffffff : rows};
+  return launch_kv4_plan(r, static_cast<cudaStream_t>(stream));
+}
+
+int dflash2_logits_topk(const void* logits, int64_t stride, int M, int V, int dtype, int B, const int32_t* row_offsets,
+                        const int32_t* history, int64_t history_stride, const int32_t* prompt_len,
+                        const int32_t* history_len, int max_len, const float* repetition, const float* frequency,
+                        const float* presence, const int32_t* tokens, const int32_t* parents, const int32_t* bias_ids,
+                        const float* bias, int n_bias, const int32_t* mask, int64_t mask_stride, int K, int32_t* cand,
+                        float* unary, void* out, int64_t out_stride, void* stream) {
+  REQUIRE(dtype == DFLASH2_BF16 || dtype == DFLASH2_F32, "dtype=%d is not DFLASH2_BF16 or DFLASH2_F32", dtype);
+  REQUIRE(M >= 0 && B >= 1, "M=%d must be >= 0 and B=%d >= 1", M, B);
+  REQUIRE(V >= 1 && V <= 0x40000000, "V=%d must be in [1, 2^30]", V);
+  REQUIRE(K >= 0 && K <= 16 && K <= V, "K=%d must be in [0, min(16, V)]", K);
+  REQUIRE(row_offsets != nullptr || M % B == 0, "M=%d rows are no whole number for each of B=%d requests", M, B);
+  if (M == 0) return DFLASH2_OK;
+  REQUIRE(logits != nullptr, "a required pointer is NULL");
+  REQUIRE(K == 0 || (cand && unary), "cand and unary are required");
+  REQUIRE(K > 0 || out != nullptr, "nothing is wanted: K = 0 and no out");
+  const uintptr_t size = dtype == DFLASH2_F32 ? 4 : 2;
+  REQUIRE(reinterpret_cast<uintptr_t>(logits) % size == 0 && reinterpret_cast<uintptr_t>(out) % size == 0,
+          "logits and out must be aligned to their type");
+  REQUIRE(stride >= V || M == 1, "stride=%lld must be at least V=%d", static_cast<long long>(stride), V);
+  REQUIRE(out == nullptr || out_stride >= V || M == 1, "out_stride=%lld must be at least V=%d",
+          static_cast<long long>(out_stride), V);
+  if (history != nullptr) {
+    REQUIRE(history_len != nullptr, "history needs history_len");
+    REQUIRE(max_len >= 0 && max_len <= (1 << 20) - 128, "max_len=%d must be in [0, 2^20 - 128]", max_len);
+    REQUIRE(history_stride >= max_len || B == 1, "history_stride=%lld must be at least max_len=%d",
+            static_cast<long long>(history_stride), max_len);
   }
-  // a window that reaches every key from every row is none (and the rows' positions less it stay above -2^31)
-  if (static_cast<int64_t>(window) >= static_cast<int64_t>(max_pages) * page_size + 2 * G) window = 0;
-  const Kv4Attention r{q, q_stride, cache, page_table, ctx_len, k_new, v_new, new_stride, B, G, Hq, Hkv, D, page_size,
-                       num_pages, max_pages, causal, window, scale, out, workspace};
-  return launch_kv4_attention(r, static_cast<cudaStream_t>(stream));
+  REQUIRE(parents == nullptr || tokens != nullptr, "parents need tokens");
+  REQUIRE(tokens == nullptr || row_offsets != nullptr || M / B <= 64, "a request's drafted rows are at most 64, got %d", M / B);
+  REQUIRE(n_bias >= 0 && n_bias <= 2047, "n_bias=%d must be in [0, 2047]", n_bias);
+  REQUIRE(n_bias == 0 || (bias_ids && bias), "bias_ids and bias are required");
+  REQUIRE(mask == nullptr || mask_stride >= (V + 31) / 32 || M == 1, "mask_stride=%lld must be at least V / 32 words",
+          static_cast<long long>(mask_stride));
+  const LogitsTopk r{logits, stride, M, V, dtype, B, row_offsets, max_len > 0 ? history : nullptr, history_stride, prompt_len,
+                     history_len, max_len, repetition, frequency, presence, tokens, parents, bias_ids, bias, n_bias, mask,
+                     mask_stride, K, cand, unary, out, out_stride};
+  return launch_logits_topk(r, static_cast<cudaStream_t>(stream));
 }
 
 static int check_ffn(int M, int H, int F, int act, int dtype) {

@@ -219,9 +219,45 @@ struct Kv4Attention {
   int B, G, Hq, Hkv, D, page_size, num_pages, max_pages, causal, window;
   float scale;
   void *out, *workspace;
+  const int32_t* parents;  // [B][G] or null: the rows are a tree's (with k_new, v_new; not causal)
 };
 size_t kv4_attention_workspace(int B, int G, int Hq, int Hkv, int D, int page_size, int max_pages, int sms);
 int launch_kv4_attention(const Kv4Attention& r, cudaStream_t st);
+
+// ---------------------------------------------------------------- pages and slots (kv4_plan.cu)
+struct Kv4Plan {
+  const int32_t *ctx, *change, *state, *place;  // place null: packed rows
+  int32_t *table, *queue, *ctx_out, *state_out, *offsets, *positions;
+  int64_t* slots;
+  int B, width, page_size, num_pages, capacity, G, rows;
+};
+constexpr int kPlanMaxSequences = 8192;  // (16 bytes of shared memory each)
+int launch_kv4_plan(const Kv4Plan& r, cudaStream_t st);
+
+// ---------------------------------------------------------------- candidates from logits (logits_topk.cu)
+struct LogitsTopk {
+  const void* logits;
+  int64_t stride;
+  int M, V, dtype, B;
+  const int32_t* row_off;  // null: M / B rows a request
+  const int32_t* history;  // null: none
+  int64_t history_stride;
+  const int32_t *prompt_len, *history_len;
+  int max_len;
+  const float *repetition, *frequency, *presence;  // null: 1, 0, 0
+  const int32_t *tokens, *parents;                 // tokens null: no drafted rows; parents null: each row's is the one before
+  const int32_t* bias_ids;
+  const float* bias;
+  int n_bias;
+  const int32_t* mask;
+  int64_t mask_stride;
+  int K;
+  int32_t* cand;
+  float* unary;
+  void* out;
+  int64_t out_stride;
+};
+int launch_logits_topk(const LogitsTopk& r, cudaStream_t st);
 
 // ---------------------------------------------------------------- selector (selector.cu)
 // depths (nullable): per-block draft length of a mixed-depth batch; slots past it get path -1.

@@ -60,6 +60,7 @@
 #include "internal.h"
 #include "kv4.cuh"
 #include "ptx.cuh"
+#include "tree.cuh"
 
 namespace dfl {
 namespace {
@@ -102,7 +103,8 @@ struct BlockCfg {
   static constexpr int kOffRow = kOffInfo + 4 * kBTile * 8;  // per row: t, lo, hi, factor, offset, query factor
   static constexpr int kOffSum = kOffRow + 6 * N * 4;        // float [4][N]
   static constexpr int kOffBar = (kOffSum + 4 * N * 4 + 15) / 16 * 16;
-  static constexpr int kSmem = 1024 + kOffBar + 384;
+  static constexpr int kOffTree = kOffBar + 384;             // (trees) uint32 [2][N]: the own rows that each row sees
+  static constexpr int kSmem = 1024 + kOffTree, kSmemTree = kSmem + 2 * N * 4 + kTreeRows * 8;  // and uint64 [64]: lines
   static constexpr uint32_t kTmemCols = 3 * N <= 64 ? 64 : (3 * N <= 128 ? 128 : (3 * N <= 256 ? 256 : 512));
 };
 
@@ -113,6 +115,7 @@ struct BlockArgs {
   const int32_t *table, *ctx;
   const __nv_bfloat16 *k_new, *v_new;
   int64_t new_stride;
+  const int32_t* parents;  // [B][G], of trees
   int B, G, Hq, Hkv, R, r_magic, rows, tile_rows, row_tiles, page_shift, num_pages, width, cap, causal, window;
   float scale_log2;
   __nv_bfloat16* out;
@@ -611,7 +614,9 @@ __device__ __forceinline__ void block_join(const BlockArgs& a, const BlockLine& 
   }
 }
 
-template <int D, int NK>
+// kTree: the block's rows are a tree's. Row t stands at position L + (its ancestors' number) and sees, of the block's
+// own rows, its ancestors and itself.
+template <int D, int NK, bool kTree>
 __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const BlockArgs a) {
   using C = BlockCfg<D, NK>;
   using L = KvLayout<D>;
@@ -640,6 +645,8 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
   volatile int* mixed = reinterpret_cast<volatile int*>(tmem_slot + 4);
   uint32_t* came_s = tmem_slot + 5;  // [side][3]: the granules that came
   const uint32_t join_full = bars + 264;  // [3]
+  uint32_t* row_tree = reinterpret_cast<uint32_t*>(smem + C::kOffTree);        // [2][N]
+  uint64_t* tree_line = reinterpret_cast<uint64_t*>(row_tree + 2 * N);         // [64]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -1017,7 +1024,8 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (w.j0 > 0 ? 0 : 1)) * N;
         if (threadIdx.x < N) {
           const int r = threadIdx.x;
-          const float sum = row_red[r] + row_red[N + r] + row_red[2 * N + r] + row_red[3 * N + r];
+          float sum = row_red[r] + row_red[N + r] + row_red[2 * N + r] + row_red[3 * N + r];
+          if (kTree && row_t[r] == kBPadding) sum = 0.f;  // (whatever a row that is not there holds)
           // (a row that saw something that is not finite has a sum, and an O, of NaN)
           row_f[r] = sum == 0.f ? 0.f : (complete ? kBSumUnit / sum : 1.f);
           if (!complete && r < nrows) a.part_ml[slot + r] = make_float2(row_t[r] != kBUnseen ? -row_t[r] : -INFINITY, sum);
@@ -1062,12 +1070,36 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
       w = next;
       const int head = w.head, row_first = w.rt * a.tile_rows;
       const int nrows = min(a.tile_rows, a.rows - row_first);
+      if (kTree) {  // each row's line of ancestors, the nearest `window` of them
+        if (warp == 0) {
+          int parent[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            parent[i] = lane + 32 * i < a.G ? __ldg(a.parents + static_cast<int64_t>(w.b) * a.G + lane + 32 * i) : -2;
+          bool bad;
+          const TreeLines tree = tree_lines(parent, a.G, bad);
+          if (bad) atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_BAD_INDEX));
+          tree_line[lane] = tree.line[0];
+          tree_line[lane + 32] = tree.line[1];
+        }
+        bar_soft();
+      }
       if (threadIdx.x < N) {
-        const int r = threadIdx.x, rr = row_first + r, t = row_token(a, rr), pos = w.seq.base + t;
+        const int r = threadIdx.x, rr = row_first + r, t = row_token(a, rr);
+        uint64_t line = 0;
+        if (kTree && r < nrows) line = tree_line[t];
+        const int pos = w.seq.base + (kTree ? __popcll(line) - 1 : t);
         const int all = w.seq.L + (a.k_new != nullptr ? a.G : 0);
-        row_t[r] = r < nrows ? kBUnseen : kBPadding;
+        const bool there = r < nrows && (!kTree || line != 0);
+        row_t[r] = there ? kBUnseen : kBPadding;
         row_lo[r] = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-        row_hi[r] = r < nrows ? (a.causal ? min(all, pos + 1) : all) : 0;
+        row_hi[r] = there ? (kTree ? w.seq.L : (a.causal ? min(all, pos + 1) : all)) : 0;
+        if (kTree) {
+          if (a.window > 0)
+            for (int n = __popcll(line); n > a.window; --n) line &= line - 1;
+          row_tree[r] = static_cast<uint32_t>(line);
+          row_tree[N + r] = static_cast<uint32_t>(line >> 32);
+        }
         row_off[r] = (t * a.Hq + head * a.R + rr - t * a.R) * D;
       }
       bar_soft();
@@ -1108,7 +1140,15 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         // the values' factor (NaN if it is)
         const float vlog = fmaf(inf.y, 0.f, static_cast<float>(static_cast<int>(__float_as_uint(inf.y) >> 23) - 127));
         const float vinv = pow2_inverse(inf.y) * kBSumUnit;
-        const bool masked = key0 < all_lo || key0 + kBTile > all_hi || __any_sync(0xffffffffu, !there);
+        const bool own = kTree && j >= w.seq.cached;  // (a tree always has rows of its own)
+        const bool masked = own || key0 < all_lo || key0 + kBTile > all_hi || __any_sync(0xffffffffu, !there);
+        // of a tree's own rows, bit `lane` of word `quad` of the row's line (there are no more than two words)
+        auto tree_seen = [&](int r) {
+          const int4 v = *reinterpret_cast<const int4*>(row_tree + (quad & 1) * N + r0 + r);
+          const bool in = quad < 2;
+          return make_int4(in ? (v.x >> lane) & 1 : 0, in ? (v.y >> lane) & 1 : 0, in ? (v.z >> lane) & 1 : 0,
+                           in ? (v.w >> lane) & 1 : 0);
+        };
         tmem_ld_wait();
         // scores and values' factors (log2 domain) relative to the rows' references
         auto weigh = [&](float a, float b) {
@@ -1122,7 +1162,16 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
           const float2 y1 = __fadd2_rn(weigh(x[r + 2], x[r + 3]), make_float2(t.z, t.w));
           x[r] = y0.x; x[r + 1] = y0.y; x[r + 2] = y1.x; x[r + 3] = y1.y;
         }
-        if (masked) {
+        if (own) {
+#pragma unroll
+          for (int r = 0; r < NH; r += 4) {
+            const int4 v = tree_seen(r);
+            if (v.x == 0) x[r] = -INFINITY;
+            if (v.y == 0) x[r + 1] = -INFINITY;
+            if (v.z == 0) x[r + 2] = -INFINITY;
+            if (v.w == 0) x[r + 3] = -INFINITY;
+          }
+        } else if (masked) {
 #pragma unroll
           for (int r = 0; r < NH; r += 4) {
             const int4 lo = *reinterpret_cast<const int4*>(row_lo + r0 + r), hi = *reinterpret_cast<const int4*>(row_hi + r0 + r);
@@ -1150,6 +1199,14 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
             const float2 g1 = __fmul2_rn(make_float2(x[r + 2], x[r + 3]), make_float2(g.z, g.w));
             const int4 lo = *reinterpret_cast<const int4*>(row_lo + r0 + r), hi = *reinterpret_cast<const int4*>(row_hi + r0 + r);
             const float2 y0 = weigh(g0.x, g0.y), y1 = weigh(g1.x, g1.y);
+            if (own) {
+              const int4 v = tree_seen(r);
+              x[r] = v.x != 0 ? y0.x : -INFINITY;
+              x[r + 1] = v.y != 0 ? y0.y : -INFINITY;
+              x[r + 2] = v.z != 0 ? y1.x : -INFINITY;
+              x[r + 3] = v.w != 0 ? y1.y : -INFINITY;
+              continue;
+            }
             x[r] = there && key >= lo.x && key < hi.x ? y0.x : -INFINITY;
             x[r + 1] = there && key >= lo.y && key < hi.y ? y0.y : -INFINITY;
             x[r + 2] = there && key >= lo.z && key < hi.z ? y1.x : -INFINITY;
@@ -1276,16 +1333,27 @@ BlockPlan block_plan(int B, int G, int Hq, int Hkv, int64_t max_ctx, int sms) {
   return p;
 }
 
-template <int D, int NK>
+template <int D, int NK, bool kTree>
 int launch_block_t(const BlockArgs& a, const BlockPlan& p, cudaStream_t st) {
   using C = BlockCfg<D, NK>;
-  static_assert(C::kSmem <= 232448, "shared memory");
+  constexpr int kSmem = kTree ? C::kSmemTree : C::kSmem;
+  static_assert(kSmem <= 232448, "shared memory");
   static unsigned done = 0;
-  auto kern = kv4_attention_kernel<D, NK>;
-  if (!ensure_smem_attr(kern, C::kSmem, &done)) return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (attention)");
+  auto kern = kv4_attention_kernel<D, NK, kTree>;
+  if (!ensure_smem_attr(kern, kSmem, &done)) return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (attention)");
   const cudaError_t e =
-      launch_pdl(kern, dim3(static_cast<unsigned>(p.ctas)), dim3(kBThreads), C::kSmem, st, nullptr, 0, a);
+      launch_pdl(kern, dim3(static_cast<unsigned>(p.ctas)), dim3(kBThreads), kSmem, st, nullptr, 0, a);
   return e == cudaSuccess ? DFLASH2_OK : fail(DFLASH2_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
+}
+
+template <int D, bool kTree>
+int launch_block_d(const BlockArgs& a, const BlockPlan& p, cudaStream_t st) {
+  switch (p.nk) {
+    case 1: return launch_block_t<D, 1, kTree>(a, p, st);
+    case 2: return launch_block_t<D, 2, kTree>(a, p, st);
+    case 4: return launch_block_t<D, 4, kTree>(a, p, st);
+    default: return launch_block_t<D, 5, kTree>(a, p, st);
+  }
 }
 
 }  // namespace
@@ -1307,6 +1375,7 @@ int launch_kv4_attention(const Kv4Attention& r, cudaStream_t st) {
   a.k_new = static_cast<const __nv_bfloat16*>(r.k_new);
   a.v_new = static_cast<const __nv_bfloat16*>(r.v_new);
   a.new_stride = r.new_stride;
+  a.parents = r.parents;
   a.B = r.B; a.G = r.G; a.Hq = r.Hq; a.Hkv = r.Hkv;
   a.R = r.Hq / r.Hkv;
   a.r_magic = ((1 << 20) + a.R - 1) / a.R;
@@ -1329,20 +1398,8 @@ int launch_kv4_attention(const Kv4Attention& r, cudaStream_t st) {
   a.ctas_inverse = ~0ull / static_cast<unsigned long long>(p.ctas);
   a.err = device_error_word();
   if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
-  if (r.D == 64) {
-    switch (p.nk) {
-      case 1: return launch_block_t<64, 1>(a, p, st);
-      case 2: return launch_block_t<64, 2>(a, p, st);
-      case 4: return launch_block_t<64, 4>(a, p, st);
-      default: return launch_block_t<64, 5>(a, p, st);
-    }
-  }
-  switch (p.nk) {
-    case 1: return launch_block_t<128, 1>(a, p, st);
-    case 2: return launch_block_t<128, 2>(a, p, st);
-    case 4: return launch_block_t<128, 4>(a, p, st);
-    default: return launch_block_t<128, 5>(a, p, st);
-  }
+  if (r.parents != nullptr) return r.D == 64 ? launch_block_d<64, true>(a, p, st) : launch_block_d<128, true>(a, p, st);
+  return r.D == 64 ? launch_block_d<64, false>(a, p, st) : launch_block_d<128, false>(a, p, st);
 }
 
 }  // namespace dfl

@@ -1,0 +1,254 @@
+// Pages and slots of a paged cache, planned on the GPU: what each sequence gains or drops becomes page-table
+// entries, slots of new rows and a queue of free pages.
+//
+// Sequence b holds L tokens in ceil(L / p) pages and changes by c: it needs max(0, ceil((L + c) / p) - ceil(L / p))
+// pages more, or gives as many back. Where its pages and rows lie among all is a prefix sum over the sequences; every
+// page and every row then finds its sequence by a binary search of those sums and writes its own entry.
+//
+// A sequence is granted if its pages fit the queue, and its rows the output, together with those of all sequences
+// before it. The sums run over refused sequences too, so that what is granted is a prefix of those that ask, and
+// each sum cut off at the largest granted one gives the granted sequences' places.
+#include <algorithm>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace dfl {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+struct PlanArgs {
+  const int32_t *ctx, *change, *state, *place;
+  int32_t *table, *queue, *ctx_out, *state_out, *offsets, *positions;
+  int64_t* slots;
+  int B, width, page_shift, num_pages, capacity, G, rows;
+  int* err;
+};
+
+struct PlanSums {
+  long long taken, given, rows;
+};
+
+// Exclusive sums over the block's threads, and the total (all threads call it).
+__device__ __forceinline__ long long block_scan(long long x, long long* warp_sums, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = x;
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, m);
+    if (lane >= m) inc += v;
+  }
+  __syncthreads();  // (the sums of a scan before have been read)
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  long long mine = warp_sums[lane];
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, mine, m);
+    if (lane >= m) mine += v;
+  }
+  total = __shfl_sync(0xffffffffu, mine, 31);
+  const long long before = __shfl_sync(0xffffffffu, mine, max(0, warp - 1));
+  return (warp > 0 ? before : 0) + inc - x;
+}
+
+// The first b with end[b] > i (end ascends; i is below the last).
+__device__ __forceinline__ int owner_of(const int* end, int n, int i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (end[mid] > i)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a) {
+  extern __shared__ int plan_smem[];
+  int* ctx = plan_smem;          // [B] lengths before
+  int* taken = ctx + a.B;        // [B] sums over the sequences up to this one: pages taken,
+  int* given = taken + a.B;      // pages given back,
+  int* row_end = given + a.B;    // rows
+  __shared__ long long warp_sums[32];
+  __shared__ int most[3];        // the largest granted sums
+  const int tid = static_cast<int>(threadIdx.x);
+  pdl_trigger();
+  pdl_wait();
+  const int page = 1 << a.page_shift;
+  const long long cap = static_cast<long long>(a.width) << a.page_shift;
+  int head = __ldg(a.state), count = __ldg(a.state + 1);
+  const bool state_ok = head >= 0 && head < a.capacity && count >= 0 && count <= a.capacity;
+  if (!state_ok && tid == 0) atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_INVALID_ARG));
+  if (tid < 3) most[tid] = 0;
+
+  // each thread a run of sequences
+  const int per = (a.B + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  auto fits = [&](int b, long long& len, long long& end) {
+    len = __ldg(a.ctx + b);
+    end = len + __ldg(a.change + b);
+    return state_ok && len >= 0 && len <= cap && end >= 0 && end <= cap;
+  };
+  auto pages_of = [&](long long n) { return (n + page - 1) >> a.page_shift; };
+  long long need = 0, back = 0;
+  for (int b = b0; b < b1; ++b) {
+    long long len, end;
+    if (!fits(b, len, end)) {
+      atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_INVALID_ARG));
+      continue;
+    }
+    const long long d = pages_of(end) - pages_of(len);
+    need += max(0ll, d);
+    back += max(0ll, -d);
+  }
+  long long total;
+  const long long need0 = block_scan(need, warp_sums, total), back0 = block_scan(back, warp_sums, total);
+  // the pages decide first: a sequence that gets none asks for no rows
+  auto granted_pages = [&](long long d, long long need_sum, long long back_sum) {
+    if (d > 0) return need_sum <= count;
+    if (d < 0) return back_sum <= a.capacity - count;
+    return true;
+  };
+  long long rows = 0;
+  need = need0;
+  back = back0;
+  for (int b = b0; b < b1; ++b) {
+    long long len, end;
+    if (!fits(b, len, end)) continue;
+    const long long d = pages_of(end) - pages_of(len);
+    need += max(0ll, d);
+    back += max(0ll, -d);
+    if (granted_pages(d, need, back))
+      rows += max(0ll, end - len);
+    else if (d < 0)  // more pages come back than there can be
+      atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_INVALID_ARG));
+  }
+  rows = block_scan(rows, warp_sums, total);
+  // then the rows
+  need = need0;
+  back = back0;
+  for (int b = b0; b < b1; ++b) {
+    long long len, end;
+    const bool ok = fits(b, len, end);
+    bool granted = ok;
+    if (ok) {
+      const long long d = pages_of(end) - pages_of(len);
+      need += max(0ll, d);
+      back += max(0ll, -d);
+      granted = granted_pages(d, need, back);
+      if (granted && end > len) {
+        rows += end - len;
+        granted = rows <= a.rows;
+      }
+      if (granted && d > 0) atomicMax(most, static_cast<int>(need));
+      if (granted && d < 0) atomicMax(most + 1, static_cast<int>(back));
+      if (granted && end > len) atomicMax(most + 2, static_cast<int>(rows));
+    }
+    ctx[b] = __ldg(a.ctx + b);
+    taken[b] = static_cast<int>(min(need, 0x7fffffffll));
+    given[b] = static_cast<int>(min(back, 0x7fffffffll));
+    row_end[b] = static_cast<int>(min(rows, 0x7fffffffll));
+  }
+  __syncthreads();
+  const int pages_taken = most[0], pages_given = most[1], rows_all = most[2];
+  for (int b = tid; b < a.B; b += kPlanThreads) {
+    taken[b] = min(taken[b], pages_taken);
+    given[b] = min(given[b], pages_given);
+    row_end[b] = min(row_end[b], rows_all);
+  }
+  __syncthreads();
+  auto before = [](const int* end, int b) { return b > 0 ? end[b - 1] : 0; };
+  // entry i of the pages waiting (i < 2 capacity)
+  auto place_in_queue = [&](int i) {
+    const long long at = static_cast<long long>(head) + i;
+    return static_cast<int>(at >= a.capacity ? at - a.capacity : at);
+  };
+  auto page_ok = [&](int p) {
+    if (p >= 0 && p < a.num_pages) return true;
+    atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_BAD_INDEX));
+    return false;
+  };
+  for (int i = tid; i < pages_taken; i += kPlanThreads) {
+    const int b = owner_of(taken, a.B, i);
+    const int p = a.queue[place_in_queue(i)];
+    page_ok(p);
+    a.table[static_cast<long long>(b) * a.width + pages_of(ctx[b]) + (i - before(taken, b))] = p;
+  }
+  for (int i = tid; i < pages_given; i += kPlanThreads) {
+    const int b = owner_of(given, a.B, i);
+    const int n = given[b] - before(given, b);  // the sequence's last pages
+    const int p = a.table[static_cast<long long>(b) * a.width + pages_of(ctx[b]) - n + (i - before(given, b))];
+    page_ok(p);
+    a.queue[place_in_queue(count + i)] = p;
+  }
+  const int items = a.place != nullptr ? a.B * a.G : a.rows;
+  for (int i = tid; i < items; i += kPlanThreads) {
+    int b = 0, j = -1;
+    bool there;
+    if (a.place != nullptr) {
+      b = i / a.G;
+      j = __ldg(a.place + i);
+      there = j >= 0 && j < row_end[b] - before(row_end, b);
+    } else {
+      there = i < rows_all;
+      if (there) {
+        b = owner_of(row_end, a.B, i);
+        j = i - before(row_end, b);
+      }
+    }
+    int64_t slot = -1;
+    int pos = -1;
+    if (there) {
+      pos = ctx[b] + j;
+      const int k = pos >> a.page_shift, have = static_cast<int>(pages_of(ctx[b]));
+      const int p = k < have ? a.table[static_cast<long long>(b) * a.width + k]
+                             : a.queue[place_in_queue(before(taken, b) + (k - have))];
+      if (page_ok(p)) slot = (static_cast<int64_t>(p) << a.page_shift) + (pos & (page - 1));
+    }
+    a.slots[i] = slot;
+    a.positions[i] = pos;
+  }
+  // (the outputs may be the inputs' own buffers: every thread has read them)
+  for (int b = tid; b < a.B; b += kPlanThreads) {
+    const int gain = row_end[b] - before(row_end, b);
+    const bool gives = given[b] > before(given, b);
+    // a sequence shrinks within its last page without giving one back: granted if it fits
+    int end = ctx[b] + gain;
+    if (gain == 0) {
+      const long long c = static_cast<long long>(ctx[b]) + __ldg(a.change + b);
+      const bool ok = state_ok && ctx[b] >= 0 && ctx[b] <= cap && c >= 0 && c < ctx[b];
+      if (ok && (gives || pages_of(c) == pages_of(ctx[b]))) end = static_cast<int>(c);
+    }
+    a.ctx_out[b] = end;
+    a.offsets[b + 1] = row_end[b];
+  }
+  if (tid == 0) {
+    a.offsets[0] = 0;
+    a.state_out[0] = state_ok ? place_in_queue(pages_taken) : head;
+    a.state_out[1] = state_ok ? count - pages_taken + pages_given : count;
+  }
+}
+
+}  // namespace
+
+int launch_kv4_plan(const Kv4Plan& r, cudaStream_t st) {
+  PlanArgs a{};
+  a.ctx = r.ctx; a.change = r.change; a.state = r.state; a.place = r.place;
+  a.table = r.table; a.queue = r.queue; a.ctx_out = r.ctx_out; a.state_out = r.state_out;
+  a.offsets = r.offsets; a.positions = r.positions; a.slots = r.slots;
+  a.B = r.B; a.width = r.width; a.num_pages = r.num_pages; a.capacity = r.capacity; a.G = r.G; a.rows = r.rows;
+  while ((1 << a.page_shift) < r.page_size) ++a.page_shift;
+  a.err = device_error_word();
+  if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
+  static unsigned done = 0;
+  if (!ensure_smem_attr(kv4_plan_kernel, kPlanMaxSequences * 16, &done))
+    return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (plan)");
+  const cudaError_t e = launch_pdl(kv4_plan_kernel, dim3(1), dim3(kPlanThreads), static_cast<size_t>(r.B) * 16, st,
+                                   nullptr, 0, a);
+  return e == cudaSuccess ? DFLASH2_OK : fail(DFLASH2_ERR_CUDA, "plan launch failed: %s", cudaGetErrorString(e));
+}
+
+}  // namespace dfl

@@ -402,6 +402,87 @@ DFLASH2_API int dflash2_kv4_attention(const void* q, int64_t q_stride, const voi
                                       int max_pages, int causal, int window, float scale, int dtype, void* out,
                                       void* workspace, size_t workspace_bytes, void* stream);
 
+/* Attention of a tree of drafted tokens over the cache: as dflash2_kv4_attention with own rows, except for which of those a
+ * row sees and where it stands. (The pages draft one path a block; a tree of the selector's candidates is verified by one
+ * such pass.) k_new and v_new are required.
+ *   parents    [B, G] int32: row t of a sequence continues row parents[t] < t of the same sequence, or its context
+ *              (-1). Less than -1: the row is not there (a tree smaller than G): it gives zeros, and so does every row
+ *              below it. A parent that is not an earlier row records DFLASH2_ERR_BAD_INDEX and counts so too.
+ *   Row t stands at position L + (its number of ancestors). It sees the cached keys, its ancestors and itself, and with
+ *   window > 0 only those after its position - window. Contents of rows that are not there may be anything.
+ *   Workspace as dflash2_kv4_attention_workspace_bytes says. */
+DFLASH2_API int dflash2_kv4_attention_tree(const void* q, int64_t q_stride, const void* cache, const int32_t* page_table,
+                                           const int32_t* ctx_len, const void* k_new, const void* v_new,
+                                           int64_t new_stride, const int32_t* parents, int B, int G, int Hq, int Hkv,
+                                           int D, int page_size, int num_pages, int max_pages, int window, float scale,
+                                           int dtype, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Pages and slots of the cache, planned on the GPU from the sequences' lengths. (The pages keep one growing buffer a
+ * sequence, dflash2.ts #contextKV; a paged cache needs what this call makes: dflash2_kv4_append's slots,
+ * dflash2_kv4_attention's page_table and ctx_len.)
+ *
+ *   ctx_len    [B] int32 cached tokens L of each sequence, in ceil(L / page_size) pages of its page-table row.
+ *   change     [B] int32: tokens that the sequence gains (> 0) or drops from its end (< 0; -L: it is done).
+ *   page_table [B, max_pages] int32, in place: entries of pages taken are written, no others are.
+ *   free_pages [capacity] int32, in place: a ring of free pages; free_state [2] int32: the place of the first of them, and
+ *              their number. Pages are taken from its front in the order of the sequences, and given back to
+ *              its end; capacity at least the cache's pages. state_out [2]: the state afterwards.
+ *   A sequence is refused, and left as it was, if the free pages do not suffice for it and those before it (pages given
+ *   back in this call are not yet counted); in packed rows (below) also if its rows do not fit. Later sequences that need
+ *   pages (rows) are then refused too. A length or change outside [0, max_pages * page_size], a state outside the ring,
+ *   or more pages given back than the ring has room for, refuses the sequence and records DFLASH2_ERR_INVALID_ARG. A
+ *   page outside [0, num_pages) records DFLASH2_ERR_BAD_INDEX; its rows' slots are -1.
+ *   ctx_out    [B] int32: the lengths afterwards (L where the sequence was refused).
+ *   row_offsets [B + 1] int32: the granted new tokens' running sum.
+ *   New tokens' rows: packed (place NULL): row row_offsets[b] + j is sequence b's j-th new token, `rows` rows in all; or
+ *   place [B, G] int32: row (b, t) is sequence b's new token place[b, t], none if that is outside [0, gain)
+ *   (which rows of a verified block or tree are kept, in their order; no number twice).
+ *   slots      [rows] or [B, G] int64, positions the same int32: each row's cache slot and position; -1 for rows of no
+ *              token and of refused sequences.
+ *   ctx_out may be ctx_len, and state_out free_state; other buffers do not overlap. B <= 8192; page_size as the cache's.
+ * ---------------------------------------------------------------------------------- */
+DFLASH2_API int dflash2_kv4_plan(const int32_t* ctx_len, const int32_t* change, int32_t* page_table, int32_t* free_pages,
+                                 const int32_t* free_state, const int32_t* place, int B, int G, int rows, int max_pages,
+                                 int page_size, int num_pages, int capacity, int32_t* ctx_out, int32_t* state_out,
+                                 int32_t* row_offsets, int64_t* slots, int32_t* positions, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * Candidates from logits: penalties for repeated tokens, token biases and a grammar mask, then the K best tokens a row,
+ * in one read of the logits. (dflash2.ts #select's per-row top-K over logits that a request's sampling parameters adjust
+ * first; the pages adjust none.) Feeds dflash2_score_edges, or a tree's verification (K = 1).
+ *
+ *   logits     [M, V] dtype, rows `stride` elements apart (any stride >= V).
+ *   B requests: request b has rows [row_offsets[b], row_offsets[b + 1]) ([B + 1] int32; a span that is not inside
+ *              [0, M] records DFLASH2_ERR_INVALID_ARG), or M / B rows each if NULL. Rows of no request are left as they were.
+ *   history    [B, max_len] int32, rows history_stride apart, or NULL: each request's tokens, history_len[b] of them (in [0,
+ *              max_len], recorded as DFLASH2_ERR_INVALID_ARG and clamped otherwise), the first prompt_len[b] of which are
+ *              its prompt (NULL: none). max_len < 2^20 - 127.
+ *   tokens     [M] int32 or NULL: the token of each row's drafted node, at most 64 rows a request (later ones record
+ *              DFLASH2_ERR_INVALID_ARG and are left as they were). A row's line, itself and its ancestors, counts as
+ *              generated. parents [M] as for dflash2_kv4_attention_tree, counted from the request's first row; NULL: each
+ *              row continues the one before it. A row that is not there gets ids -1 and values -inf; its out row is left.
+ *   repetition, frequency, presence [B] fp32, each NULL for 1, 0, 0; bias_ids [B, n_bias] int32 (negative: unused) with
+ *              bias [B, n_bias] fp32, n_bias <= 2047: the first entry of a token counts; mask [M, >= V / 32] int32
+ *              words, rows mask_stride apart, or NULL: bit v % 32 of word v / 32 set: token v is allowed.
+ *              Token ids >= V, and negative ones elsewhere than in bias_ids, record DFLASH2_ERR_BAD_INDEX and count nothing.
+ *   With c the times token v was generated:
+ *              y = x > 0 ? x / repetition : x * repetition   if v was generated or stands in the prompt;
+ *              y = y - (frequency * c + presence) if c > 0;  y = y + bias;  y = -inf if not allowed
+ *              (fp32, each step rounded: the order of close tokens is the same wherever it is computed).
+ *   cand, unary [M, K] int32, fp32: the K best tokens by y, descending, the lower token first among equals, and their y;
+ *              0 <= K <= min(16, V), both NULL for K = 0. NaN comes before every number.
+ *   out        [M, V] dtype or NULL, rows out_stride apart: y, rounded once. May be logits itself (with its stride).
+ *   No workspace. The same call gives the same bits.
+ * ---------------------------------------------------------------------------------- */
+DFLASH2_API int dflash2_logits_topk(const void* logits, int64_t stride, int M, int V, int dtype, int B,
+                                    const int32_t* row_offsets, const int32_t* history, int64_t history_stride,
+                                    const int32_t* prompt_len, const int32_t* history_len, int max_len,
+                                    const float* repetition, const float* frequency, const float* presence,
+                                    const int32_t* tokens, const int32_t* parents, const int32_t* bias_ids,
+                                    const float* bias, int n_bias, const int32_t* mask, int64_t mask_stride, int K,
+                                    int32_t* cand, float* unary, void* out, int64_t out_stride, void* stream);
+
 /* ------------------------------------------------------------------------------------
  * The gated feed-forward sublayer and its gradients (dflash2.ts #block: down(silu(gate(a)) * up(a));
  * the down projection is dflash2_proj or dflash2_proj_conv_out). The pages train nothing; the
