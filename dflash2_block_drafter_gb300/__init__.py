@@ -27,7 +27,7 @@ __all__ = [
     "dflash2_proj_workspace_bytes",
     "dflash2_kv4_page_bytes", "dflash2_kv4_cache", "dflash2_kv4_append", "dflash2_kv4_read",
     "dflash2_kv4_attention_workspace_bytes", "dflash2_kv4_attention",
-    "dflash2_kv4_attention_tree", "dflash2_kv4_plan", "dflash2_logits_topk",
+    "dflash2_kv4_attention_tree", "dflash2_kv4_plan", "dflash2_logits_topk_workspace_bytes", "dflash2_logits_topk",
     "dflash2_gated_ffn_workspace_bytes", "dflash2_gated_ffn", "dflash2_gated_ffn_backward", "ACT_CODES",
     "DTYPE_CODES",
 ]
@@ -84,8 +84,9 @@ _SIGNATURES = {
     "dflash2_kv4_attention_tree": (_i, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i,
                                         _f, _i, _vp, _vp, _sz, _vp]),
     "dflash2_kv4_plan": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "dflash2_logits_topk_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
     "dflash2_logits_topk": (_i, [_vp, _i64, _i, _i, _i, _i, _vp, _vp, _i64, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
-                                 _i, _vp, _i64, _i, _vp, _vp, _vp, _i64, _vp]),
+                                 _i, _vp, _i64, _i, _vp, _vp, _vp, _i64, _vp, _sz, _vp]),
     "dflash2_gated_ffn_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "dflash2_gated_ffn": (_i, [_vp, _i, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "dflash2_gated_ffn_backward": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -757,9 +758,13 @@ def _matrix(t, name, rows, width, dtypes):
     return _vp(t.data_ptr()), t.stride(0) if rows > 1 else max(t.shape[1], 1)
 
 
+def dflash2_logits_topk_workspace_bytes(M, V, B, ragged, max_len, drafted, n_bias, K) -> int:
+    return library().dflash2_logits_topk_workspace_bytes(M, V, B, int(bool(ragged)), max_len, int(bool(drafted)), n_bias, K)
+
+
 def dflash2_logits_topk(logits, K, requests=None, row_offsets=None, history=None, prompt_len=None, history_len=None,
                         repetition=None, frequency=None, presence=None, tokens=None, parents=None, bias_ids=None, bias=None,
-                        mask=None, cand=None, unary=None, out=None, want_out=False, stream=None):
+                        mask=None, cand=None, unary=None, out=None, want_out=False, workspace=None, stream=None):
     """The K best tokens of each row of logits [M, V] (bf16 or fp32, rows may be strided) after penalties for repeated
     tokens, biases and a grammar mask; see dflash2.h. B = `requests` requests with M / B rows each, or row_offsets
     [B + 1]; history [B, max_len] with prompt_len, history_len [B]; repetition, frequency, presence [B] fp32; tokens,
@@ -799,13 +804,19 @@ def dflash2_logits_topk(logits, K, requests=None, row_offsets=None, history=None
     if out is None and want_out:
         out = _new((M, V), logits.dtype, logits.device, stream)
     op, os_ = (None, 0) if out is None else _matrix(out, "out", M, V, (logits.dtype,))
+    n_bias = 0 if bias is None else bias.shape[1]
+    if workspace is None:
+        need = library().dflash2_logits_topk_workspace_bytes(M, V, B, int(row_offsets is not None), max_len,
+                                                             int(tokens is not None), n_bias, K)
+        workspace = _new(need, torch.uint8, logits.device, stream) if need else None
+    wp, wn = (None, 0) if workspace is None else (_dev(workspace, "workspace"), workspace.numel() * workspace.element_size())
     _check(library().dflash2_logits_topk(
         lp, ls, M, V, code, B, _dev(row_offsets, "row_offsets", i32, True), hp, hs, _dev(prompt_len, "prompt_len", i32, True),
         _dev(history_len, "history_len", i32, True), max_len, _dev(repetition, "repetition", f32, True),
         _dev(frequency, "frequency", f32, True), _dev(presence, "presence", f32, True), _dev(tokens, "tokens", i32, True),
         _dev(parents, "parents", i32, True), _dev(bias_ids, "bias_ids", i32, True), _dev(bias, "bias", f32, True),
-        0 if bias is None else bias.shape[1], mp, ms, K, _dev(cand, "cand", i32, True), _dev(unary, "unary", f32, True), op,
-        os_, _stream(stream)))
+        n_bias, mp, ms, K, _dev(cand, "cand", i32, True), _dev(unary, "unary", f32, True), op, os_, wp, wn,
+        _stream(stream)))
     return cand, unary, out
 
 

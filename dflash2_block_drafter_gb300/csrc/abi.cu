@@ -584,16 +584,33 @@ int dflash2_kv4_plan(const int32_t* ctx_len, const int32_t* change, int32_t* pag
   return launch_kv4_plan(r, static_cast<cudaStream_t>(stream));
 }
 
+static int check_logits(int M, int V, int B, int max_len, int n_bias, int K) {
+  REQUIRE(M >= 0 && B >= 1, "M=%d must be >= 0 and B=%d >= 1", M, B);
+  REQUIRE(V >= 1 && V <= 0x40000000, "V=%d must be in [1, 2^30]", V);
+  REQUIRE(K >= 0 && K <= 16 && K <= V, "K=%d must be in [0, min(16, V)]", K);
+  REQUIRE(max_len >= 0 && max_len <= (1 << 20) - 128, "max_len=%d must be in [0, 2^20 - 128]", max_len);
+  REQUIRE(n_bias >= 0 && n_bias <= 2047, "n_bias=%d must be in [0, 2047]", n_bias);
+  // tiles of 1024 tokens a row, and windows of 32768 a request, are counted in int
+  const int64_t tiles = (V + 1024LL) / 1024 + 1, windows = (V + 32767LL) / 32768;
+  REQUIRE(M * tiles <= 0x3fffffff && B * windows <= 0x3fffffff, "M=%d, V=%d, B=%d are too large", M, V, B);
+  return DFLASH2_OK;
+}
+
+size_t dflash2_logits_topk_workspace_bytes(int M, int V, int B, int ragged, int max_len, int drafted, int n_bias, int K) {
+  if (check_logits(M, V, B, max_len, n_bias, K) != DFLASH2_OK) return 0;
+  return logits_topk_workspace(M, V, B, ragged != 0, max_len, drafted != 0, n_bias, K);
+}
+
 int dflash2_logits_topk(const void* logits, int64_t stride, int M, int V, int dtype, int B, const int32_t* row_offsets,
                         const int32_t* history, int64_t history_stride, const int32_t* prompt_len,
                         const int32_t* history_len, int max_len, const float* repetition, const float* frequency,
                         const float* presence, const int32_t* tokens, const int32_t* parents, const int32_t* bias_ids,
                         const float* bias, int n_bias, const int32_t* mask, int64_t mask_stride, int K, int32_t* cand,
-                        float* unary, void* out, int64_t out_stride, void* stream) {
+                        float* unary, void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
+                        void* stream) {
   REQUIRE(dtype == DFLASH2_BF16 || dtype == DFLASH2_F32, "dtype=%d is not DFLASH2_BF16 or DFLASH2_F32", dtype);
-  REQUIRE(M >= 0 && B >= 1, "M=%d must be >= 0 and B=%d >= 1", M, B);
-  REQUIRE(V >= 1 && V <= 0x40000000, "V=%d must be in [1, 2^30]", V);
-  REQUIRE(K >= 0 && K <= 16 && K <= V, "K=%d must be in [0, min(16, V)]", K);
+  int rc = check_logits(M, V, B, max_len, n_bias, K);
+  if (rc != DFLASH2_OK) return rc;
   REQUIRE(row_offsets != nullptr || M % B == 0, "M=%d rows are no whole number for each of B=%d requests", M, B);
   if (M == 0) return DFLASH2_OK;
   REQUIRE(logits != nullptr, "a required pointer is NULL");
@@ -607,19 +624,25 @@ int dflash2_logits_topk(const void* logits, int64_t stride, int M, int V, int dt
           static_cast<long long>(out_stride), V);
   if (history != nullptr) {
     REQUIRE(history_len != nullptr, "history needs history_len");
-    REQUIRE(max_len >= 0 && max_len <= (1 << 20) - 128, "max_len=%d must be in [0, 2^20 - 128]", max_len);
     REQUIRE(history_stride >= max_len || B == 1, "history_stride=%lld must be at least max_len=%d",
             static_cast<long long>(history_stride), max_len);
   }
   REQUIRE(parents == nullptr || tokens != nullptr, "parents need tokens");
   REQUIRE(tokens == nullptr || row_offsets != nullptr || M / B <= 64, "a request's drafted rows are at most 64, got %d", M / B);
-  REQUIRE(n_bias >= 0 && n_bias <= 2047, "n_bias=%d must be in [0, 2047]", n_bias);
   REQUIRE(n_bias == 0 || (bias_ids && bias), "bias_ids and bias are required");
   REQUIRE(mask == nullptr || mask_stride >= (V + 31) / 32 || M == 1, "mask_stride=%lld must be at least V / 32 words",
           static_cast<long long>(mask_stride));
+  if (history == nullptr) max_len = 0;
+  const size_t need = logits_topk_workspace(M, V, B, row_offsets != nullptr, max_len, tokens != nullptr, n_bias, K);
+  if (need > 0) {
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(DFLASH2_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes,
+                  need);
+    REQUIRE((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0, "workspace must be 256-byte aligned");
+  }
   const LogitsTopk r{logits, stride, M, V, dtype, B, row_offsets, max_len > 0 ? history : nullptr, history_stride, prompt_len,
                      history_len, max_len, repetition, frequency, presence, tokens, parents, bias_ids, bias, n_bias, mask,
-                     mask_stride, K, cand, unary, out, out_stride};
+                     mask_stride, K, cand, unary, out, out_stride, workspace};
   return launch_logits_topk(r, static_cast<cudaStream_t>(stream));
 }
 

@@ -256,7 +256,9 @@ struct LogitsTopk {
   float* unary;
   void* out;
   int64_t out_stride;
+  void* workspace;
 };
+size_t logits_topk_workspace(int M, int V, int B, bool ragged, int max_len, bool tokens, int n_bias, int K);
 int launch_logits_topk(const LogitsTopk& r, cudaStream_t st);
 
 // ---------------------------------------------------------------- selector (selector.cu)

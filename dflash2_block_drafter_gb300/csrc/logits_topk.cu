@@ -9,17 +9,16 @@
 //   y = -inf                                      if the mask's bit v is clear
 // each step rounded to fp32, so that the order of nearly equal tokens is defined to the last bit.
 //
-// The work is one read of the logits. A cluster of CTAs shares a row, each CTA a slice of the vocabulary (16384 tokens
-// at most: 64 a thread, which stay in registers between the two looks at them), and works through a range of rows.
-// What applies to few tokens does not burden the rest: the tokens that the history, the drafted rows and the biases
-// name are collected once for all of a request's rows (a bit a token in shared memory; its rank among the set bits
-// finds its counter), computed apart from the stream, and only left out of it there.
-//
-// The K best of a slice: the K-th largest of sixteen groups' maxima bounds the K-th largest value from below, so the
-// few values that reach it are listed and ranked against each other by (value, lower token). A list that overflows (a
-// row whose large values lie in few threads' hands) is replaced by K rounds of a maximum. Only what is above -inf is
-// listed; rows with fewer than K such tokens are filled with the lowest of the others. The cluster's lists are merged
-// through distributed shared memory, a chunk of rows at a time.
+// The work is one read of the logits, and what applies to few tokens does not burden the rest. Three kernels:
+//  1. names: the tokens that a request's history, drafted rows and biases name, as a bit a token and as a list of
+//     (token, counter); rows' requests and lines of ancestors. A CTA a request and window of 32768 tokens, counters
+//     in shared memory.
+//  2. stream: every warp reads tiles of 1024 tokens of a row, 32 a lane, and writes one key a lane: the largest value
+//     of its tokens that are allowed and not named. No barriers, nothing shared; the mask is applied to `out` here.
+//  3. select: a CTA a row. The named tokens' values; then, from the keys, which are a 32nd of the row, a bound that the
+//     K best reach, the few lanes whose key reaches it, their tokens once more, and the K best of those by (value,
+//     lower token). A row where too many reach the bound (equal values) is searched in K rounds instead.
+// Only what is above -inf is a candidate; rows with fewer than K such tokens are filled with the lowest of the others.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -32,39 +31,34 @@
 namespace dfl {
 namespace {
 
-constexpr int kPickThreads = 256, kPickWarps = kPickThreads / 32;
-constexpr int kPickElems = 64;                             // tokens a thread holds
-constexpr int kPickSlice = kPickThreads * kPickElems;
-constexpr int kPickRows = 32;                              // rows a chunk
-constexpr int kPickList = 1024;
+constexpr int kWindowLog = 15, kWindow = 1 << kWindowLog;  // tokens a CTA names
+constexpr int kNameThreads = kWindow / 32;                 // a word of bits each
+constexpr int kTile = 1024;                                // tokens a warp reads at a time,
+constexpr int kLaneTokens = 32;                            // of which a lane has
+constexpr int kStreamWarps = 8, kStreamTiles = 2;          // warps a CTA, tiles a warp
+constexpr int kSelectThreads = 256, kSelectWarps = kSelectThreads / 32;
+constexpr int kEntries = 2048, kLanes = 1024;              // that reach the bound
 constexpr int kPickK = 16;
 constexpr uint32_t kCountMask = (1u << 20) - 1, kInPrompt = 1u << 20;  // a counter; over it, which bias
 constexpr int kBiasShift = 21;
 
 struct PickArgs {
   LogitsTopk r;
-  int cluster, slice, subs, cap;  // CTAs a row, tokens a CTA, how often; counters that fit
+  int each;             // rows a request, 0: as row_off says
+  int windows, cap;     // windows of the vocabulary (0: nothing is named); counters a window
+  int words;            // of bits a request
+  int tiles;            // a row
+  uint32_t* bits;       // [B][words]
+  int* named;           // [B][windows] how many
+  uint2* names;         // [B][windows][cap] (token, counter)
+  int* request;         // [M] each row's, -1: none (row_off given)
+  uint64_t* line;       // [M] the row's drafted ancestors, 0: it is not there (tokens given)
+  uint32_t* keys;       // [M][tiles][32]
   int* err;
 };
 
-struct PickShared {
-  unsigned long long list[kPickList];
-  unsigned long long best[kPickRows][kPickK];  // (key, ~token), best first; 0: none
-  uint64_t line[kPickRows];                    // the row's drafted ancestors
-  unsigned long long red[kPickWarps];
-  int request[kPickRows], first[kPickRows], state[kPickRows];  // 0: no row of any request, 1: a row, 2: not there
-  uint32_t bits[kPickSlice / 32];
-  uint32_t group_max[16];
-  int count[2];
-  int warp_sum[kPickWarps];
-  uint16_t base[kPickSlice / 32];
-};
+__device__ __forceinline__ void record(int* err, int status) { atomicCAS(err, 0, status); }
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float y;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
-  return y;
-}
 // An order-preserving key; NaN above every number (and an entry of it below all ones).
 constexpr uint32_t kKeyNan = 0xfffffffeu;
 __device__ __forceinline__ uint32_t pick_key(float v) { return v != v ? kKeyNan : float_key(v); }
@@ -72,8 +66,201 @@ __device__ __forceinline__ float pick_value(uint32_t k) { return k == kKeyNan ? 
 __device__ __forceinline__ unsigned long long pick_entry(float v, int token) {
   return (static_cast<unsigned long long>(pick_key(v)) << 32) | static_cast<uint32_t>(~token);
 }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ unsigned long long max_u64(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
+__device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v) {
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  return (static_cast<unsigned long long>(hi) << 32) | lo;
+}
 
-// Sixteen bytes of logits.
+// ------------------------------------------------------------------ names
+// The history's tokens and their places, four of them a load and four loads in flight.
+template <typename F>
+__device__ __forceinline__ void for_history(const int32_t* hist, int len, F f) {
+  const int tid = static_cast<int>(threadIdx.x);
+  const int head = min(len, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(hist) & 15u)) & 15u) / 4);
+  const int quads = (len - head) / 4, tail = head + 4 * quads;
+  if (tid < head) f(__ldg(hist + tid), tid);
+  if (tid < len - tail) f(__ldg(hist + tail + tid), tail + tid);
+  const int4* wide = reinterpret_cast<const int4*>(hist + head);
+  for (int i = tid; i < quads; i += 4 * kNameThreads) {
+    int4 q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k * kNameThreads < quads) q[k] = __ldg(wide + i + k * kNameThreads);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (i + k * kNameThreads >= quads) break;
+      const int at = head + 4 * (i + k * kNameThreads);
+      f(q[k].x, at);
+      f(q[k].y, at + 1);
+      f(q[k].z, at + 2);
+      f(q[k].w, at + 3);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kNameThreads) logits_names_kernel(const PickArgs a) {
+  const LogitsTopk& r = a.r;
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  pdl_wait();
+  const int named_ctas = r.B * a.windows;
+  if (static_cast<int>(blockIdx.x) >= named_ctas) {
+    // ---- rows' requests: the last request that starts at or before the row, if its span holds the row
+    const int x = (static_cast<int>(blockIdx.x) - named_ctas) * kNameThreads + tid;
+    for (int b = x; b < r.B; b += static_cast<int>(gridDim.x - named_ctas) * kNameThreads) {
+      const int lo = __ldg(r.row_off + b), hi = __ldg(r.row_off + b + 1);
+      if (lo < 0 || hi < lo || hi > r.M) record(a.err, DFLASH2_ERR_INVALID_ARG);
+    }
+    if (x >= r.M) return;
+    int lo = 0, hi = r.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(r.row_off + mid) <= x)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    const int first = __ldg(r.row_off + lo);
+    bool in = first >= 0 && first <= x && x < __ldg(r.row_off + lo + 1);
+    if (in && r.tokens != nullptr && x - first >= kTreeRows) {
+      record(a.err, DFLASH2_ERR_INVALID_ARG);
+      in = false;
+    }
+    a.request[x] = in ? lo : -1;
+    return;
+  }
+  extern __shared__ uint32_t counters[];  // [cap]
+  __shared__ uint32_t bits[kNameThreads];
+  __shared__ uint16_t base[kNameThreads];
+  __shared__ int warp_sum[32];
+  __shared__ uint64_t there;              // the request's drafted rows that are there
+  const int b = static_cast<int>(blockIdx.x) / a.windows, window = static_cast<int>(blockIdx.x) - b * a.windows;
+  const int lo = window << kWindowLog, len = min(kWindow, r.V - lo);
+  const int32_t* hist = nullptr;
+  int hist_len = 0, prompt = 0;
+  if (r.history != nullptr) {
+    hist = r.history + b * r.history_stride;
+    hist_len = __ldg(r.history_len + b);
+    prompt = r.prompt_len != nullptr ? __ldg(r.prompt_len + b) : 0;
+    if ((hist_len < 0 || hist_len > r.max_len) && tid == 0) record(a.err, DFLASH2_ERR_INVALID_ARG);
+    hist_len = min(max(hist_len, 0), r.max_len);
+  }
+  bits[tid] = 0u;
+  int first = 0;
+  if (r.tokens != nullptr && warp == 0) {
+    // each drafted row's line of ancestors
+    int rows = a.each;
+    first = b * a.each;
+    if (a.each == 0) {
+      first = __ldg(r.row_off + b);
+      rows = min(__ldg(r.row_off + b + 1), r.M) - first;
+      if (first < 0) rows = 0;
+    }
+    rows = min(rows, kTreeRows);
+    int parent[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int t = lane + 32 * h;
+      parent[h] = t < rows ? (r.parents != nullptr ? __ldg(r.parents + first + t) : t - 1) : -2;
+    }
+    bool bad;
+    const TreeLines tree = tree_lines(parent, rows, bad);
+    if (bad) record(a.err, DFLASH2_ERR_BAD_INDEX);
+    const uint32_t in0 = __ballot_sync(0xffffffffu, tree.line[0] != 0ull), in1 = __ballot_sync(0xffffffffu, tree.line[1] != 0ull);
+    if (lane == 0) there = (static_cast<uint64_t>(in1) << 32) | in0;
+    if (window == 0)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (lane + 32 * h < rows) a.line[first + lane + 32 * h] = tree.line[h];
+  }
+  __syncthreads();
+  auto mark = [&](int t) {
+    const int u = t - lo;
+    if (t >= 0 && t < r.V) {
+      if (u >= 0 && u < len) atomicOr(&bits[u >> 5], 1u << (u & 31));
+    } else {
+      record(a.err, DFLASH2_ERR_BAD_INDEX);
+    }
+  };
+  const int32_t* bias_ids = r.bias_ids + static_cast<int64_t>(b) * r.n_bias;
+  for_history(hist, hist_len, [&](int t, int) { mark(t); });
+  if (r.tokens != nullptr && warp == 0)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if ((there >> (lane + 32 * h)) & 1) mark(__ldg(r.tokens + first + lane + 32 * h));
+  for (int e = tid; e < r.n_bias; e += kNameThreads) {
+    const int t = __ldg(bias_ids + e);
+    if (t >= 0) mark(t);
+  }
+  __syncthreads();
+  // a named token's counter is the one of its rank among the set bits
+  const uint32_t mine = bits[tid];
+  int sum = __popc(mine);
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sum, m);
+    if (lane >= m) sum += v;
+  }
+  if (lane == 31) warp_sum[warp] = sum;
+  __syncthreads();
+  int total = warp_sum[lane];
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, total, m);
+    if (lane >= m) total += v;
+  }
+  const int before = __shfl_sync(0xffffffffu, total, max(0, warp - 1));
+  const int n = __shfl_sync(0xffffffffu, total, 31);
+  const int at = (warp > 0 ? before : 0) + sum - __popc(mine);
+  base[tid] = static_cast<uint16_t>(at);
+  for (int k = tid; k < n; k += kNameThreads) counters[k] = 0u;
+  if ((lo >> 5) + tid < a.words) a.bits[static_cast<int64_t>(b) * a.words + (lo >> 5) + tid] = mine;
+  if (tid == 0) a.named[b * a.windows + window] = n;
+  __syncthreads();
+  auto counter = [&](int u) { return counters + base[u >> 5] + __popc(bits[u >> 5] & ((1u << (u & 31)) - 1u)); };
+  if (r.n_bias > 0) {
+    for (int e = tid; e < r.n_bias; e += kNameThreads) {
+      const int u = __ldg(bias_ids + e) - lo;
+      if (u >= 0 && u < len) atomicMax(counter(u), static_cast<uint32_t>(r.n_bias - e) << kBiasShift);
+    }
+    __syncthreads();
+  }
+  for_history(hist, hist_len, [&](int t, int place) {
+    const int u = t - lo;
+    if (u < 0 || u >= len) return;
+    if (place < prompt)
+      atomicOr(counter(u), kInPrompt);
+    else
+      atomicAdd(counter(u), 1u);
+  });
+  __syncthreads();
+  uint2* names = a.names + static_cast<int64_t>(b * a.windows + window) * a.cap;
+  int k = at;
+  for (uint32_t w = mine; w != 0u; w &= w - 1u, ++k)
+    names[k] = make_uint2(static_cast<uint32_t>(lo + tid * 32 + __ffs(w) - 1), counters[k]);
+}
+
+// ------------------------------------------------------------------ stream
+// Sixteen bytes of logits. (No loads by the read-only path: `out` may be the same buffer.)
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 u;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+               : "l"(p));
+  return u;
+}
 template <typename T>
 struct PickVec;
 template <>
@@ -89,21 +276,22 @@ struct PickVec<float> {
     if (bits & 4u) u.z = 0xff800000u;
     if (bits & 8u) u.w = 0xff800000u;
   }
-  static __device__ __forceinline__ float max(const uint4& u) {
-    return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)), max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
+  static __device__ __forceinline__ float max(float m, const uint4& u) {
+    return max3_nan(max3_nan(m, __uint_as_float(u.x), __uint_as_float(u.y)), __uint_as_float(u.z), __uint_as_float(u.w));
   }
-  static __device__ __forceinline__ uint4 load_some(const float* p, int n) {
+  // elements [from, to) of them; the others are -inf
+  static __device__ __forceinline__ uint4 load_some(const float* p, int from, int to) {
     uint4 u;
-    u.x = n > 0 ? __float_as_uint(p[0]) : 0xff800000u;
-    u.y = n > 1 ? __float_as_uint(p[1]) : 0xff800000u;
-    u.z = n > 2 ? __float_as_uint(p[2]) : 0xff800000u;
-    u.w = n > 3 ? __float_as_uint(p[3]) : 0xff800000u;
+    u.x = from <= 0 && to > 0 ? __float_as_uint(p[0]) : 0xff800000u;
+    u.y = from <= 1 && to > 1 ? __float_as_uint(p[1]) : 0xff800000u;
+    u.z = from <= 2 && to > 2 ? __float_as_uint(p[2]) : 0xff800000u;
+    u.w = from <= 3 && to > 3 ? __float_as_uint(p[3]) : 0xff800000u;
     return u;
   }
-  static __device__ __forceinline__ void store_some(float* p, const uint4& u, int n) {
+  static __device__ __forceinline__ void store_some(float* p, const uint4& u, int from, int to) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (j < n) p[j] = get(u, j);
+      if (j >= from && j < to) p[j] = get(u, j);
   }
   static __device__ __forceinline__ float load(const float* p) { return *p; }
   static __device__ __forceinline__ void store(float* p, float v) { *p = v; }
@@ -113,10 +301,6 @@ struct PickVec<__nv_bfloat16> {
   static constexpr int kN = 8;
   static __device__ __forceinline__ uint32_t word(const uint4& u, int i) {
     return i == 0 ? u.x : (i == 1 ? u.y : (i == 2 ? u.z : u.w));
-  }
-  static __device__ __forceinline__ float get(const uint4& u, int j) {
-    const uint32_t w = word(u, j >> 1);
-    return __uint_as_float((j & 1) ? (w & 0xffff0000u) : (w << 16));
   }
   static __device__ __forceinline__ uint32_t drop2(uint32_t w, uint32_t bits) {
     if (bits & 1u) w = (w & 0xffff0000u) | 0xff80u;
@@ -130,455 +314,369 @@ struct PickVec<__nv_bfloat16> {
     u.w = drop2(u.w, bits >> 6);
   }
   static __device__ __forceinline__ __nv_bfloat162 two(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
-  static __device__ __forceinline__ float max(const uint4& u) {
-    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(two(u.x), two(u.y)), __hmax2_nan(two(u.z), two(u.w)));
-    return max_nan(__low2float(m), __high2float(m));
+  static __device__ __forceinline__ float max(float m, const uint4& u) {
+    const __nv_bfloat162 x = __hmax2_nan(__hmax2_nan(two(u.x), two(u.y)), __hmax2_nan(two(u.z), two(u.w)));
+    return max3_nan(m, __low2float(x), __high2float(x));
   }
-  static __device__ __forceinline__ uint4 load_some(const __nv_bfloat16* p, int n) {
+  static __device__ __forceinline__ uint4 load_some(const __nv_bfloat16* p, int from, int to) {
+    const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t lo = 2 * i < n ? reinterpret_cast<const unsigned short*>(p)[2 * i] : 0xff80u;
-      const uint32_t hi = 2 * i + 1 < n ? reinterpret_cast<const unsigned short*>(p)[2 * i + 1] : 0xff80u;
+      const uint32_t lo = 2 * i >= from && 2 * i < to ? q[2 * i] : 0xff80u;
+      const uint32_t hi = 2 * i + 1 >= from && 2 * i + 1 < to ? q[2 * i + 1] : 0xff80u;
       w[i] = lo | (hi << 16);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
-  static __device__ __forceinline__ void store_some(__nv_bfloat16* p, const uint4& u, int n) {
+  static __device__ __forceinline__ void store_some(__nv_bfloat16* p, const uint4& u, int from, int to) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (j < n) reinterpret_cast<unsigned short*>(p)[j] = static_cast<unsigned short>(word(u, j >> 1) >> (16 * (j & 1)));
+      if (j >= from && j < to) reinterpret_cast<unsigned short*>(p)[j] = static_cast<unsigned short>(word(u, j >> 1) >> (16 * (j & 1)));
   }
   static __device__ __forceinline__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   static __device__ __forceinline__ void store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 };
 
-__device__ __forceinline__ unsigned long long max_u64(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
-__device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v) {
-  const uint32_t hi = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32));
-  const uint32_t lo = __reduce_max_sync(0xffffffffu, static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
-  return (static_cast<unsigned long long>(hi) << 32) | lo;
+// A row: its request (-1: it belongs to none, or is not there), and its first element's place in sixteen bytes: the
+// tiles lie on sixteen-byte boundaries, tile x's lane l has tokens x 1024 + g 32 n + l n - off + (0 .. n - 1).
+struct PickRow {
+  int request, first;
+  bool missing;  // a drafted row that is not there
+};
+__device__ __forceinline__ PickRow pick_row(const PickArgs& a, int m) {
+  PickRow p;
+  p.request = a.each > 0 ? m / a.each : a.request[m];
+  p.first = a.each > 0 ? p.request * a.each : (p.request >= 0 ? __ldg(a.r.row_off + p.request) : 0);
+  p.missing = p.request >= 0 && a.r.tokens != nullptr && a.line[m] == 0ull;
+  return p;
 }
-__device__ __forceinline__ unsigned long long ld_cluster_u64(uint32_t addr) {
-  unsigned long long v;
-  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(addr));
-  return v;
+template <typename T>
+__device__ __forceinline__ int row_offset(const T* row) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+}
+// Bits t .. t + 31 of a row of `words` words (0 outside them); t may be negative, by less than 32.
+__device__ __forceinline__ uint32_t bits_from(const uint32_t* w, int words, int t) {
+  const int i = t >> 5;
+  const uint32_t lo = i >= 0 && i < words ? __ldg(w + i) : 0u;
+  if ((t & 31) == 0) return lo;
+  return __funnelshift_r(lo, i + 1 < words ? __ldg(w + i + 1) : 0u, t & 31);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kPickThreads, 2) logits_topk_kernel(const PickArgs a) {
+__global__ void __launch_bounds__(32 * kStreamWarps) logits_stream_kernel(const PickArgs a, int ctas_a_row) {
   using Vec = PickVec<T>;
-  constexpr int kN = Vec::kN, kGroups = kPickElems / kN;
+  constexpr int kN = Vec::kN, kG = kLaneTokens / kN;
   constexpr uint32_t kAll = (1u << kN) - 1;
-  __shared__ PickShared s;
-  extern __shared__ __align__(16) uint8_t pick_smem[];
-  uint32_t* words = reinterpret_cast<uint32_t*>(pick_smem);       // [cap] counters of the named tokens
-  float* vals = reinterpret_cast<float*>(words + a.cap);          // [cap] their adjusted values
-  uint16_t* offs = reinterpret_cast<uint16_t*>(vals + a.cap);     // [cap] their places in the slice
   const LogitsTopk& r = a.r;
-  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  const int rank = static_cast<int>(cluster_ctarank());
-  const int cluster = static_cast<int>(blockIdx.x) / a.cluster, clusters = static_cast<int>(gridDim.x) / a.cluster;
-  const int row0 = static_cast<int>(static_cast<long long>(r.M) * cluster / clusters);
-  const int row1 = static_cast<int>(static_cast<long long>(r.M) * (cluster + 1) / clusters);
-  const bool named = a.cap > 0;
+  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+  const int m = static_cast<int>(blockIdx.x) / ctas_a_row;
+  const int tile0 = ((static_cast<int>(blockIdx.x) - m * ctas_a_row) * kStreamWarps + warp) * kStreamTiles;
   pdl_trigger();
   pdl_wait();
-  auto record = [&](int status) { atomicCAS(a.err, 0, status); };
-  if (blockIdx.x == 0 && r.row_off != nullptr)
-    for (int b = tid; b < r.B; b += kPickThreads) {
-      const int lo = __ldg(r.row_off + b), hi = __ldg(r.row_off + b + 1);
-      if (lo < 0 || hi < lo || hi > r.M) record(DFLASH2_ERR_INVALID_ARG);
+  const PickRow p = pick_row(a, m);
+  if (p.request < 0 || p.missing) return;
+  const T* row = static_cast<const T*>(r.logits) + static_cast<int64_t>(m) * r.stride;
+  T* out = r.out != nullptr ? static_cast<T*>(r.out) + static_cast<int64_t>(m) * r.out_stride : nullptr;
+  const int off = row_offset(row), mask_words = (r.V + 31) / 32;
+  const bool out_wide = out != nullptr && row_offset(out) == off;
+  const uint32_t* mask = r.mask != nullptr ? reinterpret_cast<const uint32_t*>(r.mask) + static_cast<int64_t>(m) * r.mask_stride : nullptr;
+  const uint32_t* named = a.windows > 0 ? a.bits + static_cast<int64_t>(p.request) * a.words : nullptr;
+  for (int tile = tile0; tile < min(tile0 + kStreamTiles, a.tiles); ++tile) {
+    const int t0 = tile * kTile - off;  // the tile's first token
+    const bool inside = t0 >= 0 && t0 + kTile <= r.V;
+    uint4 v[kG];
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      const int t = t0 + (g * 32 + lane) * kN;
+      if (inside || (t >= 0 && t + kN <= r.V))
+        v[g] = load16(row + t);
+      else
+        v[g] = Vec::load_some(row + t, -t, r.V - t);
     }
-  const int each = r.row_off == nullptr ? r.M / r.B : 0;
-  int turn = 0;
-
-  for (int c0 = row0; c0 < row1; c0 += kPickRows) {
-    const int rows = min(kPickRows, row1 - c0);
-    // ---- the chunk's rows: their requests and lines of ancestors
-    if (tid < rows) {
-      const int m = c0 + tid;
-      int b, first, state = 1;
-      if (each > 0) {
-        b = m / each;
-        first = b * each;
-      } else {
-        int lo = 0, hi = r.B - 1;  // the last request that starts at or before the row
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (__ldg(r.row_off + mid) <= m)
-            lo = mid;
-          else
-            hi = mid - 1;
-        }
-        b = lo;
-        first = __ldg(r.row_off + b);
-        if (first < 0 || first > m || m >= __ldg(r.row_off + b + 1)) state = 0;
-      }
-      if (state == 1 && r.tokens != nullptr && m - first >= kTreeRows) {
-        record(DFLASH2_ERR_INVALID_ARG);
-        state = 0;
-      }
-      s.request[tid] = b;
-      s.first[tid] = first;
-      s.state[tid] = state;
-      s.line[tid] = (2ull << min(max(m - first, 0), kTreeRows - 1)) - 1;  // (without parents: every row before it)
+    // lane l holds bits 32 l .. of the tile: what is not allowed, and what is named
+    const uint32_t denied = mask != nullptr ? ~bits_from(mask, mask_words, t0 + 32 * lane) : 0u;
+    const uint32_t taken = named != nullptr ? bits_from(named, a.words, t0 + 32 * lane) : 0u;
+    auto share = [&](uint32_t w, int g) {  // the bits of the lane's g-th sixteen bytes
+      return (__shfl_sync(0xffffffffu, w, (g * 32 + lane) * kN / 32) >> (lane * kN & 31)) & kAll;
+    };
+    if (__any_sync(0xffffffffu, denied != 0u)) {
+#pragma unroll
+      for (int g = 0; g < kG; ++g) Vec::drop(v[g], share(denied, g));
     }
-    __syncthreads();
-    if (r.tokens != nullptr && r.parents != nullptr) {
-      int heads = 0;
-      for (int i = 0; i < rows; ++i) {
-        if (s.state[i] == 0 || (i > 0 && s.state[i - 1] != 0 && s.request[i - 1] == s.request[i])) continue;
-        if ((heads++ & (kPickWarps - 1)) != warp) continue;
-        const int b = s.request[i], first = s.first[i];
-        const int all = each > 0 ? each : min(__ldg(r.row_off + b + 1), r.M) - first;
-        int parent[2];
+    if (out != nullptr)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) parent[h] = lane + 32 * h < all ? __ldg(r.parents + first + lane + 32 * h) : -2;
-        bool bad;
-        const TreeLines tree = tree_lines(parent, min(all, kTreeRows), bad);
-        if (bad) record(DFLASH2_ERR_BAD_INDEX);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int at = first + lane + 32 * h - c0;
-          if (at >= i && at < rows && s.state[at] == 1 && s.request[at] == b) s.line[at] = tree.line[h];
-        }
+      for (int g = 0; g < kG; ++g) {
+        const int t = t0 + (g * 32 + lane) * kN;
+        if (out_wide && t >= 0 && t + kN <= r.V)
+          *reinterpret_cast<uint4*>(out + t) = v[g];
+        else
+          Vec::store_some(out + t, v[g], -t, r.V - t);
       }
-      __syncthreads();
-      if (tid < rows && s.state[tid] == 1 && s.line[tid] == 0ull) s.state[tid] = 2;
-      __syncthreads();
+    if (r.K == 0) continue;
+    if (__any_sync(0xffffffffu, taken != 0u)) {
+#pragma unroll
+      for (int g = 0; g < kG; ++g) Vec::drop(v[g], share(taken, g));
     }
-
-    for (int sub = 0; sub < a.subs; ++sub) {
-      const int lo = (sub * a.cluster + rank) * a.slice;
-      const int wlen = max(0, min(a.slice, r.V - lo));
-      for (int i0 = 0; i0 < rows;) {
-        // ---- rows [i0, i1) of one request
-        const int b = s.request[i0];
-        int i1 = i0 + 1;
-        while (i1 < rows && s.request[i1] == b && s.state[i1] != 0 && s.state[i0] != 0) ++i1;
-        const int seg0 = i0;
-        i0 = i1;
-        if (s.state[seg0] == 0) continue;
-        const int first = s.first[seg0];
-        int n = 0;  // named tokens of the slice
-        auto rank_of = [&](int u) { return s.base[u >> 5] + __popc(s.bits[u >> 5] & ((1u << (u & 31)) - 1u)); };
-        if (named) {
-          const int32_t* hist = r.history != nullptr ? r.history + b * r.history_stride : nullptr;
-          int len = 0, prompt = 0;
-          if (hist != nullptr) {
-            len = __ldg(r.history_len + b);
-            prompt = r.prompt_len != nullptr ? __ldg(r.prompt_len + b) : 0;
-            if ((len < 0 || len > r.max_len) && tid == 0) record(DFLASH2_ERR_INVALID_ARG);
-            len = min(max(len, 0), r.max_len);
-          }
-          __syncthreads();  // (the segment before is done with these)
-          for (int i = tid; i < kPickSlice / 32; i += kPickThreads) s.bits[i] = 0u;
-          __syncthreads();
-          auto mark = [&](int t) {
-            const int u = t - lo;
-            if (t >= 0 && t < r.V) {
-              if (u >= 0 && u < wlen) atomicOr(&s.bits[u >> 5], 1u << (u & 31));
-            } else {
-              record(DFLASH2_ERR_BAD_INDEX);
-            }
-          };
-          for (int i = tid; i < len; i += kPickThreads) mark(__ldg(hist + i));
-          if (r.tokens != nullptr && tid < kTreeRows) {
-            uint64_t any = 0;
-            for (int i = seg0; i < i1; ++i) any |= s.line[i];
-            if ((any >> tid) & 1) mark(__ldg(r.tokens + first + tid));
-          }
-          for (int e = tid; e < r.n_bias; e += kPickThreads) {
-            const int t = __ldg(r.bias_ids + static_cast<int64_t>(b) * r.n_bias + e);
-            if (t >= 0) mark(t);
-          }
-          __syncthreads();
-          const uint32_t w0 = s.bits[2 * tid], w1 = s.bits[2 * tid + 1];
-          const int mine = __popc(w0) + __popc(w1);
-          int inc = mine;
+    float top = -INFINITY;
 #pragma unroll
-          for (int m = 1; m < 32; m <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, inc, m);
-            if (lane >= m) inc += v;
-          }
-          if (lane == 31) s.warp_sum[warp] = inc;
-          __syncthreads();
-          int at = inc - mine;
-          for (int w = 0; w < kPickWarps; ++w) {
-            if (w < warp) at += s.warp_sum[w];
-            n += s.warp_sum[w];
-          }
-          s.base[2 * tid] = static_cast<uint16_t>(at);
-          s.base[2 * tid + 1] = static_cast<uint16_t>(at + __popc(w0));
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            for (uint32_t w = h == 0 ? w0 : w1; w != 0u; w &= w - 1u) {
-              offs[at] = static_cast<uint16_t>((2 * tid + h) * 32 + __ffs(w) - 1);
-              words[at++] = 0u;
-            }
-          __syncthreads();
-          for (int e = tid; e < r.n_bias; e += kPickThreads) {
-            const int u = __ldg(r.bias_ids + static_cast<int64_t>(b) * r.n_bias + e) - lo;
-            if (u >= 0 && u < wlen) atomicMax(&words[rank_of(u)], static_cast<uint32_t>(r.n_bias - e) << kBiasShift);
-          }
-          __syncthreads();
-          for (int i = tid; i < len; i += kPickThreads) {
-            const int u = __ldg(hist + i) - lo;
-            if (u < 0 || u >= wlen) continue;
-            if (i < prompt)
-              atomicOr(&words[rank_of(u)], kInPrompt);
-            else
-              atomicAdd(&words[rank_of(u)], 1u);
-          }
-        }
-        const float rep = r.repetition != nullptr ? __ldg(r.repetition + b) : 1.f;
-        const float freq = r.frequency != nullptr ? __ldg(r.frequency + b) : 0.f;
-        const float pres = r.presence != nullptr ? __ldg(r.presence + b) : 0.f;
-
-        for (int i = seg0; i < i1; ++i) {
-          if (s.state[i] != 1) continue;
-          const int64_t m = c0 + i;
-          const T* row = static_cast<const T*>(r.logits) + m * r.stride + lo;
-          T* out = r.out != nullptr ? static_cast<T*>(r.out) + m * r.out_stride + lo : nullptr;
-          const uint32_t* allowed = r.mask != nullptr ? reinterpret_cast<const uint32_t*>(r.mask) + m * r.mask_stride + (lo >> 5) : nullptr;
-          const bool wide = (reinterpret_cast<uintptr_t>(row) & 15u) == 0;
-          const bool out_wide = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-          uint4 v[kGroups];
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            const int e = (g * kPickThreads + tid) * kN;
-            if (wide && e + kN <= wlen)
-              v[g] = *reinterpret_cast<const uint4*>(row + e);  // (not by the read-only path: out may be the same buffer)
-            else
-              v[g] = Vec::load_some(row + e, wlen - e);
-          }
-          // the drafted ancestors' tokens count for this row
-          const uint64_t line = r.tokens != nullptr ? s.line[i] : 0ull;
-          auto count_line = [&](uint32_t d) {
-            if (tid < kTreeRows && ((line >> tid) & 1)) {
-              const int u = __ldg(r.tokens + first + tid) - lo;
-              if (u >= 0 && u < wlen) atomicAdd(&words[rank_of(u)], d);
-            }
-          };
-          count_line(1u);
-          int* count = &s.count[turn ^= 1];  // (the one before may still be read)
-          if (tid == 0) *count = 0;
-          __syncthreads();
-          float top = -INFINITY;
-          for (int k = tid; k < n; k += kPickThreads) {
-            const int u = offs[k];
-            const uint32_t w = words[k];
-            const uint32_t times = w & kCountMask;
-            float y = Vec::load(row + u);
-            if ((w & (kCountMask | kInPrompt)) != 0u) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
-            if (times != 0u) y = __fsub_rn(y, __fadd_rn(__fmul_rn(freq, static_cast<float>(times)), pres));
-            if ((w >> kBiasShift) != 0u)
-              y = __fadd_rn(y, __ldg(r.bias + static_cast<int64_t>(b) * r.n_bias + (r.n_bias - static_cast<int>(w >> kBiasShift))));
-            if (allowed != nullptr && !((__ldg(allowed + (u >> 5)) >> (u & 31)) & 1u)) y = -INFINITY;
-            vals[k] = y;
-            top = max_nan(top, y);
-          }
-#pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
-            const int e = (g * kPickThreads + tid) * kN;
-            if (e >= wlen) continue;
-            if (allowed != nullptr) Vec::drop(v[g], ~(__ldg(allowed + (e >> 5)) >> (e & 31)) & kAll);
-            if (out != nullptr) {
-              if (out_wide && e + kN <= wlen)
-                *reinterpret_cast<uint4*>(out + e) = v[g];
-              else
-                Vec::store_some(out + e, v[g], wlen - e);
-            }
-            if (n > 0) Vec::drop(v[g], (s.bits[e >> 5] >> (e & 31)) & kAll);
-            top = max_nan(top, Vec::max(v[g]));
-          }
-          const uint32_t key = pick_key(top);
-          const uint32_t most = __reduce_max_sync(lane < 16 ? 0x0000ffffu : 0xffff0000u, key);
-          if ((lane & 15) == 0) s.group_max[tid >> 4] = most;
-          __syncthreads();
-          count_line(~0u);
-          if (out != nullptr)
-            for (int k = tid; k < n; k += kPickThreads) Vec::store(out + offs[k], vals[k]);
-          if (r.K == 0) continue;
-          // the K-th largest of the groups' maxima
-          const uint32_t g = s.group_max[lane & 15];
-          int above = 0;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint32_t o = __shfl_sync(0xffffffffu, g, j);
-            above += o > g || (o == g && j < (lane & 15)) ? 1 : 0;
-          }
-          const uint32_t holder = __ballot_sync(0xffffffffu, above == r.K - 1);
-          const uint32_t bound_key = __shfl_sync(0xffffffffu, g, __ffs(holder) - 1);
-          const float bound = pick_value(bound_key);
-          const unsigned long long prior = sub > 0 && tid < r.K ? s.best[i][tid] : 0ull;
-          auto list = [&](unsigned long long entry) {
-            const int at = atomicAdd(count, 1);
-            if (at < kPickList) s.list[at] = entry;
-          };
-          auto reaches = [&](float x) { return !(x < bound) && x != -INFINITY; };
-          if (prior != 0ull) list(prior);
-          for (int k = tid; k < n; k += kPickThreads)
-            if (reaches(vals[k])) list(pick_entry(vals[k], lo + offs[k]));
-#pragma unroll
-          for (int q = 0; q < kGroups; ++q) {
-            if (!reaches(Vec::max(v[q]))) continue;
-            const int e = (q * kPickThreads + tid) * kN;
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-              if (reaches(Vec::get(v[q], j))) list(pick_entry(Vec::get(v[q], j), lo + e + j));
-          }
-          __syncthreads();
-          const int listed = *count;
-          if (listed <= kPickList) {
-            for (int x = tid; x < listed; x += kPickThreads) {
-              const unsigned long long mine = s.list[x];
-              int before = 0;
-              for (int y = 0; y < listed; ++y) before += s.list[y] > mine ? 1 : 0;
-              if (before < r.K) s.best[i][before] = mine;
-            }
-            if (tid < r.K && tid >= listed) s.best[i][tid] = 0ull;
-          } else {
-            unsigned long long last = ~0ull;
-            for (int k = 0; k < r.K; ++k) {
-              unsigned long long mine = prior < last ? prior : 0ull;
-              auto look = [&](float x, int token) {
-                if (x == -INFINITY) return;
-                const unsigned long long entry = pick_entry(x, token);
-                if (entry < last) mine = max_u64(mine, entry);
-              };
-              for (int x = tid; x < n; x += kPickThreads) look(vals[x], lo + offs[x]);
-#pragma unroll
-              for (int q = 0; q < kGroups; ++q) {
-                const int e = (q * kPickThreads + tid) * kN;
-#pragma unroll
-                for (int j = 0; j < kN; ++j) look(Vec::get(v[q], j), lo + e + j);
-              }
-              mine = warp_max_u64(mine);
-              __syncthreads();
-              if (lane == 0) s.red[warp] = mine;
-              __syncthreads();
-              unsigned long long all = 0ull;
-              for (int w = 0; w < kPickWarps; ++w) all = max_u64(all, s.red[w]);
-              if (tid == 0) s.best[i][k] = all;
-              last = all;  // (0, when nothing is left: then nothing is below it)
-            }
-          }
-        }
-      }
-    }
-    if (r.K > 0) {
-      // ---- the cluster's lists of each row, merged by one warp
-      cluster_sync_all();
-      for (int i = rank + a.cluster * warp; i < rows; i += a.cluster * kPickWarps) {
-        if (s.state[i] == 0) continue;
-        const int64_t m = c0 + i;
-        int token = -1;
-        float value = -INFINITY;
-        if (s.state[i] == 1) {
-          unsigned long long mine[8];  // 16 lists of 16 entries at most
-          const uint32_t at = smem_u32(&s.best[i][lane & 15]);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int from = 2 * q + (lane >> 4);
-            mine[q] = from < a.cluster && (lane & 15) < r.K ? ld_cluster_u64(mapa_shared(at, static_cast<uint32_t>(from))) : 0ull;
-          }
-          int found = 0;
-          for (; found < r.K; ++found) {
-            unsigned long long top = 0ull;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) top = max_u64(top, mine[q]);
-            top = warp_max_u64(top);
-            if (top == 0ull) break;
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              if (mine[q] == top) mine[q] = 0ull;
-            if (lane == found) {
-              token = static_cast<int>(~static_cast<uint32_t>(top));
-              value = pick_value(static_cast<uint32_t>(top >> 32));
-            }
-          }
-          // fewer than K tokens above -inf: all of them are here, and the lowest others follow
-          for (int t = 0; found < r.K; ++t)
-            if (__ballot_sync(0xffffffffu, token == t) == 0u) {
-              if (lane == found) token = t;
-              ++found;
-            }
-        }
-        if (lane < r.K) {
-          r.cand[m * r.K + lane] = token;
-          r.unary[m * r.K + lane] = value;
-        }
-      }
-      cluster_sync_all();  // (before the lists are written again, and before a CTA leaves)
-    }
+    for (int g = 0; g < kG; ++g) top = Vec::max(top, v[g]);
+    a.keys[(static_cast<int64_t>(m) * a.tiles + tile) * 32 + lane] = pick_key(top);
   }
 }
 
-struct PickPlan {
-  int cluster, slice, subs, cap, clusters;
-  size_t smem;
+// ------------------------------------------------------------------ select
+struct SelectShared {
+  unsigned long long entry[kEntries];
+  unsigned long long best[kPickK];
+  unsigned long long red[kSelectWarps];
+  int lane[kLanes];
+  alignas(16) uint32_t group_max[32];
+  int entries, lanes;
 };
-PickPlan pick_plan(const LogitsTopk& r, int sms) {
-  PickPlan p;
-  auto slice_of = [&](int cluster, int subs) {
-    const int n = cluster * subs;
-    return (((r.V + n - 1) / n) + 127) / 128 * 128;
+
+template <typename T>
+__global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const PickArgs a) {
+  using Vec = PickVec<T>;
+  constexpr int kN = Vec::kN;
+  __shared__ SelectShared s;
+  const LogitsTopk& r = a.r;
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int m = static_cast<int>(blockIdx.x);
+  if (tid == 0) s.entries = s.lanes = 0;
+  if (tid < kPickK) s.best[tid] = 0ull;
+  pdl_trigger();
+  pdl_wait();
+  const PickRow p = pick_row(a, m);
+  if (p.request < 0) return;
+  if (p.missing) {
+    if (tid < r.K) {
+      r.cand[static_cast<int64_t>(m) * r.K + tid] = -1;
+      r.unary[static_cast<int64_t>(m) * r.K + tid] = -INFINITY;
+    }
+    return;
+  }
+  const int b = p.request;
+  const T* row = static_cast<const T*>(r.logits) + static_cast<int64_t>(m) * r.stride;
+  T* out = r.out != nullptr ? static_cast<T*>(r.out) + static_cast<int64_t>(m) * r.out_stride : nullptr;
+  const int off = row_offset(row);
+  const uint32_t* mask = r.mask != nullptr ? reinterpret_cast<const uint32_t*>(r.mask) + static_cast<int64_t>(m) * r.mask_stride : nullptr;
+  const uint32_t* taken = a.windows > 0 ? a.bits + static_cast<int64_t>(b) * a.words : nullptr;
+  const float rep = r.repetition != nullptr ? __ldg(r.repetition + b) : 1.f;
+  const float freq = r.frequency != nullptr ? __ldg(r.frequency + b) : 0.f;
+  const float pres = r.presence != nullptr ? __ldg(r.presence + b) : 0.f;
+  // the drafted tokens on the row's line, one or two a lane of every warp
+  uint64_t line = 0;
+  int drafted[2] = {-1, -1};
+  if (r.tokens != nullptr) {
+    line = a.line[m] & ((2ull << min(m - p.first, kTreeRows - 1)) - 1ull);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if ((line >> (lane + 32 * h)) & 1) drafted[h] = __ldg(r.tokens + p.first + lane + 32 * h);
+  }
+  auto allowed = [&](int t) { return mask == nullptr || ((__ldg(mask + (t >> 5)) >> (t & 31)) & 1u); };
+  // f(token, value) of every named token that is the thread's (whole warps)
+  auto for_named = [&](auto f) {
+    for (int w = 0; w < a.windows; ++w) {
+      const int n = __ldg(a.named + b * a.windows + w);
+      const uint2* names = a.names + static_cast<int64_t>(b * a.windows + w) * a.cap;
+      for (int k0 = warp * 32; k0 < n; k0 += kSelectThreads) {
+        const bool mine = k0 + lane < n;
+        const uint2 name = mine ? __ldg(names + k0 + lane) : make_uint2(0xffffffffu, 0u);
+        const int t = static_cast<int>(name.x);
+        uint32_t times = name.y & kCountMask;
+        for (uint64_t left = line; left != 0ull; left &= left - 1ull) {
+          const int from = __ffsll(static_cast<long long>(left)) - 1;
+          if (__shfl_sync(0xffffffffu, from < 32 ? drafted[0] : drafted[1], from & 31) == t) ++times;
+        }
+        if (!mine) continue;
+        float y = Vec::load(row + t);
+        if (times != 0u || (name.y & kInPrompt) != 0u) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
+        if (times != 0u) y = __fsub_rn(y, __fadd_rn(__fmul_rn(freq, static_cast<float>(times)), pres));
+        if ((name.y >> kBiasShift) != 0u)
+          y = __fadd_rn(y, __ldg(r.bias + static_cast<int64_t>(b) * r.n_bias + (r.n_bias - static_cast<int>(name.y >> kBiasShift))));
+        if (!allowed(t)) y = -INFINITY;
+        f(t, y);
+      }
+    }
   };
-  p.cluster = 1;
-  while (p.cluster < 16 && static_cast<int64_t>(p.cluster) * kPickSlice < r.V) p.cluster *= 2;
-  // few rows: more CTAs a row, down to 1024 tokens each
-  while (p.cluster < 16 && static_cast<int64_t>(r.M) * p.cluster < 2 * sms && r.V / (2 * p.cluster) >= 1024) p.cluster *= 2;
-  p.subs = static_cast<int>((r.V + static_cast<int64_t>(p.cluster) * kPickSlice - 1) / (static_cast<int64_t>(p.cluster) * kPickSlice));
-  p.slice = slice_of(p.cluster, p.subs);
-  const bool named = r.history != nullptr || r.tokens != nullptr || r.n_bias > 0;
-  const int most = (r.history != nullptr ? r.max_len : 0) + (r.tokens != nullptr ? kTreeRows : 0) + r.n_bias;
-  p.cap = named ? (std::min(p.slice, most) + 7) / 8 * 8 : 0;
-  p.smem = static_cast<size_t>(p.cap) * 10;
-  // as many clusters as fit at once, each a range of rows
-  const int per_sm = std::max(1, std::min(2, static_cast<int>(227 * 1024 / (sizeof(PickShared) + p.smem + 1024))));
-  p.clusters = std::max(1, std::min(r.M, sms * per_sm / p.cluster));
+  // (with in-place out a named token's logit is read before it is replaced: the second look takes what stands there)
+  float top_named = -INFINITY;
+  if (r.K == 0) {
+    for_named([&](int t, float y) { Vec::store(out + t, y); });
+    return;
+  }
+  for_named([&](int, float y) { top_named = max_nan(top_named, y); });
+  const uint32_t* keys = a.keys + static_cast<int64_t>(m) * a.tiles * 32;
+  uint32_t top = 0u;
+  for (int k = tid; k < a.tiles * 8; k += kSelectThreads) {
+    const uint4 q = *reinterpret_cast<const uint4*>(keys + 4 * k);
+    top = max(max(max(top, q.x), max(q.y, q.z)), q.w);
+  }
+  uint32_t most = max(top, pick_key(top_named));
+#pragma unroll
+  for (int x = 1; x < 8; x <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
+  // (the lowest bits tell groups apart: the K-th largest is one of them, and without these bits not above it)
+  if ((lane & 7) == 0) s.group_max[tid >> 3] = (most & ~31u) | static_cast<uint32_t>(tid >> 3);
+  __syncthreads();
+  const uint32_t g = s.group_max[lane];
+  int above = 0;
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    const uint4 o = *reinterpret_cast<const uint4*>(&s.group_max[j]);
+    above += (o.x > g) + (o.y > g) + (o.z > g) + (o.w > g);
+  }
+  const uint32_t holder = __ballot_sync(0xffffffffu, above == r.K - 1);
+  constexpr uint32_t kMinusInf = 0x007fffffu;  // the key of -inf
+  const uint32_t bound = max(__shfl_sync(0xffffffffu, g, __ffs(holder) - 1) & ~31u, kMinusInf + 1u);
+  auto enter = [&](float x, int token) {
+    if (pick_key(x) < bound) return;
+    const int at = atomicAdd(&s.entries, 1);
+    if (at < kEntries) s.entry[at] = pick_entry(x, token);
+  };
+  if (__any_sync(0xffffffffu, pick_key(top_named) >= bound)) for_named([&](int t, float y) { enter(y, t); });
+  if (top >= bound)
+    for (int k = tid; k < a.tiles * 8; k += kSelectThreads) {
+      const uint4 q = *reinterpret_cast<const uint4*>(keys + 4 * k);
+      const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (x[j] >= bound) {
+          const int at = atomicAdd(&s.lanes, 1);
+          if (at < kLanes) s.lane[at] = 4 * k + j;
+        }
+    }
+  __syncthreads();
+  auto free_value = [&](int t) {  // of a token that is allowed and not named, else -inf
+    if (taken != nullptr && ((__ldg(taken + (t >> 5)) >> (t & 31)) & 1u)) return -INFINITY;
+    return allowed(t) ? Vec::load(row + t) : -INFINITY;
+  };
+  // the tokens of the lanes that reach the bound, one a lane here
+  for (int k = warp; k < min(s.lanes, kLanes); k += kSelectWarps) {
+    const int x = s.lane[k];
+    const int t = (x >> 5) * kTile + ((lane / kN) * 32 + (x & 31)) * kN + lane % kN - off;
+    if (t >= 0 && t < r.V) enter(free_value(t), t);
+  }
+  __syncthreads();
+  const int n = s.entries;
+  if (n <= kEntries && s.lanes <= kLanes) {
+    for (int x = tid; x < n; x += kSelectThreads) {
+      const unsigned long long mine = s.entry[x];
+      int before = 0;
+      for (int y = 0; y < n; ++y) before += s.entry[y] > mine ? 1 : 0;
+      if (before < r.K) s.best[before] = mine;
+    }
+    __syncthreads();
+  } else {
+    unsigned long long last = ~0ull;
+#pragma unroll 1
+    for (int k = 0; k < r.K; ++k) {
+      unsigned long long mine = 0ull;
+      auto look = [&](int t, float x) {
+        if (x == -INFINITY) return;
+        const unsigned long long entry = pick_entry(x, t);
+        if (entry < last) mine = max_u64(mine, entry);
+      };
+      for_named(look);
+      for (int t = tid; t < r.V; t += kSelectThreads) look(t, free_value(t));
+      mine = warp_max_u64(mine);
+      if (lane == 0) s.red[warp] = mine;
+      __syncthreads();
+      unsigned long long all = 0ull;
+      for (int w = 0; w < kSelectWarps; ++w) all = max_u64(all, s.red[w]);
+      if (tid == 0) s.best[k] = all;
+      last = all;  // (0, when nothing is left: then nothing is below it)
+      __syncthreads();
+    }
+  }
+  if (out != nullptr) for_named([&](int t, float y) { Vec::store(out + t, y); });
+  if (warp > 0) return;
+  const unsigned long long mine = lane < r.K ? s.best[lane] : 0ull;
+  int token = mine != 0ull ? static_cast<int>(~static_cast<uint32_t>(mine)) : -1;
+  const float value = mine != 0ull ? pick_value(static_cast<uint32_t>(mine >> 32)) : -INFINITY;
+  // fewer than K tokens above -inf: all of them are here, and the lowest others follow
+  int found = __popc(__ballot_sync(0xffffffffu, mine != 0ull));
+  for (int t = 0; found < r.K; ++t)
+    if (__ballot_sync(0xffffffffu, token == t) == 0u) {
+      if (lane == found) token = t;
+      ++found;
+    }
+  if (lane < r.K) {
+    r.cand[static_cast<int64_t>(m) * r.K + lane] = token;
+    r.unary[static_cast<int64_t>(m) * r.K + lane] = value;
+  }
+}
+
+// Sizes, and where each part lies in the workspace.
+struct PickPlan {
+  int windows, cap, words, tiles;
+  size_t bits, named, names, request, line, keys, total;
+};
+PickPlan pick_plan(int M, int V, int B, bool ragged, int max_len, bool tokens, int n_bias, int K) {
+  PickPlan p{};
+  const int most = max_len + (tokens ? kTreeRows : 0) + n_bias;
+  p.windows = most > 0 ? (V + kWindow - 1) / kWindow : 0;
+  p.cap = std::min(kWindow, most);
+  p.words = (V + 31) / 32;
+  p.tiles = (V + 7 + kTile - 1) / kTile;  // (wherever in sixteen bytes a row begins)
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  const size_t parts = static_cast<size_t>(B) * p.windows;
+  p.bits = take(p.windows > 0 ? static_cast<size_t>(B) * p.words * 4 : 0);
+  p.named = take(parts * 4);
+  p.names = take(parts * p.cap * sizeof(uint2));
+  p.request = take(ragged ? static_cast<size_t>(M) * 4 : 0);
+  p.line = take(tokens ? static_cast<size_t>(M) * 8 : 0);
+  p.keys = take(K > 0 ? static_cast<size_t>(M) * p.tiles * 128 : 0);
+  p.total = at;
   return p;
 }
 
 template <typename T>
-int launch_pick_t(const PickArgs& a, const PickPlan& p, cudaStream_t st) {
-  constexpr int kMost = 10 * kPickSlice;
-  static_assert(kMost + sizeof(PickShared) <= 232448, "shared memory");
-  static unsigned done = 0, wide = 0;
-  auto kern = logits_topk_kernel<T>;
-  if (!ensure_smem_attr(kern, kMost, &done)) return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (logits)");
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return fail(DFLASH2_ERR_CUDA, "no device");
-  static std::mutex mu;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (!(wide & (1u << (dev & 31)))) {
-      if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (logits)");
-      wide |= 1u << (dev & 31);
-    }
-  }
-  cudaLaunchAttribute cl{};
-  cl.id = cudaLaunchAttributeClusterDimension;
-  cl.val.clusterDim.x = static_cast<unsigned>(p.cluster);
-  cl.val.clusterDim.y = 1;
-  cl.val.clusterDim.z = 1;
-  const cudaError_t e = launch_pdl(kern, dim3(static_cast<unsigned>(p.cluster * p.clusters)), dim3(kPickThreads), p.smem, st, &cl, 1, a);
+int launch_pick_t(const PickArgs& a, cudaStream_t st) {
+  const int ctas_a_row = (a.tiles + kStreamWarps * kStreamTiles - 1) / (kStreamWarps * kStreamTiles);
+  cudaError_t e = launch_pdl(logits_stream_kernel<T>, dim3(static_cast<unsigned>(a.r.M) * ctas_a_row), dim3(32 * kStreamWarps), 0,
+                             st, nullptr, 0, a, ctas_a_row);
+  if (e == cudaSuccess && (a.r.K > 0 || a.windows > 0))
+    e = launch_pdl(logits_select_kernel<T>, dim3(static_cast<unsigned>(a.r.M)), dim3(kSelectThreads), 0, st, nullptr, 0, a);
   return e == cudaSuccess ? DFLASH2_OK : fail(DFLASH2_ERR_CUDA, "logits launch failed: %s", cudaGetErrorString(e));
 }
 
 }  // namespace
 
+size_t logits_topk_workspace(int M, int V, int B, bool ragged, int max_len, bool tokens, int n_bias, int K) {
+  return pick_plan(M, V, B, ragged, max_len, tokens, n_bias, K).total;
+}
+
 int launch_logits_topk(const LogitsTopk& r, cudaStream_t st) {
-  const PickPlan p = pick_plan(r, sm_count());
+  const PickPlan p = pick_plan(r.M, r.V, r.B, r.row_off != nullptr, r.max_len, r.tokens != nullptr, r.n_bias, r.K);
   PickArgs a{};
   a.r = r;
-  a.cluster = p.cluster; a.slice = p.slice; a.subs = p.subs; a.cap = p.cap;
+  a.each = r.row_off == nullptr ? r.M / r.B : 0;
+  a.windows = p.windows; a.cap = p.cap; a.words = p.words; a.tiles = p.tiles;
+  uint8_t* ws = static_cast<uint8_t*>(r.workspace);
+  a.bits = reinterpret_cast<uint32_t*>(ws + p.bits);
+  a.named = reinterpret_cast<int*>(ws + p.named);
+  a.names = reinterpret_cast<uint2*>(ws + p.names);
+  a.request = reinterpret_cast<int*>(ws + p.request);
+  a.line = reinterpret_cast<uint64_t*>(ws + p.line);
+  a.keys = reinterpret_cast<uint32_t*>(ws + p.keys);
   a.err = device_error_word();
   if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
-  return r.dtype == DFLASH2_F32 ? launch_pick_t<float>(a, p, st) : launch_pick_t<__nv_bfloat16>(a, p, st);
+  const int name_ctas = r.B * p.windows + (r.row_off != nullptr ? (r.M + kNameThreads - 1) / kNameThreads : 0);
+  if (name_ctas > 0) {
+    static unsigned done = 0;
+    if (!ensure_smem_attr(logits_names_kernel, kWindow * 4, &done))
+      return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (logits)");
+    const cudaError_t e = launch_pdl(logits_names_kernel, dim3(static_cast<unsigned>(name_ctas)), dim3(kNameThreads),
+                                     static_cast<size_t>(p.cap) * 4, st, nullptr, 0, a);
+    if (e != cudaSuccess) return fail(DFLASH2_ERR_CUDA, "logits launch failed: %s", cudaGetErrorString(e));
+  }
+  return r.dtype == DFLASH2_F32 ? launch_pick_t<float>(a, st) : launch_pick_t<__nv_bfloat16>(a, st);
 }
 
 }  // namespace dfl

@@ -473,15 +473,20 @@ DFLASH2_API int dflash2_kv4_plan(const int32_t* ctx_len, const int32_t* change, 
  *   cand, unary [M, K] int32, fp32: the K best tokens by y, descending, the lower token first among equals, and their y;
  *              0 <= K <= min(16, V), both NULL for K = 0. NaN comes before every number.
  *   out        [M, V] dtype or NULL, rows out_stride apart: y, rounded once. May be logits itself (with its stride).
- *   No workspace. The same call gives the same bits.
+ *   workspace  at least dflash2_logits_topk_workspace_bytes(M, V, B, row_offsets given, max_len (0 without history), tokens
+ *              given, n_bias, K) bytes, 256-byte aligned (NULL when that is 0), no initialisation. Calls that can run at the
+ *              same time need workspaces of their own. The same call gives the same bits.
  * ---------------------------------------------------------------------------------- */
+DFLASH2_API size_t dflash2_logits_topk_workspace_bytes(int M, int V, int B, int ragged, int max_len, int drafted, int n_bias,
+                                                       int K);
 DFLASH2_API int dflash2_logits_topk(const void* logits, int64_t stride, int M, int V, int dtype, int B,
                                     const int32_t* row_offsets, const int32_t* history, int64_t history_stride,
                                     const int32_t* prompt_len, const int32_t* history_len, int max_len,
                                     const float* repetition, const float* frequency, const float* presence,
                                     const int32_t* tokens, const int32_t* parents, const int32_t* bias_ids,
                                     const float* bias, int n_bias, const int32_t* mask, int64_t mask_stride, int K,
-                                    int32_t* cand, float* unary, void* out, int64_t out_stride, void* stream);
+                                    int32_t* cand, float* unary, void* out, int64_t out_stride, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------
  * The gated feed-forward sublayer and its gradients (dflash2.ts #block: down(silu(gate(a)) * up(a));

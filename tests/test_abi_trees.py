@@ -56,12 +56,12 @@ def test_tree_attention_rejects_bad_arguments(lib):
 def _pick(lib, **kw):
     a = dict(logits=FAKE, stride=1000, M=8, V=1000, dtype=1, B=4, off=None, hist=FAKE, hs=50, prompt=FAKE, length=FAKE,
              max_len=50, rep=FAKE, freq=FAKE, pres=FAKE, tokens=FAKE, parents=FAKE, ids=FAKE, bias=FAKE, nb=3, mask=FAKE,
-             ms=32, K=16, cand=FAKE, unary=FAKE, out=FAKE, os=1000)
+             ms=32, K=16, cand=FAKE, unary=FAKE, out=FAKE, os=1000, ws=None, wsb=0)
     a.update(kw)
     return lib.dflash2_logits_topk(a["logits"], a["stride"], a["M"], a["V"], a["dtype"], a["B"], a["off"], a["hist"], a["hs"],
                                    a["prompt"], a["length"], a["max_len"], a["rep"], a["freq"], a["pres"], a["tokens"],
                                    a["parents"], a["ids"], a["bias"], a["nb"], a["mask"], a["ms"], a["K"], a["cand"],
-                                   a["unary"], a["out"], a["os"], None)
+                                   a["unary"], a["out"], a["os"], a["ws"], a["wsb"], None)
 
 
 def test_candidates_reject_bad_arguments(lib):
@@ -71,6 +71,11 @@ def test_candidates_reject_bad_arguments(lib):
                 dict(max_len=2 ** 20), dict(hs=49), dict(tokens=None), dict(M=65 * 4), dict(nb=-1), dict(nb=2048),
                 dict(ids=None), dict(bias=None), dict(ms=31)):
         assert _pick(lib, **bad) == -1, bad
+    need = lib.dflash2_logits_topk_workspace_bytes(8, 1000, 4, 0, 50, 1, 3, 16)
+    assert need > 0 and _pick(lib) == -4 and _pick(lib, ws=FAKE, wsb=need - 1) == -4
+    assert _pick(lib, ws=ctypes.c_void_p(0x10010), wsb=need) == -1  # not 256-byte aligned
+    assert lib.dflash2_logits_topk_workspace_bytes(8, 0, 4, 0, 50, 1, 3, 16) == 0
+    assert _pick(lib, M=2 ** 25, B=2 ** 25, V=2 ** 20, stride=2 ** 20, os=2 ** 20, ms=2 ** 15) == -1
     assert _pick(lib, M=0, logits=None, cand=None, unary=None, out=None) == 0  # no rows: nothing to do
 
 
