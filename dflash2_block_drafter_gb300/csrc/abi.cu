@@ -586,12 +586,12 @@ int dflash2_kv4_plan(const int32_t* ctx_len, const int32_t* change, int32_t* pag
 
 static int check_logits(int M, int V, int B, int max_len, int n_bias, int K) {
   REQUIRE(M >= 0 && B >= 1, "M=%d must be >= 0 and B=%d >= 1", M, B);
-  REQUIRE(V >= 1 && V <= 0x40000000, "V=%d must be in [1, 2^30]", V);
+  REQUIRE(V >= 1 && V <= (1 << 22), "V=%d must be in [1, 2^22]", V);
   REQUIRE(K >= 0 && K <= 16 && K <= V, "K=%d must be in [0, min(16, V)]", K);
   REQUIRE(max_len >= 0 && max_len <= (1 << 20) - 128, "max_len=%d must be in [0, 2^20 - 128]", max_len);
   REQUIRE(n_bias >= 0 && n_bias <= 2047, "n_bias=%d must be in [0, 2047]", n_bias);
-  // tiles of 1024 tokens a row, and windows of 32768 a request, are counted in int
-  const int64_t tiles = (V + 1024LL) / 1024 + 1, windows = (V + 32767LL) / 32768;
+  // tiles of 1024 tokens a row, and windows of 2^18 a request, are counted in int
+  const int64_t tiles = (V + 1024LL) / 1024 + 1, windows = (V + 0x3ffffLL) >> 18;
   REQUIRE(M * tiles <= 0x3fffffff && B * windows <= 0x3fffffff, "M=%d, V=%d, B=%d are too large", M, V, B);
   return DFLASH2_OK;
 }

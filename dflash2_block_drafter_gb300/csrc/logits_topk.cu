@@ -9,15 +9,17 @@
 //   y = -inf                                      if the mask's bit v is clear
 // each step rounded to fp32, so that the order of nearly equal tokens is defined to the last bit.
 //
-// The work is one read of the logits, and what applies to few tokens does not burden the rest. Three kernels:
-//  1. names: the tokens that a request's history, drafted rows and biases name, as a bit a token and as a list of
-//     (token, counter); rows' requests and lines of ancestors. A CTA a request and window of 32768 tokens, counters
-//     in shared memory.
-//  2. stream: every warp reads tiles of 1024 tokens of a row, 32 a lane, and writes one key a lane: the largest value
-//     of its tokens that are allowed and not named. No barriers, nothing shared; the mask is applied to `out` here.
-//  3. select: a CTA a row. The named tokens' values; then, from the keys, which are a 32nd of the row, a bound that the
-//     K best reach, the few lanes whose key reaches it, their tokens once more, and the K best of those by (value,
-//     lower token). A row where too many reach the bound (equal values) is searched in K rounds instead.
+// The work is one read of the logits, and what applies to few tokens does not burden the rest. Two kernels:
+//  1. Most CTAs stream: every warp reads tiles of 1024 tokens of a row, 32 a lane, and writes one key a lane, the largest
+//     value of its allowed tokens. No barriers, nothing shared; the mask is applied to `out` on the way. Between them
+//     some CTAs collect what requests name, a CTA a request (and 262144 tokens): the tokens of its history, drafted
+//     rows and biases, as a bit a token and as a list of (token, counter), a token's rank among the set bits being its
+//     place there; and the rows' requests and lines of ancestors.
+//  2. A CTA a row selects. The named tokens' values are computed, and the lanes that hold a named token marked, whose
+//     keys say too much. The other keys (a 32nd of the row) and the named values give a bound that the K best reach:
+//     the K-th largest of 32 groups' maxima. The few lanes whose key reaches it are read once more, and the K best of
+//     what reaches the bound there, and of the named, are ranked by (value, lower token). A row where too many reach
+//     it (equal values) is searched in K rounds instead.
 // Only what is above -inf is a candidate; rows with fewer than K such tokens are filled with the lowest of the others.
 #include <algorithm>
 
@@ -31,13 +33,15 @@
 namespace dfl {
 namespace {
 
-constexpr int kWindowLog = 15, kWindow = 1 << kWindowLog;  // tokens a CTA names
-constexpr int kNameThreads = kWindow / 32;                 // a word of bits each
+constexpr int kWindowLog = 18, kWindow = 1 << kWindowLog;  // tokens whose names a CTA collects
 constexpr int kTile = 1024;                                // tokens a warp reads at a time,
 constexpr int kLaneTokens = 32;                            // of which a lane has
-constexpr int kStreamWarps = 8, kStreamTiles = 2;          // warps a CTA, tiles a warp
-constexpr int kSelectThreads = 256, kSelectWarps = kSelectThreads / 32;
+constexpr int kStreamThreads = 256, kStreamWarps = kStreamThreads / 32;
+constexpr int kStreamTiles = 2;                            // tiles a warp
+constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
 constexpr int kEntries = 2048, kLanes = 1024;              // that reach the bound
+constexpr int kKept = 2048;                                // named tokens' values kept between looks
+constexpr int kKeyLoads = 4;                               // sixteen bytes of keys a thread keeps
 constexpr int kPickK = 16;
 constexpr uint32_t kCountMask = (1u << 20) - 1, kInPrompt = 1u << 20;  // a counter; over it, which bias
 constexpr int kBiasShift = 21;
@@ -48,6 +52,7 @@ struct PickArgs {
   int windows, cap;     // windows of the vocabulary (0: nothing is named); counters a window
   int words;            // of bits a request
   int tiles;            // a row
+  int ctas_a_row, stream_ctas, other_ctas;  // of the first kernel
   uint32_t* bits;       // [B][words]
   int* named;           // [B][windows] how many
   uint2* names;         // [B][windows][cap] (token, counter)
@@ -93,15 +98,15 @@ __device__ __forceinline__ void for_history(const int32_t* hist, int len, F f) {
   if (tid < head) f(__ldg(hist + tid), tid);
   if (tid < len - tail) f(__ldg(hist + tail + tid), tail + tid);
   const int4* wide = reinterpret_cast<const int4*>(hist + head);
-  for (int i = tid; i < quads; i += 4 * kNameThreads) {
+  for (int i = tid; i < quads; i += 4 * kStreamThreads) {
     int4 q[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (i + k * kNameThreads < quads) q[k] = __ldg(wide + i + k * kNameThreads);
+      if (i + k * kStreamThreads < quads) q[k] = __ldg(wide + i + k * kStreamThreads);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      if (i + k * kNameThreads >= quads) break;
-      const int at = head + 4 * (i + k * kNameThreads);
+      if (i + k * kStreamThreads >= quads) break;
+      const int at = head + 4 * (i + k * kStreamThreads);
       f(q[k].x, at);
       f(q[k].y, at + 1);
       f(q[k].z, at + 2);
@@ -110,44 +115,66 @@ __device__ __forceinline__ void for_history(const int32_t* hist, int len, F f) {
   }
 }
 
-__global__ void __launch_bounds__(kNameThreads) logits_names_kernel(const PickArgs a) {
+// The request of row m in [0, M), by a binary search: the last that starts at or before it, if its span holds it (and
+// the row is among its first 64 where they are drafted); else -1.
+__device__ __forceinline__ int ragged_request(const LogitsTopk& r, int m, bool& late) {
+  int lo = 0, hi = r.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(r.row_off + mid) <= m)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int first = __ldg(r.row_off + lo);
+  const bool in = first >= 0 && first <= m && m < __ldg(r.row_off + lo + 1);
+  late = in && r.tokens != nullptr && m - first >= kTreeRows;
+  return in && !late ? lo : -1;
+}
+// A warp's work: the lines of a request's first 64 rows, from row `first` on.
+__device__ __forceinline__ TreeLines request_lines(const PickArgs& a, int b, int& first, int& rows, bool& bad) {
+  const LogitsTopk& r = a.r;
+  const int lane = static_cast<int>(threadIdx.x) & 31;
+  rows = a.each;
+  first = b * a.each;
+  if (a.each == 0) {
+    first = __ldg(r.row_off + b);
+    rows = first < 0 ? 0 : min(__ldg(r.row_off + b + 1), r.M) - first;
+  }
+  rows = min(rows, kTreeRows);
+  int parent[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int t = lane + 32 * h;
+    parent[h] = t < rows ? (r.parents != nullptr ? __ldg(r.parents + first + t) : t - 1) : -2;
+  }
+  return tree_lines(parent, rows, bad);
+}
+
+// The requests of rows x 256 .. (row_off given), and the check of the spans.
+__device__ __forceinline__ void map_rows(const PickArgs& a, int x, int ctas) {
+  const LogitsTopk& r = a.r;
+  const int m = x * kStreamThreads + static_cast<int>(threadIdx.x);
+  for (int b = m; b < r.B; b += ctas * kStreamThreads) {
+    const int lo = __ldg(r.row_off + b), hi = __ldg(r.row_off + b + 1);
+    if (lo < 0 || hi < lo || hi > r.M) record(a.err, DFLASH2_ERR_INVALID_ARG);
+  }
+  if (m >= r.M) return;
+  bool late;
+  a.request[m] = ragged_request(r, m, late);
+  if (late) record(a.err, DFLASH2_ERR_INVALID_ARG);
+}
+
+// What request b names in a window. Shared memory: bits, four words of which share a base, their first's rank.
+__device__ __forceinline__ void collect_names(const PickArgs& a, int x, uint32_t* bits) {
   const LogitsTopk& r = a.r;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
-  pdl_trigger();
-  pdl_wait();
-  const int named_ctas = r.B * a.windows;
-  if (static_cast<int>(blockIdx.x) >= named_ctas) {
-    // ---- rows' requests: the last request that starts at or before the row, if its span holds the row
-    const int x = (static_cast<int>(blockIdx.x) - named_ctas) * kNameThreads + tid;
-    for (int b = x; b < r.B; b += static_cast<int>(gridDim.x - named_ctas) * kNameThreads) {
-      const int lo = __ldg(r.row_off + b), hi = __ldg(r.row_off + b + 1);
-      if (lo < 0 || hi < lo || hi > r.M) record(a.err, DFLASH2_ERR_INVALID_ARG);
-    }
-    if (x >= r.M) return;
-    int lo = 0, hi = r.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(r.row_off + mid) <= x)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    const int first = __ldg(r.row_off + lo);
-    bool in = first >= 0 && first <= x && x < __ldg(r.row_off + lo + 1);
-    if (in && r.tokens != nullptr && x - first >= kTreeRows) {
-      record(a.err, DFLASH2_ERR_INVALID_ARG);
-      in = false;
-    }
-    a.request[x] = in ? lo : -1;
-    return;
-  }
-  extern __shared__ uint32_t counters[];  // [cap]
-  __shared__ uint32_t bits[kNameThreads];
-  __shared__ uint16_t base[kNameThreads];
-  __shared__ int warp_sum[32];
-  __shared__ uint64_t there;              // the request's drafted rows that are there
-  const int b = static_cast<int>(blockIdx.x) / a.windows, window = static_cast<int>(blockIdx.x) - b * a.windows;
+  const int b = x / a.windows, window = x - b * a.windows;
   const int lo = window << kWindowLog, len = min(kWindow, r.V - lo);
+  const int quads = (len + 127) / 128;                         // of words of bits
+  uint32_t* base = bits + quads * 4;                           // [quads]
+  __shared__ int warp_sum[kStreamWarps];
+  __shared__ uint64_t there;                                   // the request's drafted rows that are there
   const int32_t* hist = nullptr;
   int hist_len = 0, prompt = 0;
   if (r.history != nullptr) {
@@ -157,26 +184,13 @@ __global__ void __launch_bounds__(kNameThreads) logits_names_kernel(const PickAr
     if ((hist_len < 0 || hist_len > r.max_len) && tid == 0) record(a.err, DFLASH2_ERR_INVALID_ARG);
     hist_len = min(max(hist_len, 0), r.max_len);
   }
-  bits[tid] = 0u;
+  uint4* bits4 = reinterpret_cast<uint4*>(bits);
+  for (int k = tid; k < quads; k += kStreamThreads) bits4[k] = make_uint4(0u, 0u, 0u, 0u);
   int first = 0;
   if (r.tokens != nullptr && warp == 0) {
-    // each drafted row's line of ancestors
-    int rows = a.each;
-    first = b * a.each;
-    if (a.each == 0) {
-      first = __ldg(r.row_off + b);
-      rows = min(__ldg(r.row_off + b + 1), r.M) - first;
-      if (first < 0) rows = 0;
-    }
-    rows = min(rows, kTreeRows);
-    int parent[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int t = lane + 32 * h;
-      parent[h] = t < rows ? (r.parents != nullptr ? __ldg(r.parents + first + t) : t - 1) : -2;
-    }
+    int rows;
     bool bad;
-    const TreeLines tree = tree_lines(parent, rows, bad);
+    const TreeLines tree = request_lines(a, b, first, rows, bad);
     if (bad) record(a.err, DFLASH2_ERR_BAD_INDEX);
     const uint32_t in0 = __ballot_sync(0xffffffffu, tree.line[0] != 0ull), in1 = __ballot_sync(0xffffffffu, tree.line[1] != 0ull);
     if (lane == 0) there = (static_cast<uint64_t>(in1) << 32) | in0;
@@ -200,38 +214,62 @@ __global__ void __launch_bounds__(kNameThreads) logits_names_kernel(const PickAr
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       if ((there >> (lane + 32 * h)) & 1) mark(__ldg(r.tokens + first + lane + 32 * h));
-  for (int e = tid; e < r.n_bias; e += kNameThreads) {
+  for (int e = tid; e < r.n_bias; e += kStreamThreads) {
     const int t = __ldg(bias_ids + e);
     if (t >= 0) mark(t);
   }
   __syncthreads();
-  // a named token's counter is the one of its rank among the set bits
-  const uint32_t mine = bits[tid];
-  int sum = __popc(mine);
-#pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, sum, m);
-    if (lane >= m) sum += v;
-  }
-  if (lane == 31) warp_sum[warp] = sum;
+  // ranks: a warp has a range of the quads, 32 at a time
+  const int span = (quads + kStreamWarps - 1) / kStreamWarps, q0 = min(quads, warp * span), q1 = min(quads, q0 + span);
+  auto ones = [](const uint4& w) { return __popc(w.x) + __popc(w.y) + __popc(w.z) + __popc(w.w); };
+  int sum = 0;
+  for (int q = q0 + lane; q < q1; q += 32) sum += ones(bits4[q]);
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  if (lane == 0) warp_sum[warp] = sum;
   __syncthreads();
-  int total = warp_sum[lane];
+  int at = 0, n = 0;
 #pragma unroll
-  for (int m = 1; m < 32; m <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, total, m);
-    if (lane >= m) total += v;
+  for (int w = 0; w < kStreamWarps; ++w) {
+    if (w < warp) at += warp_sum[w];
+    n += warp_sum[w];
   }
-  const int before = __shfl_sync(0xffffffffu, total, max(0, warp - 1));
-  const int n = __shfl_sync(0xffffffffu, total, 31);
-  const int at = (warp > 0 ? before : 0) + sum - __popc(mine);
-  base[tid] = static_cast<uint16_t>(at);
-  for (int k = tid; k < n; k += kNameThreads) counters[k] = 0u;
-  if ((lo >> 5) + tid < a.words) a.bits[static_cast<int64_t>(b) * a.words + (lo >> 5) + tid] = mine;
   if (tid == 0) a.named[b * a.windows + window] = n;
+  uint2* names = a.names + static_cast<int64_t>(b * a.windows + window) * a.cap;
+  uint32_t* to = a.bits + static_cast<int64_t>(b) * a.words + (lo >> 5);
+  for (int qq = q0; qq < q1; qq += 32) {
+    const int q = qq + lane;
+    const uint4 w = q < q1 ? bits4[q] : make_uint4(0u, 0u, 0u, 0u);
+    const int mine = ones(w);
+    int inc = mine;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, m);
+      if (lane >= m) inc += v;
+    }
+    int k = at + inc - mine;
+    at += __shfl_sync(0xffffffffu, inc, 31);
+    if (q >= q1) continue;
+    base[q] = static_cast<uint32_t>(k);
+    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * q + i < (len + 31) / 32) to[4 * q + i] = word[i];
+      for (uint32_t left = word[i]; left != 0u; left &= left - 1u)
+        names[k++] = make_uint2(static_cast<uint32_t>(lo + (4 * q + i) * 32 + __ffs(left) - 1), 0u);
+    }
+  }
+  if (n == 0) return;
   __syncthreads();
-  auto counter = [&](int u) { return counters + base[u >> 5] + __popc(bits[u >> 5] & ((1u << (u & 31)) - 1u)); };
+  auto counter = [&](int u) {
+    const int i = (u >> 5) & 3;
+    const uint4 w = bits4[u >> 7];
+    const uint32_t below = (1u << (u & 31)) - 1u;
+    const int rank = __popc(w.x & (i > 0 ? ~0u : below)) + (i > 0 ? __popc(w.y & (i > 1 ? ~0u : below)) : 0) +
+                     (i > 1 ? __popc(w.z & (i > 2 ? ~0u : below)) : 0) + (i > 2 ? __popc(w.w & below) : 0);
+    return &names[base[u >> 7] + rank].y;
+  };
   if (r.n_bias > 0) {
-    for (int e = tid; e < r.n_bias; e += kNameThreads) {
+    for (int e = tid; e < r.n_bias; e += kStreamThreads) {
       const int u = __ldg(bias_ids + e) - lo;
       if (u >= 0 && u < len) atomicMax(counter(u), static_cast<uint32_t>(r.n_bias - e) << kBiasShift);
     }
@@ -245,11 +283,6 @@ __global__ void __launch_bounds__(kNameThreads) logits_names_kernel(const PickAr
     else
       atomicAdd(counter(u), 1u);
   });
-  __syncthreads();
-  uint2* names = a.names + static_cast<int64_t>(b * a.windows + window) * a.cap;
-  int k = at;
-  for (uint32_t w = mine; w != 0u; w &= w - 1u, ++k)
-    names[k] = make_uint2(static_cast<uint32_t>(lo + tid * 32 + __ffs(w) - 1), counters[k]);
 }
 
 // ------------------------------------------------------------------ stream
@@ -364,24 +397,36 @@ __device__ __forceinline__ uint32_t bits_from(const uint32_t* w, int words, int 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kStreamWarps) logits_stream_kernel(const PickArgs a, int ctas_a_row) {
+__device__ __forceinline__ void stream_row(const PickArgs& a, int x) {
   using Vec = PickVec<T>;
   constexpr int kN = Vec::kN, kG = kLaneTokens / kN;
   constexpr uint32_t kAll = (1u << kN) - 1;
   const LogitsTopk& r = a.r;
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
-  const int m = static_cast<int>(blockIdx.x) / ctas_a_row;
-  const int tile0 = ((static_cast<int>(blockIdx.x) - m * ctas_a_row) * kStreamWarps + warp) * kStreamTiles;
-  pdl_trigger();
-  pdl_wait();
-  const PickRow p = pick_row(a, m);
-  if (p.request < 0 || p.missing) return;
+  const int m = x / a.ctas_a_row;
+  const int tile0 = ((x - m * a.ctas_a_row) * kStreamWarps + warp) * kStreamTiles;
   const T* row = static_cast<const T*>(r.logits) + static_cast<int64_t>(m) * r.stride;
   T* out = r.out != nullptr ? static_cast<T*>(r.out) + static_cast<int64_t>(m) * r.out_stride : nullptr;
   const int off = row_offset(row), mask_words = (r.V + 31) / 32;
   const bool out_wide = out != nullptr && row_offset(out) == off;
   const uint32_t* mask = r.mask != nullptr ? reinterpret_cast<const uint32_t*>(r.mask) + static_cast<int64_t>(m) * r.mask_stride : nullptr;
-  const uint32_t* named = a.windows > 0 ? a.bits + static_cast<int64_t>(p.request) * a.words : nullptr;
+  if (out != nullptr && (a.each == 0 || r.tokens != nullptr)) {
+    // rows of no request, and drafted rows that are not there, keep what `out` holds
+    __shared__ int lives;
+    if (warp == 0) {
+      bool late, bad;
+      int first, rows;
+      const int b = a.each > 0 ? m / a.each : ragged_request(r, m, late);
+      bool yes = b >= 0;
+      if (yes && r.tokens != nullptr) {
+        const TreeLines tree = request_lines(a, b, first, rows, bad);
+        yes = __any_sync(0xffffffffu, (m - first == lane && tree.line[0] != 0ull) || (m - first == lane + 32 && tree.line[1] != 0ull));
+      }
+      if (lane == 0) lives = yes ? 1 : 0;
+    }
+    __syncthreads();
+    if (lives == 0) return;
+  }
   for (int tile = tile0; tile < min(tile0 + kStreamTiles, a.tiles); ++tile) {
     const int t0 = tile * kTile - off;  // the tile's first token
     const bool inside = t0 >= 0 && t0 + kTile <= r.V;
@@ -394,15 +439,13 @@ __global__ void __launch_bounds__(32 * kStreamWarps) logits_stream_kernel(const 
       else
         v[g] = Vec::load_some(row + t, -t, r.V - t);
     }
-    // lane l holds bits 32 l .. of the tile: what is not allowed, and what is named
-    const uint32_t denied = mask != nullptr ? ~bits_from(mask, mask_words, t0 + 32 * lane) : 0u;
-    const uint32_t taken = named != nullptr ? bits_from(named, a.words, t0 + 32 * lane) : 0u;
-    auto share = [&](uint32_t w, int g) {  // the bits of the lane's g-th sixteen bytes
-      return (__shfl_sync(0xffffffffu, w, (g * 32 + lane) * kN / 32) >> (lane * kN & 31)) & kAll;
-    };
-    if (__any_sync(0xffffffffu, denied != 0u)) {
+    if (mask != nullptr) {
+      const uint32_t denied = ~bits_from(mask, mask_words, t0 + 32 * lane);  // lane l holds bits 32 l .. of the tile
+      if (__any_sync(0xffffffffu, denied != 0u)) {
 #pragma unroll
-      for (int g = 0; g < kG; ++g) Vec::drop(v[g], share(denied, g));
+        for (int g = 0; g < kG; ++g)  // those of the lane's g-th sixteen bytes
+          Vec::drop(v[g], (__shfl_sync(0xffffffffu, denied, (g * 32 + lane) * kN / 32) >> (lane * kN & 31)) & kAll);
+      }
     }
     if (out != nullptr)
 #pragma unroll
@@ -414,14 +457,27 @@ __global__ void __launch_bounds__(32 * kStreamWarps) logits_stream_kernel(const 
           Vec::store_some(out + t, v[g], -t, r.V - t);
       }
     if (r.K == 0) continue;
-    if (__any_sync(0xffffffffu, taken != 0u)) {
-#pragma unroll
-      for (int g = 0; g < kG; ++g) Vec::drop(v[g], share(taken, g));
-    }
     float top = -INFINITY;
 #pragma unroll
     for (int g = 0; g < kG; ++g) top = Vec::max(top, v[g]);
     a.keys[(static_cast<int64_t>(m) * a.tiles + tile) * 32 + lane] = pick_key(top);
+  }
+}
+
+// The streaming CTAs, and evenly between them those that collect names and map rows.
+template <typename T>
+__global__ void __launch_bounds__(kStreamThreads) logits_stream_kernel(const PickArgs a) {
+  extern __shared__ __align__(16) uint32_t stream_smem[];
+  pdl_trigger();
+  pdl_wait();
+  const long long x = blockIdx.x, all = gridDim.x;
+  const int other = static_cast<int>(x * a.other_ctas / all);
+  if (static_cast<int>((x + 1) * a.other_ctas / all) == other) {
+    stream_row<T>(a, static_cast<int>(x) - other);
+  } else if (other < a.r.B * a.windows) {
+    collect_names(a, other, stream_smem);
+  } else {
+    map_rows(a, other - a.r.B * a.windows, a.other_ctas - a.r.B * a.windows);
   }
 }
 
@@ -430,6 +486,7 @@ struct SelectShared {
   unsigned long long entry[kEntries];
   unsigned long long best[kPickK];
   unsigned long long red[kSelectWarps];
+  float kept[kKept];
   int lane[kLanes];
   alignas(16) uint32_t group_max[32];
   int entries, lanes;
@@ -440,11 +497,14 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
   using Vec = PickVec<T>;
   constexpr int kN = Vec::kN;
   __shared__ SelectShared s;
+  extern __shared__ uint32_t marked[];  // [tiles] lanes that hold a named token
   const LogitsTopk& r = a.r;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int m = static_cast<int>(blockIdx.x);
   if (tid == 0) s.entries = s.lanes = 0;
   if (tid < kPickK) s.best[tid] = 0ull;
+  if (r.K > 0)
+    for (int k = tid; k < a.tiles; k += kSelectThreads) marked[k] = 0u;
   pdl_trigger();
   pdl_wait();
   const PickRow p = pick_row(a, m);
@@ -459,7 +519,12 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
   const int b = p.request;
   const T* row = static_cast<const T*>(r.logits) + static_cast<int64_t>(m) * r.stride;
   T* out = r.out != nullptr ? static_cast<T*>(r.out) + static_cast<int64_t>(m) * r.out_stride : nullptr;
-  const int off = row_offset(row);
+  const int off = row_offset(row), quads = r.K > 0 ? a.tiles * 8 : 0;
+  const uint4* keys = reinterpret_cast<const uint4*>(a.keys + static_cast<int64_t>(m) * a.tiles * 32);
+  uint4 key[kKeyLoads];
+#pragma unroll
+  for (int j = 0; j < kKeyLoads; ++j)
+    key[j] = tid + j * kSelectThreads < quads ? keys[tid + j * kSelectThreads] : make_uint4(0u, 0u, 0u, 0u);
   const uint32_t* mask = r.mask != nullptr ? reinterpret_cast<const uint32_t*>(r.mask) + static_cast<int64_t>(m) * r.mask_stride : nullptr;
   const uint32_t* taken = a.windows > 0 ? a.bits + static_cast<int64_t>(b) * a.words : nullptr;
   const float rep = r.repetition != nullptr ? __ldg(r.repetition + b) : 1.f;
@@ -474,50 +539,76 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
     for (int h = 0; h < 2; ++h)
       if ((line >> (lane + 32 * h)) & 1) drafted[h] = __ldg(r.tokens + p.first + lane + 32 * h);
   }
-  auto allowed = [&](int t) { return mask == nullptr || ((__ldg(mask + (t >> 5)) >> (t & 31)) & 1u); };
-  // f(token, value) of every named token that is the thread's (whole warps)
-  auto for_named = [&](auto f) {
+  auto bit_of = [](const uint32_t* w, int t) { return (__ldg(w + (t >> 5)) >> (t & 31)) & 1u; };
+  // f(token, value, place) of every named token that is the thread's, whole warps; a place below kKept is that of a value
+  // that the first look keeps
+  auto for_named = [&](bool first_look, int from, auto f) {
+    int before = 0;
     for (int w = 0; w < a.windows; ++w) {
       const int n = __ldg(a.named + b * a.windows + w);
       const uint2* names = a.names + static_cast<int64_t>(b * a.windows + w) * a.cap;
       for (int k0 = warp * 32; k0 < n; k0 += kSelectThreads) {
+        const int place = before + k0 + lane;
+        if (before + k0 + 31 < from) continue;
         const bool mine = k0 + lane < n;
         const uint2 name = mine ? __ldg(names + k0 + lane) : make_uint2(0xffffffffu, 0u);
         const int t = static_cast<int>(name.x);
+        if (!first_look && before + k0 + 31 < kKept) {
+          if (mine) f(t, s.kept[place], place);
+          continue;
+        }
+        const uint32_t ok = mine && mask != nullptr ? bit_of(mask, t) : 1u;
+        float y = mine ? Vec::load(row + t) : 0.f;
         uint32_t times = name.y & kCountMask;
         for (uint64_t left = line; left != 0ull; left &= left - 1ull) {
-          const int from = __ffsll(static_cast<long long>(left)) - 1;
-          if (__shfl_sync(0xffffffffu, from < 32 ? drafted[0] : drafted[1], from & 31) == t) ++times;
+          const int at = __ffsll(static_cast<long long>(left)) - 1;
+          if (__shfl_sync(0xffffffffu, at < 32 ? drafted[0] : drafted[1], at & 31) == t) ++times;
         }
         if (!mine) continue;
-        float y = Vec::load(row + t);
         if (times != 0u || (name.y & kInPrompt) != 0u) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
         if (times != 0u) y = __fsub_rn(y, __fadd_rn(__fmul_rn(freq, static_cast<float>(times)), pres));
         if ((name.y >> kBiasShift) != 0u)
           y = __fadd_rn(y, __ldg(r.bias + static_cast<int64_t>(b) * r.n_bias + (r.n_bias - static_cast<int>(name.y >> kBiasShift))));
-        if (!allowed(t)) y = -INFINITY;
-        f(t, y);
+        if (ok == 0u) y = -INFINITY;
+        f(t, !first_look && place < kKept ? s.kept[place] : y, place);
       }
+      before += n;
     }
   };
-  // (with in-place out a named token's logit is read before it is replaced: the second look takes what stands there)
+  // (out may be the logits themselves: a value that is not kept is stored after the last look)
   float top_named = -INFINITY;
+  __syncthreads();
+  for_named(true, 0, [&](int t, float y, int place) {
+    if (r.K > 0) atomicOr(&marked[(t + off) >> 10], 1u << ((t + off) / kN & 31));
+    top_named = max_nan(top_named, y);
+    if (place < kKept) s.kept[place] = y;
+    if (out != nullptr && place < kKept) Vec::store(out + t, y);
+  });
+  auto store_rest = [&]() {
+    if (out != nullptr)
+      for_named(true, kKept, [&](int t, float y, int place) {
+        if (place >= kKept) Vec::store(out + t, y);
+      });
+  };
   if (r.K == 0) {
-    for_named([&](int t, float y) { Vec::store(out + t, y); });
+    store_rest();
     return;
   }
-  for_named([&](int, float y) { top_named = max_nan(top_named, y); });
-  const uint32_t* keys = a.keys + static_cast<int64_t>(m) * a.tiles * 32;
+  __syncthreads();
+  // the largest key of a lane without a named token
   uint32_t top = 0u;
-  for (int k = tid; k < a.tiles * 8; k += kSelectThreads) {
-    const uint4 q = *reinterpret_cast<const uint4*>(keys + 4 * k);
-    top = max(max(max(top, q.x), max(q.y, q.z)), q.w);
-  }
-  uint32_t most = max(top, pick_key(top_named));
+  auto free_max = [&](int k, const uint4& q) {
+    const uint32_t mark = marked[k >> 3] >> (4 * k & 31);
+    top = max(top, max(max((mark & 1u) != 0u ? 0u : q.x, (mark & 2u) != 0u ? 0u : q.y),
+                       max((mark & 4u) != 0u ? 0u : q.z, (mark & 8u) != 0u ? 0u : q.w)));
+  };
 #pragma unroll
-  for (int x = 1; x < 8; x <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
+  for (int j = 0; j < kKeyLoads; ++j)
+    if (tid + j * kSelectThreads < quads) free_max(tid + j * kSelectThreads, key[j]);
+  for (int k = tid + kKeyLoads * kSelectThreads; k < quads; k += kSelectThreads) free_max(k, keys[k]);
+  const uint32_t most = __reduce_max_sync(lane < 16 ? 0x0000ffffu : 0xffff0000u, max(top, pick_key(top_named)));
   // (the lowest bits tell groups apart: the K-th largest is one of them, and without these bits not above it)
-  if ((lane & 7) == 0) s.group_max[tid >> 3] = (most & ~31u) | static_cast<uint32_t>(tid >> 3);
+  if ((lane & 15) == 0) s.group_max[tid >> 4] = (most & ~31u) | static_cast<uint32_t>(tid >> 4);
   __syncthreads();
   const uint32_t g = s.group_max[lane];
   int above = 0;
@@ -534,35 +625,41 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
     const int at = atomicAdd(&s.entries, 1);
     if (at < kEntries) s.entry[at] = pick_entry(x, token);
   };
-  if (__any_sync(0xffffffffu, pick_key(top_named) >= bound)) for_named([&](int t, float y) { enter(y, t); });
-  if (top >= bound)
-    for (int k = tid; k < a.tiles * 8; k += kSelectThreads) {
-      const uint4 q = *reinterpret_cast<const uint4*>(keys + 4 * k);
-      const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+  if (__any_sync(0xffffffffu, pick_key(top_named) >= bound)) for_named(false, 0, [&](int t, float y, int) { enter(y, t); });
+  auto reach = [&](int k, const uint4& q) {
+    const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+    if (max(max(q.x, q.y), max(q.z, q.w)) < bound) return;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (x[j] >= bound) {
-          const int at = atomicAdd(&s.lanes, 1);
-          if (at < kLanes) s.lane[at] = 4 * k + j;
-        }
-    }
+    for (int j = 0; j < 4; ++j)
+      if (x[j] >= bound) {
+        const int at = atomicAdd(&s.lanes, 1);
+        if (at < kLanes) s.lane[at] = 4 * k + j;
+      }
+  };
+#pragma unroll
+  for (int j = 0; j < kKeyLoads; ++j) reach(tid + j * kSelectThreads, key[j]);
+  for (int k = tid + kKeyLoads * kSelectThreads; k < quads; k += kSelectThreads) reach(k, keys[k]);
   __syncthreads();
   auto free_value = [&](int t) {  // of a token that is allowed and not named, else -inf
-    if (taken != nullptr && ((__ldg(taken + (t >> 5)) >> (t & 31)) & 1u)) return -INFINITY;
-    return allowed(t) ? Vec::load(row + t) : -INFINITY;
+    const uint32_t named = taken != nullptr ? bit_of(taken, t) : 0u, ok = mask != nullptr ? bit_of(mask, t) : 1u;
+    const float x = Vec::load(row + t);
+    return named == 0u && ok != 0u ? x : -INFINITY;
   };
   // the tokens of the lanes that reach the bound, one a lane here
-  for (int k = warp; k < min(s.lanes, kLanes); k += kSelectWarps) {
+  const int lanes = s.lanes;
+#pragma unroll 2
+  for (int k = warp; k < min(lanes, kLanes); k += kSelectWarps) {
     const int x = s.lane[k];
     const int t = (x >> 5) * kTile + ((lane / kN) * 32 + (x & 31)) * kN + lane % kN - off;
     if (t >= 0 && t < r.V) enter(free_value(t), t);
   }
   __syncthreads();
   const int n = s.entries;
-  if (n <= kEntries && s.lanes <= kLanes) {
+  if (n <= kEntries && lanes <= kLanes) {
     for (int x = tid; x < n; x += kSelectThreads) {
       const unsigned long long mine = s.entry[x];
       int before = 0;
+#pragma unroll 4
       for (int y = 0; y < n; ++y) before += s.entry[y] > mine ? 1 : 0;
       if (before < r.K) s.best[before] = mine;
     }
@@ -577,7 +674,7 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
         const unsigned long long entry = pick_entry(x, t);
         if (entry < last) mine = max_u64(mine, entry);
       };
-      for_named(look);
+      for_named(false, 0, [&](int t, float y, int) { look(t, y); });
       for (int t = tid; t < r.V; t += kSelectThreads) look(t, free_value(t));
       mine = warp_max_u64(mine);
       if (lane == 0) s.red[warp] = mine;
@@ -589,7 +686,7 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
       __syncthreads();
     }
   }
-  if (out != nullptr) for_named([&](int t, float y) { Vec::store(out + t, y); });
+  store_rest();
   if (warp > 0) return;
   const unsigned long long mine = lane < r.K ? s.best[lane] : 0ull;
   int token = mine != 0ull ? static_cast<int>(~static_cast<uint32_t>(mine)) : -1;
@@ -636,13 +733,19 @@ PickPlan pick_plan(int M, int V, int B, bool ragged, int max_len, bool tokens, i
   return p;
 }
 
+constexpr int kStreamShared = (kWindow / 8) + kWindow / 32;  // bits, and a base for four words of them
+
 template <typename T>
 int launch_pick_t(const PickArgs& a, cudaStream_t st) {
-  const int ctas_a_row = (a.tiles + kStreamWarps * kStreamTiles - 1) / (kStreamWarps * kStreamTiles);
-  cudaError_t e = launch_pdl(logits_stream_kernel<T>, dim3(static_cast<unsigned>(a.r.M) * ctas_a_row), dim3(32 * kStreamWarps), 0,
-                             st, nullptr, 0, a, ctas_a_row);
+  static unsigned done = 0;
+  if (!ensure_smem_attr(logits_stream_kernel<T>, kStreamShared, &done))
+    return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (logits)");
+  const int quads = (std::min(a.r.V, kWindow) + 127) / 128;
+  cudaError_t e = launch_pdl(logits_stream_kernel<T>, dim3(static_cast<unsigned>(a.stream_ctas + a.other_ctas)), dim3(kStreamThreads),
+                             a.windows > 0 ? static_cast<size_t>(quads) * 20 : 0, st, nullptr, 0, a);
   if (e == cudaSuccess && (a.r.K > 0 || a.windows > 0))
-    e = launch_pdl(logits_select_kernel<T>, dim3(static_cast<unsigned>(a.r.M)), dim3(kSelectThreads), 0, st, nullptr, 0, a);
+    e = launch_pdl(logits_select_kernel<T>, dim3(static_cast<unsigned>(a.r.M)), dim3(kSelectThreads),
+                   static_cast<size_t>(a.tiles) * 4, st, nullptr, 0, a);
   return e == cudaSuccess ? DFLASH2_OK : fail(DFLASH2_ERR_CUDA, "logits launch failed: %s", cudaGetErrorString(e));
 }
 
@@ -667,15 +770,9 @@ int launch_logits_topk(const LogitsTopk& r, cudaStream_t st) {
   a.keys = reinterpret_cast<uint32_t*>(ws + p.keys);
   a.err = device_error_word();
   if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
-  const int name_ctas = r.B * p.windows + (r.row_off != nullptr ? (r.M + kNameThreads - 1) / kNameThreads : 0);
-  if (name_ctas > 0) {
-    static unsigned done = 0;
-    if (!ensure_smem_attr(logits_names_kernel, kWindow * 4, &done))
-      return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (logits)");
-    const cudaError_t e = launch_pdl(logits_names_kernel, dim3(static_cast<unsigned>(name_ctas)), dim3(kNameThreads),
-                                     static_cast<size_t>(p.cap) * 4, st, nullptr, 0, a);
-    if (e != cudaSuccess) return fail(DFLASH2_ERR_CUDA, "logits launch failed: %s", cudaGetErrorString(e));
-  }
+  a.ctas_a_row = (a.tiles + kStreamWarps * kStreamTiles - 1) / (kStreamWarps * kStreamTiles);
+  a.stream_ctas = r.M * a.ctas_a_row;
+  a.other_ctas = r.B * p.windows + (r.row_off != nullptr ? (r.M + kStreamThreads - 1) / kStreamThreads : 0);
   return r.dtype == DFLASH2_F32 ? launch_pick_t<float>(a, st) : launch_pick_t<__nv_bfloat16>(a, st);
 }
 

@@ -452,7 +452,7 @@ DFLASH2_API int dflash2_kv4_plan(const int32_t* ctx_len, const int32_t* change, 
  * in one read of the logits. (dflash2.ts #select's per-row top-K over logits that a request's sampling parameters adjust
  * first; the pages adjust none.) Feeds dflash2_score_edges, or a tree's verification (K = 1).
  *
- *   logits     [M, V] dtype, rows `stride` elements apart (any stride >= V).
+ *   logits     [M, V] dtype, rows `stride` elements apart (any stride >= V); V <= 2^22.
  *   B requests: request b has rows [row_offsets[b], row_offsets[b + 1]) ([B + 1] int32; a span that is not inside
  *              [0, M] records DFLASH2_ERR_INVALID_ARG), or M / B rows each if NULL. Rows of no request are left as they were.
  *   history    [B, max_len] int32, rows history_stride apart, or NULL: each request's tokens, history_len[b] of them (in [0,

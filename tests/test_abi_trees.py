@@ -65,7 +65,7 @@ def _pick(lib, **kw):
 
 
 def test_candidates_reject_bad_arguments(lib):
-    for bad in (dict(dtype=2), dict(M=-1), dict(B=0), dict(V=0), dict(V=2 ** 30 + 1), dict(K=-1), dict(K=17), dict(V=15),
+    for bad in (dict(dtype=2), dict(M=-1), dict(B=0), dict(V=0), dict(V=2 ** 22 + 1), dict(K=-1), dict(K=17), dict(V=15),
                 dict(M=9), dict(logits=None), dict(cand=None), dict(unary=None), dict(K=0, out=None), dict(logits=FAKE_MIS),
                 dict(out=FAKE_MIS), dict(stride=999), dict(os=999), dict(length=None), dict(max_len=-1),
                 dict(max_len=2 ** 20), dict(hs=49), dict(tokens=None), dict(M=65 * 4), dict(nb=-1), dict(nb=2048),
