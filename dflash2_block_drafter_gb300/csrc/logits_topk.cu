@@ -38,10 +38,8 @@ constexpr int kTile = 1024;                                // tokens a warp read
 constexpr int kLaneTokens = 32;                            // of which a lane has
 constexpr int kStreamThreads = 256, kStreamWarps = kStreamThreads / 32;
 constexpr int kStreamTiles = 2;                            // tiles a warp
-constexpr int kSelectThreads = 512, kSelectWarps = kSelectThreads / 32;
-constexpr int kEntries = 2048, kLanes = 1024;              // that reach the bound
-constexpr int kKept = 2048;                                // named tokens' values kept between looks
-constexpr int kKeyLoads = 4;                               // sixteen bytes of keys a thread keeps
+constexpr int kEntries = 1024, kLanes = 512;               // that reach the bound
+constexpr int kCounters = 4096;                            // of a CTA's named tokens, in shared memory
 constexpr int kPickK = 16;
 constexpr uint32_t kCountMask = (1u << 20) - 1, kInPrompt = 1u << 20;  // a counter; over it, which bias
 constexpr int kBiasShift = 21;
@@ -53,6 +51,7 @@ struct PickArgs {
   int words;            // of bits a request
   int tiles;            // a row
   int ctas_a_row, stream_ctas, other_ctas;  // of the first kernel
+  int counters, kept;   // named tokens' counters and values that shared memory holds, at most
   uint32_t* bits;       // [B][words]
   int* named;           // [B][windows] how many
   uint2* names;         // [B][windows][cap] (token, counter)
@@ -203,7 +202,8 @@ __device__ __forceinline__ void collect_names(const PickArgs& a, int x, uint32_t
   auto mark = [&](int t) {
     const int u = t - lo;
     if (t >= 0 && t < r.V) {
-      if (u >= 0 && u < len) atomicOr(&bits[u >> 5], 1u << (u & 31));
+      // (most of a history repeats)
+      if (u >= 0 && u < len && !((bits[u >> 5] >> (u & 31)) & 1u)) atomicOr(&bits[u >> 5], 1u << (u & 31));
     } else {
       record(a.err, DFLASH2_ERR_BAD_INDEX);
     }
@@ -246,43 +246,55 @@ __device__ __forceinline__ void collect_names(const PickArgs& a, int x, uint32_t
       const int v = __shfl_up_sync(0xffffffffu, inc, m);
       if (lane >= m) inc += v;
     }
-    int k = at + inc - mine;
+    if (q < q1) base[q] = static_cast<uint32_t>(at + inc - mine);
     at += __shfl_sync(0xffffffffu, inc, 31);
-    if (q >= q1) continue;
-    base[q] = static_cast<uint32_t>(k);
-    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (4 * q + i < (len + 31) / 32) to[4 * q + i] = word[i];
-      for (uint32_t left = word[i]; left != 0u; left &= left - 1u)
-        names[k++] = make_uint2(static_cast<uint32_t>(lo + (4 * q + i) * 32 + __ffs(left) - 1), 0u);
-    }
   }
+  for (int w = tid; w < (len + 31) / 32; w += kStreamThreads) to[w] = bits[w];
   if (n == 0) return;
+  // counters beside the bits if they fit there (an SM's atomics on global memory go at one a clock)
+  uint32_t* counters = a.counters >= n ? base + quads : nullptr;
+  for (int k = tid; k < n; k += kStreamThreads) (counters != nullptr ? counters[k] : names[k].y) = 0u;
   __syncthreads();
-  auto counter = [&](int u) {
+  auto place_of = [&](int u) {
     const int i = (u >> 5) & 3;
     const uint4 w = bits4[u >> 7];
     const uint32_t below = (1u << (u & 31)) - 1u;
-    const int rank = __popc(w.x & (i > 0 ? ~0u : below)) + (i > 0 ? __popc(w.y & (i > 1 ? ~0u : below)) : 0) +
-                     (i > 1 ? __popc(w.z & (i > 2 ? ~0u : below)) : 0) + (i > 2 ? __popc(w.w & below) : 0);
-    return &names[base[u >> 7] + rank].y;
+    return static_cast<int>(base[u >> 7]) + __popc(w.x & (i > 0 ? ~0u : below)) + (i > 0 ? __popc(w.y & (i > 1 ? ~0u : below)) : 0) +
+           (i > 1 ? __popc(w.z & (i > 2 ? ~0u : below)) : 0) + (i > 2 ? __popc(w.w & below) : 0);
   };
+  auto counter = [&](int k) { return counters != nullptr ? counters + k : &names[k].y; };
+  // (a token that is named more than once writes its name more than once, the same each time)
+  auto place_name = [&](int t) {
+    const int u = t - lo;
+    if (t < 0 || u < 0 || u >= len) return -1;
+    const int k = place_of(u);
+    names[k].x = static_cast<uint32_t>(t);
+    return k;
+  };
+  if (r.tokens != nullptr && warp == 0)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if ((there >> (lane + 32 * h)) & 1) place_name(__ldg(r.tokens + first + lane + 32 * h));
   if (r.n_bias > 0) {
     for (int e = tid; e < r.n_bias; e += kStreamThreads) {
-      const int u = __ldg(bias_ids + e) - lo;
-      if (u >= 0 && u < len) atomicMax(counter(u), static_cast<uint32_t>(r.n_bias - e) << kBiasShift);
+      const int k = place_name(__ldg(bias_ids + e));
+      if (k >= 0) atomicMax(counter(k), static_cast<uint32_t>(r.n_bias - e) << kBiasShift);
     }
     __syncthreads();
   }
-  for_history(hist, hist_len, [&](int t, int place) {
-    const int u = t - lo;
-    if (u < 0 || u >= len) return;
-    if (place < prompt)
-      atomicOr(counter(u), kInPrompt);
+  for_history(hist, hist_len, [&](int t, int at_place) {
+    const int k = place_name(t);
+    if (k < 0) return;
+    if (at_place < prompt)
+      atomicOr(counter(k), kInPrompt);
+    else if (counters != nullptr)
+      atomicAdd(counters + k, 1u);
     else
-      atomicAdd(counter(u), 1u);
+      atomicAdd(&names[k].y, 1u);
   });
+  if (counters == nullptr) return;
+  __syncthreads();
+  for (int k = tid; k < n; k += kStreamThreads) names[k].y = counters[k];
 }
 
 // ------------------------------------------------------------------ stream
@@ -485,26 +497,27 @@ __global__ void __launch_bounds__(kStreamThreads) logits_stream_kernel(const Pic
 struct SelectShared {
   unsigned long long entry[kEntries];
   unsigned long long best[kPickK];
-  unsigned long long red[kSelectWarps];
-  float kept[kKept];
+  unsigned long long red[32];
   int lane[kLanes];
   alignas(16) uint32_t group_max[32];
   int entries, lanes;
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const PickArgs a) {
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 6 : (kThreads == 512 ? 3 : 1)) logits_select_kernel(const PickArgs a) {
   using Vec = PickVec<T>;
-  constexpr int kN = Vec::kN;
+  constexpr int kN = Vec::kN, kWarps = kThreads / 32;
+  constexpr int kKeyLoads = kThreads >= 512 ? 2048 / kThreads : 0;  // sixteen bytes of keys a thread keeps
   __shared__ SelectShared s;
   extern __shared__ uint32_t marked[];  // [tiles] lanes that hold a named token
+  float* kept = reinterpret_cast<float*>(marked + a.tiles);  // [kept] named tokens' values
   const LogitsTopk& r = a.r;
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int m = static_cast<int>(blockIdx.x);
   if (tid == 0) s.entries = s.lanes = 0;
   if (tid < kPickK) s.best[tid] = 0ull;
   if (r.K > 0)
-    for (int k = tid; k < a.tiles; k += kSelectThreads) marked[k] = 0u;
+    for (int k = tid; k < a.tiles; k += kThreads) marked[k] = 0u;
   pdl_trigger();
   pdl_wait();
   const PickRow p = pick_row(a, m);
@@ -521,10 +534,10 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
   T* out = r.out != nullptr ? static_cast<T*>(r.out) + static_cast<int64_t>(m) * r.out_stride : nullptr;
   const int off = row_offset(row), quads = r.K > 0 ? a.tiles * 8 : 0;
   const uint4* keys = reinterpret_cast<const uint4*>(a.keys + static_cast<int64_t>(m) * a.tiles * 32);
-  uint4 key[kKeyLoads];
+  uint4 key[kKeyLoads > 0 ? kKeyLoads : 1];
 #pragma unroll
   for (int j = 0; j < kKeyLoads; ++j)
-    key[j] = tid + j * kSelectThreads < quads ? keys[tid + j * kSelectThreads] : make_uint4(0u, 0u, 0u, 0u);
+    key[j] = tid + j * kThreads < quads ? keys[tid + j * kThreads] : make_uint4(0u, 0u, 0u, 0u);
   const uint32_t* mask = r.mask != nullptr ? reinterpret_cast<const uint32_t*>(r.mask) + static_cast<int64_t>(m) * r.mask_stride : nullptr;
   const uint32_t* taken = a.windows > 0 ? a.bits + static_cast<int64_t>(b) * a.words : nullptr;
   const float rep = r.repetition != nullptr ? __ldg(r.repetition + b) : 1.f;
@@ -540,75 +553,89 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
       if ((line >> (lane + 32 * h)) & 1) drafted[h] = __ldg(r.tokens + p.first + lane + 32 * h);
   }
   auto bit_of = [](const uint32_t* w, int t) { return (__ldg(w + (t >> 5)) >> (t & 31)) & 1u; };
-  // f(token, value, place) of every named token that is the thread's, whole warps; a place below kKept is that of a value
-  // that the first look keeps
-  auto for_named = [&](bool first_look, int from, auto f) {
-    int before = 0;
-    for (int w = 0; w < a.windows; ++w) {
-      const int n = __ldg(a.named + b * a.windows + w);
-      const uint2* names = a.names + static_cast<int64_t>(b * a.windows + w) * a.cap;
-      for (int k0 = warp * 32; k0 < n; k0 += kSelectThreads) {
-        const int place = before + k0 + lane;
-        if (before + k0 + 31 < from) continue;
-        const bool mine = k0 + lane < n;
-        const uint2 name = mine ? __ldg(names + k0 + lane) : make_uint2(0xffffffffu, 0u);
-        const int t = static_cast<int>(name.x);
-        if (!first_look && before + k0 + 31 < kKept) {
-          if (mine) f(t, s.kept[place], place);
-          continue;
-        }
-        const uint32_t ok = mine && mask != nullptr ? bit_of(mask, t) : 1u;
-        float y = mine ? Vec::load(row + t) : 0.f;
-        uint32_t times = name.y & kCountMask;
+  int named = 0;
+  for (int w = 0; w < a.windows; ++w) named += __ldg(a.named + b * a.windows + w);
+  auto name_at = [&](int place) {  // of the request's lists, one behind the other
+    int w = b * a.windows;
+    for (int n; place >= (n = __ldg(a.named + w)); ++w) place -= n;
+    return __ldg(a.names + static_cast<int64_t>(w) * a.cap + place);
+  };
+  // f(token, value, place) of the thread's named tokens from place `from` on (a multiple of 32; whole warps)
+  auto for_named = [&](int from, auto f) {
+    for (int p0 = from + warp * 32; p0 < named; p0 += 2 * kThreads) {
+      uint2 name[2];
+      float y[2];
+      uint32_t ok[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int place = p0 + h * kThreads + lane;
+        name[h] = place < named ? name_at(place) : make_uint2(0xffffffffu, 0u);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool mine = name[h].x != 0xffffffffu;
+        ok[h] = mine && mask != nullptr ? bit_of(mask, static_cast<int>(name[h].x)) : 1u;
+        y[h] = mine ? Vec::load(row + name[h].x) : 0.f;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int t = static_cast<int>(name[h].x);
+        uint32_t times = name[h].y & kCountMask;
         for (uint64_t left = line; left != 0ull; left &= left - 1ull) {
           const int at = __ffsll(static_cast<long long>(left)) - 1;
           if (__shfl_sync(0xffffffffu, at < 32 ? drafted[0] : drafted[1], at & 31) == t) ++times;
         }
-        if (!mine) continue;
-        if (times != 0u || (name.y & kInPrompt) != 0u) y = y > 0.f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
-        if (times != 0u) y = __fsub_rn(y, __fadd_rn(__fmul_rn(freq, static_cast<float>(times)), pres));
-        if ((name.y >> kBiasShift) != 0u)
-          y = __fadd_rn(y, __ldg(r.bias + static_cast<int64_t>(b) * r.n_bias + (r.n_bias - static_cast<int>(name.y >> kBiasShift))));
-        if (ok == 0u) y = -INFINITY;
-        f(t, !first_look && place < kKept ? s.kept[place] : y, place);
+        if (name[h].x == 0xffffffffu) continue;
+        float x = y[h];
+        if (times != 0u || (name[h].y & kInPrompt) != 0u) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
+        if (times != 0u) x = __fsub_rn(x, __fadd_rn(__fmul_rn(freq, static_cast<float>(times)), pres));
+        if ((name[h].y >> kBiasShift) != 0u)
+          x = __fadd_rn(x, __ldg(r.bias + static_cast<int64_t>(b) * r.n_bias + (r.n_bias - static_cast<int>(name[h].y >> kBiasShift))));
+        f(t, ok[h] != 0u ? x : -INFINITY, p0 + h * kThreads + lane);
       }
-      before += n;
     }
   };
   // (out may be the logits themselves: a value that is not kept is stored after the last look)
   float top_named = -INFINITY;
   __syncthreads();
-  for_named(true, 0, [&](int t, float y, int place) {
+  for_named(0, [&](int t, float y, int place) {
     if (r.K > 0) atomicOr(&marked[(t + off) >> 10], 1u << ((t + off) / kN & 31));
     top_named = max_nan(top_named, y);
-    if (place < kKept) s.kept[place] = y;
-    if (out != nullptr && place < kKept) Vec::store(out + t, y);
+    if (place < a.kept) kept[place] = y;
+    if (out != nullptr && place < a.kept) Vec::store(out + t, y);
   });
+  // once more, those that reach a key
+  auto again = [&](uint32_t key, auto f) {
+    for (int place = tid; place < min(named, a.kept); place += kThreads)
+      if (pick_key(kept[place]) >= key) f(static_cast<int>(name_at(place).x), kept[place]);
+    for_named(a.kept, [&](int t, float y, int) { f(t, y); });
+  };
   auto store_rest = [&]() {
-    if (out != nullptr)
-      for_named(true, kKept, [&](int t, float y, int place) {
-        if (place >= kKept) Vec::store(out + t, y);
-      });
+    if (out != nullptr) for_named(a.kept, [&](int t, float y, int) { Vec::store(out + t, y); });
   };
   if (r.K == 0) {
     store_rest();
     return;
   }
   __syncthreads();
-  // the largest key of a lane without a named token
-  uint32_t top = 0u;
-  auto free_max = [&](int k, const uint4& q) {
+  // the largest key of a lane without a named token, and of any
+  uint32_t top = 0u, top_any = 0u;
+  auto look_at = [&](int k, const uint4& q) {
     const uint32_t mark = marked[k >> 3] >> (4 * k & 31);
+    top_any = max(top_any, max(max(q.x, q.y), max(q.z, q.w)));
     top = max(top, max(max((mark & 1u) != 0u ? 0u : q.x, (mark & 2u) != 0u ? 0u : q.y),
                        max((mark & 4u) != 0u ? 0u : q.z, (mark & 8u) != 0u ? 0u : q.w)));
   };
 #pragma unroll
   for (int j = 0; j < kKeyLoads; ++j)
-    if (tid + j * kSelectThreads < quads) free_max(tid + j * kSelectThreads, key[j]);
-  for (int k = tid + kKeyLoads * kSelectThreads; k < quads; k += kSelectThreads) free_max(k, keys[k]);
-  const uint32_t most = __reduce_max_sync(lane < 16 ? 0x0000ffffu : 0xffff0000u, max(top, pick_key(top_named)));
+    if (tid + j * kThreads < quads) look_at(tid + j * kThreads, key[j]);
+#pragma unroll 4
+  for (int k = tid + kKeyLoads * kThreads; k < quads; k += kThreads) look_at(k, keys[k]);
+  uint32_t most = max(top, pick_key(top_named));
+#pragma unroll
+  for (int x = 1; x < kThreads / 32; x <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
   // (the lowest bits tell groups apart: the K-th largest is one of them, and without these bits not above it)
-  if ((lane & 15) == 0) s.group_max[tid >> 4] = (most & ~31u) | static_cast<uint32_t>(tid >> 4);
+  if (tid % (kThreads / 32) == 0) s.group_max[tid / (kThreads / 32)] = (most & ~31u) | static_cast<uint32_t>(tid / (kThreads / 32));
   __syncthreads();
   const uint32_t g = s.group_max[lane];
   int above = 0;
@@ -625,10 +652,10 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
     const int at = atomicAdd(&s.entries, 1);
     if (at < kEntries) s.entry[at] = pick_entry(x, token);
   };
-  if (__any_sync(0xffffffffu, pick_key(top_named) >= bound)) for_named(false, 0, [&](int t, float y, int) { enter(y, t); });
-  auto reach = [&](int k, const uint4& q) {
-    const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+  if (__any_sync(0xffffffffu, pick_key(top_named) >= bound)) again(bound, [&](int t, float y) { enter(y, t); });
+  auto list_lanes = [&](int k, const uint4& q) {
     if (max(max(q.x, q.y), max(q.z, q.w)) < bound) return;
+    const uint32_t x[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (x[j] >= bound) {
@@ -636,9 +663,12 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
         if (at < kLanes) s.lane[at] = 4 * k + j;
       }
   };
+  if (top_any >= bound) {
 #pragma unroll
-  for (int j = 0; j < kKeyLoads; ++j) reach(tid + j * kSelectThreads, key[j]);
-  for (int k = tid + kKeyLoads * kSelectThreads; k < quads; k += kSelectThreads) reach(k, keys[k]);
+    for (int j = 0; j < kKeyLoads; ++j) list_lanes(tid + j * kThreads, key[j]);
+#pragma unroll 4
+    for (int k = tid + kKeyLoads * kThreads; k < quads; k += kThreads) list_lanes(k, keys[k]);
+  }
   __syncthreads();
   auto free_value = [&](int t) {  // of a token that is allowed and not named, else -inf
     const uint32_t named = taken != nullptr ? bit_of(taken, t) : 0u, ok = mask != nullptr ? bit_of(mask, t) : 1u;
@@ -647,8 +677,8 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
   };
   // the tokens of the lanes that reach the bound, one a lane here
   const int lanes = s.lanes;
-#pragma unroll 2
-  for (int k = warp; k < min(lanes, kLanes); k += kSelectWarps) {
+#pragma unroll 4
+  for (int k = warp; k < min(lanes, kLanes); k += kWarps) {
     const int x = s.lane[k];
     const int t = (x >> 5) * kTile + ((lane / kN) * 32 + (x & 31)) * kN + lane % kN - off;
     if (t >= 0 && t < r.V) enter(free_value(t), t);
@@ -656,7 +686,7 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
   __syncthreads();
   const int n = s.entries;
   if (n <= kEntries && lanes <= kLanes) {
-    for (int x = tid; x < n; x += kSelectThreads) {
+    for (int x = tid; x < n; x += kThreads) {
       const unsigned long long mine = s.entry[x];
       int before = 0;
 #pragma unroll 4
@@ -674,13 +704,13 @@ __global__ void __launch_bounds__(kSelectThreads) logits_select_kernel(const Pic
         const unsigned long long entry = pick_entry(x, t);
         if (entry < last) mine = max_u64(mine, entry);
       };
-      for_named(false, 0, [&](int t, float y, int) { look(t, y); });
-      for (int t = tid; t < r.V; t += kSelectThreads) look(t, free_value(t));
+      again(0u, [&](int t, float y) { look(t, y); });
+      for (int t = tid; t < r.V; t += kThreads) look(t, free_value(t));
       mine = warp_max_u64(mine);
       if (lane == 0) s.red[warp] = mine;
       __syncthreads();
       unsigned long long all = 0ull;
-      for (int w = 0; w < kSelectWarps; ++w) all = max_u64(all, s.red[w]);
+      for (int w = 0; w < kWarps; ++w) all = max_u64(all, s.red[w]);
       if (tid == 0) s.best[k] = all;
       last = all;  // (0, when nothing is left: then nothing is below it)
       __syncthreads();
@@ -733,20 +763,36 @@ PickPlan pick_plan(int M, int V, int B, bool ragged, int max_len, bool tokens, i
   return p;
 }
 
-constexpr int kStreamShared = (kWindow / 8) + kWindow / 32;  // bits, and a base for four words of them
+// bits, a base for four words of them, counters
+constexpr int kStreamShared = kWindow / 8 + kWindow / 32 + kCounters * 4;
+constexpr int kSelectShared = (1 << 22) / kTile * 4 + 8 + 8192 * 4;  // marks, and kept values
+
+template <typename T, int kThreads>
+int launch_select(PickArgs a, cudaStream_t st) {
+  static unsigned done = 0;
+  if (!ensure_smem_attr(logits_select_kernel<T, kThreads>, kSelectShared, &done))
+    return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (logits)");
+  a.kept = std::min(a.windows * a.cap, 8 * kThreads);
+  const cudaError_t e = launch_pdl(logits_select_kernel<T, kThreads>, dim3(static_cast<unsigned>(a.r.M)), dim3(kThreads),
+                                   static_cast<size_t>(a.tiles + a.kept) * 4, st, nullptr, 0, a);
+  return e == cudaSuccess ? DFLASH2_OK : fail(DFLASH2_ERR_CUDA, "logits launch failed: %s", cudaGetErrorString(e));
+}
 
 template <typename T>
-int launch_pick_t(const PickArgs& a, cudaStream_t st) {
+int launch_pick_t(PickArgs& a, cudaStream_t st) {
   static unsigned done = 0;
   if (!ensure_smem_attr(logits_stream_kernel<T>, kStreamShared, &done))
     return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (logits)");
   const int quads = (std::min(a.r.V, kWindow) + 127) / 128;
-  cudaError_t e = launch_pdl(logits_stream_kernel<T>, dim3(static_cast<unsigned>(a.stream_ctas + a.other_ctas)), dim3(kStreamThreads),
-                             a.windows > 0 ? static_cast<size_t>(quads) * 20 : 0, st, nullptr, 0, a);
-  if (e == cudaSuccess && (a.r.K > 0 || a.windows > 0))
-    e = launch_pdl(logits_select_kernel<T>, dim3(static_cast<unsigned>(a.r.M)), dim3(kSelectThreads),
-                   static_cast<size_t>(a.tiles) * 4, st, nullptr, 0, a);
-  return e == cudaSuccess ? DFLASH2_OK : fail(DFLASH2_ERR_CUDA, "logits launch failed: %s", cudaGetErrorString(e));
+  a.counters = a.cap <= kCounters ? a.cap : 0;
+  const cudaError_t e = launch_pdl(logits_stream_kernel<T>, dim3(static_cast<unsigned>(a.stream_ctas + a.other_ctas)),
+                                   dim3(kStreamThreads), a.windows > 0 ? static_cast<size_t>(quads) * 20 + a.counters * 4 : 0, st,
+                                   nullptr, 0, a);
+  if (e != cudaSuccess) return fail(DFLASH2_ERR_CUDA, "logits launch failed: %s", cudaGetErrorString(e));
+  if (a.r.K == 0 && a.windows == 0) return DFLASH2_OK;
+  const int sms = sm_count();
+  if (a.r.M <= sms) return launch_select<T, 1024>(a, st);
+  return a.r.M <= 3 * sms ? launch_select<T, 512>(a, st) : launch_select<T, 256>(a, st);
 }
 
 }  // namespace
