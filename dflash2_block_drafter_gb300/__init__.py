@@ -12,6 +12,8 @@ bias / scores, int32 for ids. Outputs are allocated here when not passed in.
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 
 import torch
@@ -140,9 +142,9 @@ def _dev(t, name, dtype=None, optional=False):
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if dtype is not None and t.dtype is not dtype and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    return _vp(t.data_ptr())
+    return t.data_ptr()  # (ctypes takes the number as it is)
 
 
 def _code(t):
@@ -704,15 +706,29 @@ def dflash2_kv4_attention_tree(q, cache, page_table, ctx_len, page_size, scale, 
 
 
 def _output(t, name, shape, dtype, device, stream):
-    """The output tensor `name`: allocated when not given, else checked for its size (_dev checks the rest)."""
-    n = 1
-    for x in shape:
-        n *= x
+    """(output tensor `name`, its pointer): allocated when not given, else checked."""
     if t is None:
-        return _new(shape, dtype, device, stream)
+        t = _new(shape, dtype, device, stream)
+        return t, t.data_ptr()
+    n = math.prod(shape)
     if t.numel() < n:
         raise ValueError(f"{name} holds {t.numel()} elements, fewer than the {n} the call writes")
-    return t
+    return t, _dev(t, name, dtype)
+
+
+def _array(t, name, n, dtype):
+    """The pointer of an optional dense array of n elements, or None."""
+    if t is None:
+        return None
+    if t.numel() != n:
+        raise ValueError(f"{name} holds {t.numel()} elements, expected {n}")
+    return _dev(t, name, dtype)
+
+
+def _current(t, name):
+    """Refuses a tensor of another device than the current one, on which the call would run."""
+    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
 
 
 def dflash2_kv4_plan(ctx_len, change, page_table, free_pages, free_state, page_size, num_pages, rows=0, place=None,
@@ -730,19 +746,19 @@ def dflash2_kv4_plan(ctx_len, change, page_table, free_pages, free_state, page_s
         raise ValueError("free_pages must be [capacity] and free_state hold its first place and its count")
     if place is not None and (place.dim() != 2 or place.shape[0] != B):
         raise ValueError(f"place must be [{B}, G], got {tuple(place.shape)}")
+    _current(ctx_len, "ctx_len")
     i32, dev = torch.int32, ctx_len.device
     shape = (max(0, rows),) if place is None else tuple(place.shape)
-    ctx_out = _output(ctx_out, "ctx_out", (B,), i32, dev, stream)
-    state_out = _output(state_out, "state_out", (2,), i32, dev, stream)
-    offsets = _output(offsets, "offsets", (B + 1,), i32, dev, stream)
-    slots = _output(slots, "slots", shape, torch.int64, dev, stream)
-    positions = _output(positions, "positions", shape, i32, dev, stream)
+    ctx_out, cp = _output(ctx_out, "ctx_out", (B,), i32, dev, stream)
+    state_out, sp = _output(state_out, "state_out", (2,), i32, dev, stream)
+    offsets, op = _output(offsets, "offsets", (B + 1,), i32, dev, stream)
+    slots, lp = _output(slots, "slots", shape, torch.int64, dev, stream)
+    positions, pp = _output(positions, "positions", shape, i32, dev, stream)
     _check(library().dflash2_kv4_plan(
         _dev(ctx_len, "ctx_len", i32), _dev(change, "change", i32), _dev(page_table, "page_table", i32),
         _dev(free_pages, "free_pages", i32), _dev(free_state, "free_state", i32), _dev(place, "place", i32, True), B,
-        0 if place is None else shape[1], rows, page_table.shape[1], page_size, num_pages, free_pages.shape[0],
-        _dev(ctx_out, "ctx_out", i32), _dev(state_out, "state_out", i32), _dev(offsets, "offsets", i32),
-        _dev(slots, "slots", torch.int64), _dev(positions, "positions", i32), _stream(stream)))
+        0 if place is None else shape[1], rows, page_table.shape[1], page_size, num_pages, free_pages.shape[0], cp, sp, op, lp,
+        pp, _stream(stream)))
     return ctx_out, state_out, offsets, slots, positions
 
 
@@ -753,11 +769,13 @@ def _matrix(t, name, rows, width, dtypes):
                          f"{tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__}")
     if not t.is_cuda or t.dtype not in dtypes:
         raise ValueError(f"{name} must be a CUDA tensor of {' or '.join(str(x) for x in dtypes)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    step, unit = t.stride()
+    if unit != 1 and t.shape[1] > 1:
         raise ValueError(f"{name}: each row must be dense")
-    return _vp(t.data_ptr()), t.stride(0) if rows > 1 else max(t.shape[1], 1)
+    return t.data_ptr(), step if rows > 1 else max(t.shape[1], 1)
 
 
+@functools.lru_cache(maxsize=256)
 def dflash2_logits_topk_workspace_bytes(M, V, B, ragged, max_len, drafted, n_bias, K) -> int:
     return library().dflash2_logits_topk_workspace_bytes(M, V, B, int(bool(ragged)), max_len, int(bool(drafted)), n_bias, K)
 
@@ -772,51 +790,47 @@ def dflash2_logits_topk(logits, K, requests=None, row_offsets=None, history=None
     unary [M, K] fp32, out [M, V] or None); cand and unary are None for K = 0."""
     if logits.dim() != 2:
         raise ValueError(f"logits must be [M, V], got shape {tuple(logits.shape)}")
+    _current(logits, "logits")
     M, V = logits.shape
-    if requests is None:
-        requests = row_offsets.numel() - 1 if row_offsets is not None else M
-    B = requests
-    if row_offsets is not None and row_offsets.numel() != B + 1:
-        raise ValueError(f"row_offsets holds {row_offsets.numel()} entries, expected B + 1 = {B + 1}")
-    i32, f32, types = torch.int32, torch.float32, (torch.bfloat16, torch.float32)
+    B = requests if requests is not None else (row_offsets.numel() - 1 if row_offsets is not None else M)
+    i32, f32, dev, dt = torch.int32, torch.float32, logits.device, logits.dtype
     code = _code(logits)
-    lp, ls = _matrix(logits, "logits", M, V, types)
+    rp = _array(row_offsets, "row_offsets", B + 1, i32)
+    lp, ls = _matrix(logits, "logits", M, V, (dt,))
     hp, hs, max_len = None, 0, 0
     if history is not None:
-        max_len = history.shape[-1]
         if history_len is None:
             raise ValueError("history needs history_len")
         hp, hs = _matrix(history, "history", B, 0, (i32,))
-    for t, n, name in ((prompt_len, B, "prompt_len"), (history_len, B, "history_len"), (repetition, B, "repetition"),
-                       (frequency, B, "frequency"), (presence, B, "presence"), (tokens, M, "tokens"), (parents, M, "parents")):
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{name} holds {t.numel()} elements, expected {n}")
+        max_len = history.shape[1]
+    per_request = (_array(repetition, "repetition", B, f32), _array(frequency, "frequency", B, f32),
+                   _array(presence, "presence", B, f32))
     if (bias_ids is None) != (bias is None):
         raise ValueError("bias_ids and bias go together")
-    if bias is not None and (bias_ids.dim() != 2 or bias_ids.shape[0] != B or bias.shape != bias_ids.shape):
-        raise ValueError(f"bias_ids and bias must both be [{B}, n], got {tuple(bias_ids.shape)} and {tuple(bias.shape)}")
+    n_bias = 0
+    if bias is not None:
+        if bias_ids.dim() != 2 or bias_ids.shape[0] != B or bias.shape != bias_ids.shape:
+            raise ValueError(f"bias_ids and bias must both be [{B}, n], got {tuple(bias_ids.shape)} and {tuple(bias.shape)}")
+        n_bias = bias.shape[1]
     mp, ms = (None, 0) if mask is None else _matrix(mask, "mask", M, (V + 31) // 32, (i32,))
+    cp = up = None
     if K > 0:
-        cand = _output(cand, "cand", (M, K), i32, logits.device, stream)
-        unary = _output(unary, "unary", (M, K), f32, logits.device, stream)
+        cand, cp = _output(cand, "cand", (M, K), i32, dev, stream)
+        unary, up = _output(unary, "unary", (M, K), f32, dev, stream)
     else:
         cand = unary = None
     if out is None and want_out:
-        out = _new((M, V), logits.dtype, logits.device, stream)
-    op, os_ = (None, 0) if out is None else _matrix(out, "out", M, V, (logits.dtype,))
-    n_bias = 0 if bias is None else bias.shape[1]
+        out = _new((M, V), dt, dev, stream)
+    op, os_ = (None, 0) if out is None else _matrix(out, "out", M, V, (dt,))
     if workspace is None:
-        need = library().dflash2_logits_topk_workspace_bytes(M, V, B, int(row_offsets is not None), max_len,
-                                                             int(tokens is not None), n_bias, K)
-        workspace = _new(need, torch.uint8, logits.device, stream) if need else None
+        need = dflash2_logits_topk_workspace_bytes(M, V, B, row_offsets is not None, max_len, tokens is not None, n_bias, K)
+        workspace = _new(need, torch.uint8, dev, stream) if need else None
     wp, wn = (None, 0) if workspace is None else (_dev(workspace, "workspace"), workspace.numel() * workspace.element_size())
     _check(library().dflash2_logits_topk(
-        lp, ls, M, V, code, B, _dev(row_offsets, "row_offsets", i32, True), hp, hs, _dev(prompt_len, "prompt_len", i32, True),
-        _dev(history_len, "history_len", i32, True), max_len, _dev(repetition, "repetition", f32, True),
-        _dev(frequency, "frequency", f32, True), _dev(presence, "presence", f32, True), _dev(tokens, "tokens", i32, True),
-        _dev(parents, "parents", i32, True), _dev(bias_ids, "bias_ids", i32, True), _dev(bias, "bias", f32, True),
-        n_bias, mp, ms, K, _dev(cand, "cand", i32, True), _dev(unary, "unary", f32, True), op, os_, wp, wn,
-        _stream(stream)))
+        lp, ls, M, V, code, B, rp, hp, hs, _array(prompt_len, "prompt_len", B, i32),
+        _array(history_len, "history_len", B, i32), max_len, *per_request, _array(tokens, "tokens", M, i32),
+        _array(parents, "parents", M, i32), _dev(bias_ids, "bias_ids", i32, True), _dev(bias, "bias", f32, True), n_bias, mp, ms,
+        K, cp, up, op, os_, wp, wn, _stream(stream)))
     return cand, unary, out
 
 

@@ -92,12 +92,10 @@ def test_python_checks():
                        ("slots holds", dict(slots=torch.zeros(7, dtype=torch.int64))),
                        ("offsets holds", dict(offsets=ints(4))), ("state_out holds", dict(state_out=ints(1))),
                        ("ctx_out holds", dict(ctx_out=ints(3))), ("positions holds", dict(positions=ints(7)))):
-        outs = dict(ctx_out=ints(4), state_out=ints(2), offsets=ints(5), slots=torch.zeros(8, dtype=torch.int64),
-                    positions=ints(8))
         with pytest.raises(ValueError, match=match):
-            plan(**dict(outs, **bad))
+            plan(**bad)
     with pytest.raises(ValueError, match="CUDA"):
-        plan(ctx_out=ints(4), state_out=ints(2), offsets=ints(5), slots=torch.zeros(8, dtype=torch.int64), positions=ints(8))
+        plan()
     pick = lambda **kw: d.dflash2_logits_topk(**dict(dict(logits=torch.zeros(4, 64), K=4), **kw))
     with pytest.raises(ValueError, match="CUDA"):
         pick()
