@@ -36,13 +36,13 @@ namespace {
 constexpr int kWindowLog = 18, kWindow = 1 << kWindowLog;  // tokens whose names a CTA collects
 constexpr int kTile = 1024;                                // tokens a warp reads at a time,
 constexpr int kLaneTokens = 32;                            // of which a lane has
-constexpr int kStreamThreads = 256, kStreamWarps = kStreamThreads / 32;
-constexpr int kStreamTiles = 2;                            // tiles a warp
+constexpr int kStreamThreads = 512, kStreamWarps = kStreamThreads / 32;
+constexpr int kStreamTiles = 4;                            // tiles a warp, at most
 constexpr int kEntries = 1024, kLanes = 512;               // that reach the bound
-constexpr int kCounters = 4096;                            // of a CTA's named tokens, in shared memory
 constexpr int kPickK = 16;
 constexpr uint32_t kCountMask = (1u << 20) - 1, kInPrompt = 1u << 20;  // a counter; over it, which bias
 constexpr int kBiasShift = 21;
+constexpr uint32_t kDrafted = 1u << 31;  // beside a named token: one of the request's drafted rows has it
 
 struct PickArgs {
   LogitsTopk r;
@@ -50,7 +50,7 @@ struct PickArgs {
   int windows, cap;     // windows of the vocabulary (0: nothing is named); counters a window
   int words;            // of bits a request
   int tiles;            // a row
-  int ctas_a_row, stream_ctas, other_ctas;  // of the first kernel
+  int warp_tiles, ctas_a_row, stream_ctas, other_ctas;  // of the first kernel
   int counters, kept;   // named tokens' counters and values that shared memory holds, at most
   uint32_t* bits;       // [B][words]
   int* named;           // [B][windows] how many
@@ -150,7 +150,7 @@ __device__ __forceinline__ TreeLines request_lines(const PickArgs& a, int b, int
   return tree_lines(parent, rows, bad);
 }
 
-// The requests of rows x 256 .. (row_off given), and the check of the spans.
+// The requests of rows x 512 .. (row_off given), and the check of the spans.
 __device__ __forceinline__ void map_rows(const PickArgs& a, int x, int ctas) {
   const LogitsTopk& r = a.r;
   const int m = x * kStreamThreads + static_cast<int>(threadIdx.x);
@@ -251,50 +251,54 @@ __device__ __forceinline__ void collect_names(const PickArgs& a, int x, uint32_t
   }
   for (int w = tid; w < (len + 31) / 32; w += kStreamThreads) to[w] = bits[w];
   if (n == 0) return;
-  // counters beside the bits if they fit there (an SM's atomics on global memory go at one a clock)
-  uint32_t* counters = a.counters >= n ? base + quads : nullptr;
-  for (int k = tid; k < n; k += kStreamThreads) (counters != nullptr ? counters[k] : names[k].y) = 0u;
+  // counters of 16 bits, and a bit for the prompt's, beside the bits if they fit there (an SM's atomics on global memory
+  // go at one a clock, and on one address far slower)
+  uint32_t* counts = a.counters > 0 ? base + quads : nullptr;  // [counters / 2]
+  uint32_t* in_prompt = counts + a.counters / 2;               // [counters / 32]
+  for (int k = tid; k < n; k += kStreamThreads) names[k].y = 0u;
+  for (int k = tid; k < (a.counters > 0 ? n / 2 + 1 : 0); k += kStreamThreads) counts[k] = 0u;
+  for (int k = tid; k < (a.counters > 0 ? n / 32 + 1 : 0); k += kStreamThreads) in_prompt[k] = 0u;
   __syncthreads();
-  auto place_of = [&](int u) {
-    const int i = (u >> 5) & 3;
-    const uint4 w = bits4[u >> 7];
-    const uint32_t below = (1u << (u & 31)) - 1u;
-    return static_cast<int>(base[u >> 7]) + __popc(w.x & (i > 0 ? ~0u : below)) + (i > 0 ? __popc(w.y & (i > 1 ? ~0u : below)) : 0) +
-           (i > 1 ? __popc(w.z & (i > 2 ? ~0u : below)) : 0) + (i > 2 ? __popc(w.w & below) : 0);
-  };
-  auto counter = [&](int k) { return counters != nullptr ? counters + k : &names[k].y; };
   // (a token that is named more than once writes its name more than once, the same each time)
   auto place_name = [&](int t) {
     const int u = t - lo;
     if (t < 0 || u < 0 || u >= len) return -1;
-    const int k = place_of(u);
+    const int i = (u >> 5) & 3;
+    const uint4 w = bits4[u >> 7];
+    const uint32_t below = (1u << (u & 31)) - 1u;
+    const int k = static_cast<int>(base[u >> 7]) + __popc(w.x & (i > 0 ? ~0u : below)) + (i > 0 ? __popc(w.y & (i > 1 ? ~0u : below)) : 0) +
+                  (i > 1 ? __popc(w.z & (i > 2 ? ~0u : below)) : 0) + (i > 2 ? __popc(w.w & below) : 0);
     names[k].x = static_cast<uint32_t>(t);
     return k;
   };
-  if (r.tokens != nullptr && warp == 0)
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if ((there >> (lane + 32 * h)) & 1) place_name(__ldg(r.tokens + first + lane + 32 * h));
   if (r.n_bias > 0) {
     for (int e = tid; e < r.n_bias; e += kStreamThreads) {
       const int k = place_name(__ldg(bias_ids + e));
-      if (k >= 0) atomicMax(counter(k), static_cast<uint32_t>(r.n_bias - e) << kBiasShift);
+      if (k >= 0) atomicMax(&names[k].y, static_cast<uint32_t>(r.n_bias - e) << kBiasShift);
     }
     __syncthreads();
   }
   for_history(hist, hist_len, [&](int t, int at_place) {
     const int k = place_name(t);
     if (k < 0) return;
-    if (at_place < prompt)
-      atomicOr(counter(k), kInPrompt);
-    else if (counters != nullptr)
-      atomicAdd(counters + k, 1u);
+    if (counts == nullptr)
+      at_place < prompt ? atomicOr(&names[k].y, kInPrompt) : atomicAdd(&names[k].y, 1u);
+    else if (at_place < prompt)
+      atomicOr(in_prompt + (k >> 5), 1u << (k & 31));
     else
-      atomicAdd(&names[k].y, 1u);
+      atomicAdd(counts + (k >> 1), 1u << (16 * (k & 1)));
   });
-  if (counters == nullptr) return;
   __syncthreads();
-  for (int k = tid; k < n; k += kStreamThreads) names[k].y = counters[k];
+  if (counts != nullptr)
+    for (int k = tid; k < n; k += kStreamThreads)
+      names[k].y += ((counts[k >> 1] >> (16 * (k & 1))) & 0xffffu) + (((in_prompt[k >> 5] >> (k & 31)) & 1u) != 0u ? kInPrompt : 0u);
+  if (r.tokens != nullptr && warp == 0)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if ((there >> (lane + 32 * h)) & 1) {
+        const int t = __ldg(r.tokens + first + lane + 32 * h), k = place_name(t);
+        if (k >= 0) names[k].x = static_cast<uint32_t>(t) | kDrafted;
+      }
 }
 
 // ------------------------------------------------------------------ stream
@@ -306,6 +310,15 @@ __device__ __forceinline__ uint4 load16(const void* p) {
                : "l"(p));
   return u;
 }
+// Four bits as the top bits of four bytes, whose signs are then spread over the bytes of elements.
+__device__ __forceinline__ uint32_t spread4(uint32_t bits) { return (bits & 15u) * 0x10204080u; }
+template <uint32_t kSelect>
+__device__ __forceinline__ uint32_t signs(uint32_t x) {  // (8 + i: the sign of byte i)
+  uint32_t y;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(y) : "r"(x), "n"(kSelect));
+  return y;
+}
+__device__ __forceinline__ uint32_t choose(uint32_t mask, uint32_t a, uint32_t b) { return (a & mask) | (b & ~mask); }
 template <typename T>
 struct PickVec;
 template <>
@@ -316,10 +329,11 @@ struct PickVec<float> {
   }
   // elements whose bit is set become -inf
   static __device__ __forceinline__ void drop(uint4& u, uint32_t bits) {
-    if (bits & 1u) u.x = 0xff800000u;
-    if (bits & 2u) u.y = 0xff800000u;
-    if (bits & 4u) u.z = 0xff800000u;
-    if (bits & 8u) u.w = 0xff800000u;
+    const uint32_t x = spread4(bits);
+    u.x = choose(signs<0x8888>(x), 0xff800000u, u.x);
+    u.y = choose(signs<0x9999>(x), 0xff800000u, u.y);
+    u.z = choose(signs<0xaaaa>(x), 0xff800000u, u.z);
+    u.w = choose(signs<0xbbbb>(x), 0xff800000u, u.w);
   }
   static __device__ __forceinline__ float max(float m, const uint4& u) {
     return max3_nan(max3_nan(m, __uint_as_float(u.x), __uint_as_float(u.y)), __uint_as_float(u.z), __uint_as_float(u.w));
@@ -347,16 +361,12 @@ struct PickVec<__nv_bfloat16> {
   static __device__ __forceinline__ uint32_t word(const uint4& u, int i) {
     return i == 0 ? u.x : (i == 1 ? u.y : (i == 2 ? u.z : u.w));
   }
-  static __device__ __forceinline__ uint32_t drop2(uint32_t w, uint32_t bits) {
-    if (bits & 1u) w = (w & 0xffff0000u) | 0xff80u;
-    if (bits & 2u) w = (w & 0xffffu) | 0xff800000u;
-    return w;
-  }
   static __device__ __forceinline__ void drop(uint4& u, uint32_t bits) {
-    u.x = drop2(u.x, bits);
-    u.y = drop2(u.y, bits >> 2);
-    u.z = drop2(u.z, bits >> 4);
-    u.w = drop2(u.w, bits >> 6);
+    const uint32_t x = spread4(bits), y = spread4(bits >> 4);
+    u.x = choose(signs<0x9988>(x), 0xff80ff80u, u.x);
+    u.y = choose(signs<0xbbaa>(x), 0xff80ff80u, u.y);
+    u.z = choose(signs<0x9988>(y), 0xff80ff80u, u.z);
+    u.w = choose(signs<0xbbaa>(y), 0xff80ff80u, u.w);
   }
   static __device__ __forceinline__ __nv_bfloat162 two(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
   static __device__ __forceinline__ float max(float m, const uint4& u) {
@@ -412,11 +422,10 @@ template <typename T>
 __device__ __forceinline__ void stream_row(const PickArgs& a, int x) {
   using Vec = PickVec<T>;
   constexpr int kN = Vec::kN, kG = kLaneTokens / kN;
-  constexpr uint32_t kAll = (1u << kN) - 1;
   const LogitsTopk& r = a.r;
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
   const int m = x / a.ctas_a_row;
-  const int tile0 = ((x - m * a.ctas_a_row) * kStreamWarps + warp) * kStreamTiles;
+  const int tile0 = ((x - m * a.ctas_a_row) * kStreamWarps + warp) * a.warp_tiles;
   const T* row = static_cast<const T*>(r.logits) + static_cast<int64_t>(m) * r.stride;
   T* out = r.out != nullptr ? static_cast<T*>(r.out) + static_cast<int64_t>(m) * r.out_stride : nullptr;
   const int off = row_offset(row), mask_words = (r.V + 31) / 32;
@@ -439,7 +448,7 @@ __device__ __forceinline__ void stream_row(const PickArgs& a, int x) {
     __syncthreads();
     if (lives == 0) return;
   }
-  for (int tile = tile0; tile < min(tile0 + kStreamTiles, a.tiles); ++tile) {
+  for (int tile = tile0; tile < min(tile0 + a.warp_tiles, a.tiles); ++tile) {
     const int t0 = tile * kTile - off;  // the tile's first token
     const bool inside = t0 >= 0 && t0 + kTile <= r.V;
     uint4 v[kG];
@@ -456,7 +465,7 @@ __device__ __forceinline__ void stream_row(const PickArgs& a, int x) {
       if (__any_sync(0xffffffffu, denied != 0u)) {
 #pragma unroll
         for (int g = 0; g < kG; ++g)  // those of the lane's g-th sixteen bytes
-          Vec::drop(v[g], (__shfl_sync(0xffffffffu, denied, (g * 32 + lane) * kN / 32) >> (lane * kN & 31)) & kAll);
+          Vec::drop(v[g], __shfl_sync(0xffffffffu, denied, (g * 32 + lane) * kN / 32) >> (lane * kN & 31));
       }
     }
     if (out != nullptr)
@@ -508,6 +517,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 6 : (kThreads == 5
   using Vec = PickVec<T>;
   constexpr int kN = Vec::kN, kWarps = kThreads / 32;
   constexpr int kKeyLoads = kThreads >= 512 ? 2048 / kThreads : 0;  // sixteen bytes of keys a thread keeps
+  constexpr int kBatch = kThreads == 1024 ? 4 : 2;                  // named tokens a thread has in flight
   __shared__ SelectShared s;
   extern __shared__ uint32_t marked[];  // [tiles] lanes that hold a named token
   float* kept = reinterpret_cast<float*>(marked + a.tiles);  // [kept] named tokens' values
@@ -562,30 +572,32 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 6 : (kThreads == 5
   };
   // f(token, value, place) of the thread's named tokens from place `from` on (a multiple of 32; whole warps)
   auto for_named = [&](int from, auto f) {
-    for (int p0 = from + warp * 32; p0 < named; p0 += 2 * kThreads) {
-      uint2 name[2];
-      float y[2];
-      uint32_t ok[2];
+    for (int p0 = from + warp * 32; p0 < named; p0 += kBatch * kThreads) {
+      uint2 name[kBatch];
+      float y[kBatch];
+      int token[kBatch];
+      uint32_t ok[kBatch];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kBatch; ++h) {
         const int place = p0 + h * kThreads + lane;
         name[h] = place < named ? name_at(place) : make_uint2(0xffffffffu, 0u);
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool mine = name[h].x != 0xffffffffu;
-        ok[h] = mine && mask != nullptr ? bit_of(mask, static_cast<int>(name[h].x)) : 1u;
-        y[h] = mine ? Vec::load(row + name[h].x) : 0.f;
+      for (int h = 0; h < kBatch; ++h) {
+        token[h] = name[h].x != 0xffffffffu ? static_cast<int>(name[h].x & ~kDrafted) : -1;
+        ok[h] = token[h] >= 0 && mask != nullptr ? bit_of(mask, token[h]) : 1u;
+        y[h] = token[h] >= 0 ? Vec::load(row + token[h]) : 0.f;
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int t = static_cast<int>(name[h].x);
+      for (int h = 0; h < kBatch; ++h) {
+        const int t = token[h];
         uint32_t times = name[h].y & kCountMask;
-        for (uint64_t left = line; left != 0ull; left &= left - 1ull) {
-          const int at = __ffsll(static_cast<long long>(left)) - 1;
-          if (__shfl_sync(0xffffffffu, at < 32 ? drafted[0] : drafted[1], at & 31) == t) ++times;
-        }
-        if (name[h].x == 0xffffffffu) continue;
+        if (__any_sync(0xffffffffu, t >= 0 && (name[h].x & kDrafted) != 0u))
+          for (uint64_t left = line; left != 0ull; left &= left - 1ull) {
+            const int at = __ffsll(static_cast<long long>(left)) - 1;
+            if (__shfl_sync(0xffffffffu, at < 32 ? drafted[0] : drafted[1], at & 31) == t) ++times;
+          }
+        if (t < 0) continue;
         float x = y[h];
         if (times != 0u || (name[h].y & kInPrompt) != 0u) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
         if (times != 0u) x = __fsub_rn(x, __fadd_rn(__fmul_rn(freq, static_cast<float>(times)), pres));
@@ -607,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 6 : (kThreads == 5
   // once more, those that reach a key
   auto again = [&](uint32_t key, auto f) {
     for (int place = tid; place < min(named, a.kept); place += kThreads)
-      if (pick_key(kept[place]) >= key) f(static_cast<int>(name_at(place).x), kept[place]);
+      if (pick_key(kept[place]) >= key) f(static_cast<int>(name_at(place).x & ~kDrafted), kept[place]);
     for_named(a.kept, [&](int t, float y, int) { f(t, y); });
   };
   auto store_rest = [&]() {
@@ -764,7 +776,7 @@ PickPlan pick_plan(int M, int V, int B, bool ragged, int max_len, bool tokens, i
 }
 
 // bits, a base for four words of them, counters
-constexpr int kStreamShared = kWindow / 8 + kWindow / 32 + kCounters * 4;
+constexpr int kStreamShared = 112 * 1024;  // (two CTAs an SM)
 constexpr int kSelectShared = (1 << 22) / kTile * 4 + 8 + 8192 * 4;  // marks, and kept values
 
 template <typename T, int kThreads>
@@ -784,9 +796,11 @@ int launch_pick_t(PickArgs& a, cudaStream_t st) {
   if (!ensure_smem_attr(logits_stream_kernel<T>, kStreamShared, &done))
     return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (logits)");
   const int quads = (std::min(a.r.V, kWindow) + 127) / 128;
-  a.counters = a.cap <= kCounters ? a.cap : 0;
+  // (a multiple of 32, and one word more of each kind)
+  const int counters = (a.cap + 63) / 32 * 32, shared = quads * 20 + counters / 2 * 4 + counters / 32 * 4;
+  a.counters = a.windows > 0 && a.r.max_len <= 0xffff && shared <= kStreamShared ? counters : 0;
   const cudaError_t e = launch_pdl(logits_stream_kernel<T>, dim3(static_cast<unsigned>(a.stream_ctas + a.other_ctas)),
-                                   dim3(kStreamThreads), a.windows > 0 ? static_cast<size_t>(quads) * 20 + a.counters * 4 : 0, st,
+                                   dim3(kStreamThreads), a.windows == 0 ? 0 : static_cast<size_t>(a.counters > 0 ? shared : quads * 20), st,
                                    nullptr, 0, a);
   if (e != cudaSuccess) return fail(DFLASH2_ERR_CUDA, "logits launch failed: %s", cudaGetErrorString(e));
   if (a.r.K == 0 && a.windows == 0) return DFLASH2_OK;
@@ -816,7 +830,9 @@ int launch_logits_topk(const LogitsTopk& r, cudaStream_t st) {
   a.keys = reinterpret_cast<uint32_t*>(ws + p.keys);
   a.err = device_error_word();
   if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
-  a.ctas_a_row = (a.tiles + kStreamWarps * kStreamTiles - 1) / (kStreamWarps * kStreamTiles);
+  // tiles a warp: one while the SMs have warps left for the next (two CTAs each)
+  a.warp_tiles = static_cast<int>(std::min<int64_t>(kStreamTiles, 1 + static_cast<int64_t>(r.M) * a.tiles / (2 * kStreamWarps * sm_count())));
+  a.ctas_a_row = (a.tiles + kStreamWarps * a.warp_tiles - 1) / (kStreamWarps * a.warp_tiles);
   a.stream_ctas = r.M * a.ctas_a_row;
   a.other_ctas = r.B * p.windows + (r.row_off != nullptr ? (r.M + kStreamThreads - 1) / kStreamThreads : 0);
   return r.dtype == DFLASH2_F32 ? launch_pick_t<float>(a, st) : launch_pick_t<__nv_bfloat16>(a, st);
