@@ -14,8 +14,8 @@
 // each other, so that a thread needs four pairs of factors a tile instead of 128. Tiles with rows further apart, with
 // masks, or of the tree's own rows take a path that reads a factor a key.
 //
-// Ranges of the line leave partial results in the workspace; which ranges share an item is written beside them by the
-// one that ends it, and a second kernel joins them, a warp a row. (So no CTA waits for another.)
+// Ranges of the line leave partial results in the workspace. A range can end one item that earlier ones began; it says
+// which there, and a second kernel joins the parts of these, a warp a row. (So no CTA waits for another.)
 #include <algorithm>
 
 #include "kv4_block.cuh"
@@ -37,7 +37,8 @@ struct WideCfg {
   static constexpr int kRaw = 4 * L::kGranuleBytes, kSlots = 3;
   static constexpr int kOffInfo = kOffRaw + 2 * kSlots * kRaw; // WideInfo [4]
   static constexpr int kOffLine = kOffInfo + 4 * 1120;         // uint64 [2][64]: of two items in turn
-  static constexpr int kOffBar = kOffLine + 2 * kTreeRows * 8;
+  static constexpr int kOffQs = kOffLine + 2 * kTreeRows * 8;  // float [2][128]: what a row's scores are multiplied by
+  static constexpr int kOffBar = kOffQs + 2 * kWRows * 4;
   static constexpr int kSmem = 1024 + kOffBar + 384;
   // 640 x 96 registers at launch, shared out
   static constexpr int kSoftRegs = 144, kOtherRegs = 64;
@@ -50,25 +51,35 @@ struct WideInfo {
 };
 static_assert(sizeof(WideInfo) <= 1120, "info");
 
+// (Tensor-memory loads and stores are whole warps': each is preceded by a barrier of the warp, since nothing else keeps the
+// compiler from leaving lanes apart after a condition of their own.)
 __device__ __forceinline__ void tmem_ld32(uint32_t t, float (&x)[32]) {
+  __syncwarp();
   tmem_ld_32x32b_x32(t, reinterpret_cast<uint32_t(&)[32]>(x));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t t, uint32_t (&r)[16]) {
+  __syncwarp();
+  tmem_ld_32x32b_x16(t, r);
+}
 __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t (&r)[16]) {
+  __syncwarp();
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(t),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t t, const float (&x)[32]) {
-  uint32_t a[16], b[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    a[i] = __float_as_uint(x[i]);
-    b[i] = __float_as_uint(x[16 + i]);
-  }
-  tmem_st16(t, a);
-  tmem_st16(t + 16, b);
+__device__ __forceinline__ void tmem_ld8(uint32_t t, float (&x)[8]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  __syncwarp();
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(t));
+}
+__device__ __forceinline__ void tmem_st4(uint32_t t, const uint32_t (&r)[4]) {
+  __syncwarp();
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
 }
 // One MMA whose A operand lies in tensor memory.
 template <bool first>
@@ -80,6 +91,18 @@ __device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b_lo, 
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
       "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "n"(first ? 0 : 1)
       : "memory");
+}
+
+// One lane of a (converged) warp. (What it runs is known to be one thread's, so that the products' descriptors stay in
+// uniform registers.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // A row's largest value as a power of two (0: nothing but zeros), from its (scale, bias) pairs.
@@ -96,7 +119,7 @@ __device__ __forceinline__ float row_largest(const uint32_t (&par)[2]) {
 
 struct WideArgs {
   BlockArgs a;
-  int2* entry;  // [item] the ranges that share it
+  int2* entry;  // [CTA] the item that ends in its range and began in an earlier one (-1: none), and the range where
 };
 
 template <int D>
@@ -112,9 +135,10 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_wide_kernel(const WideArgs w
   uint64_t* tree_line = reinterpret_cast<uint64_t*>(smem + C::kOffLine);
   const uint32_t bars = smem_u32(smem + C::kOffBar);
   const uint32_t kfull = bars, kempty = bars + 16, vfull = bars + 32, vempty = bars + 48;  // [2] each: operand buffers
-  const uint32_t sfull = bars + 64, pfull = bars + 80, odone = bars + 96, qfull = bars + 112;  // [2] each: row tiles
-  const uint32_t raw_full = bars + 128, raw_empty = bars + 176;                            // [side][3]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 224);
+  const uint32_t sfull = bars + 64, pfull = bars + 96, odone = bars + 128;  // [row tile][buffer of scores]
+  const uint32_t qfull = bars + 160;                                        // [row tile]
+  const uint32_t raw_full = bars + 176, raw_empty = bars + 224;             // [side][3]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + 272);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   uint32_t* came_s = tmem_slot + 2;  // [side][3]: the granules that came
 
@@ -125,10 +149,12 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_wide_kernel(const WideArgs w
       mbar_init(vfull + 8 * i, kBDeqWarps / 2);
       mbar_init(kempty + 8 * i, 1);
       mbar_init(vempty + 8 * i, 1);
+      mbar_init(qfull + 8 * i, 4);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(sfull + 8 * i, 1);
       mbar_init(pfull + 8 * i, 4);
       mbar_init(odone + 8 * i, 1);
-      mbar_init(qfull + 8 * i, 4);
     }
     for (int i = 0; i < 6; ++i) {
       mbar_init(raw_full + 8 * i, 1);
@@ -144,13 +170,17 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_wide_kernel(const WideArgs w
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;  // S (then P) of the row tiles at columns 0 and 128, O at 256 and 384
+  const uint32_t tmem = *tmem_slot;  // S (then P) of a row tile: two buffers of 64 keys from column 0 or 128, O from 256 or 384
   pdl_trigger();
   pdl_wait();
   const BlockRange range = block_range(a, kWSetup, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
   // an item's rows: one tile of them, or two of equal size
   auto rows_of = [&](const Walk& w) { return min(a.tile_rows, a.rows - w.rt * a.tile_rows); };
   auto tiles_of = [&](int rows) { return rows > kWRows ? 2 : 1; };
+  // halves of a tile of keys that hold any: the tree's own rows lie in the first
+  auto halves_of = [&](const Walk& w, int j) {
+    return j >= w.seq.cached || w.seq.hi - ((w.seq.lo >> kBTileLog) + j) * kBTile <= kBTile / 2 ? 1 : 2;
+  };
 
   if (warp >= kBSoftWarps && warp < kBSoftWarps + kBDeqWarps) {
     // ------------------------------------------------------------------ dequant: four warps a side, 32 keys each
@@ -244,34 +274,53 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_wide_kernel(const WideArgs w
             for (int k = 0; k < 4; ++k) st_shared_v4(to[k] + tile + i * kStep * 128, dequant_word(cw[k], s24, s20, b));
           }
         } else {
-          // the sequence's own rows
+          // the sequence's own rows: their powers of two, then (read again) the operands. (Loops, here and below: code that
+          // runs once an item is fetched for it, and straight lines of it take longer than their work.)
+          const uint32_t kOdd = 0x7fffffffu;  // a row that is not finite: values as for cached rows, keys become NaN
+          float most = 0.f, least = 3e38f;
           wait_on(empty + 8 * buf, par, abort_flag, a.err);
 #pragma unroll 1
           for (int i = 0; i < NCH; ++i) {
             const int t = sub + i * kStep, key = dw * 32 + t;
-            float f = 0.f;
-            uint4 u[4];
+            uint32_t m = 0;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) u[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (dw * 32 + i * kStep < a.G) {
-              uint32_t m = 0;
+            for (int k = 0; k < 4; ++k)
+              if (key < a.G) m = max(m, max_abs8(__ldg(reinterpret_cast<const uint4*>(own_src + key * a.new_stride + ch * 32 + 8 * k))));
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (key < a.G) u[k] = __ldg(reinterpret_cast<const uint4*>(own_src + key * a.new_stride + ch * 32 + 8 * k));
-#pragma unroll
-              for (int k = 0; k < 4; ++k) m = max(m, max_abs8(u[k]));
-#pragma unroll
-              for (int x = 1; x < NCH; x <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
-              const float p2 = pow2_of(__uint_as_float(m), low);
-              const bool odd = side == 1 && m >= kBInfinity;
-              f = odd ? __uint_as_float(0x7fffffffu) : p2;
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                u[k] = odd ? make_uint4(0u, 0u, 0u, 0u) : convert_word(u[k], pow2_inverse(p2));
+            for (int x = 1; x < NCH; x <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
+            const float own = m >= kBInfinity ? __uint_as_float(kOdd) : pow2_of(__uint_as_float(m), low);
+            if (m >= kBInfinity) {
+              if (side == 1) least = 0.f;
+            } else if (m > 0) {
+              least = fminf(least, own);
+              most = fmaxf(most, own);
             }
+            if (ch == 0) inf[2 * t] = own;
+          }
+          most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+          least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(least)));
+          if (most == 0.f) most = 1.f;
+          const bool mixed = least * kWSpread < most;
+          __syncwarp();
+#pragma unroll 1
+          for (int i = 0; i < NCH; ++i) {
+            const int t = sub + i * kStep, key = dw * 32 + t;
+            const float own = inf[2 * t], p2 = mixed ? own : most;
+            const bool odd = __float_as_uint(own) == kOdd;
+            const uint32_t none = side == 0 && odd ? 0x7fff7fffu : 0u;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) st_shared_v4(to[k] + tile + i * kStep * 128, u[k]);
-            if (ch == 0) inf[2 * t] = side == 0 || key < a.G ? f : -1.f;
+            for (int k = 0; k < 4; ++k) {
+              uint4 u = make_uint4(none, none, none, none);
+              if (key < a.G && !odd)
+                u = convert_word(__ldg(reinterpret_cast<const uint4*>(own_src + key * a.new_stride + ch * 32 + 8 * k)), pow2_inverse(p2));
+              st_shared_v4(to[k] + tile + i * kStep * 128, u);
+            }
+            __syncwarp();
+            if (ch == 0) inf[2 * t] = side == 0 ? (odd ? 1.f : p2) : (key < a.G ? (odd ? own : p2) : -1.f);
+          }
+          if (lane == 0) {
+            (side == 0 ? info->k : info->v)[dw] = most;
+            (side == 0 ? info->mixed_k : info->mixed_v)[dw] = mixed ? 1u : 0u;
           }
         }
         fence_proxy_async_smem();
@@ -282,10 +331,10 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_wide_kernel(const WideArgs w
   } else if (warp == kBMmaWarp || warp == kBMmaWarp + 1) {
     // ------------------------------------------------------------------ MMA issuers: S, and O
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t it = 0, done[2] = {0u, 0u}, pieces[2] = {0u, 0u};  // tiles of keys; a row tile's products, its items
       if (warp == kBMmaWarp) {
-        constexpr uint32_t kFmt = (1u << 4) | (static_cast<uint32_t>(kBTile >> 3) << 17) | (8u << 24);  // f32 <- f16, M = 128
+        constexpr uint32_t kFmt = (1u << 4) | (static_cast<uint32_t>(64 >> 3) << 17) | (8u << 24);  // f32 <- f16, M = 128, N = 64
         const uint64_t kd = desc_kmajor_sw128(smem_u32(smem)), qd = desc_kmajor_sw128(smem_u32(smem + C::kOffQ));
         const uint32_t hi = static_cast<uint32_t>(kd >> 32), k_lo = static_cast<uint32_t>(kd), q_lo = static_cast<uint32_t>(qd);
         for (Walk w(a, range); w.valid(); w.next(a)) {
@@ -298,19 +347,21 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_wide_kernel(const WideArgs w
           for (int j = w.j0; j < w.j1; ++j, ++it) {
             const uint32_t buf = it & 1u, k = k_lo + buf * (C::kTileBytes / 16);
             wait_on(kfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
+            const int nh = halves_of(w, j);
 #pragma unroll 1
-            for (int t = 0; t < nt; ++t) {
-              if (done[t] > 0) wait_on(odone + 8 * t, (done[t] - 1) & 1u, abort_flag, a.err);  // P is read
-              ++done[t];
+            for (int x = 0; x < nh * nt; ++x) {
+              const int t = nt == 2 ? x & 1 : 0;
+              const uint32_t n = done[t]++, at = 2 * t + (n & 1u);
+              if (n > 1) wait_on(odone + 8 * at, ((n >> 1) - 1) & 1u, abort_flag, a.err);  // P is read
               tc_fence_after();
-              const uint32_t q = q_lo + t * (C::kTileBytes / 16), d = tmem + t * kBTile;
-              mma_lean<true>(d, q, k, hi, hi, kFmt);
+              const uint32_t q = q_lo + t * (C::kTileBytes / 16), d = tmem + at * 64, kh = k + (nt == 2 ? x >> 1 : x) * (64 * 128 / 16);
+              mma_lean<true>(d, q, kh, hi, hi, kFmt);
 #pragma unroll
               for (int s = 1; s < D / 16; ++s) {
                 const uint32_t o = (s >> 2) * (kBTile * 128 / 16) + 2 * (s & 3);
-                mma_lean<false>(d, q + o, k + o, hi, hi, kFmt);
+                mma_lean<false>(d, q + o, kh + o, hi, hi, kFmt);
               }
-              mma_commit(sfull + 8 * t);
+              mma_commit(sfull + 8 * at);
             }
             mma_commit(kempty + 8 * buf);
           }
@@ -325,19 +376,21 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_wide_kernel(const WideArgs w
           for (int j = w.j0; j < w.j1; ++j, ++it) {
             const uint32_t buf = it & 1u, v = v_lo + buf * (C::kTileBytes / 16);
             wait_on(vfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
+            const int nh = halves_of(w, j);
 #pragma unroll 1
-            for (int t = 0; t < nt; ++t) {
-              wait_on(pfull + 8 * t, done[t] & 1u, abort_flag, a.err);
-              ++done[t];
+            for (int x = 0; x < nh * nt; ++x) {
+              const int t = nt == 2 ? x & 1 : 0, h = nt == 2 ? x >> 1 : x;
+              const uint32_t n = done[t]++, at = 2 * t + (n & 1u);
+              wait_on(pfull + 8 * at, (n >> 1) & 1u, abort_flag, a.err);
               tc_fence_after();
-              const uint32_t p = tmem + t * kBTile, d = tmem + 256 + t * kWRows;
-              if (j > w.j0)
-                mma_tmem<false>(d, p, v, hi, kFmt);
+              const uint32_t p = tmem + at * 64, d = tmem + 256 + t * kWRows, vh = v + h * (4 * 128);
+              if (j > w.j0 || h > 0)
+                mma_tmem<false>(d, p, vh, hi, kFmt);
               else
-                mma_tmem<true>(d, p, v, hi, kFmt);
+                mma_tmem<true>(d, p, vh, hi, kFmt);
 #pragma unroll
-              for (int s = 1; s < kBTile / 16; ++s) mma_tmem<false>(d, p + 8 * s, v + 128 * s, hi, kFmt);
-              mma_commit(odone + 8 * t);
+              for (int s = 1; s < 4; ++s) mma_tmem<false>(d, p + 8 * s, vh + 128 * s, hi, kFmt);
+              mma_commit(odone + 8 * at);
             }
             mma_commit(vempty + 8 * buf);
           }
@@ -398,16 +451,33 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_wide_kernel(const WideArgs w
     const int t = warp >> 2, in_tile = threadIdx.x & (kWRows - 1);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + t * kBTile, to = tmem + lanes + 256 + t * kWRows;
-    uint32_t it = 0, done = 0, piece = 0;  // tiles of keys; this row tile's, and its items
-    for (Walk w(a, range); w.valid(); w.next(a), ++piece) {
-      const int nrows = rows_of(w), nt = tiles_of(nrows);
-      const int per = nt == 1 ? nrows : (nrows + 1) / 2;     // rows a tile
-      // the lines of ancestors: the first warp of each row tile, which alone need not wait for the other's
-      if ((warp & 3) == 0) {
-        int parent[2];
+    float* qs_of = reinterpret_cast<float*>(smem + C::kOffQs) + t * kWRows;
+    struct Row {             // of the thread, in its item
+      int r, tok, head_row;  // its place among the item's rows, its token and its query head
+      bool exists, there;
+      uint64_t line;         // the own rows that it sees
+      int row_lo, all_lo;    // its first cached key; the last of the warp's rows' first
+      float qs;              // what its scores are multiplied by
+    };
+    // An item's rows, as far as they are this row tile's: lines of ancestors, and Q over each row's own power of two; a row
+    // that is not finite becomes NaN, one that is not there zeros. (Every S of the item before is done.)
+    auto load_item = [&](const Walk& w, Row& row) {
+      const int nrows = rows_of(w), nt = tiles_of(nrows), per = nt == 1 ? nrows : (nrows + 1) / 2;
+      constexpr int kPieces = D / 8, kAt = 32 / kPieces;   // lanes a row, rows at a time
+      auto place = [&](int in, int& r, int& tok, int& head_row) {
+        r = t * per + in;
+        const bool exists = t < nt && in < per && r < nrows;
+        const int rr = w.rt * a.tile_rows + (exists ? r : 0);
+        tok = row_token(a, rr);
+        head_row = w.head * a.R + rr - tok * a.R;
+        return exists;
+      };
+      int parent[2] = {-2, -2};
+      if ((warp & 3) == 0)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          parent[i] = lane + 32 * i < a.G ? __ldg(a.parents + static_cast<int64_t>(w.b) * a.G + lane + 32 * i) : -2;
+          if (lane + 32 * i < a.G) parent[i] = __ldg(a.parents + static_cast<int64_t>(w.b) * a.G + lane + 32 * i);
+      if ((warp & 3) == 0) {
         bool bad;
         const TreeLines tree = tree_lines(parent, a.G, bad);
         if (bad) atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_BAD_INDEX));
@@ -415,189 +485,86 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_wide_kernel(const WideArgs w
         tree_line[t * kTreeRows + lane + 32] = tree.line[1];
       }
       asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + t), "n"(kWRows) : "memory");
-      if (t < nt) {
-        const int r = t * per + in_tile;                     // of the item's rows
-        const bool exists = in_tile < per && r < nrows;
-        const int rr = w.rt * a.tile_rows + (exists ? r : 0), tok = row_token(a, rr);
-        uint64_t line = exists ? tree_line[t * kTreeRows + tok] : 0ull;
-        const bool there = line != 0ull;
-        const int pos = w.seq.L + __popcll(line) - 1;
-        const int row_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-        if (a.window > 0)
-          for (int n = __popcll(line); n > a.window; --n) line &= line - 1ull;
-        const int all_lo = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(there ? row_lo : 0)));
-        // ---- Q over the row's own power of two; a row that is not finite becomes NaN, one that is not there zeros
-        float qs;
-        {
-          const __nv_bfloat16* q = a.q + (static_cast<int64_t>(w.b) * a.G + tok) * a.q_stride + (w.head * a.R + rr - tok * a.R) * D;
-          uint32_t m = 0;
-          if (there)
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) m = max(m, max_abs8(__ldg(reinterpret_cast<const uint4*>(q) + c)));
+      if (t >= nt) return;
+      const int pc = piece_of_word<D>(lane % kPieces);
+      uint8_t* q_to = smem + C::kOffQ + t * C::kTileBytes + (pc >> 3) * (kWRows * 128);
+      const float lift = a.scale_log2 < 0.f ? -kBLiftQ : kBLiftQ;
+#pragma unroll 1
+      for (int i0 = 0; i0 < kPieces; i0 += 4) {  // (rolled: code that runs once an item is fetched for it)
+        uint4 v[4];
+        bool there[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          int r, tok, head_row;
+          there[i] = place((warp & 3) * 32 + (i0 + i) * kAt + lane / kPieces, r, tok, head_row) && tree_line[t * kTreeRows + tok] != 0ull;
+          v[i] = there[i] ? __ldg(reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(w.b) * a.G + tok) * a.q_stride + head_row * D) +
+                                  lane % kPieces)
+                          : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int in = (warp & 3) * 32 + (i0 + i) * kAt + lane / kPieces;
+          uint32_t m = max_abs8(v[i]);
+#pragma unroll
+          for (int x = 1; x < kPieces; x <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, x));
           const float own = pow2_of(__uint_as_float(m), kBPow2LowQV);
-          qs = own * (1.f / kBLiftQ) * fabsf(a.scale_log2);
-          const float by = (a.scale_log2 < 0.f ? -kBLiftQ : kBLiftQ) * pow2_inverse(own);
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (there) v = m < kBInfinity ? convert_word(__ldg(reinterpret_cast<const uint4*>(q) + c), by)
-                                          : make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-            const int pc = piece_of_word<D>(c);
-            *reinterpret_cast<uint4*>(smem + C::kOffQ + t * C::kTileBytes + (pc >> 3) * (kWRows * 128) + in_tile * 128 +
-                                      (((pc & 7) ^ (in_tile & 7)) << 4)) = v;
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(qfull + 8 * t);
+          const uint4 u = m < kBInfinity ? convert_word(v[i], lift * pow2_inverse(own))
+                                         : make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+          *reinterpret_cast<uint4*>(q_to + in * 128 + (((pc & 7) ^ (in & 7)) << 4)) = u;
+          if (lane % kPieces == 0) qs_of[in] = own * (1.f / kBLiftQ) * fabsf(a.scale_log2);
         }
-        float ref = there ? kBUnseen : kBPadding, l = 0.f;   // minus the reference; the sum
-        // raises the reference where the tile's largest number passes it, in straight-line code; O and the sum follow
-        auto raise = [&](float most, bool rescale) {
-          const float next = kBLift - most;
-          float shrink = 1.f;
-          if (ref != kBPadding && most > -INFINITY && most + ref > kBSlack && next < ref) {
-            shrink = ref == kBUnseen ? 0.f : ex2_approx(next - ref);
-            ref = next;
-            l *= shrink;
-          }
-          if (!rescale) return;
-          tc_fence_after();  // (the product before is done: the scores came after it)
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32(to + c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= shrink;
-            tmem_st32(to + c, o);
-          }
-          tmem_st_wait();
-        };
-#pragma unroll 1
-        for (int j = w.j0; j < w.j1; ++j, ++it, ++done) {
-          const uint32_t buf = it & 1u;
-          // (the scores first: where items of one row tile came before, only they tell the second's warps how far the
-          // values' barrier has come)
-          wait_on(sfull + 8 * t, done & 1u, abort_flag, a.err);
-          wait_on(vfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
-          __syncwarp();
-          tc_fence_after();
-          const WideInfo* info = info_of(it);
-          const bool own = j >= w.seq.cached;
-          const int key0 = own ? w.seq.L : ((w.seq.lo >> kBTileLog) + j) * kBTile;
-          bool plain = !own && key0 >= all_lo;
-          if (plain) {
-            const uint4 th = *reinterpret_cast<const uint4*>(info->there), mk = *reinterpret_cast<const uint4*>(info->mixed_k),
-                        mv = *reinterpret_cast<const uint4*>(info->mixed_v);
-            plain = (th.x & th.y & th.z & th.w) == ~0u && (mk.x | mk.y | mk.z | mk.w | mv.x | mv.y | mv.z | mv.w) == 0u;
-          }
-          float x[32];
-          if (plain) {
-            const float4 k4 = *reinterpret_cast<const float4*>(info->k), v4 = *reinterpret_cast<const float4*>(info->v);
-            const float fk[4] = {k4.x * qs, k4.y * qs, k4.z * qs, k4.w * qs}, fv[4] = {v4.x, v4.y, v4.z, v4.w};
-            float most = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32(ts + 32 * c, x);
-              tmem_ld_wait();
-              float m0 = x[0], m1 = x[1];
-#pragma unroll
-              for (int i = 2; i < 32; i += 2) {
-                m0 = fmaxf(m0, x[i]);
-                m1 = fmaxf(m1, x[i + 1]);
-              }
-              const float vlog = static_cast<float>(static_cast<int>(__float_as_uint(fv[c]) >> 23) - 127);
-              most = fmaxf(most, fmaf(fmaxf(m0, m1), fk[c], vlog));
-            }
-            if (__any_sync(0xffffffffu, most + ref > kBSlack)) raise(most, j > w.j0);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32(ts + 32 * c, x);
-              const float off = static_cast<float>(static_cast<int>(__float_as_uint(fv[c]) >> 23) - 127) + ref;
-              tmem_ld_wait();
-              float2 sum = make_float2(0.f, 0.f);
-              uint32_t p[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float2 y = __ffma2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(fk[c], fk[c]), make_float2(off, off));
-                const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                sum = __fadd2_rn(sum, e);
-                const __half2 h = __floats2half2_rn(e.x, e.y);
-                p[i] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              l = fmaf(sum.x + sum.y, pow2_inverse(fv[c]) * kBSumUnit, l);
-              tmem_st16(ts + 16 * c, p);
-            }
-          } else {
-            // masks, and a factor a key
-            float most = -INFINITY;
-            auto seen_of = [&](int c) {
-              if (own) return c < 2 ? static_cast<uint32_t>(line >> (32 * c)) : 0u;
-              const int from = row_lo - key0 - 32 * c;         // the group's first key that the row sees
-              return from >= 32 ? 0u : info->there[c] & (from > 0 ? ~0u << from : ~0u);
-            };
-            auto value = [&](float s, const float2& f) {       // with the values' factor (NaN if it is)
-              return fmaf(s, f.x * qs, fmaf(f.y, 0.f, static_cast<float>(static_cast<int>(__float_as_uint(f.y) >> 23) - 127)));
-            };
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t seen = seen_of(c);
-              tmem_ld32(ts + 32 * c, x);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if ((seen >> i) & 1u) most = fmaxf(most, value(x[i], info->key[32 * c + i]));
-            }
-            if (__any_sync(0xffffffffu, most + ref > kBSlack)) raise(most, j > w.j0);
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t seen = seen_of(c);
-              tmem_ld32(ts + 32 * c, x);
-              tmem_ld_wait();
-              uint32_t p[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float e[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const float2 f = info->key[32 * c + 2 * i + h];
-                  const bool in = (seen >> (2 * i + h)) & 1u;
-                  e[h] = in ? ex2_approx(value(x[2 * i + h], f) + ref) : 0.f;
-                  l = in ? fmaf(e[h], pow2_inverse(f.y) * kBSumUnit, l) : l;
-                }
-                const __half2 h2 = __floats2half2_rn(e[0], e[1]);
-                p[i] = *reinterpret_cast<const uint32_t*>(&h2);
-              }
-              tmem_st16(ts + 16 * c, p);
-            }
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(pfull + 8 * t);
-        }
-        // ---- the item's result, or this range's part of it
-        wait_on(odone + 8 * t, (done - 1) & 1u, abort_flag, a.err);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qfull + 8 * t);
+      row.exists = place(in_tile, row.r, row.tok, row.head_row);
+      row.line = row.exists ? tree_line[t * kTreeRows + row.tok] : 0ull;
+      row.there = row.line != 0ull;
+      const int pos = w.seq.L + __popcll(row.line) - 1;
+      row.row_lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      if (a.window > 0)
+        for (int n = __popcll(row.line); n > a.window; --n) row.line &= row.line - 1ull;
+      row.all_lo = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(row.there ? row.row_lo : 0)));
+      row.qs = qs_of[in_tile];
+      __syncwarp();
+    };
+    uint32_t it = 0, n = 0;  // tiles of keys; this row tile's halves of them
+    Row row, me;
+    Walk next(a, range), w = next;
+    if (threadIdx.x == 0) {
+      int2 e = make_int2(-1, 0);
+      if (next.valid() && next.j0 > 0 && next.j1 == next.seq.tiles)
+        e = make_int2((next.b * a.Hkv + next.head) * a.row_tiles + next.rt,
+                      BlockParts(range.line, next.start, kWSetup, next.seq.tiles).c0);
+      wa.entry[blockIdx.x] = e;
+    }
+    float ref = 0.f, l = 0.f;  // minus the reference; the sum
+    bool mine = false;         // the item before had rows of this tile
+    for (;;) {
+      if (next.valid()) load_item(next, row);  // (its scores are computed while the item before is finished)
+      if (mine) {
+        // ---- the result of the item before, or this range's part of it
+        wait_on(odone + 16 * t + 8 * ((n - 1) & 1u), ((n - 1) >> 1) & 1u, abort_flag, a.err);
         __syncwarp();
         tc_fence_after();
         const bool complete = w.j0 == 0 && w.j1 == w.seq.tiles;
-        if (!there) l = 0.f;  // (whatever a row that is not there holds)
+        if (!me.there) l = 0.f;  // (whatever a row that is not there holds)
         const float g = l == 0.f ? 0.f : (complete ? kBSumUnit / l : 1.f);
-        const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (w.j0 > 0 ? 0 : 1)) * (2 * kWRows) + r;
-        __nv_bfloat16* out = a.out + ((static_cast<int64_t>(w.b) * a.G + tok) * a.Hq + w.head * a.R + rr - tok * a.R) * D;
+        const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (w.j0 > 0 ? 0 : 1)) * (2 * kWRows) + me.r;
+        __nv_bfloat16* out = a.out + ((static_cast<int64_t>(w.b) * a.G + me.tok) * a.Hq + me.head_row) * D;
         float* part = a.part_o + slot * D;
-        if (exists && !complete) a.part_ml[slot] = make_float2(ref != kBUnseen && there ? -ref : -INFINITY, l);
+        if (me.exists && !complete) a.part_ml[slot] = make_float2(ref != kBUnseen && me.there ? -ref : -INFINITY, l);
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[32];
-          tmem_ld32(to + c, o);
+        for (int c = 0; c < D; c += 16) {
+          uint32_t raw[16];
+          float o[16];
+          tmem_ld16(to + c, raw);
           tmem_ld_wait();
-          if (!exists) continue;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = g != 0.f ? o[i] * g : 0.f;  // (O of a row that saw nothing is not looked at)
-          if (complete) {
+          for (int i = 0; i < 16; ++i) o[i] = g != 0.f ? __uint_as_float(raw[i]) * g : 0.f;  // (O of a row that saw nothing is not looked at)
+          if (complete && me.exists) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {  // positions hold channels 0, 4, 1, 5, 2, 6, 3, 7 of a word
+            for (int k = 0; k < 2; ++k) {  // positions hold channels 0, 4, 1, 5, 2, 6, 3, 7 of a word
               uint32_t u[4];
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -607,19 +574,190 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_wide_kernel(const WideArgs w
               }
               *reinterpret_cast<uint4*>(out + word_of_piece<D>(c / 8 + k) * 8) = make_uint4(u[0], u[1], u[2], u[3]);
             }
-          } else {
+          } else if (me.exists) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4)
+            for (int i = 0; i < 16; i += 4)
               __stcg(reinterpret_cast<float4*>(part + c + i), make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]));
           }
         }
+        __syncwarp();
         tc_fence_before();
-        if (threadIdx.x == 0 && w.j1 == w.seq.tiles) {
-          const BlockParts parts(range.line, w.start, kWSetup, w.seq.tiles);
-          wa.entry[(static_cast<int64_t>(w.b) * a.Hkv + w.head) * a.row_tiles + w.rt] = make_int2(parts.c0, parts.c1);
-        }
-      } else {
+      }
+      if (!next.valid()) break;
+      w = next;
+      me = row;
+      next.next(a);
+      mine = t < tiles_of(rows_of(w));
+      if (next.valid()) {  // its queries and parents are on their way meanwhile
+        const int rows = rows_of(next), tiles = tiles_of(rows), r = t * (tiles == 1 ? rows : (rows + 1) / 2) + in_tile;
+        const int rr = next.rt * a.tile_rows + min(r, rows - 1), tok = row_token(a, rr);
+        const __nv_bfloat16* q = a.q + (static_cast<int64_t>(next.b) * a.G + tok) * a.q_stride + (next.head * a.R + rr - tok * a.R) * D;
+#pragma unroll
+        for (int x = 0; x < D; x += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(q + x));
+        if (in_tile < a.G) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.parents + static_cast<int64_t>(next.b) * a.G + in_tile));
+      }
+      if (!mine) {
         it += static_cast<uint32_t>(w.j1 - w.j0);
+        continue;
+      }
+      ref = me.there ? kBUnseen : kBPadding;
+      l = 0.f;
+#pragma unroll 1
+      for (int j = w.j0; j < w.j1; ++j, ++it) {
+        const bool own = j >= w.seq.cached;
+        const int key0 = own ? w.seq.L : ((w.seq.lo >> kBTileLog) + j) * kBTile;
+        const int nh = halves_of(w, j);
+#pragma unroll 1
+        for (int h = 0; h < nh; ++h, ++n) {
+          const uint32_t at = n & 1u;
+          // (the scores first: where items of one row tile came before, only they tell the second's warps how far the
+          // values' barrier has come)
+          wait_on(sfull + 16 * t + 8 * at, (n >> 1) & 1u, abort_flag, a.err);
+          if (h == 0) wait_on(vfull + 8 * (it & 1u), (it >> 1) & 1u, abort_flag, a.err);
+          __syncwarp();
+          tc_fence_after();
+          float x[64];  // the half's scores, then numbers
+          tmem_ld32(ts + 64 * at, reinterpret_cast<float(&)[32]>(x[0]));
+          tmem_ld32(ts + 64 * at + 32, reinterpret_cast<float(&)[32]>(x[32]));
+          const WideInfo* info = info_of(it);
+          const uint2 th = *reinterpret_cast<const uint2*>(info->there + 2 * h), mk = *reinterpret_cast<const uint2*>(info->mixed_k + 2 * h),
+                      mv = *reinterpret_cast<const uint2*>(info->mixed_v + 2 * h);
+          const float2 k2 = *reinterpret_cast<const float2*>(info->k + 2 * h), v2 = *reinterpret_cast<const float2*>(info->v + 2 * h);
+          const bool mixed = (mk.x | mk.y | mv.x | mv.y) != 0u;
+          const bool plain = !own && !mixed && key0 >= me.all_lo && (th.x & th.y) == ~0u;
+          const float fk[2] = {k2.x * me.qs, k2.y * me.qs}, fv[2] = {v2.x, v2.y};
+          auto log_of = [](float f) { return static_cast<float>(static_cast<int>(__float_as_uint(f) >> 23) - 127); };
+          // raises the reference where the half's largest number passes it, in straight-line code; O and the sum follow
+          auto raise = [&](float most) {
+            if (!__any_sync(0xffffffffu, most + ref > kBSlack)) return;
+            const float up = kBLift - most;
+            float shrink = 1.f;
+            if (ref != kBPadding && most > -INFINITY && most + ref > kBSlack && up < ref) {
+              shrink = ref == kBUnseen ? 0.f : ex2_approx(up - ref);
+              ref = up;
+              l *= shrink;
+            }
+            if (j == w.j0 && h == 0) return;
+            wait_on(odone + 16 * t + 8 * (at ^ 1u), ((n - 1) >> 1) & 1u, abort_flag, a.err);  // the half before is in O
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+              tmem_st16(to + c, o);
+            }
+            tmem_st_wait();
+          };
+          // which of the half's keys the row sees
+          uint32_t seen[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int from = me.row_lo - key0 - 64 * h - 32 * c;  // the group's first key after the window's start
+            seen[c] = own ? static_cast<uint32_t>(me.line >> (32 * c))
+                          : (from >= 32 || !me.there ? 0u : (c == 0 ? th.x : th.y) & (from > 0 ? ~0u << from : ~0u));
+          }
+          // probabilities times the values' factors, over S, and their sum without those
+          auto weigh = [&]() {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float2 sum = make_float2(0.f, 0.f);
+              uint32_t p[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 y = __fadd2_rn(make_float2(x[32 * c + 2 * i], x[32 * c + 2 * i + 1]), make_float2(ref, ref));
+                const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                sum = __fadd2_rn(sum, e);
+                const __half2 h2 = __floats2half2_rn(e.x, e.y);
+                p[i] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              l = fmaf(sum.x + sum.y, pow2_inverse(fv[c]) * kBSumUnit, l);
+              tmem_st16(ts + 64 * at + 16 * c, p);
+            }
+          };
+          tmem_ld_wait();
+          if (plain) {
+            // (The reference is subtracted from rounded numbers, among them the maximum it was set to: inside the FMA, the
+            // largest of very large scores could pass any slack by its own rounding.)
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float vlog = log_of(fv[c]);
+#pragma unroll
+              for (int i = 32 * c; i < 32 * c + 32; i += 2) {
+                const float2 z = __ffma2_rn(make_float2(x[i], x[i + 1]), make_float2(fk[c], fk[c]), make_float2(vlog, vlog));
+                x[i] = z.x;
+                x[i + 1] = z.y;
+                m0 = fmaxf(m0, z.x);
+                m1 = fmaxf(m1, z.y);
+              }
+            }
+            raise(fmaxf(m0, m1));
+            weigh();
+          } else if (!mixed) {
+            float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const float vlog = log_of(fv[c]);
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 z = __ffma2_rn(make_float2(x[32 * c + i], x[32 * c + i + 1]), make_float2(fk[c], fk[c]), make_float2(vlog, vlog));
+                x[32 * c + i] = (seen[c] & (1u << i)) != 0u ? z.x : -INFINITY;
+                x[32 * c + i + 1] = (seen[c] & (2u << i)) != 0u ? z.y : -INFINITY;
+                m0 = fmaxf(m0, x[32 * c + i]);
+                m1 = fmaxf(m1, x[32 * c + i + 1]);
+              }
+            }
+            raise(fmaxf(m0, m1));
+            weigh();
+          } else {
+            // rows that lie far apart: a factor a key
+            // (eight keys at a time: the numbers are made twice, from S, of which P takes the first half behind it)
+            auto numbers = [&](int i0, float (&z)[8]) {
+              tmem_ld8(ts + 64 * at + i0, z);
+              const uint32_t bits = (i0 < 32 ? seen[0] : seen[1]) >> (i0 & 31);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 k = info->key[64 * h + i0 + i];  // (the values' may be NaN)
+                z[i] = (bits & (1u << i)) != 0u ? fmaf(z[i], k.x * me.qs, fmaf(k.y, 0.f, log_of(k.y))) : -INFINITY;
+              }
+            };
+            float most = -INFINITY;
+#pragma unroll 1
+            for (int i0 = 0; i0 < 64; i0 += 8) {
+              float z[8];
+              numbers(i0, z);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) most = fmaxf(most, z[i]);
+            }
+            raise(most);
+#pragma unroll 1
+            for (int i0 = 0; i0 < 64; i0 += 8) {
+              float z[8], sum = 0.f;
+              uint32_t p[4];
+              numbers(i0, z);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float e0 = ex2_approx(z[2 * i] + ref), e1 = ex2_approx(z[2 * i + 1] + ref);
+                const float4 k = *reinterpret_cast<const float4*>(info->key + 64 * h + i0 + 2 * i);
+                sum = fmaf(e0, pow2_inverse(k.y), fmaf(e1, pow2_inverse(k.w), sum));
+                const __half2 h2 = __floats2half2_rn(e0, e1);
+                p[i] = *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              l = fmaf(sum, kBSumUnit, l);
+              tmem_st4(ts + 64 * at + i0 / 2, p);
+            }
+          }
+          __syncwarp();
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(pfull + 16 * t + 8 * at);
+        }
       }
     }
   }
@@ -631,59 +769,60 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_wide_kernel(const WideArgs w
   }
 }
 
-// Joins the parts of items that several ranges share: a warp a row, 32 rows a CTA.
-constexpr int kJoinRows = 32, kJoinThreads = 256;
+// Joins the parts of items that several ranges share: a warp a row, eight rows a CTA.
+constexpr int kJoinRows = 8, kJoinThreads = 256;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv4_wide_join_kernel(const WideArgs wa) {
   const BlockArgs& a = wa.a;
   constexpr int kCtas = 2 * kWRows / kJoinRows, kE = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int item = static_cast<int>(blockIdx.x) / kCtas, rt = item % a.row_tiles, bh = item / a.row_tiles;
-  const int b = bh / a.Hkv, head = bh - b * a.Hkv;
   pdl_trigger();
   pdl_wait();
-  const int2 e = __ldg(wa.entry + item);
-  if (e.x == e.y) return;  // (written by the range that had all of it)
-  const int n = e.y - e.x + 1, nrows = min(a.tile_rows, a.rows - rt * a.tile_rows);
-  for (int i = 0; i < kJoinRows / (kJoinThreads / 32); ++i) {
-    const int r = (static_cast<int>(blockIdx.x) - item * kCtas) * kJoinRows + i * (kJoinThreads / 32) + warp;
-    if (r >= nrows) break;
-    auto slot = [&](int p) { return (static_cast<int64_t>(e.x + p) * 2 + (p == 0 ? 1 : 0)) * (2 * kWRows) + r; };
-    float top = -INFINITY;
-    for (int p = lane; p < n; p += 32) top = fmaxf(top, __ldcg(a.part_ml + slot(p)).x);
+  const int range = static_cast<int>(blockIdx.x) / kCtas;
+  const int2 e = __ldcg(wa.entry + range);
+  if (e.x < 0) return;
+  const int rt = e.x % a.row_tiles, bh = e.x / a.row_tiles, b = bh / a.Hkv, head = bh - b * a.Hkv;
+  const int n = range - e.y + 1, nrows = min(a.tile_rows, a.rows - rt * a.tile_rows);
+  const int r = (static_cast<int>(blockIdx.x) - range * kCtas) * kJoinRows + warp;
+  if (r >= nrows) return;
+  auto slot = [&](int p) { return (static_cast<int64_t>(e.y + p) * 2 + (p == 0 ? 1 : 0)) * (2 * kWRows) + r; };
+  float top = -INFINITY, sum = 0.f, acc[kE] = {};
+  for (int p0 = 0; p0 < n; p0 += 8) {  // eight parts at a time, asked for before their weights are known
+    const float2 ml = lane < 8 && p0 + lane < n ? __ldcg(a.part_ml + slot(p0 + lane)) : make_float2(-INFINITY, 0.f);
+    float v[8][kE];
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    float acc[kE] = {}, sum = 0.f;
-    for (int p0 = 0; p0 < n; p0 += 32) {
-      const float2 ml = p0 + lane < n ? __ldcg(a.part_ml + slot(p0 + lane)) : make_float2(-INFINITY, 0.f);
-      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - top);
-      sum = fmaf(f, ml.y, sum);
-#pragma unroll 4
-      for (int p = 0; p < min(32, n - p0); ++p) {
-        const float weight = __shfl_sync(0xffffffffu, f, p);
-        const float* from = a.part_o + slot(p0 + p) * D + lane * kE;
-        float v[kE];
+    for (int p = 0; p < 8; ++p)
 #pragma unroll
-        for (int x = 0; x < kE; x += 2) {
-          const float2 u = __ldcg(reinterpret_cast<const float2*>(from + x));
-          v[x] = u.x;
-          v[x + 1] = u.y;
-        }
-        if (weight != 0.f)  // (0: nothing of the row there)
-#pragma unroll
-          for (int x = 0; x < kE; ++x) acc[x] = fmaf(weight, v[x], acc[x]);
+      for (int x = 0; x < kE; x += 2) {
+        const float2 u = p0 + p < n ? __ldcg(reinterpret_cast<const float2*>(a.part_o + slot(p0 + p) * D + lane * kE + x)) : make_float2(0.f, 0.f);
+        v[p][x] = u.x;
+        v[p][x + 1] = u.y;
       }
-    }
+    float most = fmaxf(top, ml.x);
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-    const float inv = sum == 0.f ? 0.f : kBSumUnit / sum;
-    const int rr = rt * a.tile_rows + r, t = row_token(a, rr);
-    __nv_bfloat16* out = a.out + ((static_cast<int64_t>(b) * a.G + t) * a.Hq + head * a.R + rr - t * a.R) * D;
+    for (int m = 16; m > 0; m >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, m));
+    const float shrink = top == -INFINITY ? 0.f : ex2_approx(top - most), f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - most);
+    top = most;
+    sum = fmaf(f, ml.y, sum * shrink);
 #pragma unroll
-    for (int x = 0; x < kE; ++x) {
-      const int p = lane * kE + x;
-      out[word_of_piece<D>(p >> 3) * 8 + ((p & 7) >> 1) + 4 * (p & 1)] = __float2bfloat16_rn(inv != 0.f ? acc[x] * inv : 0.f);
+    for (int x = 0; x < kE; ++x) acc[x] *= shrink;
+#pragma unroll
+    for (int p = 0; p < 8; ++p) {
+      const float weight = __shfl_sync(0xffffffffu, f, p);
+      if (weight != 0.f)  // (0: nothing of the row there)
+#pragma unroll
+        for (int x = 0; x < kE; ++x) acc[x] = fmaf(weight, v[p][x], acc[x]);
     }
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+  const float inv = sum == 0.f ? 0.f : kBSumUnit / sum;
+  const int rr = rt * a.tile_rows + r, t = row_token(a, rr);
+  __nv_bfloat16* out = a.out + ((static_cast<int64_t>(b) * a.G + t) * a.Hq + head * a.R + rr - t * a.R) * D;
+#pragma unroll
+  for (int x = 0; x < kE; ++x) {
+    const int p = lane * kE + x;
+    out[word_of_piece<D>(p >> 3) * 8 + ((p & 7) >> 1) + 4 * (p & 1)] = __float2bfloat16_rn(inv != 0.f ? acc[x] * inv : 0.f);
   }
 }
 
@@ -702,7 +841,7 @@ WidePlan wide_plan(int B, int G, int Hq, int Hkv, int D, int64_t max_ctx, int sm
   const size_t slots = static_cast<size_t>(p.ctas) * 2 * (2 * kWRows);
   p.ml = slots * D * sizeof(float);
   p.entry = p.ml + slots * sizeof(float2);
-  p.total = p.entry + static_cast<size_t>(p.items) * sizeof(int2);
+  p.total = p.entry + static_cast<size_t>(p.ctas) * sizeof(int2);
   return p;
 }
 
@@ -715,7 +854,7 @@ int launch_wide_t(const WideArgs& a, const WidePlan& p, cudaStream_t st) {
   if (!ensure_smem_attr(kv4_wide_kernel<D>, C::kSmem, &done)) return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (attention)");
   cudaError_t e = launch_pdl(kv4_wide_kernel<D>, dim3(static_cast<unsigned>(p.ctas)), dim3(kBThreads), C::kSmem, st, nullptr, 0, a);
   if (e == cudaSuccess)
-    e = launch_pdl(kv4_wide_join_kernel<D>, dim3(static_cast<unsigned>(p.items * (2 * kWRows / kJoinRows))), dim3(kJoinThreads), 0, st,
+    e = launch_pdl(kv4_wide_join_kernel<D>, dim3(static_cast<unsigned>(p.ctas * (2 * kWRows / kJoinRows))), dim3(kJoinThreads), 0, st,
                    nullptr, 0, a);
   return e == cudaSuccess ? DFLASH2_OK : fail(DFLASH2_ERR_CUDA, "attention launch failed: %s", cudaGetErrorString(e));
 }
