@@ -1,6 +1,5 @@
 // C ABI entry points: host-side validation, workspace carving and dispatch to the kernels.
 // Nothing here allocates device memory; every failure returns a status before any launch.
-#include <algorithm>
 #include <atomic>
 #include <chrono>
 #include <cstdarg>
@@ -512,9 +511,7 @@ static int check_kv4_attention(int B, int G, int Hq, int Hkv, int D, int page_si
 
 size_t dflash2_kv4_attention_workspace_bytes(int B, int G, int Hq, int Hkv, int D, int page_size, int max_pages) {
   if (check_kv4_attention(B, G, Hq, Hkv, D, page_size, 1, max_pages, DFLASH2_BF16) != DFLASH2_OK) return 0;
-  const int sms = sm_count();
-  const size_t need = kv4_attention_workspace(B, G, Hq, Hkv, D, page_size, max_pages, sms);
-  return kv4_wide_eligible(B, G, Hq, Hkv) ? std::max(need, kv4_wide_workspace(B, G, Hq, Hkv, D, page_size, max_pages, sms)) : need;
+  return kv4_attention_workspace(B, G, Hq, Hkv, D, page_size, max_pages, sm_count());
 }
 
 static int kv4_attention_call(Kv4Attention r, int dtype, size_t workspace_bytes, void* stream) {
@@ -532,8 +529,7 @@ static int kv4_attention_call(Kv4Attention r, int dtype, size_t workspace_bytes,
   REQUIRE(r.window >= 0, "window=%d must be >= 0 (0: none)", r.window);
   REQUIRE(r.causal == 0 || r.causal == 1, "causal=%d must be 0 or 1", r.causal);
   REQUIRE(r.scale == r.scale && r.scale - r.scale == 0.f, "scale must be finite");
-  const bool wide = r.parents != nullptr && kv4_wide_eligible(r.B, r.G, r.Hq, r.Hkv);
-  const size_t need = (wide ? kv4_wide_workspace : kv4_attention_workspace)(r.B, r.G, r.Hq, r.Hkv, r.D, r.page_size, r.max_pages, sm_count());
+  const size_t need = kv4_attention_workspace(r.B, r.G, r.Hq, r.Hkv, r.D, r.page_size, r.max_pages, sm_count());
   if (need > 0) {
     if (r.workspace == nullptr || workspace_bytes < need)
       return fail(DFLASH2_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu bytes needed", workspace_bytes,
@@ -542,7 +538,7 @@ static int kv4_attention_call(Kv4Attention r, int dtype, size_t workspace_bytes,
   }
   // a window that reaches every key from every row is none (and the rows' positions less it stay above -2^31)
   if (static_cast<int64_t>(r.window) >= static_cast<int64_t>(r.max_pages) * r.page_size + 2 * r.G) r.window = 0;
-  return wide ? launch_kv4_wide(r, static_cast<cudaStream_t>(stream)) : launch_kv4_attention(r, static_cast<cudaStream_t>(stream));
+  return launch_kv4_attention(r, static_cast<cudaStream_t>(stream));
 }
 
 int dflash2_kv4_attention(const void* q, int64_t q_stride, const void* cache, const int32_t* page_table,

@@ -223,11 +223,6 @@ struct Kv4Attention {
 };
 size_t kv4_attention_workspace(int B, int G, int Hq, int Hkv, int D, int page_size, int max_pages, int sms);
 int launch_kv4_attention(const Kv4Attention& r, cudaStream_t st);
-// Trees of more rows a key/value head than this run with rows on the tensor core's 128-row side (kv4_wide.cu).
-constexpr int kWideRows = 96;
-bool kv4_wide_eligible(int B, int G, int Hq, int Hkv);
-size_t kv4_wide_workspace(int B, int G, int Hq, int Hkv, int D, int page_size, int max_pages, int sms);
-int launch_kv4_wide(const Kv4Attention& r, cudaStream_t st);
 
 // ---------------------------------------------------------------- pages and slots (kv4_plan.cu)
 struct Kv4Plan {

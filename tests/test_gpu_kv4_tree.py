@@ -69,25 +69,20 @@ def test_windows_follow_each_rows_position(torch, window):
         _check(_host(out), want, sd, f"window {window} D={D}")
 
 
-def test_a_chain_is_causal_attention(torch):
-    """Bit for bit up to 96 rows a key head, where one kernel runs both; within both kernels' errors above."""
+def test_a_chain_is_causal_attention_bit_for_bit(torch):
     import dflash2_block_drafter_gb300 as d
     rng = np.random.default_rng(1)
     for lens, G, window in (([700, 20, 0], 16, 0), ([900, 5], 24, 100), ([3000], 64, 100)):
         parents = np.stack([_tree(rng, G, "chain") for _ in lens])
-        out, want, sd, a = _call(torch, d, rng, lens, G, 8, 2, 128, 64, parents, window)
+        out, _, _, a = _call(torch, d, rng, lens, G, 8, 2, 128, 64, parents, window)
         same = d.dflash2_kv4_attention(*a[:6], k_new=a[6], v_new=a[7], causal=True, window=window)
-        if 4 * G <= 96:
-            assert torch.equal(out, same)
-        else:
-            _check(_host(out), want, sd, "tree")
-            _check(_host(same), want, sd, "causal")
+        assert torch.equal(out, same)
     assert d.dflash2_poll_error() == 0
 
 
 @pytest.mark.parametrize("D,G,Hq,Hkv", [(128, 20, 5, 1), (128, 64, 10, 2), (64, 64, 4, 1), (64, 33, 12, 1), (128, 64, 64, 1)])
 def test_many_rows_a_key_head(torch, D, G, Hq, Hkv):
-    """100 to 4096 rows a head: one or two tiles of rows, several items; ragged contexts, absent rows, a window."""
+    """100 to 4096 rows a head: several tiles of rows; ragged contexts, absent rows, a window."""
     import dflash2_block_drafter_gb300 as d
     rng = np.random.default_rng(Hq + D)
     lens = [0, 1, 127, 128, 129, 640, 2000]
