@@ -11,7 +11,7 @@ prepare and finish (MAX DFlash2TransformerBlock; dflash2.ts #block):
     x = x + conv_finish(h Wd^T, coef)
 
 The context's rows enter the cache with ``append_context`` once their tokens are verified (the pages
-project them from the target's hidden states; here they are given). The RMSNorm of each head of q and k and the
+project them from the target's hidden states; here they are given); ``ContextPages`` keeps their pages, on the device. The RMSNorm of each head of q and k and the
 rotary positions, which the pages put between projection and attention, are the caller's: ``positions(q, k)``
 may change both in place there; without it neither is applied.
 """
@@ -24,7 +24,8 @@ import torch
 
 from . import (dflash2_conv_finish, dflash2_conv_prepare, dflash2_conv_prepare_workspace_bytes, dflash2_gated_ffn,
                dflash2_gated_ffn_workspace_bytes, dflash2_kv4_append, dflash2_kv4_attention,
-               dflash2_kv4_attention_workspace_bytes, dflash2_kv4_cache, dflash2_proj, dflash2_proj_workspace_bytes)
+               dflash2_kv4_attention_workspace_bytes, dflash2_kv4_cache, dflash2_kv4_plan, dflash2_proj,
+               dflash2_proj_workspace_bytes)
 from .tail import SiteWeights, capture
 
 
@@ -37,6 +38,28 @@ class LayerWeights:
     w_gate: torch.Tensor  # [F, H]
     w_up: torch.Tensor    # [F, H]
     w_down: torch.Tensor  # [H, F]
+
+
+class ContextPages:
+    """Page table, lengths and free pages of B sequences over a cache of num_pages pages, kept on the device
+    (``dflash2_kv4_plan`` in place). One serves every layer whose caches have the same pages."""
+
+    def __init__(self, B: int, num_pages: int, max_pages: int, page_size: int = 64, device="cuda"):
+        i32 = dict(dtype=torch.int32, device=device)
+        self.num_pages, self.page_size = num_pages, page_size
+        self.table = torch.full((B, max_pages), -1, **i32)
+        self.lengths = torch.zeros(B, **i32)
+        self.free = torch.arange(num_pages, **i32)
+        self.state = torch.tensor([0, num_pages], **i32)
+        self.offsets = torch.zeros(B + 1, **i32)
+
+    def gain(self, change: torch.Tensor, rows: int = 0, place: Optional[torch.Tensor] = None, slots=None, positions=None):
+        """change [B]: tokens that each sequence gains, or (negative) drops from its end. Returns (slots, positions) of the
+        new tokens' rows: `rows` packed ones, or place's [B, G]. A sequence for which no page was free keeps its length."""
+        *_, slots, positions = dflash2_kv4_plan(
+            self.lengths, change, self.table, self.free, self.state, self.page_size, self.num_pages, rows=rows, place=place,
+            ctx_out=self.lengths, state_out=self.state, offsets=self.offsets, slots=slots, positions=positions)
+        return slots, positions
 
 
 class LayerRunner:
