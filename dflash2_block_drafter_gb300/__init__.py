@@ -792,7 +792,7 @@ def dflash2_logits_topk(logits, K, requests=None, row_offsets=None, history=None
         raise ValueError(f"logits must be [M, V], got shape {tuple(logits.shape)}")
     _current(logits, "logits")
     M, V = logits.shape
-    B = requests if requests is not None else (row_offsets.numel() - 1 if row_offsets is not None else M)
+    B = requests if requests is not None else (row_offsets.numel() - 1 if row_offsets is not None else max(M, 1))
     i32, f32, dev, dt = torch.int32, torch.float32, logits.device, logits.dtype
     code = _code(logits)
     rp = _array(row_offsets, "row_offsets", B + 1, i32)

@@ -569,15 +569,18 @@ int dflash2_kv4_plan(const int32_t* ctx_len, const int32_t* change, int32_t* pag
   REQUIRE(B >= 1 && B <= kPlanMaxSequences, "B=%d must be in [1, %d]", B, kPlanMaxSequences);
   REQUIRE(page_size >= 16 && page_size <= 4096 && (page_size & (page_size - 1)) == 0,
           "page_size=%d must be a power of two in [16, 4096]", page_size);
-  REQUIRE(num_pages >= 1 && capacity >= 1, "num_pages=%d and capacity=%d must be >= 1", num_pages, capacity);
+  // (entries, pages and rows are counted in int, by steps of all threads: 2^31 - 2^16 leaves room for the last step)
+  constexpr int kMost = 0x7fff0000;
+  REQUIRE(num_pages >= 1 && capacity >= 1 && capacity <= kMost,
+          "num_pages=%d must be >= 1 and capacity=%d in [1, 2^31 - 2^16]", num_pages, capacity);
   REQUIRE(max_pages >= 1 && static_cast<int64_t>(max_pages) * page_size <= 0x7fffff00LL,
           "max_pages=%d must be >= 1, and a sequence's pages hold less than 2^31 tokens", max_pages);
   REQUIRE(ctx_len && change && page_table && free_pages && free_state && ctx_out && state_out && row_offsets,
           "a required pointer is NULL");
   if (place != nullptr)
-    REQUIRE(G >= 1 && static_cast<int64_t>(B) * G <= 0x7fffff00LL, "G=%d must be >= 1 and B * G below 2^31", G);
+    REQUIRE(G >= 1 && static_cast<int64_t>(B) * G <= kMost, "G=%d must be >= 1 and B * G at most 2^31 - 2^16", G);
   else
-    REQUIRE(rows >= 0 && rows <= 0x7fffff00, "rows=%d must be in [0, 2^31 - 256]", rows);
+    REQUIRE(rows >= 0 && rows <= kMost, "rows=%d must be in [0, 2^31 - 2^16]", rows);
   REQUIRE((place == nullptr && rows == 0) || (slots && positions), "slots and positions are required");
   const Kv4Plan r{ctx_len, change, free_state, place, page_table, free_pages, ctx_out, state_out, row_offsets, positions,
                   slots, B, max_pages, page_size, num_pages, capacity, G, place != nullptr ? 0x7fffffff : rows};

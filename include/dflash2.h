@@ -440,7 +440,8 @@ DFLASH2_API int dflash2_kv4_attention_tree(const void* q, int64_t q_stride, cons
  *   (which rows of a verified block or tree are kept, in their order; no number twice).
  *   slots      [rows] or [B, G] int64, positions the same int32: each row's cache slot and position; -1 for rows of no
  *              token and of refused sequences.
- *   ctx_out may be ctx_len, and state_out free_state; other buffers do not overlap. B <= 8192; page_size as the cache's.
+ *   ctx_out may be ctx_len, and state_out free_state; other buffers do not overlap. B <= 8192; page_size as the cache's;
+ *   capacity, rows and B * G at most 2^31 - 2^16.
  * ---------------------------------------------------------------------------------- */
 DFLASH2_API int dflash2_kv4_plan(const int32_t* ctx_len, const int32_t* change, int32_t* page_table, int32_t* free_pages,
                                  const int32_t* free_state, const int32_t* place, int B, int G, int rows, int max_pages,

@@ -34,6 +34,11 @@ def test_plan_rejects_bad_arguments(lib):
         assert _plan(lib, **bad) == -1, bad
 
 
+def test_plan_refuses_counts_that_its_steps_would_pass(lib):
+    for bad in (dict(rows=2 ** 31 - 1024), dict(cap=2 ** 31 - 1024), dict(B=8191, place=FAKE, G=262176)):
+        assert _plan(lib, **bad) == -1, bad
+
+
 def _tree(lib, **kw):
     a = dict(q=FAKE, qs=5120, cache=FAKE, table=FAKE, ctx=FAKE, kn=FAKE, vn=FAKE, ns=1024, par=FAKE, B=2, G=16, Hq=40, Hkv=8,
              D=128, page=64, pages=10, width=4, window=0, scale=0.1, dtype=0, out=FAKE, ws=None, wsb=0)
