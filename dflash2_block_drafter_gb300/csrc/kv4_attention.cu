@@ -158,6 +158,18 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// One lane of a (converged) warp. (What it runs is known to be one thread's, so that the products' descriptors stay in
+// uniform registers.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // One MMA whose descriptors share the upper words; `first` overwrites the accumulator.
 template <bool first>
 __device__ __forceinline__ void mma_lean(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t a_hi, uint32_t b_hi,
@@ -810,7 +822,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
   } else if (warp == kBMmaWarp || warp == kBMmaWarp + 1) {
     // ------------------------------------------------------------------ MMA issuers: S, and O
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kFmt = (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);  // f32 <- f16, M = 128
       uint32_t it = 0, piece = 0;
       // descriptors: the lower words of the operands' first steps (address / 16, leading offset), and the
