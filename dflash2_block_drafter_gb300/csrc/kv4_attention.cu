@@ -82,8 +82,10 @@ template <int D, int NK>                    // N = 16 NK rows
 struct BlockCfg {
   static constexpr int N = 16 * NK;
   // the change from one item to the next, in tiles (measured: 15 of 3.1 thousand cycles with 80 rows, 5 of
-  // 2.0 with 16)
-  static constexpr int kSetup = NK <= 2 ? 3 : NK;
+  // 2.0 with 16). A tree's has its lines of ancestors and the masks of its own rows besides, and a row tile of it takes
+  // 19 of 2.2 thousand cycles longer than its tiles: 32 trees of 32 rows over 256 to 4096 keys take 147 us with 5 there, 130
+  // with 9 and 134 with 12; of 4 rows (NK = 2) 46 with 3, 44 with 4.
+  static constexpr int setup(bool tree) { return NK <= 2 ? (tree ? 4 : 3) : (tree ? NK + 4 : NK); }
   // registers a thread: 640 x 96 at launch, then shared out. With 80 rows 144 / 64 takes 128 to 130 us for 64
   // blocks over 256 .. 4096 keys where 120 / 80 takes 147, 136 / 64 133 and 152 / 56 132; with 16 rows, whose softmax
   // threads need few, 120 / 80 takes 111 us for 64 tokens over 1 .. 8192 keys and 152 / 56 128.
@@ -520,14 +522,14 @@ struct BlockJoin {
 
 // Joins the parts of an item, or of a group: the softmax threads. The parts come into the operands' place (the
 // products are done) by bulk copies, three in flight: an SM reads 64 bytes a clock from L2.
-template <int D, int NK>
+template <int D, int NK, bool kTree>
 __device__ __forceinline__ void block_join(const BlockArgs& a, const BlockLine& line, const BlockJoin& j, uint8_t* smem,
                                            uint32_t full, volatile int* abort_flag) {
   using C = BlockCfg<D, NK>;
   constexpr int N = C::N, kSlot = N * D * 4, kItems = N * D / 4 / kBSoft;
   static_assert(3 * kSlot <= 4 * C::kTileBytes, "the parts' place");
   const int me = static_cast<int>(blockIdx.x);
-  const BlockParts parts(line, j.start, C::kSetup, j.tiles);
+  const BlockParts parts(line, j.start, C::setup(kTree), j.tiles);
   const int head = j.head, row_first = j.rt * a.tile_rows;
   const int nrows = min(a.tile_rows, a.rows - row_first), count = parts.inputs(me);
   // the parts' maxima and sums, then their weights, per row; at most 25 of 169 CTAs
@@ -632,7 +634,8 @@ template <int D, int NK, bool kTree>
 __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const BlockArgs a) {
   using C = BlockCfg<D, NK>;
   using L = KvLayout<D>;
-  using Walk = BlockWalk<C::kSetup>;
+  constexpr int kSetup = C::setup(kTree);
+  using Walk = BlockWalk<kSetup>;
   constexpr int N = C::N, NH = N / 2;  // rows, a softmax thread's rows
   constexpr int NCH = D / 32;   // 32-channel chunks of a row
   extern __shared__ uint8_t smem_raw[];
@@ -691,7 +694,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
   const uint32_t tmem = *tmem_slot;
   pdl_trigger();
   pdl_wait();
-  const BlockRange range = block_range(a, C::kSetup, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+  const BlockRange range = block_range(a, kSetup, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
 
   if (warp >= kBSoftWarps && warp < kBSoftWarps + kBDeqWarps) {
     // ------------------------------------------------------------------ dequant
@@ -1023,6 +1026,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     uint32_t it = 0;
     Walk w(a, range);
     bool gave = false;  // the last piece goes on in the next range
+    int tree_of = -1;   // the sequence whose lines of ancestors are in shared memory
     BlockJoin join{w.start, w.b, w.head, w.rt, w.seq.tiles, w.valid() && w.j0 > 0 && w.j1 == w.seq.tiles, false};
     Walk next = w;
     for (bool first = true;; first = false) {
@@ -1082,7 +1086,8 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
       w = next;
       const int head = w.head, row_first = w.rt * a.tile_rows;
       const int nrows = min(a.tile_rows, a.rows - row_first);
-      if (kTree) {  // each row's line of ancestors, the nearest `window` of them
+      if (kTree && w.b != tree_of) {  // each row's line of ancestors (the items of a sequence follow one another)
+        tree_of = w.b;
         if (warp == 0) {
           int parent[2];
 #pragma unroll
@@ -1306,7 +1311,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
       }
       gave = w.j1 < w.seq.tiles;
       if (gave && w.j0 > 0)  // (the range lies inside the item)
-        join.leads = BlockParts(range.line, w.start, C::kSetup, w.seq.tiles).leads(static_cast<int>(blockIdx.x));
+        join.leads = BlockParts(range.line, w.start, kSetup, w.seq.tiles).leads(static_cast<int>(blockIdx.x));
       next.next(a);
     }
     auto give = [&]() {  // this range's part is complete
@@ -1316,7 +1321,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
     };
     if (gave && !join.leads) give();
     if (join.ends || join.leads) {
-      block_join<D, NK>(a, range.line, join, smem, join_full, abort_flag);
+      block_join<D, NK, kTree>(a, range.line, join, smem, join_full, abort_flag);
       if (join.leads) give();
     }
   }

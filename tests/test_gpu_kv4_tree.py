@@ -69,14 +69,16 @@ def test_windows_follow_each_rows_position(torch, window):
         _check(_host(out), want, sd, f"window {window} D={D}")
 
 
-def test_a_chain_is_causal_attention_bit_for_bit(torch):
+def test_a_chain_is_causal_attention(torch):
+    """(Both within their roundings of the same numbers; how the work is cut, and so the order of sums, differs.)"""
     import dflash2_block_drafter_gb300 as d
     rng = np.random.default_rng(1)
     for lens, G, window in (([700, 20, 0], 16, 0), ([900, 5], 24, 100), ([3000], 64, 100)):
         parents = np.stack([_tree(rng, G, "chain") for _ in lens])
-        out, _, _, a = _call(torch, d, rng, lens, G, 8, 2, 128, 64, parents, window)
+        out, want, sd, a = _call(torch, d, rng, lens, G, 8, 2, 128, 64, parents, window)
         same = d.dflash2_kv4_attention(*a[:6], k_new=a[6], v_new=a[7], causal=True, window=window)
-        assert torch.equal(out, same)
+        _check(_host(out), want, sd, "tree")
+        _check(_host(same), want, sd, "causal")
     assert d.dflash2_poll_error() == 0
 
 
