@@ -526,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 6 : (kThreads == 5
   const int m = static_cast<int>(blockIdx.x);
   if (tid == 0) s.entries = s.lanes = 0;
   if (tid < kPickK) s.best[tid] = 0ull;
+  if (tid < 32) s.group_max[tid] = static_cast<uint32_t>(tid);
   if (r.K > 0)
     for (int k = tid; k < a.tiles; k += kThreads) marked[k] = 0u;
   pdl_trigger();
@@ -630,24 +631,32 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 6 : (kThreads == 5
     return;
   }
   __syncthreads();
-  // the largest key of a lane without a named token, and of any
-  uint32_t top = 0u, top_any = 0u;
+  // the largest keys of lanes without a named token, and of any. In 32 groups, by a lane's place in its tile: those of a
+  // short row are spread over all of them. (By runs of threads, 1024 tokens were one group, and a row of them
+  // entered whole: 4096 rows took 680 us.) Named tokens count by the threads that hold them.
+  uint32_t top[4] = {0u, 0u, 0u, 0u}, top_any = 0u;
   auto look_at = [&](int k, const uint4& q) {
     const uint32_t mark = marked[k >> 3] >> (4 * k & 31);
+    const uint32_t v[4] = {q.x, q.y, q.z, q.w};
     top_any = max(top_any, max(max(q.x, q.y), max(q.z, q.w)));
-    top = max(top, max(max((mark & 1u) != 0u ? 0u : q.x, (mark & 2u) != 0u ? 0u : q.y),
-                       max((mark & 4u) != 0u ? 0u : q.z, (mark & 8u) != 0u ? 0u : q.w)));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top[j] = max(top[j], (mark >> j & 1u) != 0u ? 0u : v[j]);
   };
 #pragma unroll
   for (int j = 0; j < kKeyLoads; ++j)
     if (tid + j * kThreads < quads) look_at(tid + j * kThreads, key[j]);
 #pragma unroll 4
   for (int k = tid + kKeyLoads * kThreads; k < quads; k += kThreads) look_at(k, keys[k]);
-  uint32_t most = max(top, pick_key(top_named));
+  const uint32_t named_key = pick_key(top_named);
 #pragma unroll
-  for (int x = 1; x < kThreads / 32; x <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, x));
-  // (the lowest bits tell groups apart: the K-th largest is one of them, and without these bits not above it)
-  if (tid % (kThreads / 32) == 0) s.group_max[tid / (kThreads / 32)] = (most & ~31u) | static_cast<uint32_t>(tid / (kThreads / 32));
+  for (int j = 0; j < 4; ++j) {
+    uint32_t most = (warp & 3) == j ? max(top[j], named_key) : top[j];
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 8));
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, 16));
+    // (the lowest bits tell groups apart: the K-th largest is one of them, and without these bits not above it)
+    const uint32_t group = static_cast<uint32_t>(4 * lane + j);
+    if (lane < 8) atomicMax(&s.group_max[group], (most & ~31u) | group);
+  }
   __syncthreads();
   const uint32_t g = s.group_max[lane];
   int above = 0;
@@ -664,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 6 : (kThreads == 5
     const int at = atomicAdd(&s.entries, 1);
     if (at < kEntries) s.entry[at] = pick_entry(x, token);
   };
-  if (__any_sync(0xffffffffu, pick_key(top_named) >= bound)) again(bound, [&](int t, float y) { enter(y, t); });
+  if (__any_sync(0xffffffffu, named_key >= bound)) again(bound, [&](int t, float y) { enter(y, t); });
   auto list_lanes = [&](int k, const uint4& q) {
     if (max(max(q.x, q.y), max(q.z, q.w)) < bound) return;
     const uint32_t x[4] = {q.x, q.y, q.z, q.w};
