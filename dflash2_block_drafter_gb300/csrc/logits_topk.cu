@@ -50,7 +50,7 @@ struct PickArgs {
   int windows, cap;     // windows of the vocabulary (0: nothing is named); counters a window
   int words;            // of bits a request
   int tiles;            // a row
-  int warp_tiles, ctas_a_row, stream_ctas, other_ctas;  // of the first kernel
+  int warp_tiles, row_warps, stream_ctas, other_ctas;  // of the first kernel
   int counters, kept;   // named tokens' counters and values that shared memory holds, at most
   uint32_t* bits;       // [B][words]
   int* named;           // [B][windows] how many
@@ -424,8 +424,9 @@ __device__ __forceinline__ void stream_row(const PickArgs& a, int x) {
   constexpr int kN = Vec::kN, kG = kLaneTokens / kN;
   const LogitsTopk& r = a.r;
   const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
-  const int m = x / a.ctas_a_row;
-  const int tile0 = ((x - m * a.ctas_a_row) * kStreamWarps + warp) * a.warp_tiles;
+  const int at = x * kStreamWarps + warp, m = at / a.row_warps;  // (rows side by side: short ones leave no warp idle)
+  if (m >= r.M) return;
+  const int tile0 = (at - m * a.row_warps) * a.warp_tiles;
   const T* row = static_cast<const T*>(r.logits) + static_cast<int64_t>(m) * r.stride;
   T* out = r.out != nullptr ? static_cast<T*>(r.out) + static_cast<int64_t>(m) * r.out_stride : nullptr;
   const int off = row_offset(row), mask_words = (r.V + 31) / 32;
@@ -433,20 +434,15 @@ __device__ __forceinline__ void stream_row(const PickArgs& a, int x) {
   const uint32_t* mask = r.mask != nullptr ? reinterpret_cast<const uint32_t*>(r.mask) + static_cast<int64_t>(m) * r.mask_stride : nullptr;
   if (out != nullptr && (a.each == 0 || r.tokens != nullptr)) {
     // rows of no request, and drafted rows that are not there, keep what `out` holds
-    __shared__ int lives;
-    if (warp == 0) {
-      bool late, bad;
-      int first, rows;
-      const int b = a.each > 0 ? m / a.each : ragged_request(r, m, late);
-      bool yes = b >= 0;
-      if (yes && r.tokens != nullptr) {
-        const TreeLines tree = request_lines(a, b, first, rows, bad);
-        yes = __any_sync(0xffffffffu, (m - first == lane && tree.line[0] != 0ull) || (m - first == lane + 32 && tree.line[1] != 0ull));
-      }
-      if (lane == 0) lives = yes ? 1 : 0;
+    bool late, bad;
+    int first, rows;
+    const int b = a.each > 0 ? m / a.each : ragged_request(r, m, late);
+    if (b < 0) return;
+    if (r.tokens != nullptr) {
+      const TreeLines tree = request_lines(a, b, first, rows, bad);
+      if (!__any_sync(0xffffffffu, (m - first == lane && tree.line[0] != 0ull) || (m - first == lane + 32 && tree.line[1] != 0ull)))
+        return;
     }
-    __syncthreads();
-    if (lives == 0) return;
   }
   for (int tile = tile0; tile < min(tile0 + a.warp_tiles, a.tiles); ++tile) {
     const int t0 = tile * kTile - off;  // the tile's first token
@@ -841,8 +837,8 @@ int launch_logits_topk(const LogitsTopk& r, cudaStream_t st) {
   if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
   // tiles a warp: one while the SMs have warps left for the next (two CTAs each)
   a.warp_tiles = static_cast<int>(std::min<int64_t>(kStreamTiles, 1 + static_cast<int64_t>(r.M) * a.tiles / (2 * kStreamWarps * sm_count())));
-  a.ctas_a_row = (a.tiles + kStreamWarps * a.warp_tiles - 1) / (kStreamWarps * a.warp_tiles);
-  a.stream_ctas = r.M * a.ctas_a_row;
+  a.row_warps = (a.tiles + a.warp_tiles - 1) / a.warp_tiles;
+  a.stream_ctas = (r.M * a.row_warps + kStreamWarps - 1) / kStreamWarps;
   a.other_ctas = r.B * p.windows + (r.row_off != nullptr ? (r.M + kStreamThreads - 1) / kStreamThreads : 0);
   return r.dtype == DFLASH2_F32 ? launch_pick_t<float>(a, st) : launch_pick_t<__nv_bfloat16>(a, st);
 }
