@@ -20,6 +20,12 @@
 //     the K-th largest of 32 groups' maxima. The few lanes whose key reaches it are read once more, and the K best of
 //     what reaches the bound there, and of the named, are ranked by (value, lower token). A row where too many reach
 //     it (equal values) is searched in K rounds instead.
+// What bounds it: 64 x 15 rows of 248320 fp32 tokens take 162 us, 0.88 of the copy rate; 64 bf16 rows under masks, adjusted
+// logits wanted, 25 us of which the stream is 15; one block's 15 rows 14.5 us and rows with histories of 30000 tokens 48:
+// the latency of two launches and, of the names, of a history's atomics, their ranks and the named tokens' values.
+// (One kernel that kept a row's slices in the registers or shared memory of a cluster took 792 us for the first:
+// barriers, and 27 instructions a token.)
+//
 // Only what is above -inf is a candidate; rows with fewer than K such tokens are filled with the lowest of the others.
 #include <algorithm>
 
@@ -509,7 +515,7 @@ struct SelectShared {
 };
 
 template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 6 : (kThreads == 512 ? 3 : 1)) logits_select_kernel(const PickArgs a) {
+__global__ void __launch_bounds__(kThreads, kThreads <= 512 ? 1536 / kThreads : 1) logits_select_kernel(const PickArgs a) {
   using Vec = PickVec<T>;
   constexpr int kN = Vec::kN, kWarps = kThreads / 32;
   constexpr int kKeyLoads = kThreads >= 512 ? 2048 / kThreads : 0;  // sixteen bytes of keys a thread keeps
@@ -789,6 +795,7 @@ int launch_select(PickArgs a, cudaStream_t st) {
   static unsigned done = 0;
   if (!ensure_smem_attr(logits_select_kernel<T, kThreads>, kSelectShared, &done))
     return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (logits)");
+  // named tokens' values, kept for the second look (those histories: 47 us, with none kept 52)
   a.kept = std::min(a.windows * a.cap, 8 * kThreads);
   const cudaError_t e = launch_pdl(logits_select_kernel<T, kThreads>, dim3(static_cast<unsigned>(a.r.M)), dim3(kThreads),
                                    static_cast<size_t>(a.tiles + a.kept) * 4, st, nullptr, 0, a);
@@ -803,15 +810,23 @@ int launch_pick_t(PickArgs& a, cudaStream_t st) {
   const int quads = (std::min(a.r.V, kWindow) + 127) / 128;
   // (a multiple of 32, and one word more of each kind)
   const int counters = (a.cap + 63) / 32 * 32, shared = quads * 20 + counters / 2 * 4 + counters / 32 * 4;
+  // (counters in shared memory, of 16 bits: 63 rows with histories of 30000 tokens take 47 us, with counters in the
+  // workspace 57; where counts or places do not fit they are there)
   a.counters = a.windows > 0 && a.r.max_len <= 0xffff && shared <= kStreamShared ? counters : 0;
   const cudaError_t e = launch_pdl(logits_stream_kernel<T>, dim3(static_cast<unsigned>(a.stream_ctas + a.other_ctas)),
                                    dim3(kStreamThreads), a.windows == 0 ? 0 : static_cast<size_t>(a.counters > 0 ? shared : quads * 20), st,
                                    nullptr, 0, a);
   if (e != cudaSuccess) return fail(DFLASH2_ERR_CUDA, "logits launch failed: %s", cudaGetErrorString(e));
   if (a.r.K == 0 && a.windows == 0) return DFLASH2_OK;
+  // Threads a row. Up to a row an SM, the row's own time counts: 1024 (15 rows of 248320 tokens take 14.4 us, with 512
+  // 15.8, with 256 18.6; 63 rows with histories of 30000 tokens 47, 66, 85). Up to three 512 (288 tree rows of 248320 tokens
+  // 38.5 us; with 1024 41.1, with 256 40.7). Above them the number of rows in flight: 256 (960 rows 162 us; with 512 163,
+  // with 1024 184; 4096 rows of 8000 tokens 97, with 512 126), and 128 where a row's keys are few (16384 rows of 1000 tokens
+  // 64 us, with 256 104; 4096 of 8000 52 and 59; but 600 of 32771 18.9 and 18.2, 960 of 248320 194 and 162).
   const int sms = sm_count();
   if (a.r.M <= sms) return launch_select<T, 1024>(a, st);
-  return a.r.M <= 3 * sms ? launch_select<T, 512>(a, st) : launch_select<T, 256>(a, st);
+  if (a.r.M <= 3 * sms) return launch_select<T, 512>(a, st);
+  return a.tiles > 16 ? launch_select<T, 256>(a, st) : launch_select<T, 128>(a, st);
 }
 
 }  // namespace
@@ -835,7 +850,8 @@ int launch_logits_topk(const LogitsTopk& r, cudaStream_t st) {
   a.keys = reinterpret_cast<uint32_t*>(ws + p.keys);
   a.err = device_error_word();
   if (a.err == nullptr) return fail(DFLASH2_ERR_CUDA, "no device error word");
-  // tiles a warp: one while the SMs have warps left for the next (two CTAs each)
+  // tiles a warp: one while the SMs have warps left for the next (two CTAs each). (15 rows of 248320 tokens: one and four
+  // take 14.4 and 14.2 us; 960 rows 166.5 and 162, 288 rows under masks 48 and 38.)
   a.warp_tiles = static_cast<int>(std::min<int64_t>(kStreamTiles, 1 + static_cast<int64_t>(r.M) * a.tiles / (2 * kStreamWarps * sm_count())));
   a.row_warps = (a.tiles + a.warp_tiles - 1) / a.warp_tiles;
   a.stream_ctas = (r.M * a.row_warps + kStreamWarps - 1) / kStreamWarps;
