@@ -28,18 +28,25 @@
 // not, to which a mask may hide it. The sums take the factor off again, in fp32.
 //
 // Warps: 8 softmax (two per 32 TMEM lanes, half of the rows each), 8 dequant (four for K, four for V, 32
-// keys of a tile each: codes -> fp16 operand tiles in shared memory, 128-byte swizzle), 2 MMA (one thread
-// each for S and for O: issuing eight MMAs takes about as long as running them), 2 copy (a ring of bulk
+// keys of a tile each: codes -> fp16 operand tiles in shared memory, 128-byte swizzle), 2 MMA (one elected
+// thread each for S and for O: an MMA takes some 20 cycles to issue, and 100 from a thread picked by its number, for
+// which descriptors do not stay in uniform registers: 32 trees of 32 rows 162 us instead of 147), 2 copy (a ring of bulk
 // copies for K, one for V). K, V and S are double-buffered. The softmax warps, whose sums stay in registers,
 // take some of the others' (kSoftRegs).
 //
-// What a tile takes: about 3.0 thousand cycles with 80 rows, where the softmax warps' chain (scores from TMEM,
+// What a tile takes: about 2.3 thousand cycles with 80 rows, where the softmax warps' chain (scores from TMEM,
 // the check, exponentials, the operand's stores and their fence) is the longest, and 1.9 with 16, where the
 // conversion of codes is; each scheduler issues in 49 % and 57 % of the cycles. 64 blocks of 16 rows and five
-// query heads a key head over 256 to 4096 keys of 128 channels take 128 us, 64 single tokens over 1 to 8192 keys 112 us
+// query heads a key head over 256 to 4096 keys of 128 channels take 125 us, 64 single tokens over 1 to 8192 keys 112 us
 // (2.7 TB/s of the cache). What was slower (each against the code of its time): sixteen softmax warps; two sets of dequant warps taking tiles in
 // turn (118 us for the tokens); K converted into TMEM (155 us: the loops then miss the instruction cache); the
-// check split into an arrival and a later wait (172 us for the blocks); the next tile's codes read ahead (126 us).
+// check split into an arrival and a later wait (172 us for the blocks); the next tile's codes read ahead (126 us); the
+// scores' buffer given back together with the operand (130 us for the tokens).
+//
+// Trees: a row's own keys are its line of ancestors, 64 bits that the own tile's masks are taken from; all else is the
+// same code. 32 trees of 32 rows (160 rows a key head) over 256 to 4096 keys take 131 us, one of 64 rows over 32768 keys
+// 86: the same chain a tile, for which shared memory moves 224 KB (operands into the products 104, their making 64), 1.7
+// of the 2.3 thousand cycles at 128 bytes a clock. One of 8 rows over 1024 keys takes 17 us: start 4, three tiles and the join.
 //
 // CTAs are persistent, one an SM: all (sequence, head, row tile) items, each its tiles and a constant for
 // the change from one item to the next, form one line that is cut into equal ranges, whatever the lengths.
