@@ -147,6 +147,20 @@ def test_everything_at_once(torch, dtype, tokens, ragged):
         _check(torch, c, 0, in_place=True)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("B,rows,V", [(20, 10, 3001), (50, 10, 17501), (50, 10, 2001), (500, 1, 37)])
+def test_more_rows_than_three_a_multiprocessor(torch, dtype, B, rows, V):
+    """Fewer threads a row from 153 and 457 rows on, by the rows' length; then rows of equal values, whose every token
+    reaches the bound."""
+    rng = np.random.default_rng(V)
+    c = _case(rng, B, rows, V, dtype, 150, "tree", False, 3, 0.6)
+    _check(torch, c, 16)
+    _check(torch, c, 2, in_place=True)
+    c = _case(rng, B, rows, V, dtype)
+    c["logits"][::2] = 1.5
+    _check(torch, c, 16, want_out=False)
+
+
 @pytest.mark.parametrize("part", ["history", "tokens", "bias", "mask", "penalties"])
 def test_each_part_alone(torch, part):
     rng = np.random.default_rng(8)
