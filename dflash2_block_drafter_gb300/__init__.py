@@ -695,6 +695,7 @@ def dflash2_kv4_attention_tree(q, cache, page_table, ctx_len, page_size, scale, 
     [B, G, q_heads, head_dim] bf16."""
     if k_new is None or v_new is None or parents is None:
         raise ValueError("a tree needs k_new, v_new and parents")
+    _current(q, "q")
     sizes, rows, out, (wp, wn, _keep) = _kv4_attention_args(q, cache, page_table, ctx_len, page_size, k_new, v_new, out,
                                                             workspace, stream)
     if tuple(parents.shape) != sizes[:2]:
@@ -713,7 +714,14 @@ def _output(t, name, shape, dtype, device, stream):
     n = math.prod(shape)
     if t.numel() < n:
         raise ValueError(f"{name} holds {t.numel()} elements, fewer than the {n} the call writes")
-    return t, _dev(t, name, dtype)
+    return t, _dense(t, name, dtype)
+
+
+def _dense(t, name, dtype):
+    """_dev of a required array, its checks in the order that costs a good call least."""
+    if t is not None and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    return _dev(t, name, dtype)
 
 
 def _array(t, name, n, dtype):
@@ -722,13 +730,22 @@ def _array(t, name, n, dtype):
         return None
     if t.numel() != n:
         raise ValueError(f"{name} holds {t.numel()} elements, expected {n}")
-    return _dev(t, name, dtype)
+    return _dense(t, name, dtype)
 
 
 def _current(t, name):
-    """Refuses a tensor of another device than the current one, on which the call would run."""
-    if t.is_cuda and t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    """Refuses a tensor of another device than the current one, on which the call would run; the current device."""
+    if not t.is_cuda:
+        return None
+    device = torch._C._cuda_getDevice()
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+    return device
+
+
+def _stream_of(device, stream):
+    """_stream for a call whose device is known."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None and device is not None else _stream(stream)
 
 
 def dflash2_kv4_plan(ctx_len, change, page_table, free_pages, free_state, page_size, num_pages, rows=0, place=None,
@@ -746,7 +763,7 @@ def dflash2_kv4_plan(ctx_len, change, page_table, free_pages, free_state, page_s
         raise ValueError("free_pages must be [capacity] and free_state hold its first place and its count")
     if place is not None and (place.dim() != 2 or place.shape[0] != B):
         raise ValueError(f"place must be [{B}, G], got {tuple(place.shape)}")
-    _current(ctx_len, "ctx_len")
+    device = _current(ctx_len, "ctx_len")
     i32, dev = torch.int32, ctx_len.device
     shape = (max(0, rows),) if place is None else tuple(place.shape)
     ctx_out, cp = _output(ctx_out, "ctx_out", (B,), i32, dev, stream)
@@ -755,24 +772,24 @@ def dflash2_kv4_plan(ctx_len, change, page_table, free_pages, free_state, page_s
     slots, lp = _output(slots, "slots", shape, torch.int64, dev, stream)
     positions, pp = _output(positions, "positions", shape, i32, dev, stream)
     _check(library().dflash2_kv4_plan(
-        _dev(ctx_len, "ctx_len", i32), _dev(change, "change", i32), _dev(page_table, "page_table", i32),
-        _dev(free_pages, "free_pages", i32), _dev(free_state, "free_state", i32), _dev(place, "place", i32, True), B,
+        _dense(ctx_len, "ctx_len", i32), _dense(change, "change", i32), _dense(page_table, "page_table", i32),
+        _dense(free_pages, "free_pages", i32), _dense(free_state, "free_state", i32),
+        None if place is None else _dense(place, "place", i32), B,
         0 if place is None else shape[1], rows, page_table.shape[1], page_size, num_pages, free_pages.shape[0], cp, sp, op, lp,
-        pp, _stream(stream)))
+        pp, _stream_of(device, stream)))
     return ctx_out, state_out, offsets, slots, positions
 
 
-def _matrix(t, name, rows, width, dtypes):
+def _matrix(t, name, rows, width, dtype):
     """(pointer, row stride) of a [rows, >= width] tensor whose rows are dense and may lie apart."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] != rows or t.shape[1] < width:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.size(0) != rows or t.size(1) < width:
         raise ValueError(f"{name} must be [{rows}, {width}], got "
                          f"{tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__}")
-    if not t.is_cuda or t.dtype not in dtypes:
-        raise ValueError(f"{name} must be a CUDA tensor of {' or '.join(str(x) for x in dtypes)}")
-    step, unit = t.stride()
-    if unit != 1 and t.shape[1] > 1:
+    if not t.is_cuda or t.dtype is not dtype:
+        raise ValueError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.stride(1) != 1 and t.size(1) > 1:
         raise ValueError(f"{name}: each row must be dense")
-    return t.data_ptr(), step if rows > 1 else max(t.shape[1], 1)
+    return t.data_ptr(), t.stride(0) if rows > 1 else max(t.size(1), 1)
 
 
 @functools.lru_cache(maxsize=256)
@@ -790,18 +807,18 @@ def dflash2_logits_topk(logits, K, requests=None, row_offsets=None, history=None
     unary [M, K] fp32, out [M, V] or None); cand and unary are None for K = 0."""
     if logits.dim() != 2:
         raise ValueError(f"logits must be [M, V], got shape {tuple(logits.shape)}")
-    _current(logits, "logits")
+    device = _current(logits, "logits")
     M, V = logits.shape
     B = requests if requests is not None else (row_offsets.numel() - 1 if row_offsets is not None else max(M, 1))
     i32, f32, dev, dt = torch.int32, torch.float32, logits.device, logits.dtype
     code = _code(logits)
     rp = _array(row_offsets, "row_offsets", B + 1, i32)
-    lp, ls = _matrix(logits, "logits", M, V, (dt,))
+    lp, ls = _matrix(logits, "logits", M, V, dt)
     hp, hs, max_len = None, 0, 0
     if history is not None:
         if history_len is None:
             raise ValueError("history needs history_len")
-        hp, hs = _matrix(history, "history", B, 0, (i32,))
+        hp, hs = _matrix(history, "history", B, 0, i32)
         max_len = history.shape[1]
     per_request = (_array(repetition, "repetition", B, f32), _array(frequency, "frequency", B, f32),
                    _array(presence, "presence", B, f32))
@@ -812,7 +829,7 @@ def dflash2_logits_topk(logits, K, requests=None, row_offsets=None, history=None
         if bias_ids.dim() != 2 or bias_ids.shape[0] != B or bias.shape != bias_ids.shape:
             raise ValueError(f"bias_ids and bias must both be [{B}, n], got {tuple(bias_ids.shape)} and {tuple(bias.shape)}")
         n_bias = bias.shape[1]
-    mp, ms = (None, 0) if mask is None else _matrix(mask, "mask", M, (V + 31) // 32, (i32,))
+    mp, ms = (None, 0) if mask is None else _matrix(mask, "mask", M, (V + 31) // 32, i32)
     cp = up = None
     if K > 0:
         cand, cp = _output(cand, "cand", (M, K), i32, dev, stream)
@@ -821,7 +838,7 @@ def dflash2_logits_topk(logits, K, requests=None, row_offsets=None, history=None
         cand = unary = None
     if out is None and want_out:
         out = _new((M, V), dt, dev, stream)
-    op, os_ = (None, 0) if out is None else _matrix(out, "out", M, V, (dt,))
+    op, os_ = (None, 0) if out is None else _matrix(out, "out", M, V, dt)
     if workspace is None:
         need = dflash2_logits_topk_workspace_bytes(M, V, B, row_offsets is not None, max_len, tokens is not None, n_bias, K)
         workspace = _new(need, torch.uint8, dev, stream) if need else None
@@ -829,8 +846,9 @@ def dflash2_logits_topk(logits, K, requests=None, row_offsets=None, history=None
     _check(library().dflash2_logits_topk(
         lp, ls, M, V, code, B, rp, hp, hs, _array(prompt_len, "prompt_len", B, i32),
         _array(history_len, "history_len", B, i32), max_len, *per_request, _array(tokens, "tokens", M, i32),
-        _array(parents, "parents", M, i32), _dev(bias_ids, "bias_ids", i32, True), _dev(bias, "bias", f32, True), n_bias, mp, ms,
-        K, cp, up, op, os_, wp, wn, _stream(stream)))
+        _array(parents, "parents", M, i32), None if bias is None else _dense(bias_ids, "bias_ids", i32),
+        None if bias is None else _dense(bias, "bias", f32), n_bias, mp, ms, K, cp, up, op, os_, wp, wn,
+        _stream_of(device, stream)))
     return cand, unary, out
 
 
