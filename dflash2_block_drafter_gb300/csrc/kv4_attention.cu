@@ -217,6 +217,11 @@ __device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, volatile 
       break;
     }
 }
+// The last releases of two buffers that took `tiles` tiles in turn: no role waits for those, and a CTA must not leave
+// before they have arrived on its barriers. (Tile i completes phase i / 2 of buffer i % 2.)
+__device__ __forceinline__ void await_releases(uint32_t empty, uint32_t tiles, volatile int* abort_flag, int* err) {
+  for (uint32_t i = tiles - min(tiles, 2u); i < tiles; ++i) wait_on(empty + 8 * (i & 1u), (i >> 1) & 1u, abort_flag, err);
+}
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -858,6 +863,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
             mma_commit(kempty + 8 * buf);
           }
         }
+        await_releases(kempty, it, abort_flag, a.err);
       } else {
         const uint64_t vd = desc_keys_sw128(smem_u32(smem + C::kOffV)), pd = desc_keys_sw128(smem_u32(smem + C::kOffP));
         const uint32_t hi = static_cast<uint32_t>(vd >> 32), v_lo = static_cast<uint32_t>(vd), p = static_cast<uint32_t>(pd);
@@ -880,6 +886,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
             mma_commit(odone);
             mma_commit(vempty + 8 * buf);
           }
+        await_releases(vempty, it, abort_flag, a.err);
       }
       if (*abort_flag != 0) {  // the MMAs in flight end before the CTA leaves
         const uint64_t t0 = globaltimer_ns();

@@ -1,0 +1,57 @@
+"""GPU: attention over the 4-bit cache launched back to back, so that a CTA's shared and tensor memory serve the next launch's
+CTA as soon as it has left. Every launch gives the first one's bits."""
+import numpy as np
+import pytest
+
+from tests.test_gpu_kv4 import _cached, _dev, _rows, torch  # noqa: F401 (fixture)
+from tests.test_gpu_kv4_tree import _tree
+
+pytestmark = pytest.mark.gpu
+
+LAUNCHES, REPLAYS = 40, 25
+
+
+def _repeat(torch, call, out):
+    """LAUNCHES a graph, REPLAYS of it: each launch against the first one's result."""
+    import dflash2_block_drafter_gb300 as d
+    call(out[0])
+    first = out[0].clone()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        for i in range(LAUNCHES):
+            call(out[i % len(out)])
+    for r in range(REPLAYS):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        for o in out:
+            assert torch.equal(o, first), f"replay {r}"
+    assert d.dflash2_poll_error() == 0
+
+
+def _inputs(torch, rng, lens, G, Hq, Hkv, D, page):
+    import dflash2_block_drafter_gb300 as d
+    B = len(lens)
+    cache, table, ctx, _, _ = _cached(torch, d, rng, lens, Hkv, D, page)
+    q, k, v = (_dev(torch, _rows(rng, B, G, h, D)) for h in (Hq, Hkv, Hkv))
+    out = torch.empty((8, B, G, Hq, D), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(max(1, d.dflash2_kv4_attention_workspace_bytes(B, G, Hq, Hkv, D, page, table.shape[1])),
+                     dtype=torch.uint8, device="cuda")
+    return cache, table, ctx, q, k, v, out, ws
+
+
+# ranges of one, two, three and more tiles; 16, 32, 64 and 80 rows a CTA; several items a CTA, and items cut into parts
+@pytest.mark.parametrize("lens,G,Hq,Hkv,D", [([0], 4, 2, 2, 64), ([100] * 3, 4, 8, 2, 128), ([200], 40, 1, 1, 64),
+                                             ([129, 300, 0], 16, 10, 2, 128), ([4000], 1, 16, 2, 128),
+                                             ([700] * 40, 16, 20, 4, 128), ([9000], 64, 5, 1, 64)])
+def test_blocks_and_trees_behind_one_another(torch, lens, G, Hq, Hkv, D):
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(len(lens) + G)
+    cache, table, ctx, q, k, v, out, ws = _inputs(torch, rng, lens, G, Hq, Hkv, D, 32)
+    _repeat(torch, lambda o: d.dflash2_kv4_attention(q, cache, table, ctx, 32, D ** -0.5, k_new=k, v_new=v, causal=True, out=o,
+                                                     workspace=ws), out)
+    parents = torch.tensor(np.stack([_tree(rng, G, "any") for _ in lens]), dtype=torch.int32, device="cuda")
+    _repeat(torch, lambda o: d.dflash2_kv4_attention_tree(q, cache, table, ctx, 32, D ** -0.5, k, v, parents, out=o,
+                                                          workspace=ws), out)
