@@ -206,7 +206,8 @@ __device__ __forceinline__ void tmem_st8(uint32_t t, const float* x) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// (Suspended, not spinning: the issue slots belong to the warps that work.)
+// (Suspended, not spinning: the issue slots belong to the warps that work. Lanes may part here and in votes: what the whole
+// warp has to execute together, as tensor memory's loads and waits, comes behind a __syncwarp.)
 __device__ __forceinline__ void wait_on(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
   if (mbar_try_wait(bar, parity)) return;
   const uint64_t t0 = globaltimer_ns();
@@ -1180,6 +1181,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
           return make_int4(in ? (v.x >> lane) & 1 : 0, in ? (v.y >> lane) & 1 : 0, in ? (v.z >> lane) & 1 : 0,
                            in ? (v.w >> lane) & 1 : 0);
         };
+        __syncwarp();
         tmem_ld_wait();
         // scores and values' factors (log2 domain) relative to the rows' references
         auto weigh = [&](float a, float b) {
@@ -1311,6 +1313,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         }
         // the next tile's scores travel while the fence completes (x is free), if they are there
         loaded = j + 1 < w.j1 && ready(it + 1);
+        __syncwarp();
         if (loaded) load_s(it + 1);
         fence_proxy_async_smem();
         tc_fence_before();

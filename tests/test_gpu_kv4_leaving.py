@@ -3,7 +3,8 @@ CTA as soon as it has left. Every launch gives the first one's bits."""
 import numpy as np
 import pytest
 
-from tests.test_gpu_kv4 import _cached, _dev, _rows, torch  # noqa: F401 (fixture)
+from oracle import tree_oracle as T
+from tests.test_gpu_kv4 import S, _cached, _check, _dev, _host, _rows, torch  # noqa: F401 (fixture)
 from tests.test_gpu_kv4_tree import _tree
 
 pytestmark = pytest.mark.gpu
@@ -55,3 +56,31 @@ def test_blocks_and_trees_behind_one_another(torch, lens, G, Hq, Hkv, D):
     parents = torch.tensor(np.stack([_tree(rng, G, "any") for _ in lens]), dtype=torch.int32, device="cuda")
     _repeat(torch, lambda o: d.dflash2_kv4_attention_tree(q, cache, table, ctx, 32, D ** -0.5, k, v, parents, out=o,
                                                           workspace=ws), out)
+
+
+@pytest.mark.parametrize("G,Hq,D", [(4, 4, 64), (16, 10, 128), (64, 6, 128)])
+def test_references_raised_in_every_tile(torch, G, Hq, D):
+    """Scores that grow by 12 powers of two a tile: the warps leave their common path for the raise, and wait for the last
+    product, in each of a range's several tiles. (40 sequences over the same pages.)"""
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(G)
+    B, Hkv, n, page = 40, 2, 1500, 64
+    k, v, q = _rows(rng, n, Hkv, D), _rows(rng, n, Hkv, D), _rows(rng, B, G, Hq, D)
+    k[:, :, 0] = S.bf16(np.arange(n) // 128 * 12.0 * np.log(2.0))[:, None]
+    q[..., 0] = S.bf16(D ** 0.5)
+    kn, vn = _rows(rng, B, G, Hkv, D), _rows(rng, B, G, Hkv, D)
+    cache = d.dflash2_kv4_cache(-(-n // page), Hkv, D, page)
+    d.dflash2_kv4_append(_dev(torch, k), _dev(torch, v), torch.arange(n, device="cuda"), cache, page)
+    table = torch.arange(cache.shape[0], dtype=torch.int32, device="cuda").repeat(B, 1)
+    ctx = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    parents = np.stack([_tree(rng, G, "any") for _ in range(B)])
+    args = [_dev(torch, q), cache, table, ctx, page, D ** -0.5, _dev(torch, kn), _dev(torch, vn),
+            torch.tensor(parents, dtype=torch.int32, device="cuda")]
+    out = torch.empty((8, B, G, Hq, D), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(d.dflash2_kv4_attention_workspace_bytes(B, G, Hq, Hkv, D, page, table.shape[1]), dtype=torch.uint8,
+                     device="cuda")
+    _repeat(torch, lambda o: d.dflash2_kv4_attention_tree(*args, out=o, workspace=ws), out)
+    K, V = S.kv4_values(k), S.kv4_values(v)
+    for b in (0, 17, B - 1):
+        want, sd = S.attention(q[b], np.concatenate([K, kn[b]]), np.concatenate([V, vn[b]]), T.tree_seen(parents[b], n), D ** -0.5)
+        _check(_host(out[0])[b], want, sd, f"G={G}, sequence {b}")
