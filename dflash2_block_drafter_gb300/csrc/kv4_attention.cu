@@ -711,6 +711,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
 
   if (warp >= kBSoftWarps && warp < kBSoftWarps + kBDeqWarps) {
     // ------------------------------------------------------------------ dequant
+    __syncwarp();
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
     const int side = (warp - kBSoftWarps) >> 2, dw = warp & 3;  // K or V; keys 32 dw .. of each tile
     const uint32_t low = side == 0 ? kBPow2Low : kBPow2LowQV;
@@ -835,119 +836,123 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
         if (lane == 0) mbar_arrive(full + 8 * buf);
       }
     }
-  } else if (warp == kBMmaWarp || warp == kBMmaWarp + 1) {
-    // ------------------------------------------------------------------ MMA issuers: S, and O
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    if (elect_one()) {
-      constexpr uint32_t kFmt = (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);  // f32 <- f16, M = 128
-      uint32_t it = 0, piece = 0;
-      // descriptors: the lower words of the operands' first steps (address / 16, leading offset), and the
-      // upper word (stride 1024 bytes, 128-byte swizzle), the same for all
-      if (warp == kBMmaWarp) {
-        const uint64_t kd = desc_kmajor_sw128(smem_u32(smem)), qd = desc_kmajor_sw128(smem_u32(smem + C::kOffQ));
-        const uint32_t hi = static_cast<uint32_t>(kd >> 32), k_lo = static_cast<uint32_t>(kd), q = static_cast<uint32_t>(qd);
-        for (Walk w(a, range); w.valid(); w.next(a), ++piece) {
-          wait_on(qfull, piece & 1u, abort_flag, a.err);
-#pragma unroll 1
-          for (int j = w.j0; j < w.j1; ++j, ++it) {
-            const uint32_t buf = it & 1u;
-            wait_on(sempty + 8 * buf, ((it >> 1) & 1u) ^ 1u, abort_flag, a.err);
-            wait_on(kfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
-            tc_fence_after();
-            const uint32_t k = k_lo + buf * (C::kTileBytes / 16), d = tmem + buf * N;
-            mma_lean<true>(d, k, q, hi, hi, kFmt);
-#pragma unroll
-            for (int s = 1; s < D / 16; ++s)
-              mma_lean<false>(d, k + (s >> 2) * (kBTile * 128 / 16) + 2 * (s & 3), q + (s >> 2) * (N * 128 / 16) + 2 * (s & 3),
-                              hi, hi, kFmt);
-            mma_commit(sfull + 8 * buf);
-            mma_commit(kempty + 8 * buf);
-          }
-        }
-        await_releases(kempty, it, abort_flag, a.err);
-      } else {
-        const uint64_t vd = desc_keys_sw128(smem_u32(smem + C::kOffV)), pd = desc_keys_sw128(smem_u32(smem + C::kOffP));
-        const uint32_t hi = static_cast<uint32_t>(vd >> 32), v_lo = static_cast<uint32_t>(vd), p = static_cast<uint32_t>(pd);
-        constexpr uint32_t id = kFmt | (1u << 15) | (1u << 16);
-        const uint32_t d = tmem + 2 * N;
-        for (Walk w(a, range); w.valid(); w.next(a))
-#pragma unroll 1
-          for (int j = w.j0; j < w.j1; ++j, ++it) {
-            const uint32_t buf = it & 1u;
-            wait_on(vfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
-            wait_on(pfull, it & 1u, abort_flag, a.err);
-            tc_fence_after();
-            const uint32_t v = v_lo + buf * (C::kTileBytes / 16);
-            if (j > w.j0)
-              mma_lean<false>(d, v, p, hi, hi, id);
-            else
-              mma_lean<true>(d, v, p, hi, hi, id);
-#pragma unroll
-            for (int s = 1; s < kBTile / 16; ++s) mma_lean<false>(d, v + 128 * s, p + 128 * s, hi, hi, id);
-            mma_commit(odone);
-            mma_commit(vempty + 8 * buf);
-          }
-        await_releases(vempty, it, abort_flag, a.err);
-      }
-      if (*abort_flag != 0) {  // the MMAs in flight end before the CTA leaves
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 2000000ull) {
-        }
-      }
-    }
+  } else if (warp >= kBMmaWarp) {
+    // (a warpgroup, four warps, gives its registers up by one instruction that it executes together)
     __syncwarp();
-  } else if (warp >= kBCopyWarp) {
-    // ------------------------------------------------------------------ copies of one side
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kOtherRegs));
-    // A lane per granule looks up its page; the first granule of each run that lies together in a page
-    // (the tile, a page, or a granule) is copied with the rest of its run.
-    const int side = warp - kBCopyWarp;
-    const int granules = (1 << a.page_shift) / kKvGranule, run = min(granules, kBTile / kKvGranule);
-    const uint32_t rfull = raw_full + side * 24, rempty = raw_empty + side * 24;
-    uint32_t stage = 0, phase = 1;
-    for (Walk w(a, range); w.valid(); w.next(a)) {
-      const int last = min(w.j1, w.seq.cached);
-      for (int j0 = w.j0; j0 < last; j0 += 4) {  // pages of four tiles at a time: 32 granules
-        const int g0 = ((w.seq.lo >> kBTileLog) + j0) * (kBTile / kKvGranule) + lane;  // the lane's granule of the sequence
-        const int key = g0 * kKvGranule;
-        int page = -1;
-        // a granule that some row sees (a window may have left the others' pages behind)
-        if (j0 + lane / 8 < last && key < w.seq.hi && key + kKvGranule > w.seq.lo) {
-          page = __ldg(a.table + static_cast<int64_t>(w.b) * a.width + (key >> a.page_shift));
-          if (page < 0 || page >= a.num_pages) {
-            atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_BAD_INDEX));
-            page = -1;
+    if (warp < kBCopyWarp) {
+      // ------------------------------------------------------------------ MMA issuers: S, and O
+      if (elect_one()) {
+        constexpr uint32_t kFmt = (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (8u << 24);  // f32 <- f16, M = 128
+        uint32_t it = 0, piece = 0;
+        // descriptors: the lower words of the operands' first steps (address / 16, leading offset), and the
+        // upper word (stride 1024 bytes, 128-byte swizzle), the same for all
+        if (warp == kBMmaWarp) {
+          const uint64_t kd = desc_kmajor_sw128(smem_u32(smem)), qd = desc_kmajor_sw128(smem_u32(smem + C::kOffQ));
+          const uint32_t hi = static_cast<uint32_t>(kd >> 32), k_lo = static_cast<uint32_t>(kd), q = static_cast<uint32_t>(qd);
+          for (Walk w(a, range); w.valid(); w.next(a), ++piece) {
+            wait_on(qfull, piece & 1u, abort_flag, a.err);
+#pragma unroll 1
+            for (int j = w.j0; j < w.j1; ++j, ++it) {
+              const uint32_t buf = it & 1u;
+              wait_on(sempty + 8 * buf, ((it >> 1) & 1u) ^ 1u, abort_flag, a.err);
+              wait_on(kfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
+              tc_fence_after();
+              const uint32_t k = k_lo + buf * (C::kTileBytes / 16), d = tmem + buf * N;
+              mma_lean<true>(d, k, q, hi, hi, kFmt);
+#pragma unroll
+              for (int s = 1; s < D / 16; ++s)
+                mma_lean<false>(d, k + (s >> 2) * (kBTile * 128 / 16) + 2 * (s & 3), q + (s >> 2) * (N * 128 / 16) + 2 * (s & 3),
+                                hi, hi, kFmt);
+              mma_commit(sfull + 8 * buf);
+              mma_commit(kempty + 8 * buf);
+            }
+          }
+          await_releases(kempty, it, abort_flag, a.err);
+        } else {
+          const uint64_t vd = desc_keys_sw128(smem_u32(smem + C::kOffV)), pd = desc_keys_sw128(smem_u32(smem + C::kOffP));
+          const uint32_t hi = static_cast<uint32_t>(vd >> 32), v_lo = static_cast<uint32_t>(vd), p = static_cast<uint32_t>(pd);
+          constexpr uint32_t id = kFmt | (1u << 15) | (1u << 16);
+          const uint32_t d = tmem + 2 * N;
+          for (Walk w(a, range); w.valid(); w.next(a))
+#pragma unroll 1
+            for (int j = w.j0; j < w.j1; ++j, ++it) {
+              const uint32_t buf = it & 1u;
+              wait_on(vfull + 8 * buf, (it >> 1) & 1u, abort_flag, a.err);
+              wait_on(pfull, it & 1u, abort_flag, a.err);
+              tc_fence_after();
+              const uint32_t v = v_lo + buf * (C::kTileBytes / 16);
+              if (j > w.j0)
+                mma_lean<false>(d, v, p, hi, hi, id);
+              else
+                mma_lean<true>(d, v, p, hi, hi, id);
+#pragma unroll
+              for (int s = 1; s < kBTile / 16; ++s) mma_lean<false>(d, v + 128 * s, p + 128 * s, hi, hi, id);
+              mma_commit(odone);
+              mma_commit(vempty + 8 * buf);
+            }
+          await_releases(vempty, it, abort_flag, a.err);
+        }
+        if (*abort_flag != 0) {  // the MMAs in flight end before the CTA leaves
+          const uint64_t t0 = globaltimer_ns();
+          while (globaltimer_ns() - t0 < 2000000ull) {
           }
         }
-        const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
-        for (int j = j0; j < min(j0 + 4, last); ++j) {
-          const uint32_t got = (have >> (8 * (j - j0))) & 0xffu;
-          wait_on(rempty + 8 * stage, phase, abort_flag, a.err);
-          if (lane == 0) {
-            came_s[side * 3 + stage] = got;
-            mbar_arrive_expect_tx(rfull + 8 * stage, static_cast<uint32_t>(__popc(got)) * L::kGranuleBytes);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------------ copies of one side
+      // A lane per granule looks up its page; the first granule of each run that lies together in a page
+      // (the tile, a page, or a granule) is copied with the rest of its run.
+      const int side = warp - kBCopyWarp;
+      const int granules = (1 << a.page_shift) / kKvGranule, run = min(granules, kBTile / kKvGranule);
+      const uint32_t rfull = raw_full + side * 24, rempty = raw_empty + side * 24;
+      uint32_t stage = 0, phase = 1;
+      for (Walk w(a, range); w.valid(); w.next(a)) {
+        const int last = min(w.j1, w.seq.cached);
+        for (int j0 = w.j0; j0 < last; j0 += 4) {  // pages of four tiles at a time: 32 granules
+          const int g0 = ((w.seq.lo >> kBTileLog) + j0) * (kBTile / kKvGranule) + lane;  // the lane's granule of the sequence
+          const int key = g0 * kKvGranule;
+          int page = -1;
+          // a granule that some row sees (a window may have left the others' pages behind)
+          if (j0 + lane / 8 < last && key < w.seq.hi && key + kKvGranule > w.seq.lo) {
+            page = __ldg(a.table + static_cast<int64_t>(w.b) * a.width + (key >> a.page_shift));
+            if (page < 0 || page >= a.num_pages) {
+              atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_BAD_INDEX));
+              page = -1;
+            }
           }
-          __syncwarp();
-          const int g = lane & 7, first = g & ~(run - 1);
-          // the granules of this lane's run that came, copied by the lane of the first of them (those no
-          // row sees lie at the run's ends, so what came is contiguous)
-          const uint32_t mine = (got >> first) & ((1u << run) - 1u);
-          if (lane / 8 == j - j0 && mine != 0u && g == first + __ffs(mine) - 1)
-            bulk_load(smem_u32(smem + C::kOffRaw + (side * C::kRawStages + stage) * C::kRaw + g * L::kGranuleBytes),
-                      a.cache + (((static_cast<int64_t>(page) * a.Hkv + w.head) * 2 + side) * granules +
-                                 (g0 & (granules - 1))) *
-                                    static_cast<int64_t>(L::kGranuleBytes),
-                      static_cast<uint32_t>(__popc(mine)) * L::kGranuleBytes, rfull + 8 * stage);
-          __syncwarp();
-          if (++stage == C::kRawStages) {
-            stage = 0;
-            phase ^= 1u;
+          const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
+          for (int j = j0; j < min(j0 + 4, last); ++j) {
+            const uint32_t got = (have >> (8 * (j - j0))) & 0xffu;
+            wait_on(rempty + 8 * stage, phase, abort_flag, a.err);
+            if (lane == 0) {
+              came_s[side * 3 + stage] = got;
+              mbar_arrive_expect_tx(rfull + 8 * stage, static_cast<uint32_t>(__popc(got)) * L::kGranuleBytes);
+            }
+            __syncwarp();
+            const int g = lane & 7, first = g & ~(run - 1);
+            // the granules of this lane's run that came, copied by the lane of the first of them (those no
+            // row sees lie at the run's ends, so what came is contiguous)
+            const uint32_t mine = (got >> first) & ((1u << run) - 1u);
+            if (lane / 8 == j - j0 && mine != 0u && g == first + __ffs(mine) - 1)
+              bulk_load(smem_u32(smem + C::kOffRaw + (side * C::kRawStages + stage) * C::kRaw + g * L::kGranuleBytes),
+                        a.cache + (((static_cast<int64_t>(page) * a.Hkv + w.head) * 2 + side) * granules +
+                                   (g0 & (granules - 1))) *
+                                      static_cast<int64_t>(L::kGranuleBytes),
+                        static_cast<uint32_t>(__popc(mine)) * L::kGranuleBytes, rfull + 8 * stage);
+            __syncwarp();
+            if (++stage == C::kRawStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
         }
       }
     }
   } else {
     // ------------------------------------------------------------------ softmax
+    __syncwarp();
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     const int quad = warp & 3;                    // TMEM lanes 32 quad .., rows (warp / 4) NH ..
     const int key_in = quad * 32 + lane;          // the thread's key of each tile; at the end, its channel
