@@ -86,7 +86,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a
   pdl_wait();
   const int page = 1 << a.page_shift;
   const long long cap = static_cast<long long>(a.width) << a.page_shift;
-  int head = __ldg(a.state), count = __ldg(a.state + 1);
+  // (ordinary loads, not the read-only path's: lengths and state may be outputs too)
+  int head = a.state[0], count = a.state[1];
   const bool state_ok = head >= 0 && head < a.capacity && count >= 0 && count <= a.capacity;
   if (!state_ok && tid == 0) atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_INVALID_ARG));
   if (tid < 3) most[tid] = 0;
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a
   // what each sequence asks for: pages (more, or fewer) and tokens; nothing fits a length outside its pages
   constexpr int kBad = -0x7fffffff - 1;
   for (int b = tid; b < a.B; b += kPlanThreads) {
-    const int len = __ldg(a.ctx + b), change = __ldg(a.change + b);
+    const int len = a.ctx[b], change = a.change[b];
     const long long end = static_cast<long long>(len) + change;
     const bool fits = state_ok && len >= 0 && len <= cap && end >= 0 && end <= cap;
     if (!fits) atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_INVALID_ARG));
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a
     bool there;
     if (a.place != nullptr) {
       b = i / a.G;
-      j = __ldg(a.place + i);
+      j = a.place[i];
       there = j >= 0 && j < row_end[b] - before(row_end, b);
     } else {
       there = i < rows_all;
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv4_plan_kernel(const PlanArgs a
     // a sequence shrinks within its last page without giving one back: granted if it fits
     int end = ctx[b] + gain;
     if (gain == 0) {
-      const long long c = static_cast<long long>(ctx[b]) + __ldg(a.change + b);
+      const long long c = static_cast<long long>(ctx[b]) + a.change[b];
       const bool ok = state_ok && ctx[b] >= 0 && ctx[b] <= cap && c >= 0 && c < ctx[b];
       if (ok && (gives || pages_of(static_cast<int>(c)) == pages_of(ctx[b]))) end = static_cast<int>(c);
     }
