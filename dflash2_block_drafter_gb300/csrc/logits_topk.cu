@@ -565,13 +565,14 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 512 ? 1536 / kThreads : 
     for (int h = 0; h < 2; ++h)
       if ((line >> (lane + 32 * h)) & 1) drafted[h] = __ldg(r.tokens + p.first + lane + 32 * h);
   }
-  auto bit_of = [](const uint32_t* w, int t) { return (__ldg(w + (t >> 5)) >> (t & 31)) & 1u; };
+  auto bit_of = [](const uint32_t* w, int t) { return (w[t >> 5] >> (t & 31)) & 1u; };
   int named = 0;
-  for (int w = 0; w < a.windows; ++w) named += __ldg(a.named + b * a.windows + w);
+  // (what the first kernel writes is read by ordinary loads: this one may have started before it ended)
+  for (int w = 0; w < a.windows; ++w) named += a.named[b * a.windows + w];
   auto name_at = [&](int place) {  // of the request's lists, one behind the other
     int w = b * a.windows;
-    for (int n; place >= (n = __ldg(a.named + w)); ++w) place -= n;
-    return __ldg(a.names + static_cast<int64_t>(w) * a.cap + place);
+    for (int n; place >= (n = a.named[w]); ++w) place -= n;
+    return a.names[static_cast<int64_t>(w) * a.cap + place];
   };
   // f(token, value, place) of the thread's named tokens from place `from` on (a multiple of 32; whole warps)
   auto for_named = [&](int from, auto f) {
