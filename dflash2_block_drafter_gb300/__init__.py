@@ -5,8 +5,8 @@ through its C ABI (include/dflash2.h) with ctypes. PyTorch provides device memor
 current stream. There is no CPU fallback: if the library is missing or no GPU is present the
 calls raise.
 
-The functions carry the C names. Tensors are torch tensors on the current CUDA device,
-contiguous, dtype torch.bfloat16 or torch.float32 (activations/weights), float32 for base /
+The functions carry the C names. Tensors are torch tensors on the current CUDA device (those of
+another are refused, and so is a stream of another), contiguous, dtype torch.bfloat16 or torch.float32 (activations/weights), float32 for base /
 bias / scores, int32 for ids. Outputs are allocated here when not passed in.
 """
 from __future__ import annotations
@@ -125,12 +125,31 @@ def _check(rc: int):
         raise Dflash2Error(rc, f"{name}: {msg}")
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream):
     if stream is None:
         if torch.cuda.is_initialized():  # the handle alone: a Stream object costs more than the call's checks
-            return _vp(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
+            return _vp(torch._C._cuda_getCurrentRawStream(_current_device()))
         stream = torch.cuda.current_stream()
-    return _vp(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    if not hasattr(stream, "cuda_stream"):
+        return _vp(int(stream))
+    index = getattr(stream, "device_index", None)
+    if index is not None and index != _current_device():
+        raise ValueError(f"stream is of cuda:{index}, the current device is cuda:{_current_device()}")
+    return _vp(stream.cuda_stream)
+
+
+def _on_current(t, name):
+    """The current device, on which the call runs; refuses a tensor of another one, whose address means nothing there. None
+    for a tensor that is on no GPU (refused where its address is taken)."""
+    if not t.is_cuda:
+        return None
+    device = _current_device()
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{device}")
+    return device
 
 
 def _dev(t, name, dtype=None, optional=False):
@@ -140,6 +159,8 @@ def _dev(t, name, dtype=None, optional=False):
         raise ValueError(f"{name} is required")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != _current_device():
+        _on_current(t, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype is not dtype and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
@@ -580,15 +601,17 @@ def _kv4_cache_shape(cache, head_dim, page_size):
     return cache.shape[0], cache.shape[1]
 
 
-def _kv4_rows(t, name, rows, heads, head_dim, lead=None):
+def _kv4_rows(t, name, rows, heads, head_dim, lead=None, device=None):
     """(pointer, row stride) of a [rows, heads, head_dim] or [B, G, heads, head_dim] (`lead`: B, G) bf16 tensor
     whose leading dimensions walk `rows` equally spaced rows; the last two are dense."""
     if not isinstance(t, torch.Tensor) or t.dim() not in (3, 4) or (t.dim() == 4 and lead and tuple(t.shape[:2]) != lead):
         raise ValueError(f"{name} must be a tensor of {rows} rows of [{heads}, {head_dim}]"
                          f"{f' or [{lead[0]}, {lead[1]}] of them' if lead else ''}, got "
                          f"{tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__}")
-    if not t.is_cuda or t.dtype != torch.bfloat16:
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
         raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    if t.get_device() != (_current_device() if device is None else device):
+        _on_current(t, name)
     shape, stride = t.shape, t.stride()
     if shape[-2:] != (heads, head_dim) or t.numel() != rows * heads * head_dim:
         raise ValueError(f"{name} must hold {rows} rows of [{heads}, {head_dim}], got {tuple(shape)}")
@@ -643,21 +666,23 @@ def dflash2_kv4_attention_workspace_bytes(B, G, q_heads, kv_heads, head_dim, pag
 
 
 def _kv4_attention_args(q, cache, page_table, ctx_len, page_size, k_new, v_new, out, workspace, stream):
-    """Checks and pointers that the attention calls share: (sizes, rows, out, workspace pointer and bytes)."""
+    """Checks and pointers that the attention calls share: (sizes, rows, out and its pointer, workspace pointer and bytes,
+    device)."""
     if q.dim() != 4:
         raise ValueError(f"q must be [B, G, q_heads, head_dim], got shape {tuple(q.shape)}")
+    device = _on_current(q, "q")
     B, G, Hq, D = q.shape
     pages, Hkv = _kv4_cache_shape(cache, D, page_size)
     if page_table.dim() != 2 or page_table.shape[0] != B or ctx_len.numel() != B:
         raise ValueError(f"page_table must be [{B}, max_pages] and ctx_len [{B}]")
-    qp, qs = _kv4_rows(q, "q", B * G, Hq, D)
+    qp, qs = _kv4_rows(q, "q", B * G, Hq, D, None, device)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
     kp = vp = None
     ns = 0
     if k_new is not None:
-        kp, ns = _kv4_rows(k_new, "k_new", B * G, Hkv, D, (B, G))
-        vp, vs = _kv4_rows(v_new, "v_new", B * G, Hkv, D, (B, G))
+        kp, ns = _kv4_rows(k_new, "k_new", B * G, Hkv, D, (B, G), device)
+        vp, vs = _kv4_rows(v_new, "v_new", B * G, Hkv, D, (B, G), device)
         if vs != ns:
             raise ValueError(f"k_new and v_new must have the same row stride, got {ns} and {vs}")
     if out is None:
@@ -670,9 +695,9 @@ def _kv4_attention_args(q, cache, page_table, ctx_len, page_size, k_new, v_new, 
         workspace = _new(need, torch.uint8, q.device, stream) if need else None
     ws = (None, 0, None) if workspace is None else (_dev(workspace, "workspace"),
                                                     workspace.numel() * workspace.element_size(), workspace)
-    rows = (qp, qs, _dev(cache, "cache", torch.uint8), _dev(page_table, "page_table", torch.int32),
-            _dev(ctx_len, "ctx_len", torch.int32), kp, vp, ns)
-    return (B, G, Hq, Hkv, D, page_size, pages, width), rows, out, ws
+    rows = (qp, qs, _dense(cache, "cache", torch.uint8, device), _dense(page_table, "page_table", torch.int32, device),
+            _dense(ctx_len, "ctx_len", torch.int32, device), kp, vp, ns)
+    return (B, G, Hq, Hkv, D, page_size, pages, width), rows, (out, _dev(out, "out", torch.bfloat16)), ws, device
 
 
 def dflash2_kv4_attention(q, cache, page_table, ctx_len, page_size, scale, k_new=None, v_new=None, causal=False,
@@ -681,10 +706,10 @@ def dflash2_kv4_attention(q, cache, page_table, ctx_len, page_size, scale, k_new
     rows (page_table [B, max_pages], ctx_len [B], int32) and its own rows k_new, v_new
     [B, G, kv_heads, head_dim] when given; see dflash2.h for what a row sees. Returns out
     [B, G, q_heads, head_dim] bf16."""
-    sizes, rows, out, (wp, wn, _keep) = _kv4_attention_args(q, cache, page_table, ctx_len, page_size, k_new, v_new, out,
-                                                            workspace, stream)
+    sizes, rows, (out, op), (wp, wn, _keep), device = _kv4_attention_args(q, cache, page_table, ctx_len, page_size, k_new,
+                                                                          v_new, out, workspace, stream)
     _check(library().dflash2_kv4_attention(*rows, *sizes, int(bool(causal)), max(-1, min(window, 2 ** 31 - 1)), scale, BF16,
-                                           _dev(out, "out", torch.bfloat16), wp, wn, _stream(stream)))
+                                           op, wp, wn, _stream_of(device, stream)))
     return out
 
 
@@ -695,52 +720,41 @@ def dflash2_kv4_attention_tree(q, cache, page_table, ctx_len, page_size, scale, 
     [B, G, q_heads, head_dim] bf16."""
     if k_new is None or v_new is None or parents is None:
         raise ValueError("a tree needs k_new, v_new and parents")
-    _current(q, "q")
-    sizes, rows, out, (wp, wn, _keep) = _kv4_attention_args(q, cache, page_table, ctx_len, page_size, k_new, v_new, out,
-                                                            workspace, stream)
+    sizes, rows, (out, op), (wp, wn, _keep), device = _kv4_attention_args(q, cache, page_table, ctx_len, page_size, k_new,
+                                                                          v_new, out, workspace, stream)
     if tuple(parents.shape) != sizes[:2]:
         raise ValueError(f"parents must be [{sizes[0]}, {sizes[1]}], got {tuple(parents.shape)}")
-    _check(library().dflash2_kv4_attention_tree(*rows, _dev(parents, "parents", torch.int32), *sizes,
-                                                max(-1, min(window, 2 ** 31 - 1)), scale, BF16,
-                                                _dev(out, "out", torch.bfloat16), wp, wn, _stream(stream)))
+    _check(library().dflash2_kv4_attention_tree(*rows, _dense(parents, "parents", torch.int32, device), *sizes,
+                                                max(-1, min(window, 2 ** 31 - 1)), scale, BF16, op, wp, wn,
+                                                _stream_of(device, stream)))
     return out
 
 
-def _output(t, name, shape, dtype, device, stream):
-    """(output tensor `name`, its pointer): allocated when not given, else checked."""
+def _output(t, name, shape, dtype, like, device, stream):
+    """(output tensor `name`, its pointer): allocated beside `like` when not given, else checked."""
     if t is None:
-        t = _new(shape, dtype, device, stream)
+        t = _new(shape, dtype, like.device, stream)
         return t, t.data_ptr()
     n = math.prod(shape)
     if t.numel() < n:
         raise ValueError(f"{name} holds {t.numel()} elements, fewer than the {n} the call writes")
-    return t, _dense(t, name, dtype)
+    return t, _dense(t, name, dtype, device)
 
 
-def _dense(t, name, dtype):
-    """_dev of a required array, its checks in the order that costs a good call least."""
-    if t is not None and t.dtype is dtype and t.is_cuda and t.is_contiguous():
+def _dense(t, name, dtype, device):
+    """_dev of a required array, its checks in the order that costs a good call least. `device`: the current one."""
+    if t is not None and t.dtype is dtype and t.get_device() == device and t.is_contiguous():
         return t.data_ptr()
     return _dev(t, name, dtype)
 
 
-def _array(t, name, n, dtype):
+def _array(t, name, n, dtype, device):
     """The pointer of an optional dense array of n elements, or None."""
     if t is None:
         return None
     if t.numel() != n:
         raise ValueError(f"{name} holds {t.numel()} elements, expected {n}")
-    return _dense(t, name, dtype)
-
-
-def _current(t, name):
-    """Refuses a tensor of another device than the current one, on which the call would run; the current device."""
-    if not t.is_cuda:
-        return None
-    device = torch._C._cuda_getDevice()
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
-    return device
+    return _dense(t, name, dtype, device)
 
 
 def _stream_of(device, stream):
@@ -763,30 +777,32 @@ def dflash2_kv4_plan(ctx_len, change, page_table, free_pages, free_state, page_s
         raise ValueError("free_pages must be [capacity] and free_state hold its first place and its count")
     if place is not None and (place.dim() != 2 or place.shape[0] != B):
         raise ValueError(f"place must be [{B}, G], got {tuple(place.shape)}")
-    device = _current(ctx_len, "ctx_len")
-    i32, dev = torch.int32, ctx_len.device
+    i32, device = torch.int32, _on_current(ctx_len, "ctx_len")
     shape = (max(0, rows),) if place is None else tuple(place.shape)
-    ctx_out, cp = _output(ctx_out, "ctx_out", (B,), i32, dev, stream)
-    state_out, sp = _output(state_out, "state_out", (2,), i32, dev, stream)
-    offsets, op = _output(offsets, "offsets", (B + 1,), i32, dev, stream)
-    slots, lp = _output(slots, "slots", shape, torch.int64, dev, stream)
-    positions, pp = _output(positions, "positions", shape, i32, dev, stream)
+    ctx_out, cp = _output(ctx_out, "ctx_out", (B,), i32, ctx_len, device, stream)
+    state_out, sp = _output(state_out, "state_out", (2,), i32, ctx_len, device, stream)
+    offsets, op = _output(offsets, "offsets", (B + 1,), i32, ctx_len, device, stream)
+    slots, lp = _output(slots, "slots", shape, torch.int64, ctx_len, device, stream)
+    positions, pp = _output(positions, "positions", shape, i32, ctx_len, device, stream)
     _check(library().dflash2_kv4_plan(
-        _dense(ctx_len, "ctx_len", i32), _dense(change, "change", i32), _dense(page_table, "page_table", i32),
-        _dense(free_pages, "free_pages", i32), _dense(free_state, "free_state", i32),
-        None if place is None else _dense(place, "place", i32), B,
+        _dense(ctx_len, "ctx_len", i32, device), _dense(change, "change", i32, device),
+        _dense(page_table, "page_table", i32, device), _dense(free_pages, "free_pages", i32, device),
+        _dense(free_state, "free_state", i32, device),
+        None if place is None else _dense(place, "place", i32, device), B,
         0 if place is None else shape[1], rows, page_table.shape[1], page_size, num_pages, free_pages.shape[0], cp, sp, op, lp,
         pp, _stream_of(device, stream)))
     return ctx_out, state_out, offsets, slots, positions
 
 
-def _matrix(t, name, rows, width, dtype):
+def _matrix(t, name, rows, width, dtype, device):
     """(pointer, row stride) of a [rows, >= width] tensor whose rows are dense and may lie apart."""
     if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.size(0) != rows or t.size(1) < width:
         raise ValueError(f"{name} must be [{rows}, {width}], got "
                          f"{tuple(t.shape) if isinstance(t, torch.Tensor) else type(t).__name__}")
     if not t.is_cuda or t.dtype is not dtype:
         raise ValueError(f"{name} must be a CUDA tensor of {dtype}")
+    if t.get_device() != device:
+        _on_current(t, name)
     if t.stride(1) != 1 and t.size(1) > 1:
         raise ValueError(f"{name}: each row must be dense")
     return t.data_ptr(), t.stride(0) if rows > 1 else max(t.size(1), 1)
@@ -807,21 +823,21 @@ def dflash2_logits_topk(logits, K, requests=None, row_offsets=None, history=None
     unary [M, K] fp32, out [M, V] or None); cand and unary are None for K = 0."""
     if logits.dim() != 2:
         raise ValueError(f"logits must be [M, V], got shape {tuple(logits.shape)}")
-    device = _current(logits, "logits")
+    device = _on_current(logits, "logits")
     M, V = logits.shape
     B = requests if requests is not None else (row_offsets.numel() - 1 if row_offsets is not None else max(M, 1))
-    i32, f32, dev, dt = torch.int32, torch.float32, logits.device, logits.dtype
+    i32, f32, dt = torch.int32, torch.float32, logits.dtype
     code = _code(logits)
-    rp = _array(row_offsets, "row_offsets", B + 1, i32)
-    lp, ls = _matrix(logits, "logits", M, V, dt)
+    rp = _array(row_offsets, "row_offsets", B + 1, i32, device)
+    lp, ls = _matrix(logits, "logits", M, V, dt, device)
     hp, hs, max_len = None, 0, 0
     if history is not None:
         if history_len is None:
             raise ValueError("history needs history_len")
-        hp, hs = _matrix(history, "history", B, 0, i32)
+        hp, hs = _matrix(history, "history", B, 0, i32, device)
         max_len = history.shape[1]
-    per_request = (_array(repetition, "repetition", B, f32), _array(frequency, "frequency", B, f32),
-                   _array(presence, "presence", B, f32))
+    per_request = (_array(repetition, "repetition", B, f32, device), _array(frequency, "frequency", B, f32, device),
+                   _array(presence, "presence", B, f32, device))
     if (bias_ids is None) != (bias is None):
         raise ValueError("bias_ids and bias go together")
     n_bias = 0
@@ -829,25 +845,25 @@ def dflash2_logits_topk(logits, K, requests=None, row_offsets=None, history=None
         if bias_ids.dim() != 2 or bias_ids.shape[0] != B or bias.shape != bias_ids.shape:
             raise ValueError(f"bias_ids and bias must both be [{B}, n], got {tuple(bias_ids.shape)} and {tuple(bias.shape)}")
         n_bias = bias.shape[1]
-    mp, ms = (None, 0) if mask is None else _matrix(mask, "mask", M, (V + 31) // 32, i32)
+    mp, ms = (None, 0) if mask is None else _matrix(mask, "mask", M, (V + 31) // 32, i32, device)
     cp = up = None
     if K > 0:
-        cand, cp = _output(cand, "cand", (M, K), i32, dev, stream)
-        unary, up = _output(unary, "unary", (M, K), f32, dev, stream)
+        cand, cp = _output(cand, "cand", (M, K), i32, logits, device, stream)
+        unary, up = _output(unary, "unary", (M, K), f32, logits, device, stream)
     else:
         cand = unary = None
     if out is None and want_out:
-        out = _new((M, V), dt, dev, stream)
-    op, os_ = (None, 0) if out is None else _matrix(out, "out", M, V, dt)
+        out = _new((M, V), dt, logits.device, stream)
+    op, os_ = (None, 0) if out is None else _matrix(out, "out", M, V, dt, device)
     if workspace is None:
         need = dflash2_logits_topk_workspace_bytes(M, V, B, row_offsets is not None, max_len, tokens is not None, n_bias, K)
-        workspace = _new(need, torch.uint8, dev, stream) if need else None
+        workspace = _new(need, torch.uint8, logits.device, stream) if need else None
     wp, wn = (None, 0) if workspace is None else (_dev(workspace, "workspace"), workspace.numel() * workspace.element_size())
     _check(library().dflash2_logits_topk(
-        lp, ls, M, V, code, B, rp, hp, hs, _array(prompt_len, "prompt_len", B, i32),
-        _array(history_len, "history_len", B, i32), max_len, *per_request, _array(tokens, "tokens", M, i32),
-        _array(parents, "parents", M, i32), None if bias is None else _dense(bias_ids, "bias_ids", i32),
-        None if bias is None else _dense(bias, "bias", f32), n_bias, mp, ms, K, cp, up, op, os_, wp, wn,
+        lp, ls, M, V, code, B, rp, hp, hs, _array(prompt_len, "prompt_len", B, i32, device),
+        _array(history_len, "history_len", B, i32, device), max_len, *per_request, _array(tokens, "tokens", M, i32, device),
+        _array(parents, "parents", M, i32, device), None if bias is None else _dense(bias_ids, "bias_ids", i32, device),
+        None if bias is None else _dense(bias, "bias", f32, device), n_bias, mp, ms, K, cp, up, op, os_, wp, wn,
         _stream_of(device, stream)))
     return cand, unary, out
 
