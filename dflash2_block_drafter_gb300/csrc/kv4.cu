@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_rows_kernel(const KvRowsArgs
 #pragma unroll
       for (int u = 0; u < kRowsUnroll; ++u) {
         const int t = t0 + u * rows;
-        int64_t slot = t < t_end ? __ldg(a.slots + t) : -1;
+        int64_t slot = t < t_end ? a.slots[t] : -1;  // (an ordinary load: the kernel in front may have written it)
         if (slot >= end) {  // past the cache: recorded, skipped
           atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_BAD_INDEX));
           slot = -1;

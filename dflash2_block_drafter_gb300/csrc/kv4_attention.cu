@@ -121,7 +121,7 @@ struct BlockArgs {
   const __nv_bfloat16* q;
   int64_t q_stride;
   const uint8_t* cache;
-  const int32_t *table, *ctx;
+  const int32_t *table, *ctx;  // (read by ordinary loads: the kernel in front may write them while this one starts)
   const __nv_bfloat16 *k_new, *v_new;
   int64_t new_stride;
   const int32_t* parents;  // [B][G], of trees
@@ -238,7 +238,7 @@ struct BlockSeq {
 __device__ __forceinline__ BlockSeq block_seq(const BlockArgs& a, int b) {
   BlockSeq s;
   const int own = a.k_new != nullptr ? 1 : 0;
-  s.L = min(max(__ldg(a.ctx + b), 0), a.cap);  // (block_range records a length outside)
+  s.L = min(max(a.ctx[b], 0), a.cap);  // (block_range records a length outside)
   s.base = s.L + (own - 1) * a.G;
   s.lo = a.window > 0 ? max(0, min(s.L, s.base - a.window + 1)) : 0;
   s.hi = a.causal ? max(0, min(s.L, s.base + a.G)) : s.L;
@@ -303,7 +303,7 @@ __device__ __forceinline__ BlockRange block_range(const BlockArgs& a, int setup,
   };
   long long mine = 0;
   for (int b = lane * per; b < min(a.B, (lane + 1) * per); ++b) {
-    const int len = __ldg(a.ctx + b);
+    const int len = a.ctx[b];
     if (len < 0 || len > a.cap) atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_INVALID_ARG));
     mine += block_seq(a, b).tiles + setup;
   }
@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kBThreads, 1) kv4_attention_kernel(const Block
           int page = -1;
           // a granule that some row sees (a window may have left the others' pages behind)
           if (j0 + lane / 8 < last && key < w.seq.hi && key + kKvGranule > w.seq.lo) {
-            page = __ldg(a.table + static_cast<int64_t>(w.b) * a.width + (key >> a.page_shift));
+            page = a.table[static_cast<int64_t>(w.b) * a.width + (key >> a.page_shift)];
             if (page < 0 || page >= a.num_pages) {
               atomicCAS(a.err, 0, static_cast<int>(DFLASH2_ERR_BAD_INDEX));
               page = -1;
