@@ -23,6 +23,11 @@ int g_sms[kMaxDevices];
 std::mutex g_mu;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// each to its element's type (a kernel's access to one that is not would fault); NULL is
+template <typename... T>
+bool aligned(const T*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) % alignof(T) == 0) && ...);
+}
 }  // namespace
 
 int fail(int status, const char* fmt, ...) {
@@ -476,7 +481,8 @@ int dflash2_kv4_append(const void* k, const void* v, int64_t k_stride, int64_t v
   REQUIRE(T >= 0, "T=%d must be >= 0", T);
   if (T == 0) return DFLASH2_OK;
   REQUIRE(k && v && slots && cache, "a required pointer is NULL");
-  REQUIRE(aligned16(k) && aligned16(v) && aligned16(cache), "k, v and cache must be 16-byte aligned");
+  REQUIRE(aligned16(k) && aligned16(v) && aligned16(cache) && aligned(slots),
+          "k, v and cache must be 16-byte aligned, slots 8-byte aligned");
   const int64_t row = static_cast<int64_t>(heads) * D;
   REQUIRE(k_stride >= row && k_stride % 8 == 0 && v_stride >= row && v_stride % 8 == 0,
           "row strides %lld, %lld must be multiples of 8 and at least heads * head_dim = %lld",
@@ -492,7 +498,8 @@ int dflash2_kv4_read(const void* cache, const int64_t* slots, int T, int heads, 
   REQUIRE(T >= 0, "T=%d must be >= 0", T);
   if (T == 0) return DFLASH2_OK;
   REQUIRE(k && v && slots && cache, "a required pointer is NULL");
-  REQUIRE(aligned16(k) && aligned16(v) && aligned16(cache), "k, v and cache must be 16-byte aligned");
+  REQUIRE(aligned16(k) && aligned16(v) && aligned16(cache) && aligned(slots),
+          "k, v and cache must be 16-byte aligned, slots 8-byte aligned");
   const Kv4Rows r{nullptr, nullptr, 0, 0, slots, T, heads, D, page_size, num_pages, const_cast<void*>(cache), k, v};
   return launch_kv4_rows(r, static_cast<cudaStream_t>(stream));
 }
@@ -521,6 +528,7 @@ static int kv4_attention_call(Kv4Attention r, int dtype, size_t workspace_bytes,
   REQUIRE((r.k_new == nullptr) == (r.v_new == nullptr), "k_new and v_new must be both set or both NULL");
   REQUIRE(aligned16(r.q) && aligned16(r.cache) && aligned16(r.out) && aligned16(r.k_new) && aligned16(r.v_new),
           "q, cache, k_new, v_new and out must be 16-byte aligned");
+  REQUIRE(aligned(r.table, r.ctx, r.parents), "page_table, ctx_len and parents must be 4-byte aligned");
   REQUIRE(r.q_stride >= static_cast<int64_t>(r.Hq) * r.D && r.q_stride % 8 == 0,
           "q_stride=%lld must be a multiple of 8 and at least Hq * head_dim", static_cast<long long>(r.q_stride));
   if (r.k_new != nullptr)
@@ -582,6 +590,8 @@ int dflash2_kv4_plan(const int32_t* ctx_len, const int32_t* change, int32_t* pag
   else
     REQUIRE(rows >= 0 && rows <= kMost, "rows=%d must be in [0, 2^31 - 2^16]", rows);
   REQUIRE((place == nullptr && rows == 0) || (slots && positions), "slots and positions are required");
+  REQUIRE(aligned(ctx_len, change, page_table, free_pages, free_state, place, ctx_out, state_out, row_offsets, slots, positions),
+          "every array must be aligned to its elements");
   const Kv4Plan r{ctx_len, change, free_state, place, page_table, free_pages, ctx_out, state_out, row_offsets, positions,
                   slots, B, max_pages, page_size, num_pages, capacity, G, place != nullptr ? 0x7fffffff : rows};
   return launch_kv4_plan(r, static_cast<cudaStream_t>(stream));
@@ -622,6 +632,9 @@ int dflash2_logits_topk(const void* logits, int64_t stride, int M, int V, int dt
   const uintptr_t size = dtype == DFLASH2_F32 ? 4 : 2;
   REQUIRE(reinterpret_cast<uintptr_t>(logits) % size == 0 && reinterpret_cast<uintptr_t>(out) % size == 0,
           "logits and out must be aligned to their type");
+  REQUIRE(aligned(row_offsets, history, prompt_len, history_len, repetition, frequency, presence, tokens, parents, bias_ids, bias,
+                  mask, cand, unary),
+          "every array must be aligned to its elements");
   REQUIRE(stride >= V || M == 1, "stride=%lld must be at least V=%d", static_cast<long long>(stride), V);
   REQUIRE(out == nullptr || out_stride >= V || M == 1, "out_stride=%lld must be at least V=%d",
           static_cast<long long>(out_stride), V);
