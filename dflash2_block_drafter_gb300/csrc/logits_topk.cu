@@ -18,8 +18,11 @@
 //  2. A CTA a row selects. The named tokens' values are computed, and the lanes that hold a named token marked, whose
 //     keys say too much. The other keys (a 32nd of the row) and the named values give a bound that the K best reach:
 //     the K-th largest of 32 groups' maxima. The few lanes whose key reaches it are read once more, and the K best of
-//     what reaches the bound there, and of the named, are ranked by (value, lower token). A row where too many reach
-//     it (equal values) is searched in K rounds instead.
+//     what reaches the bound there, and of the named, are ranked by (value, lower token). Where more reach it than can be
+//     ranked (equal values; strong penalties for a history that names nearly every lane), the best of each of 1024
+//     shares of them give a nearer bound, for two passes more. K rounds search a row for few tokens, or where its own fall
+//     into few shares. (63 rows of 32771 with 30000 generated tokens, K = 16: 47 us under penalties of 1.1, 0.1 and 0.1, 92
+//     under 1.5, 1 and 1; in K rounds 222.)
 // What bounds it: 64 x 15 rows of 248320 fp32 tokens take 162 us, 0.88 of the copy rate; 64 bf16 rows under masks, adjusted
 // logits wanted, 25 us of which the stream is 15; one block's 15 rows 14.5 us and rows with histories of 30000 tokens 48:
 // the latency of two launches and, of the names, of a history's atomics, their ranks and the named tokens' values.
@@ -45,6 +48,7 @@ constexpr int kLaneTokens = 32;                            // of which a lane ha
 constexpr int kStreamThreads = 512, kStreamWarps = kStreamThreads / 32;
 constexpr int kStreamTiles = 4;                            // tiles a warp, at most
 constexpr int kEntries = 1024, kLanes = 512;               // that reach the bound
+constexpr int kFewWanted = 4;                              // K up to which a row where more reach it is searched at once
 constexpr int kPickK = 16;
 constexpr uint32_t kCountMask = (1u << 20) - 1, kInPrompt = 1u << 20;  // a counter; over it, which bias
 constexpr int kBiasShift = 21;
@@ -505,8 +509,13 @@ __global__ void __launch_bounds__(kStreamThreads) logits_stream_kernel(const Pic
 }
 
 // ------------------------------------------------------------------ select
+// Which of kEntries shares a token falls into, spread by a product's upper bits (multiplicative hashing, Knuth).
+__device__ __forceinline__ int share_of(int token) { return static_cast<int>((static_cast<uint32_t>(token) * 0x9e3779b1u) >> 22); }
+static_assert(kEntries == 1 << 10, "shares");
+
 struct SelectShared {
   unsigned long long entry[kEntries];
+  unsigned long long least;
   unsigned long long best[kPickK];
   unsigned long long red[32];
   int lane[kLanes];
@@ -671,12 +680,6 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 512 ? 1536 / kThreads : 
   const uint32_t holder = __ballot_sync(0xffffffffu, above == r.K - 1);
   constexpr uint32_t kMinusInf = 0x007fffffu;  // the key of -inf
   const uint32_t bound = max(__shfl_sync(0xffffffffu, g, __ffs(holder) - 1) & ~31u, kMinusInf + 1u);
-  auto enter = [&](float x, int token) {
-    if (pick_key(x) < bound) return;
-    const int at = atomicAdd(&s.entries, 1);
-    if (at < kEntries) s.entry[at] = pick_entry(x, token);
-  };
-  if (__any_sync(0xffffffffu, named_key >= bound)) again(bound, [&](int t, float y) { enter(y, t); });
   auto list_lanes = [&](int k, const uint4& q) {
     if (max(max(q.x, q.y), max(q.z, q.w)) < bound) return;
     const uint32_t x[4] = {q.x, q.y, q.z, q.w};
@@ -693,23 +696,74 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 512 ? 1536 / kThreads : 
 #pragma unroll 4
     for (int k = tid + kKeyLoads * kThreads; k < quads; k += kThreads) list_lanes(k, keys[k]);
   }
-  __syncthreads();
   auto free_value = [&](int t) {  // of a token that is allowed and not named, else -inf
     const uint32_t named = taken != nullptr ? bit_of(taken, t) : 0u, ok = mask != nullptr ? bit_of(mask, t) : 1u;
     const float x = Vec::load(row + t);
     return named == 0u && ok != 0u ? x : -INFINITY;
   };
-  // the tokens of the lanes that reach the bound, one a lane here
-  const int lanes = s.lanes;
+  // Pass 0: what reaches the bound. Where that is more than can be ranked, pass 1 keeps the best of each of 1024 shares of
+  // it, whose K-th largest is a bound that few besides the K best reach, and pass 2 takes those. (A named token's lane counts
+  // by the token's own logit, and where a history names nearly all lanes the bound is weak: 63 rows of 32771 under
+  // penalties of 1.5, 1 and 1 for 30000 generated tokens list up to 1024 lanes and 7432 values.)
+  unsigned long long least = static_cast<unsigned long long>(bound) << 32;
+  int n;
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+    const uint32_t least_key = static_cast<uint32_t>(least >> 32);
+    auto take = [&](float x, int token) {
+      const unsigned long long e = pick_entry(x, token);
+      if (e < least) return;
+      if (pass == 1) {
+        unsigned long long* share = &s.entry[share_of(token)];
+        if (e > *share) atomicMax(share, e);
+        return;
+      }
+      const int at = atomicAdd(&s.entries, 1);
+      if (at < kEntries) s.entry[at] = e;
+    };
+    if (__any_sync(0xffffffffu, named_key >= least_key)) again(least_key, [&](int t, float y) { take(y, t); });
+    __syncthreads();
+    auto take_lane = [&](int x) {  // the tokens of the row's lane x, one a lane here
+      const int t = (x >> 5) * kTile + ((lane / kN) * 32 + (x & 31)) * kN + lane % kN - off;
+      const bool full = *reinterpret_cast<volatile int*>(&s.entries) > kEntries;  // (too many: the rest is not looked at)
+      if (t >= 0 && t < r.V && !full) take(free_value(t), t);
+    };
+    const int lanes = s.lanes;
+    if (lanes <= kLanes) {
 #pragma unroll 4
-  for (int k = warp; k < min(lanes, kLanes); k += kWarps) {
-    const int x = s.lane[k];
-    const int t = (x >> 5) * kTile + ((lane / kN) * 32 + (x & 31)) * kN + lane % kN - off;
-    if (t >= 0 && t < r.V) enter(free_value(t), t);
+      for (int k = warp; k < lanes; k += kWarps) take_lane(s.lane[k]);
+    } else {  // more than are listed: the keys once more
+      const uint32_t* each = reinterpret_cast<const uint32_t*>(keys);
+      for (int x0 = warp * 32; x0 < 4 * quads; x0 += kThreads)
+        for (uint32_t hit = __ballot_sync(0xffffffffu, each[x0 + lane] >= least_key); hit != 0u; hit &= hit - 1u)
+          take_lane(x0 + __ffs(hit) - 1);
+    }
+    __syncthreads();
+    n = s.entries;
+    // (up to four tokens the search below, a pass a token, is as fast: 15 rows of 248320 equal values take 76 us for one, 121
+    // for two and 748 for sixteen by it, 200 by shares)
+    if (pass == 2 || (pass == 0 && (n <= kEntries || r.K <= kFewWanted))) break;
+    __syncthreads();
+    if (pass == 0) {
+      for (int x = tid; x < kEntries; x += kThreads) s.entry[x] = 0ull;
+      if (tid == 0) {
+        s.entries = 0;
+        s.least = 0ull;
+      }
+      __syncthreads();
+      continue;
+    }
+    for (int x = tid; x < kEntries; x += kThreads) {
+      const unsigned long long mine = s.entry[x];
+      int before = 0;
+#pragma unroll 4
+      for (int y = 0; y < kEntries; ++y) before += s.entry[y] > mine ? 1 : 0;
+      if (before == r.K - 1 && mine != 0ull) s.least = mine;
+    }
+    __syncthreads();
+    least = max_u64(least, s.least);  // (fewer than K shares have any: as it was)
   }
-  __syncthreads();
-  const int n = s.entries;
-  if (n <= kEntries && lanes <= kLanes) {
+  if (n <= kEntries) {
     for (int x = tid; x < n; x += kThreads) {
       const unsigned long long mine = s.entry[x];
       int before = 0;
@@ -718,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 512 ? 1536 / kThreads : 
       if (before < r.K) s.best[before] = mine;
     }
     __syncthreads();
-  } else {
+  } else {  // (tokens of few shares)
     unsigned long long last = ~0ull;
 #pragma unroll 1
     for (int k = 0; k < r.K; ++k) {

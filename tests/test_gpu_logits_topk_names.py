@@ -58,6 +58,7 @@ def test_equal_values_and_more_names_than_are_kept(torch, dtype, size, kept):
     _check(torch, c, 16)
     _check(torch, c, 16, in_place=True)
     _check(torch, c, 1, want_out=False)
+    _check(torch, c, 4, in_place=True)
 
 
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
