@@ -429,8 +429,8 @@ DFLASH2_API int dflash2_kv4_attention_tree(const void* q, int64_t q_stride, cons
  *              their number. Pages are taken from its front in the order of the sequences, and given back to
  *              its end; capacity at least the cache's pages. state_out [2]: the state afterwards.
  *   A sequence is refused, and left as it was, if the free pages do not suffice for it and those before it (pages given
- *   back in this call are not yet counted); in packed rows (below) also if its rows do not fit. Later sequences that need
- *   pages (rows) are then refused too. A length or change outside [0, max_pages * page_size], a state outside the ring,
+ *   back in this call are not yet counted); also if its rows and theirs do not fit: `rows` in packed rows (below),
+ *   2^31 - 1 new tokens in all with place. Later sequences that need pages (rows) are then refused too. A length or change outside [0, max_pages * page_size], a state outside the ring,
  *   or more pages given back than the ring has room for, refuses the sequence and records DFLASH2_ERR_INVALID_ARG. A
  *   page outside [0, num_pages) records DFLASH2_ERR_BAD_INDEX; its rows' slots are -1.
  *   ctx_out    [B] int32: the lengths afterwards (L where the sequence was refused).
@@ -475,8 +475,11 @@ DFLASH2_API int dflash2_kv4_plan(const int32_t* ctx_len, const int32_t* change, 
  *              0 <= K <= min(16, V), both NULL for K = 0. NaN comes before every number.
  *   out        [M, V] dtype or NULL, rows out_stride apart: y, rounded once. May be logits itself (with its stride).
  *   workspace  at least dflash2_logits_topk_workspace_bytes(M, V, B, row_offsets given, max_len (0 without history), tokens
- *              given, n_bias, K) bytes, 256-byte aligned (NULL when that is 0), no initialisation. Calls that can run at the
- *              same time need workspaces of their own. The same call gives the same bits.
+ *              given, n_bias, K) bytes, 256-byte aligned (NULL when that is 0), no initialisation. It goes by what the call
+ *              could hold, not by the lengths: V / 8 a request and V / 8 a row, and for each request (and each 2^18 tokens of
+ *              the vocabulary) 8 (max_len + n_bias + 64), at most 2^21. (4096 requests with room for 32768 tokens: 1.07 GB beside
+ *              a history of 0.54 GB; pass no more of max_len than is needed.) Calls that can run at the same time need
+ *              workspaces of their own. The same call gives the same bits.
  * ---------------------------------------------------------------------------------- */
 DFLASH2_API size_t dflash2_logits_topk_workspace_bytes(int M, int V, int B, int ragged, int max_len, int drafted, int n_bias,
                                                        int K);

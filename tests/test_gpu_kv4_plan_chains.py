@@ -65,3 +65,28 @@ def test_a_chain_of_plans_in_place(torch, captured, B, page, rows, place):
     for name, x in zip(("ctx", "state", "table", "queue"), (c, s, t, q)):
         np.testing.assert_array_equal(x.cpu().numpy(), want[name], err_msg=name)
     assert d.dflash2_poll_error() == 0
+
+
+def test_gains_past_32_bits_together(torch):
+    """Rows in places: each sequence's gain fits, all together pass what row_offsets can count, so the last is refused."""
+    import dflash2_block_drafter_gb300 as d
+    page, width, pages = 4096, 300000, 700000
+    gain = [10 ** 9, 10 ** 9, 5 * 10 ** 8, 0, -3]
+    ctx = _i32(torch, [0, 5, 7, 9, 4])
+    table = torch.full((5, width), -7, dtype=torch.int32, device="cuda")
+    table[:, 0] = _i32(torch, [0, 1, 2, 3, 4])
+    queue = torch.arange(pages, dtype=torch.int32, device="cuda")
+    place = _i32(torch, [[gain[0] - 1, 0], [0, gain[1] - 1], [0, 1], [0, 0], [0, 0]])
+    before = table.clone()
+    new, state, off, slots, pos = d.dflash2_kv4_plan(ctx, _i32(torch, gain), table, queue, _i32(torch, [5, pages - 5]), page, pages,
+                                                     place=place)
+    assert d.dflash2_poll_error() == 0
+    assert new.tolist() == [10 ** 9, 10 ** 9 + 5, 7, 9, 1]
+    assert off.tolist() == [0, 10 ** 9, 2 * 10 ** 9, 2 * 10 ** 9, 2 * 10 ** 9, 2 * 10 ** 9]
+    need = [-(-10 ** 9 // page), -(-(10 ** 9 + 5) // page) - 1]
+    assert state.tolist() == [5 + sum(need), pages - 5 - sum(need)]
+    assert pos.tolist() == [[10 ** 9 - 1, 0], [5, 10 ** 9 + 4], [-1, -1], [-1, -1], [-1, -1]]
+    last = lambda b, p: int(table[b, p // page]) * page + p % page
+    assert slots.tolist() == [[last(0, 10 ** 9 - 1), last(0, 0)], [page + 5, last(1, 10 ** 9 + 4)], [-1, -1], [-1, -1], [-1, -1]]
+    assert torch.equal(table[0, :need[0]], torch.arange(5, 5 + need[0], dtype=torch.int32, device="cuda"))
+    assert torch.equal(table[2:], before[2:])
