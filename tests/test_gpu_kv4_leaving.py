@@ -84,3 +84,40 @@ def test_references_raised_in_every_tile(torch, G, Hq, D):
     for b in (0, 17, B - 1):
         want, sd = S.attention(q[b], np.concatenate([K, kn[b]]), np.concatenate([V, vn[b]]), T.tree_seen(parents[b], n), D ** -0.5)
         _check(_host(out[0])[b], want, sd, f"G={G}, sequence {b}")
+
+
+def test_two_graphs_of_one_workspace_in_turn(torch):
+    """A graph of blocks and one of trees, cut into other parts, replayed one after the other over the same workspace."""
+    import dflash2_block_drafter_gb300 as d
+    rng = np.random.default_rng(1)
+    made = []
+    for lens, G, Hq, Hkv, D in (([5000, 40], 16, 10, 2, 128), ([3000] * 3, 40, 4, 1, 64)):
+        cache, table, ctx, q, k, v, out, _ = _inputs(torch, rng, lens, G, Hq, Hkv, D, 32)
+        parents = torch.tensor(np.stack([_tree(rng, G, "any") for _ in lens]), dtype=torch.int32, device="cuda")
+        size = d.dflash2_kv4_attention_workspace_bytes(len(lens), G, Hq, Hkv, D, 32, table.shape[1])
+        made.append((cache, table, ctx, q, k, v, out[0], parents, D, size))
+    ws = torch.empty(max(m[-1] for m in made), dtype=torch.uint8, device="cuda")
+    block, tree = made
+    calls = [lambda: d.dflash2_kv4_attention(block[3], *block[:3], 32, block[8] ** -0.5, k_new=block[4], v_new=block[5],
+                                             out=block[6], workspace=ws),
+             lambda: d.dflash2_kv4_attention_tree(tree[3], *tree[:3], 32, tree[8] ** -0.5, tree[4], tree[5], tree[7], out=tree[6],
+                                                  workspace=ws)]
+    first, graphs = [], []
+    for call, m in zip(calls, made):
+        call()
+        torch.cuda.synchronize()
+        first.append(m[6].clone())
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    for r in range(200):
+        for m in made:
+            m[6].fill_(float("nan"))
+        for g in graphs:
+            g.replay()
+        if r % 3 == 0:
+            calls[r % 2]()  # and an eager call between
+        torch.cuda.synchronize()
+        for m, want in zip(made, first):
+            assert torch.equal(m[6], want), f"round {r}"
+    assert d.dflash2_poll_error() == 0

@@ -76,3 +76,24 @@ def test_long_generated_histories_under_strong_penalties(torch, dtype, V, n):
     _check(torch, c, 16, want_out=False)
     _check(torch, c, 16, in_place=True)
     _check(torch, c, 5)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_more_names_than_are_kept_over_a_vocabulary_of_two_windows(torch, dtype):
+    rng = np.random.default_rng(3)
+    c = _named(rng, (2, 2, 300001, 40000), dtype, mask=0.7)
+    assert (c["history"][0] < 2 ** 18).sum() > 8192 and (c["history"][0] >= 2 ** 18).any()
+    _check(torch, c, 16)
+    _check(torch, c, 16, in_place=True)
+    c["logits"][:] = -0.5
+    c["rep"][0], c["freq"][0], c["pres"][0] = 1.0, 0.0, 0.0
+    _check(torch, c, 16, in_place=True)
+    _check(torch, c, 3)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_the_largest_vocabulary(torch, dtype):
+    c = _case(np.random.default_rng(4), 2, 1, 1 << 22, dtype, 500, "tree", bias=40, mask=0.9)
+    c["ids"][0, 0], c["bias"][0, 0] = (1 << 22) - 1, 30.0
+    _check(torch, c, 16, pad=1, shift=3)
+    _check(torch, c, 2, in_place=True)
