@@ -34,7 +34,7 @@
 // copies for K, one for V). K, V and S are double-buffered. The softmax warps, whose sums stay in registers,
 // take some of the others' (kSoftRegs).
 //
-// What a tile takes: about 2.3 thousand cycles with 80 rows, where the softmax warps' chain (scores from TMEM,
+// What a tile takes: 2.3 to 2.5 thousand cycles with 80 rows, where the softmax warps' chain (scores from TMEM,
 // the check, exponentials, the operand's stores and their fence) is the longest, and 1.9 with 16, where the
 // conversion of codes is; each scheduler issues in 49 % and 57 % of the cycles. 64 blocks of 16 rows and five
 // query heads a key head over 256 to 4096 keys of 128 channels take 125 us, 64 single tokens over 1 to 8192 keys 112 us
@@ -44,9 +44,9 @@
 // scores' buffer given back together with the operand (130 us for the tokens).
 //
 // Trees: a row's own keys are its line of ancestors, 64 bits that the own tile's masks are taken from; all else is the
-// same code. 32 trees of 32 rows (160 rows a key head) over 256 to 4096 keys take 131 us, one of 64 rows over 32768 keys
-// 86: the same chain a tile, for which shared memory moves 224 KB (operands into the products 104, their making 64), 1.7
-// of the 2.3 thousand cycles at 128 bytes a clock. One of 8 rows over 1024 keys takes 17 us: start 4, three tiles and the join.
+// same code. 32 trees of 32 rows (160 rows a key head) over 256 to 4096 keys take 140 us (131 to 149 by the lengths drawn, 62
+// to 79 thousand keys in all), one of 64 rows over 32768 keys 87: the same chain a tile, for which shared memory moves 224
+// KB (operands into the products 104, their making 64), 1.7 of its thousand cycles at 128 bytes a clock. One of 8 rows over 1024 keys takes 17 us: start 4, three tiles and the join.
 //
 // CTAs are persistent, one an SM: all (sequence, head, row tile) items, each its tiles and a constant for
 // the change from one item to the next, form one line that is cut into equal ranges, whatever the lengths.
@@ -57,6 +57,9 @@
 // flag holds the call's own 64-bit number, so the workspace needs no initialisation, and its reader clears it
 // for a replay. A block over 32768 keys, 19 parts a head, takes 42 us of which the joins are 12; a kernel of
 // its own for them took 20.
+//
+// A CTA leaves only when everything that arrives on its barriers by itself has arrived: the copies by those who wait for them,
+// the products' releases by their issuers (await_releases).
 //
 // No wait blocks for ever, no loop but over tiles, parts and rows, and no wait is skipped: after a timeout the
 // roles run on (their results are void and the error word says so), so that every barrier stays balanced.
@@ -91,7 +94,7 @@ struct BlockCfg {
   // the change from one item to the next, in tiles (measured: 15 of 3.1 thousand cycles with 80 rows, 5 of
   // 2.0 with 16). A tree's has its lines of ancestors and the masks of its own rows besides, and a row tile of it takes
   // 19 of 2.2 thousand cycles longer than its tiles: 32 trees of 32 rows over 256 to 4096 keys take 147 us with 5 there, 130
-  // with 9 and 134 with 12; of 4 rows (NK = 2) 46 with 3, 44 with 4.
+  // with 9 and 134 with 12 (one draw of lengths); of 4 rows (NK = 2) 46 with 3, 44 with 4.
   static constexpr int setup(bool tree) { return NK <= 2 ? (tree ? 4 : 3) : (tree ? NK + 4 : NK); }
   // registers a thread: 640 x 96 at launch, then shared out. With 80 rows 144 / 64 takes 128 to 130 us for 64
   // blocks over 256 .. 4096 keys where 120 / 80 takes 147, 136 / 64 133 and 152 / 56 132; with 16 rows, whose softmax

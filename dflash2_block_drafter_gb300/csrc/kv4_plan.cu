@@ -9,8 +9,8 @@
 // before it. The sums run over refused sequences too, so that what is granted is a prefix of those that ask, and
 // each sum cut off at the largest granted one gives the granted sequences' places.
 //
-// What bounds it: latency. 64 sequences' blocks of 16 rows take 5.4 us in a graph, a launch and four passes over
-// shared memory; 98304 packed rows 11 us and 4096 sequences 11.5, of which the cluster's start and end and the three
+// What bounds it: latency. 64 sequences' blocks of 16 rows take 5.3 us in a graph, a launch and four passes over
+// shared memory; 98304 packed rows 12 us and 4096 sequences 11.3, of which the cluster's start and end and the three
 // scans are most (the rows' bytes, 1.2 MB, would take 0.2).
 #include <algorithm>
 
@@ -255,7 +255,7 @@ int launch_kv4_plan(const Kv4Plan& r, cudaStream_t st) {
   if (!ensure_smem_attr(kv4_plan_kernel, kPlanMaxSequences * 16, &done))
     return fail(DFLASH2_ERR_CUDA, "cudaFuncSetAttribute failed (plan)");
   // One CTA up to four rows a thread (64 sequences of 16 rows: 5.4 us, on a cluster 5.7); a cluster above, each CTA with
-  // sums of its own (98304 packed rows 11 us, on one CTA 44; 4096 sequences of a row 11 and 22).
+  // sums of its own (98304 packed rows 11 us, on one CTA 44; 4096 sequences of a row 11 and 22; each pair side by side).
   const int64_t rows = r.place != nullptr ? static_cast<int64_t>(r.B) * r.G : r.rows;
   const unsigned ctas = rows + r.B > 4 * kPlanThreads ? kPlanCluster : 1;
   cudaLaunchAttribute cl{};

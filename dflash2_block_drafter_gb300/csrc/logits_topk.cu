@@ -23,9 +23,10 @@
 //     shares of them give a nearer bound, for two passes more. K rounds search a row for few tokens, or where its own fall
 //     into few shares. (63 rows of 32771 with 30000 generated tokens, K = 16: 47 us under penalties of 1.1, 0.1 and 0.1, 92
 //     under 1.5, 1 and 1; in K rounds 222.)
-// What bounds it: 64 x 15 rows of 248320 fp32 tokens take 162 us, 0.88 of the copy rate; 64 bf16 rows under masks, adjusted
-// logits wanted, 25 us of which the stream is 15; one block's 15 rows 14.5 us and rows with histories of 30000 tokens 48:
-// the latency of two launches and, of the names, of a history's atomics, their ranks and the named tokens' values.
+// What bounds it: 64 x 15 rows of 248320 fp32 tokens take 168 us, 0.85 of the copy rate; 64 bf16 rows under masks, adjusted
+// logits wanted, 30 us (25 where logits and out stay in L2 from call to call); one block's 15 rows 14.9 us and rows with
+// histories of 30000 tokens 50: the latency of two launches and, of the names, of a history's atomics, their ranks and the
+// named tokens' values. (In the rules below each pair of figures was measured side by side.)
 // (One kernel that kept a row's slices in the registers or shared memory of a cluster took 792 us for the first:
 // barriers, and 27 instructions a token.)
 //
