@@ -20,9 +20,9 @@
 //     the K-th largest of 32 groups' maxima. The few lanes whose key reaches it are read once more, and the K best of
 //     what reaches the bound there, and of the named, are ranked by (value, lower token). Where more reach it than can be
 //     ranked (equal values; strong penalties for a history that names nearly every lane), the best of each of 1024
-//     shares of them give a nearer bound, for two passes more. K rounds search a row for few tokens, or where its own fall
-//     into few shares. (63 rows of 32771 with 30000 generated tokens, K = 16: 47 us under penalties of 1.1, 0.1 and 0.1, 92
-//     under 1.5, 1 and 1; in K rounds 222.)
+//     shares of them give a nearer bound, for two passes more; a row of which up to four tokens are wanted, or whose tokens
+//     fall into few shares, is searched in K rounds instead. (63 rows of 32771 with 30000 generated tokens, K = 16: 47 us
+//     under penalties of 1.1, 0.1 and 0.1, 92 under 1.5, 1 and 1; in K rounds 222.)
 // What bounds it: 64 x 15 rows of 248320 fp32 tokens take 168 us, 0.85 of the copy rate; 64 bf16 rows under masks, adjusted
 // logits wanted, 30 us (25 where logits and out stay in L2 from call to call); one block's 15 rows 14.9 us and rows with
 // histories of 30000 tokens 50: the latency of two launches and, of the names, of a history's atomics, their ranks and the
@@ -129,15 +129,16 @@ __device__ __forceinline__ void for_history(const int32_t* hist, int len, F f) {
 // the row is among its first 64 where they are drafted); else -1.
 __device__ __forceinline__ int ragged_request(const LogitsTopk& r, int m, bool& late) {
   int lo = 0, hi = r.B - 1;
+  // (ordinary loads: the spans may be what a page plan in front has just written)
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(r.row_off + mid) <= m)
+    if (r.row_off[mid] <= m)
       lo = mid;
     else
       hi = mid - 1;
   }
-  const int first = __ldg(r.row_off + lo);
-  const bool in = first >= 0 && first <= m && m < __ldg(r.row_off + lo + 1);
+  const int first = r.row_off[lo];
+  const bool in = first >= 0 && first <= m && m < r.row_off[lo + 1];
   late = in && r.tokens != nullptr && m - first >= kTreeRows;
   return in && !late ? lo : -1;
 }
@@ -148,8 +149,8 @@ __device__ __forceinline__ TreeLines request_lines(const PickArgs& a, int b, int
   rows = a.each;
   first = b * a.each;
   if (a.each == 0) {
-    first = __ldg(r.row_off + b);
-    rows = first < 0 ? 0 : min(__ldg(r.row_off + b + 1), r.M) - first;
+    first = r.row_off[b];
+    rows = first < 0 ? 0 : min(r.row_off[b + 1], r.M) - first;
   }
   rows = min(rows, kTreeRows);
   int parent[2];
@@ -166,7 +167,7 @@ __device__ __forceinline__ void map_rows(const PickArgs& a, int x, int ctas) {
   const LogitsTopk& r = a.r;
   const int m = x * kStreamThreads + static_cast<int>(threadIdx.x);
   for (int b = m; b < r.B; b += ctas * kStreamThreads) {
-    const int lo = __ldg(r.row_off + b), hi = __ldg(r.row_off + b + 1);
+    const int lo = r.row_off[b], hi = r.row_off[b + 1];
     if (lo < 0 || hi < lo || hi > r.M) record(a.err, DFLASH2_ERR_INVALID_ARG);
   }
   if (m >= r.M) return;
@@ -413,7 +414,7 @@ struct PickRow {
 __device__ __forceinline__ PickRow pick_row(const PickArgs& a, int m) {
   PickRow p;
   p.request = a.each > 0 ? m / a.each : a.request[m];
-  p.first = a.each > 0 ? p.request * a.each : (p.request >= 0 ? __ldg(a.r.row_off + p.request) : 0);
+  p.first = a.each > 0 ? p.request * a.each : (p.request >= 0 ? a.r.row_off[p.request] : 0);
   p.missing = p.request >= 0 && a.r.tokens != nullptr && a.line[m] == 0ull;
   return p;
 }
@@ -773,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 512 ? 1536 / kThreads : 
       if (before < r.K) s.best[before] = mine;
     }
     __syncthreads();
-  } else {  // (tokens of few shares)
+  } else {  // (few wanted, or tokens of few shares)
     unsigned long long last = ~0ull;
 #pragma unroll 1
     for (int k = 0; k < r.K; ++k) {
